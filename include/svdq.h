@@ -330,6 +330,84 @@ int svdq_calibrate_scale(const void* x, int64_t B, int64_t M, int64_t ldx, const
                          size_t workspace_bytes, svdq_stream_t stream);
 
 /* --------------------------------------------------------------------------------------
+ * MXFP4 tensors made on the device. An MXFP4 tensor of rows x K holds Q(x) of a matrix whose
+ * products sum over K: per block of 32 consecutive elements of a row one power of two 2^e, the
+ * smallest with max|x| <= 6 * 2^e (e in [-127, 127], E8M0 byte e + 127), and the E2M1 codes of
+ * x / 2^e rounded to nearest, ties to the even code ([MS] step 2, the rule of svdq_linear's
+ * activations without a smoothing scale). A block with an infinity or a NaN gets the byte 255
+ * (NaN) and reads as NaN, and so does every output that it enters.
+ *
+ * Two caller-owned device arrays, both 256-byte aligned, of svdq_mx_layout's sizes, in the
+ * layouts of SVDQ_SEC_RCODES and SVDQ_SEC_RSCALES with Kp = K rounded up to 256: the codes in
+ * 1 KB tiles of 16 rows x 128 codes (rows rounded up to 16), the scale bytes in 256-byte tiles
+ * of 64 rows x 4 blocks (rows rounded up to 64). The padding along K is written as zeros; the
+ * padding rows are neither written nor read.
+ *
+ * dtype is SVDQ_F32, SVDQ_BF16 or SVDQ_F16 (the other calls of this header take no SVDQ_F16).
+ * Sizes are 1 .. 2^30, and the arrays' sizes are what memory holds: offsets are 64-bit. The
+ * calls keep no state; two calls on two streams are independent when their workspaces are.
+ * ------------------------------------------------------------------------------------ */
+enum { SVDQ_F16 = 3 };
+typedef enum {
+  SVDQ_ACT_SILU = 0,      /* g / (1 + e^-g) */
+  SVDQ_ACT_GELU = 1,      /* g * Phi(g), the normal distribution function */
+  SVDQ_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+  SVDQ_ACT_RELU = 3       /* max(g, 0) */
+} svdq_act;
+
+/* Bytes of the two arrays of a rows x K tensor. Errors: EINVAL. */
+int svdq_mx_layout(int64_t rows, int64_t K, size_t* code_bytes, size_t* scale_bytes);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_mx_quantize — Q(x) and / or Q(x^T) of x [R, C] (strides sr, sc in elements, any sign
+ * of neither: >= 0) in one pass. codes / scales: the R x C tensor (blocks along C); codes_t /
+ * scales_t: the C x R tensor (blocks along R), as the other operand order or a backward
+ * product wants it. Either pair may be NULL, not both.
+ * Errors: EINVAL (shape, strides, alignment, nothing to do), EDTYPE, EHIP.
+ * ------------------------------------------------------------------------------------ */
+int svdq_mx_quantize(const void* x, int64_t R, int64_t C, int64_t sr, int64_t sc, int dtype, void* codes,
+                     void* scales, void* codes_t, void* scales_t, svdq_stream_t stream);
+
+/* svdq_mx_dequantize — the values of a rows x K tensor, rounded to dtype (exact in f32 and
+ * bf16 while below 2^128), out [rows, K] with row stride ldo. Errors as above. */
+int svdq_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, int dtype, void* out,
+                       int64_t ldo, svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_mx_matmul — Y = D( A B^T + bias ) of two MXFP4 tensors a [M, K] and b [N, K]: block-scaled
+ * FP4 matrix cores, float32 sums, one rounding to dtype. bias: [N] of dtype, or NULL.
+ * y: [M, N] of dtype, row stride ldy >= N.
+ * Errors: EINVAL (shape, stride, alignment), EDTYPE, EHIP.
+ * ------------------------------------------------------------------------------------ */
+int svdq_mx_matmul(const void* a_codes, const void* a_scales, int64_t M, const void* b_codes, const void* b_scales,
+                   int64_t N, int64_t K, const void* bias, int dtype, void* y, int64_t ldy, svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_mx_gated — the gated projections of a feed-forward block in one kernel:
+ *   [g | u] = A W^T,  h = D( act(g) * u )
+ * a [M, K]; w [2F, K]: the F gate rows, then the F up rows. act is applied to the float32 sums.
+ * h: [M, F], row stride ldh >= F. gu: NULL, or [M, 2F] (row stride ldgu >= 2F) receiving
+ * D(g) | D(u) for svdq_mx_gated_grad. Errors: EINVAL, EDTYPE, EHIP.
+ * ------------------------------------------------------------------------------------ */
+int svdq_mx_gated(const void* a_codes, const void* a_scales, int64_t M, const void* w_codes, const void* w_scales,
+                  int64_t F, int64_t K, int act, int dtype, void* h, int64_t ldh, void* gu, int64_t ldgu,
+                  svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_mx_gated_grad — the gradients of the pre-activations, quantised for the two products
+ * behind them in one pass: with d = [dg | du], dg = dh * u * act'(g), du = dh * act(g),
+ *   codes / scales:     Q(d)   [M, 2F]  (times the weight quantised along 2F: dx)
+ *   codes_t / scales_t: Q(d^T) [2F, M]  (with the input quantised along M: dw)
+ * The codes are those of the formulas in binary64 on the given dh and gu (binary32, and
+ * binary64 where that lies too near a border between two codes); a magnitude below 2^-126
+ * counts as float32 keeps it. Either pair may be NULL, not both.
+ * dh: [M, F] row stride ldh >= F; gu: [M, 2F] row stride ldgu >= 2F; both of dtype.
+ * Errors: EINVAL, EDTYPE, EHIP.
+ * ------------------------------------------------------------------------------------ */
+int svdq_mx_gated_grad(const void* dh, int64_t ldh, const void* gu, int64_t ldgu, int64_t M, int64_t F, int act,
+                       int dtype, void* codes, void* scales, void* codes_t, void* scales_t, svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
  * Kernel timing (profiling aid; not on any page). Between svdq_profile_begin and
  * svdq_profile_end, each svdq_linear call records a HIP event pair around every kernel it
  * launches whose stage bit is set in stage_mask, on the call's stream, for up to max_calls

@@ -48,12 +48,21 @@ SIGNATURES = {
     "svdq_profile_end": (c_int, [ctypes.POINTER(ctypes.c_float), c_int, ctypes.POINTER(c_int)]),
     "svdq_ceiling": (c_int, [c_int, ctypes.c_int64, c_vp, ctypes.c_size_t, c_vp, ctypes.c_size_t, c_vp,
                              ctypes.POINTER(ctypes.c_double)]),
+    "svdq_mx_layout": (c_int, [c_i64, c_i64, ctypes.POINTER(c_sz), ctypes.POINTER(c_sz)]),
+    "svdq_mx_quantize": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "svdq_mx_dequantize": (c_int, [c_vp, c_vp, c_i64, c_i64, c_int, c_vp, c_i64, c_vp]),
+    "svdq_mx_matmul": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_vp, c_i64, c_vp]),
+    "svdq_mx_gated": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_vp, c_i64, c_vp, c_i64,
+                              c_vp]),
+    "svdq_mx_gated_grad": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_vp, c_vp, c_vp, c_vp,
+                                   c_vp]),
 }
 NSTAGES = 4
 STAGE_NAMES = ("amax", "act_quant_down", "down_reduce", "gemm")
 
 SVDQ_OK, SVDQ_EINVAL, SVDQ_EDTYPE, SVDQ_EUNSUPPORTED, SVDQ_EHIP = 0, 1, 2, 3, 4
 SVDQ_F32, SVDQ_BF16, SVDQ_F64 = 0, 1, 2
+SVDQ_F16 = 3  # svdq_mx_* only
 SVDQ_FMT_INT, SVDQ_FMT_MX = 0, 1
 SEC_SCALE, SEC_RCODES, SEC_RSCALES, SEC_L1T, SEC_L2T, SEC_RECIP, SEC_GLOBAL, SEC_END = 0, 1, 2, 3, 4, 5, 6, 7
 NSEC = 8

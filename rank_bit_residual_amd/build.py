@@ -31,6 +31,9 @@ HIP_SOURCES = {
     "k_calib.hip": [],
     "k_svd.hip": [],
     "k_ceiling.hip": [],
+    "k_mx_quant.hip": ["-ffp-contract=off"],
+    "k_mx_gemm.hip": [],
+    "mx_capi.hip": [],
     "capi.hip": [],
 }
 CXX = os.environ.get("CXX", "g++")

@@ -1,0 +1,76 @@
+// MXFP4 tensors made on the device: parameter blocks and launchers of k_mx_quant.hip and
+// k_mx_gemm.hip (called from mx_capi.hip). Every launcher enqueues on `stream` and returns the
+// hipError_t of the launch; arguments were checked by the caller.
+//
+// An MXFP4 tensor of `rows` x K (blocks of 32 along K) is two arrays. With kq = 2 ceil(K / 256)
+// stages of 128 codes per row (codes past K are 0, their blocks' scale byte 0):
+//   codes   1 KB tiles of 16 rows x 128 codes (mx_code_tile_offset), rows rounded up to 16
+//   scales  E8M0 bytes, 256-byte tiles of 64 rows x 4 blocks (mx_scale_tiled_index), rows
+//           rounded up to 64
+// Both are the layouts of the prepared MXFP4 weights. Rows past `rows` are neither written nor
+// read. A scale byte of 255 is NaN: a block that held an infinity or a NaN (its codes are 0).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace svdq {
+
+inline int64_t mx_kq(int64_t K) { return (K + 255) / 256 * 2; }
+inline int64_t mx_code_bytes(int64_t rows, int64_t K) { return (rows + 15) / 16 * mx_kq(K) * 1024; }
+inline int64_t mx_scale_bytes(int64_t rows, int64_t K) { return (rows + 63) / 64 * mx_kq(K) * 256; }
+
+// One MXFP4 tensor to write, or codes == NULL.
+struct MxOut {
+  uint8_t* codes;
+  uint8_t* scales;
+  int kq;
+};
+
+struct MxQuantParams {
+  const void* x;  // element (r, c) at r * sr + c * sc
+  int64_t R, C, sr, sc;
+  MxOut rows;  // R x C
+  MxOut cols;  // C x R: the transpose
+};
+
+struct MxDequantParams {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int kq;
+  int64_t rows, K;
+  void* out;
+  int64_t ldo;
+};
+
+struct MxGemmParams {
+  const uint8_t* a_codes;
+  const uint8_t* a_scales;
+  const uint8_t* b_codes;
+  const uint8_t* b_scales;
+  int M, N;    // output rows and columns
+  int b_rows;  // rows of b: N, or 2 N for the gated product (gate rows, then up rows)
+  int kq;
+  const void* bias;  // [N] or NULL
+  void* y;           // [M][ldy]
+  int64_t ldy;
+  void* gu;  // gated: [M][ldgu] pre-activations (gate, then up), or NULL
+  int64_t ldgu;
+  int act;
+};
+
+struct MxGradParams {
+  const void* dh;  // [M][ldh]
+  const void* gu;  // [M][ldgu]: gate pre-activations, then up
+  int64_t M, F, ldh, ldgu;
+  int act;
+  MxOut rows;  // M x 2F: [dg | du]
+  MxOut cols;  // 2F x M: the transpose
+};
+
+hipError_t launch_mx_quantize(const MxQuantParams& p, int dtype, hipStream_t stream);
+hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t stream);
+hipError_t launch_mx_gated_grad(const MxGradParams& p, int dtype, hipStream_t stream);
+hipError_t launch_mx_product(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream);
+
+}  // namespace svdq

@@ -1,0 +1,120 @@
+// Device helpers of the MXFP4-tensor kernels: storage types with conversions that keep NaN,
+// eight codes at a time from packed values, and the gated activations with their derivatives.
+#pragma once
+
+#include "device_common.h"
+
+#include "../../include/svdq.h"
+
+namespace svdq {
+namespace dev {
+
+// Storage types: `pair` is two 16-bit values in one word (the lower index in the low half).
+struct MxF32 {
+  typedef float T;
+  static constexpr int size = 4;
+  __device__ static inline float load(T v) { return v; }
+  __device__ static inline T store(float v) { return v; }
+};
+struct MxBF16 {
+  typedef uint16_t T;
+  static constexpr int size = 2;
+  __device__ static inline float load(T v) { return __uint_as_float((u32)v << 16); }
+  __device__ static inline T store(float v) { return (T)pack_bf16x2(v, v); }
+  __device__ static inline u32 pack(float a, float b) { return pack_bf16x2(a, b); }
+  // v_cvt_scalef32_pk_fp4_bf16 over four pairs, see fp4_pack8_bf16
+  __device__ static inline u32 codes8(const u32* pairs, float scale) { return fp4_pack8_bf16(pairs, scale); }
+  // larger of two non-negative values' bits, in both halves at once
+  static constexpr u32 inf = 0x7F80;
+};
+struct MxF16 {
+  typedef uint16_t T;
+  static constexpr int size = 2;
+  __device__ static inline float load(T v) { return (float)__builtin_bit_cast(_Float16, v); }
+  __device__ static inline T store(float v) { return __builtin_bit_cast(T, (_Float16)v); }
+  __device__ static inline u32 pack(float a, float b) { return (u32)store(a) | ((u32)store(b) << 16); }
+  __device__ static inline u32 codes8(const u32* pairs, float scale) {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    u32 r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(h2, pairs[0]), scale, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(h2, pairs[1]), scale, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(h2, pairs[2]), scale, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(h2, pairs[3]), scale, 3);
+    return r;
+  }
+  static constexpr u32 inf = 0x7C00;
+};
+
+// Scale byte of a block from the bits of its largest magnitude as float32; 255 (NaN) from
+// infinity on.
+__device__ inline u32 mx_scale_byte(u32 amax_bits) {
+  return amax_bits >= 0x7F800000u ? 255u : (u32)(mx_exponent(__uint_as_float(amax_bits)) + 127);
+}
+// 2^e of a scale byte below 255.
+__device__ inline float mx_scale_value(u32 byte) { return pow2f((int)byte - 127); }
+
+// ---- gated activations ------------------------------------------------------------------
+// act(g) and act'(g), and bounds on the relative error of act and the absolute error of act'
+// when F is float (unused for double). Where a factor nears the bottom of the float32 range the
+// bound is the value itself.
+//   silu       g s,  s = 1 / (1 + e^-w), w = g
+//   gelu_tanh  g s with w = 2 sqrt(2 / pi) (g + 0.044715 g^3), which equals
+//              g (1 + tanh(w / 2)) / 2 without its cancellation for negative g
+//     act' = s (1 + g (1 - s) w'). v_exp_f32 on w log2(e) is off by (2 + |w|) 2^-23 relative,
+//     the sigmoid by at most (2 + |w|) 2^-22; 1 - s by that times s absolutely, which g w'
+//     multiplies: together act' is within s (1 + |g w'|) (3 + |w|) 2^-21.
+//   gelu       g P, P = erfc(-g / sqrt 2) / 2; act' = P + g e^(-g^2 / 2) / sqrt(2 pi). Rounding
+//     the argument moves erfc by g^2 2^-24 relative, erfcf and the exponential by a few ulps.
+//   relu       max(g, 0), 1 where g > 0
+// NaN and infinite g give NaN in at least one of the two.
+template <class F>
+struct ActValue {
+  F a, d;
+  float rel_a, abs_d;
+};
+
+__device__ inline float act_exp(float v) { return __expf(v); }
+__device__ inline double act_exp(double v) { return exp(v); }
+__device__ inline float act_rcp(float v) { return __builtin_amdgcn_rcpf(v); }
+__device__ inline double act_rcp(double v) { return 1.0 / v; }
+__device__ inline float act_erfc(float v) { return erfcf(v); }
+__device__ inline double act_erfc(double v) { return erfc(v); }
+
+template <int ACT, class F>
+__device__ inline ActValue<F> act_value(F g) {
+  ActValue<F> r;
+  if constexpr (ACT == SVDQ_ACT_RELU) {
+    r.a = g < F(0) ? F(0) : g;
+    r.d = g > F(0) ? F(1) : (g == g ? F(0) : g);
+    r.rel_a = 0x1p-22f;
+    r.abs_d = 0x1p-22f;
+  } else if constexpr (ACT == SVDQ_ACT_GELU) {
+    const F p = F(0.5) * act_erfc(F(-0.70710678118654752440) * g);
+    const F q = g * (F(0.39894228040143267794) * act_exp(F(-0.5) * g * g));
+    r.a = g * p;
+    r.d = p + q;
+    const float g2 = (float)(g * g);
+    r.rel_a = g < F(-10) ? 1.f : (3.f + g2) * 0x1p-20f;
+    r.abs_d = ((float)p + fabsf((float)q)) * r.rel_a;
+  } else {
+    F w = g, dw = F(1), gc = g;
+    if constexpr (ACT == SVDQ_ACT_GELU_TANH) {
+      // past 30 the sigmoid is 0 or 1 and w' times 1 - s no longer counts, but g^3 could overflow
+      gc = g > F(30) ? F(30) : (g < F(-30) ? F(-30) : g);
+      const F c = F(1.59576912160573071176);
+      w = c * (gc + F(0.044715) * (gc * gc * gc));
+      dw = c * (F(1) + F(0.134145) * (gc * gc));
+    }
+    const F s = act_rcp(F(1) + act_exp(-w));
+    const F t = (gc * dw) * (F(1) - s);
+    r.a = g * s;
+    r.d = s * (F(1) + t);
+    const float ew = w < F(-60) ? 1.f : (3.f + fabsf((float)w)) * 0x1p-21f;
+    r.rel_a = ew;
+    r.abs_d = (float)s * (1.f + fabsf((float)(gc * dw))) * ew;
+  }
+  return r;
+}
+
+}  // namespace dev
+}  // namespace svdq

@@ -1,0 +1,156 @@
+"""MXFP4 tensor operators without a GPU: the oracle's own checks, the layout query and every refusal."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import rank_bit_residual_amd as R
+from oracle import mx as X
+from rank_bit_residual_amd import _lib
+
+A = 1 << 20  # a 256-byte aligned address that no refused call reads
+
+
+# ----------------------------------------------------------------------------- oracle
+def test_oracle_blocks():
+    x = np.zeros((3, 70))
+    x[0, 3] = 6.0
+    x[1, 40] = 6.0000001
+    x[2, 69] = np.inf
+    codes, s = X.quantize(x)
+    assert s.tolist() == [[127, 0, 0], [0, 128, 0], [0, 0, 255]]
+    assert codes[0, 3] == 7 and codes[1, 40] == 5 and not codes[2].any()
+    v = X.values(x)
+    assert np.isnan(v[2, 64:]).all() and not np.isnan(v[:2]).any() and v[0, 3] == 6
+
+
+@pytest.mark.parametrize("name", X.ACTS)
+def test_oracle_gradient_against_differences(name):
+    """act' against a central difference: its error is h^2 / 6 |act'''| (below 1 here) plus the rounding
+    2^-52 |act| / h."""
+    g = np.linspace(-6, 6, 193) + 1e-3
+    h = 1e-4
+    diff = (X.act(name, g + h) - X.act(name, g - h)) / (2 * h)
+    assert np.abs(diff - X.act_grad(name, g)).max() < h * h / 2 + 2.0**-52 * 6 / h
+
+
+def test_oracle_gated_gradient_against_differences():
+    rng = np.random.default_rng(3)
+    gu, dh = rng.standard_normal((4, 10)), rng.standard_normal((4, 5))
+    h = 1e-5
+    for name in X.ACTS:
+        d = X.gated_grad(dh, gu, name)
+        for j in range(10):
+            step = np.zeros_like(gu)
+            step[:, j] = h
+            f = lambda z: (dh * X.act(name, z[:, :5]) * z[:, 5:]).sum(1)  # noqa: E731
+            assert np.allclose((f(gu + step) - f(gu - step)) / (2 * h), d[:, j], atol=1e-8)
+
+
+# ----------------------------------------------------------------------------- C ABI
+def _layout(rows, K):
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    st = _lib.load().svdq_mx_layout(rows, K, ctypes.byref(a), ctypes.byref(b))
+    return st, a.value, b.value
+
+
+def test_layout():
+    assert _layout(1, 1) == (0, 2 * 1024, 2 * 256)
+    assert _layout(17, 256) == (0, 2 * 2 * 1024, 2 * 256)
+    assert _layout(65, 257) == (0, 5 * 4 * 1024, 2 * 4 * 256)
+    assert _layout(1 << 20, 1 << 16) == (0, 1 << 35, 1 << 31)  # past 32 bits
+    for rows, K in ((0, 4), (4, 0), (-1, 4), ((1 << 30) + 1, 4), (4, (1 << 30) + 1)):
+        assert _layout(rows, K)[0] == _lib.SVDQ_EINVAL
+    assert _lib.load().svdq_mx_layout(4, 4, None, None) == _lib.SVDQ_EINVAL
+
+
+def _refused(status, st):
+    assert st == status, (st, _lib.load().svdq_last_error())
+    assert _lib.load().svdq_last_error()
+
+
+F32, BF16, F64, F16 = _lib.SVDQ_F32, _lib.SVDQ_BF16, _lib.SVDQ_F64, _lib.SVDQ_F16
+EINVAL, EDTYPE = _lib.SVDQ_EINVAL, _lib.SVDQ_EDTYPE
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=F64), EDTYPE), (dict(dtype=7), EDTYPE), (dict(R=0), EINVAL), (dict(C=0), EINVAL),
+    (dict(C=(1 << 30) + 1), EINVAL), (dict(x=None), EINVAL), (dict(x=A + 1), EINVAL), (dict(sr=-1), EINVAL),
+    (dict(sc=-4), EINVAL), (dict(codes=None), EINVAL), (dict(scales=None), EINVAL), (dict(codes=A + 16), EINVAL),
+    (dict(scales_t=None), EINVAL), (dict(codes_t=A + 128), EINVAL),
+    (dict(codes=None, scales=None, codes_t=None, scales_t=None), EINVAL),
+])
+def test_quantize_refusals(change, status):
+    a = dict(x=A, R=4, C=40, sr=40, sc=1, dtype=BF16, codes=A, scales=A, codes_t=A, scales_t=A)
+    a.update(change)
+    _refused(status, _lib.load().svdq_mx_quantize(*a.values(), None))
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=F64), EDTYPE), (dict(rows=0), EINVAL), (dict(K=-3), EINVAL), (dict(codes=None), EINVAL),
+    (dict(scales=A + 4), EINVAL), (dict(out=None), EINVAL), (dict(out=A + 1), EINVAL), (dict(ldo=39), EINVAL),
+])
+def test_dequantize_refusals(change, status):
+    a = dict(codes=A, scales=A, rows=4, K=40, dtype=F16, out=A, ldo=40)
+    a.update(change)
+    _refused(status, _lib.load().svdq_mx_dequantize(*a.values(), None))
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=F64), EDTYPE), (dict(M=0), EINVAL), (dict(N=0), EINVAL), (dict(K=0), EINVAL), (dict(ac=None), EINVAL),
+    (dict(asc=None), EINVAL), (dict(bc=A + 8), EINVAL), (dict(bs=None), EINVAL), (dict(bias=A + 2), EINVAL),
+    (dict(y=None), EINVAL), (dict(y=A + 2), EINVAL), (dict(ldy=7), EINVAL),
+])
+def test_matmul_refusals(change, status):
+    a = dict(ac=A, asc=A, M=4, bc=A, bs=A, N=8, K=40, bias=None, dtype=F32, y=A, ldy=8)
+    a.update(change)
+    _refused(status, _lib.load().svdq_mx_matmul(*a.values(), None))
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=F64), EDTYPE), (dict(M=0), EINVAL), (dict(F=0), EINVAL), (dict(F=1 << 30), EINVAL), (dict(K=0), EINVAL),
+    (dict(act=4), EINVAL), (dict(act=-1), EINVAL), (dict(ac=None), EINVAL), (dict(ws=None), EINVAL), (dict(h=None), EINVAL),
+    (dict(ldh=7), EINVAL), (dict(gu=A, ldgu=15), EINVAL), (dict(gu=A + 1, ldgu=16), EINVAL),
+])
+def test_gated_refusals(change, status):
+    a = dict(ac=A, asc=A, M=4, wc=A, ws=A, F=8, K=40, act=0, dtype=BF16, h=A, ldh=8, gu=None, ldgu=0)
+    a.update(change)
+    _refused(status, _lib.load().svdq_mx_gated(*a.values(), None))
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=F64), EDTYPE), (dict(M=0), EINVAL), (dict(F=0), EINVAL), (dict(F=1 << 30), EINVAL), (dict(act=9), EINVAL),
+    (dict(dh=None), EINVAL), (dict(ldh=7), EINVAL), (dict(gu=None), EINVAL), (dict(ldgu=15), EINVAL), (dict(gu=A + 1), EINVAL),
+    (dict(codes=None), EINVAL), (dict(scales_t=A + 1), EINVAL),
+    (dict(codes=None, scales=None, codes_t=None, scales_t=None), EINVAL),
+])
+def test_gated_grad_refusals(change, status):
+    a = dict(dh=A, ldh=8, gu=A, ldgu=16, M=4, F=8, act=0, dtype=BF16, codes=A, scales=A, codes_t=A, scales_t=A)
+    a.update(change)
+    _refused(status, _lib.load().svdq_mx_gated_grad(*a.values(), None))
+
+
+# ----------------------------------------------------------------------------- binding
+def _fake(rows, cols, short=0):
+    _, a, b = _layout(rows, cols)
+    return R.MxTensor(torch.zeros(a - short, dtype=torch.uint8), torch.zeros(b, dtype=torch.uint8), rows, cols)
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_types():
+    x = torch.zeros(4, 64)
+    for call in (lambda: R.mx_quantize(x), lambda: R.mx_dequantize(_fake(4, 64)), lambda: R.mx_matmul(x, _fake(4, 64)),
+                 lambda: R.mx_gated(x, _fake(8, 64)), lambda: R.mx_gated_grad(x, torch.zeros(4, 128))):
+        with pytest.raises(RuntimeError):
+            call()
+    for call in (lambda: R.mx_quantize(x.numpy()), lambda: R.mx_dequantize(x), lambda: R.mx_matmul(x, x),
+                 lambda: R.mx_gated(x, x), lambda: R.mx_gated_backward(x, x, x, x)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        R.mx_dequantize(_fake(20, 64, short=1))
+    with pytest.raises(ValueError):
+        R.mx_gated(x, _fake(8, 64), act="swish")
+    with pytest.raises(ValueError):
+        R.mx_gated_grad(x, x, act="tanh")
