@@ -373,25 +373,32 @@ int svdq_mx_quantize(const void* x, int64_t R, int64_t C, int64_t sr, int64_t sc
 int svdq_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, int dtype, void* out,
                        int64_t ldo, svdq_stream_t stream);
 
+/* Workspace of svdq_mx_matmul (gated = 0) and svdq_mx_gated (gated = 1, N = F): device scratch of any
+ * contents for the calls that split a long K over the chip, 0 bytes for the others. Calls that may overlap
+ * in time need one each. Errors: EINVAL. */
+int svdq_mx_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated, size_t* bytes_out);
+
 /* --------------------------------------------------------------------------------------
  * svdq_mx_matmul — Y = D( A B^T + bias ) of two MXFP4 tensors a [M, K] and b [N, K]: block-scaled
  * FP4 matrix cores, float32 sums, one rounding to dtype. bias: [N] of dtype, or NULL.
- * y: [M, N] of dtype, row stride ldy >= N.
- * Errors: EINVAL (shape, stride, alignment), EDTYPE, EHIP.
+ * y: [M, N] of dtype, row stride ldy >= N. K is at most 2^27. workspace: 256-byte aligned, at least
+ * svdq_mx_workspace_bytes (NULL where that is 0).
+ * Errors: EINVAL (shape, stride, alignment, workspace), EDTYPE, EHIP.
  * ------------------------------------------------------------------------------------ */
 int svdq_mx_matmul(const void* a_codes, const void* a_scales, int64_t M, const void* b_codes, const void* b_scales,
-                   int64_t N, int64_t K, const void* bias, int dtype, void* y, int64_t ldy, svdq_stream_t stream);
+                   int64_t N, int64_t K, const void* bias, int dtype, void* y, int64_t ldy, void* workspace,
+                   size_t workspace_bytes, svdq_stream_t stream);
 
 /* --------------------------------------------------------------------------------------
  * svdq_mx_gated — the gated projections of a feed-forward block in one kernel:
  *   [g | u] = A W^T,  h = D( act(g) * u )
  * a [M, K]; w [2F, K]: the F gate rows, then the F up rows. act is applied to the float32 sums.
  * h: [M, F], row stride ldh >= F. gu: NULL, or [M, 2F] (row stride ldgu >= 2F) receiving
- * D(g) | D(u) for svdq_mx_gated_grad. Errors: EINVAL, EDTYPE, EHIP.
+ * D(g) | D(u) for svdq_mx_gated_grad. K and workspace as above. Errors: EINVAL, EDTYPE, EHIP.
  * ------------------------------------------------------------------------------------ */
 int svdq_mx_gated(const void* a_codes, const void* a_scales, int64_t M, const void* w_codes, const void* w_scales,
                   int64_t F, int64_t K, int act, int dtype, void* h, int64_t ldh, void* gu, int64_t ldgu,
-                  svdq_stream_t stream);
+                  void* workspace, size_t workspace_bytes, svdq_stream_t stream);
 
 /* --------------------------------------------------------------------------------------
  * svdq_mx_gated_grad — the gradients of the pre-activations, quantised for the two products

@@ -51,9 +51,11 @@ SIGNATURES = {
     "svdq_mx_layout": (c_int, [c_i64, c_i64, ctypes.POINTER(c_sz), ctypes.POINTER(c_sz)]),
     "svdq_mx_quantize": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "svdq_mx_dequantize": (c_int, [c_vp, c_vp, c_i64, c_i64, c_int, c_vp, c_i64, c_vp]),
-    "svdq_mx_matmul": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_vp, c_i64, c_vp]),
+    "svdq_mx_workspace_bytes": (c_int, [c_i64, c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]),
+    "svdq_mx_matmul": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_vp, c_i64, c_vp, c_sz,
+                               c_vp]),
     "svdq_mx_gated": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_vp, c_i64, c_vp, c_i64,
-                              c_vp]),
+                              c_vp, c_sz, c_vp]),
     "svdq_mx_gated_grad": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_vp, c_vp, c_vp, c_vp,
                                    c_vp]),
 }

@@ -5,17 +5,27 @@
 // lane's own E8M0 byte: exactly one block of an MXFP4 tensor. Products of codes and their scales are
 // exact; sums are float32.
 //
-// Simplest form: a wave owns a 32 x 32 output tile and reads its operands straight from memory.
+// Tiles (k_mx_tile): a BM x BN output tile per block of 4 x 2 waves, two per SIMD. K advances in stages of
+// 128 codes (64 bytes per row), which land in a ring of four LDS buffers through direct global->LDS
+// loads issued two stages ahead; a wave waits on its own loads, one barrier per stage publishes them,
+// and a stage's operands are read from LDS under the previous slice's MFMAs. Both operands come in
+// 1 KB tiles of 16 rows, one contiguous kilobyte per wave-wide load. LDS rows are 64 bytes; chunk c of row r sits
+// at c ^ ((r >> 2) & 3), so that 16 consecutive rows' 16-byte reads meet distinct banks.
+// The gated product is the same kernel on a B tile that holds, for each wave, half gate rows and half up rows of
+// the same output columns: a lane ends with g and u of its outputs in registers, and the activation and the
+// product are its epilogue.
+#include <atomic>
 #include <type_traits>
 
 #include "mx.h"
 #include "mx_device.h"
+#include "gemm_pipe.h"
 
 namespace svdq {
 namespace dev {
 
 template <class F>
-__device__ inline void with_act(int act, F f) {
+__device__ __forceinline__ void with_act(int act, F f) {
   switch (act) {
     case SVDQ_ACT_SILU: f(std::integral_constant<int, SVDQ_ACT_SILU>()); break;
     case SVDQ_ACT_GELU: f(std::integral_constant<int, SVDQ_ACT_GELU>()); break;
@@ -24,60 +34,374 @@ __device__ inline void with_act(int act, F f) {
   }
 }
 
-template <class DT, bool GATED>
-__global__ __launch_bounds__(256) void k_mx_product(MxGemmParams p, int tiles_n) {
+// ------------------------------------------------------------------------------ tiles
+template <int BM, int BN>
+struct TileCfg {
+  static constexpr int NWV = 8, WN = 2, WM = NWV / WN;
+  static constexpr int TM = BM / WM, TN = BN / WN;  // per-wave tile
+  static constexpr int MT = TM / 32, NT = TN / 32;
+  static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;
+  static constexpr int A_PER_WAVE = A_BYTES / 1024 / NWV, B_PER_WAVE = B_BYTES / 1024 / NWV;
+  static_assert(A_PER_WAVE * NWV * 1024 == A_BYTES && B_PER_WAVE * NWV * 1024 == B_BYTES, "whole wave-wide loads");
+  static_assert(TM % 32 == 0 && TN % 64 == 0, "wave tiles are whole MFMA tiles, in gate and up halves");
+  static constexpr int SCALE_BYTES = 1024;  // 256 rows x 4 bytes per operand
+  static constexpr int STAGE = A_BYTES + B_BYTES + 2 * SCALE_BYTES;
+  static constexpr int LPS = A_PER_WAVE + B_PER_WAVE + 1;  // loads per stage and wave
+  static constexpr int NS = 4, DIST = 2;                   // ring depth, stages in flight ahead
+  static constexpr int SMEM = NS * STAGE;
+};
+
+__device__ inline int lds_swizzle(int row, int chunk) { return row * 64 + ((chunk ^ ((row >> 2) & 3)) << 4); }
+
+__device__ inline int records(int64_t bytes) { return (int)(u32)(bytes < 0xFFFFFFFFll ? bytes : 0xFFFFFFFFll); }
+
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Writes a block's tile of VT x values from the lanes of the waves to out[r0 .., c0 ..] (row stride ld, limits rows x
+// cols): value(i, j, v) is this lane's accumulator entry of 32 x 32 tile (i, j), of NJ column tiles per
+// wave. Rounded, staged through the idle ring and stored 16 bytes a lane (at any alignment). The output is not
+// read again here, so it streams past the caches.
+template <class DT, class C, int BM, int NJ, class V>
+__device__ __forceinline__ void store_tile(uint8_t* smem, typename DT::T* out, int64_t ld, int rows, int cols, int r0,
+                                           int c0, int wm, int wn, int lane, V value) {
   typedef typename DT::T T;
-  const int t = threadIdx.x, lane = t & 63, l32 = lane & 31, g = lane >> 5;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (t >> 6);
-  const int64_t tm = id / tiles_n;
-  const int64_t m0 = tm * 32, n0 = (id - tm * tiles_n) * 32;
-  if (m0 >= p.M) return;
-  const int64_t row = m0 + l32 < p.M ? m0 + l32 : p.M - 1;
-  const int64_t col = n0 + l32 < p.N ? n0 + l32 : p.N - 1;
-  const uint8_t* ac = p.a_codes + (((row >> 4) * p.kq) << 10) + ((row & 15) << 6) + g * 16;
-  const uint8_t* as = p.a_scales + mx_scale_tiled_index(row, 0, p.kq) + g;
-  const uint8_t *bc[2], *bs[2];
-  for (int h = 0; h < (GATED ? 2 : 1); h++) {
-    const int64_t br = col + (int64_t)h * p.N;
-    bc[h] = p.b_codes + mx_code_tile_offset(br, p.kq) + g * 16;
-    bs[h] = p.b_scales + mx_scale_tiled_index(br, 0, p.kq) + g;
-  }
-  v16f acc[2];
-  for (int v = 0; v < 16; v++) acc[0][v] = acc[1][v] = 0.f;
-  for (int s = 0; s < p.kq; s++) {
+  constexpr int W = C::WN * NJ * 32;                                    // tile columns
+  constexpr int PH = (BM * W * DT::size + C::SMEM - 1) / C::SMEM;       // phases of BM / PH rows
+  static_assert(PH == 1 || PH == 2 || PH == 4, "phases split the wave rows evenly");
+  constexpr int PR = BM / PH;
+  const int l32 = lane & 31, g = lane >> 5, t = threadIdx.x;
 #pragma unroll
-    for (int ks = 0; ks < 2; ks++) {
-      const v4i a = *reinterpret_cast<const v4i*>(ac + (int64_t)s * 1024 + 32 * ks);
-      const int sa = as[(int64_t)s * 256 + 2 * ks];
+  for (int ph = 0; ph < PH; ph++) {
+    __syncthreads();
+    if (PH == 1 || wm / (C::WM / PH) == ph) {
 #pragma unroll
-      for (int h = 0; h < (GATED ? 2 : 1); h++) {
-        const v4i b = *reinterpret_cast<const v4i*>(bc[h] + (int64_t)s * 1024 + 32 * ks);
-        const int sb = bs[h][(int64_t)s * 256 + 2 * ks];
-        acc[h] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(v8i{a[0], a[1], a[2], a[3], 0, 0, 0, 0},
-                                                                 v8i{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, acc[h], 4, 4, 0,
-                                                                 sa, 0, sb);
+      for (int i = 0; i < C::MT; i++)
+#pragma unroll
+        for (int j = 0; j < NJ; j++) {
+          const int rb = wm * C::TM + 32 * i + 4 * g - ph * PR, cb = wn * NJ * 32 + 32 * j;
+          if constexpr (DT::size == 4) {
+            float* tile = reinterpret_cast<float*>(smem);
+#pragma unroll
+            for (int v = 0; v < 16; v++) tile[(rb + 8 * (v / 4) + v % 4) * W + cb + l32] = value(i, j, v);
+          } else {
+            // rows (r, r + 1) of a column in one word; neighbouring lanes swap words and each keeps one row's
+            // pair of columns
+            const bool odd = l32 & 1;
+            const u32 sel = odd ? 0x03020706u : 0x05040100u;
+            uint16_t* tile = reinterpret_cast<uint16_t*>(smem) + (odd ? W : 0) + cb + (l32 & ~1);
+#pragma unroll
+            for (int v = 0; v < 16; v += 2) {
+              const u32 own = DT::pack(value(i, j, v), value(i, j, v + 1));
+              const u32 nb = (u32)__builtin_amdgcn_mov_dpp((int)own, 0xB1, 0xF, 0xF, true);
+              *reinterpret_cast<u32*>(tile + (rb + 8 * (v / 4) + v % 4) * W) = __builtin_amdgcn_perm(nb, own, sel);
+            }
+          }
+        }
+    }
+    __syncthreads();
+    constexpr int E = 16 / DT::size, CPR = W / E;
+    const T* tile = reinterpret_cast<const T*>(smem);
+    for (int c = t; c < PR * CPR; c += 64 * C::NWV) {
+      const int r = c / CPR, cc = (c - r * CPR) * E;
+      const int row = r0 + ph * PR + r, col = c0 + cc;
+      if (row >= rows || col >= cols) continue;
+      const v4i v = *reinterpret_cast<const v4i*>(tile + r * W + cc);
+      T* dst = out + (int64_t)row * ld + col;
+      if (col + E <= cols) {
+        __builtin_nontemporal_store(v, reinterpret_cast<v4i_any*>(dst));
+      } else {
+#pragma unroll
+        for (int q = 0; q < E; q++)
+          if (col + q < cols) dst[q] = tile[r * W + cc + q];
       }
     }
   }
-  if (n0 + l32 >= p.N) return;
-  T* y = reinterpret_cast<T*>(p.y) + n0 + l32;
-  float bias = 0.f;
-  if (!GATED && p.bias) bias = DT::load(reinterpret_cast<const T*>(p.bias)[n0 + l32]);
-#pragma unroll
-  for (int v = 0; v < 16; v++) {
-    const int64_t r = m0 + 8 * (v / 4) + 4 * g + (v % 4);
-    if (r >= p.M) continue;
+}
+
+// Block: tile `tid` of tiles_m x tiles_n, stages [s0, s1) of K (an even number, at least two). SPLIT: the
+// block's share of K, as float32 sums into its part of p.part; else the finished output.
+template <class DT, int BM, int BN, bool GATED, bool SPLIT>
+__global__ __launch_bounds__(512) void k_mx_tile(MxGemmParams p) {
+  typedef TileCfg<BM, BN> C;
+  typedef typename DT::T T;
+  constexpr int COLS = GATED ? BN / 2 : BN;  // output columns of a tile
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int l32 = lane & 31, g = lane >> 5;
+
+  // ---- tile order: blocks i, i + 8, ... share an XCD, whose blocks walk groups of 4 row tiles column by column
+  const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + COLS - 1) / COLS;
+  const int ntiles = tiles_m * tiles_n;
+  int split = 0, tid = blockIdx.x;
+  if (SPLIT) {
+    split = blockIdx.x / ntiles;
+    tid = blockIdx.x - split * ntiles;
+  }
+  if ((ntiles & 7) == 0) tid = (tid & 7) * (ntiles >> 3) + (tid >> 3);
+  const int GM = 4;
+  const int group = tid / (GM * tiles_n), gm0 = group * GM;
+  const int gsz = (tiles_m - gm0) < GM ? (tiles_m - gm0) : GM;
+  const int in_g = tid - group * GM * tiles_n;
+  const int m0 = (gm0 + in_g % gsz) * BM, n0 = (in_g / gsz) * COLS;
+  int s0 = 0, nst = p.kq;
+  if (SPLIT) {
+    const int pairs = p.kq / 2;
+    s0 = (int)((int64_t)pairs * split / p.splits) * 2;
+    nst = (int)((int64_t)pairs * (split + 1) / p.splits) * 2 - s0;
+  }
+
+  // row of b behind row rr of the B tile: gated, a wave's columns are half gate rows and half up rows
+  auto b_row = [&](int rr) {
+    int64_t r;
     if constexpr (GATED) {
-      float a = 0.f;
-      with_act(p.act, [&](auto c) { a = act_value<decltype(c)::value, float>(acc[0][v]).a; });
-      y[r * p.ldy] = DT::store(a * acc[1][v]);
+      const int w = rr / C::TN, in = rr % C::TN, half = in / (C::TN / 2);
+      r = (int64_t)n0 + w * (C::TN / 2) + in % (C::TN / 2) + (half ? p.N : 0);
+    } else {
+      r = (int64_t)n0 + rr;
+    }
+    return (int)(r < p.b_rows ? r : p.b_rows - 1);
+  };
+  auto a_row = [&](int rr) { return m0 + rr < p.M ? m0 + rr : p.M - 1; };
+
+  // ---- sources of this wave's loads: one buffer resource each, based at the 1 KB tile of its first row, so that
+  // offsets within it stay below 2 (kq + 1) KB whatever the arrays' sizes; rows past the end repeat the last
+  const int64_t a_end = (int64_t)((p.M + 15) >> 4) * p.kq << 10, b_end = (int64_t)((p.b_rows + 15) >> 4) * p.kq << 10;
+  const uint8_t *a_base[C::A_PER_WAVE], *b_base[C::B_PER_WAVE];
+  int a_rec[C::A_PER_WAVE], b_rec[C::B_PER_WAVE], a_off[C::A_PER_WAVE], b_off[C::B_PER_WAVE];
+  const int lr = lane >> 2, chunk = (lane & 3) ^ ((lr >> 2) & 3);
+#pragma unroll
+  for (int j = 0; j < C::A_PER_WAVE; j++) {
+    const int rr = 16 * (wave + C::NWV * j), first = a_row(rr) >> 4, row = a_row(rr + lr);
+    const int64_t at = ((int64_t)first * p.kq + s0) << 10;
+    a_base[j] = p.a_codes + at;
+    a_rec[j] = records(a_end - at);
+    a_off[j] = (((row >> 4) - first) * p.kq << 10) + ((row & 15) << 6) + chunk * 16;
+  }
+#pragma unroll
+  for (int j = 0; j < C::B_PER_WAVE; j++) {
+    const int rr = 16 * (wave + C::NWV * j), first = b_row(rr) >> 4, row = b_row(rr + lr);
+    const int64_t at = ((int64_t)first * p.kq + s0) << 10;
+    b_base[j] = p.b_codes + at;
+    b_rec[j] = records(b_end - at);
+    b_off[j] = (((row >> 4) - first) * p.kq << 10) + ((row & 15) << 6) + chunk * 16;
+  }
+  // scale words: waves 0-3 load 64 rows of A each, waves 4-7 of B (past the tile: its first rows again)
+  const int sw = wave & 3;
+  const uint8_t* s_base;
+  int s_rec, s_off, s_dst;
+  {
+    const bool isb = wave >= 4;
+    const int rr = 64 * sw < (isb ? BN : BM) ? 64 * sw : 0;
+    const int first = (isb ? b_row(rr) : a_row(rr)) >> 6, row = isb ? b_row(rr + lane) : a_row(rr + lane);
+    const int64_t at = ((int64_t)first * p.kq + s0) << 8;
+    const int64_t end = (int64_t)(((isb ? p.b_rows : p.M) + 63) >> 6) * p.kq << 8;
+    s_base = (isb ? p.b_scales : p.a_scales) + at;
+    s_rec = records(end - at);
+    s_off = (((row >> 6) - first) * p.kq << 8) + ((row & 63) << 2);
+    s_dst = C::A_BYTES + C::B_BYTES + (isb ? C::SCALE_BYTES : 0) + sw * 256;
+  }
+
+  auto issue = [&](int st) {
+    uint8_t* base = smem + (st % C::NS) * C::STAGE;
+#pragma unroll
+    for (int j = 0; j < C::A_PER_WAVE; j++)
+      buffer_to_lds16(a_base[j], a_rec[j], base + (wave + C::NWV * j) * 1024, a_off[j], st * 1024);
+#pragma unroll
+    for (int j = 0; j < C::B_PER_WAVE; j++)
+      buffer_to_lds16(b_base[j], b_rec[j], base + C::A_BYTES + (wave + C::NWV * j) * 1024, b_off[j], st * 1024);
+    buffer_to_lds4(s_base, s_rec, base + s_dst, s_off, st * 256);
+  };
+
+  v16f acc[C::MT][C::NT];
+#pragma unroll
+  for (int i = 0; i < C::MT; i++)
+#pragma unroll
+    for (int j = 0; j < C::NT; j++)
+#pragma unroll
+      for (int v = 0; v < 16; v++) acc[i][j][v] = 0.f;
+
+  struct Frag {
+    v4i a[C::MT], b[C::NT];
+  };
+  struct Scales {
+    u32 a[C::MT], b[C::NT];
+  };
+  // a 64-code slice's operands: rows 32 apart share the swizzle
+  int fa_off[2], fb_off[2];
+#pragma unroll
+  for (int ks = 0; ks < 2; ks++) {
+    fa_off[ks] = lds_swizzle(wm * C::TM + l32, 2 * ks + g);
+    fb_off[ks] = C::A_BYTES + lds_swizzle(wn * C::TN + l32, 2 * ks + g);
+  }
+  const int sa_lane = C::A_BYTES + C::B_BYTES + (wm * C::TM + l32) * 4;
+  const int sb_lane = C::A_BYTES + C::B_BYTES + C::SCALE_BYTES + (wn * C::TN + l32) * 4;
+  auto read_frag = [&](const uint8_t* base, int ks, Frag& f) {
+#pragma unroll
+    for (int i = 0; i < C::MT; i++) f.a[i] = *reinterpret_cast<const v4i*>(base + fa_off[ks] + 2048 * i);
+#pragma unroll
+    for (int j = 0; j < C::NT; j++) f.b[j] = *reinterpret_cast<const v4i*>(base + fb_off[ks] + 2048 * j);
+  };
+  // a scale word holds a stage's four block bytes; lane (l32, g) uses block 2 ks + g in slice ks: shifted by 8 g
+  // once, the MFMA picks byte 2 ks
+  const int gsh = 8 * g;
+  auto read_scales = [&](const uint8_t* base, Scales& sc) {
+#pragma unroll
+    for (int i = 0; i < C::MT; i++) sc.a[i] = *reinterpret_cast<const u32*>(base + sa_lane + 128 * i) >> gsh;
+#pragma unroll
+    for (int j = 0; j < C::NT; j++) sc.b[j] = *reinterpret_cast<const u32*>(base + sb_lane + 128 * j) >> gsh;
+  };
+  auto mma = [&](const Frag& f, const Scales& sc, auto ks_c) {
+    constexpr int KS = decltype(ks_c)::value;
+#pragma unroll
+    for (int i = 0; i < C::MT; i++)
+#pragma unroll
+      for (int j = 0; j < C::NT; j++)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            v8i{f.a[i][0], f.a[i][1], f.a[i][2], f.a[i][3], 0, 0, 0, 0},
+            v8i{f.b[j][0], f.b[j][1], f.b[j][2], f.b[j][3], 0, 0, 0, 0}, acc[i][j], 4, 4, 2 * KS, (int)sc.a[i], 2 * KS,
+            (int)sc.b[j]);
+  };
+  typedef std::integral_constant<int, 0> Slice0;
+  typedef std::integral_constant<int, 1> Slice1;
+
+  // ---- pipeline. Stage s + 2 is issued at the top of iteration s; slice 1 of stage s is read under slice 0's
+  // MFMAs; then the wave waits for its own loads of stage s + 1, one barrier publishes every wave's, and stage
+  // s + 1's scales and slice 0 are read under slice 1's MFMAs. The same barrier makes refilling buffer
+  // (s + 3) % 4 = (s - 1) % 4 safe in iteration s + 1: every wave's reads of stage s - 1 were consumed before it.
+  static_assert(C::NS == C::DIST + 2 && C::DIST == 2, "written for two stages in flight");
+  constexpr int NR = C::MT + C::NT, NM = C::MT * C::NT;
+  constexpr int P1 = NM - 1 < NR ? NM - 1 : NR;
+  issue(0);
+  issue(1);
+  wait_vmcnt<C::LPS>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frag fa, fb, f1;
+  Scales sa, sb;
+  read_scales(smem, sa);
+  read_frag(smem, 0, fa);
+
+  auto stage = [&](int s, Frag& cur0, Scales& scur, Frag& nxt0, Scales& snxt, auto ahead_c) {
+    constexpr int AHEAD = decltype(ahead_c)::value;  // stages in flight after s + 1; -1: s is the last
+    const uint8_t* base = smem + (s % C::NS) * C::STAGE;
+    read_frag(base, 1, f1);
+    mma(cur0, scur, Slice0());
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+    for (int q = 0; q < P1; q++) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+    if constexpr (NR > P1) __builtin_amdgcn_sched_group_barrier(0x100, NR - P1, 0);
+    if constexpr (NM - 1 > P1) __builtin_amdgcn_sched_group_barrier(0x008, NM - 1 - P1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (AHEAD >= 0) {
+      wait_vmcnt<C::LPS * AHEAD>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      const uint8_t* nb = smem + ((s + 1) % C::NS) * C::STAGE;
+      read_scales(nb, snxt);
+      read_frag(nb, 0, nxt0);
+    }
+    mma(f1, scur, Slice1());
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+    for (int q = 0; q < 2 * NR; q++) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (q < NM - 1) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, NM - 1 > 2 * NR ? NM - 1 - 2 * NR : 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  typedef std::integral_constant<int, 1> Steady;
+  typedef std::integral_constant<int, 0> LastButOne;
+  typedef std::integral_constant<int, -1> Last;
+  for (int s = 0; s < nst - 2; s += 2) {
+    issue(s + 2);
+    stage(s, fa, sa, fb, sb, Steady());
+    issue(s + 3);
+    stage(s + 1, fb, sb, fa, sa, Steady());
+  }
+  stage(nst - 2, fa, sa, fb, sb, LastButOne());
+  stage(nst - 1, fb, sb, fa, sa, Last());
+
+  // ---- epilogue
+  if constexpr (SPLIT) {
+    float* part = p.part + (int64_t)split * p.M * p.b_rows;
+    if constexpr (GATED) {
+      store_tile<MxF32, C, BM, C::NT / 2>(smem, part, p.b_rows, p.M, p.N, m0, n0, wm, wn, lane,
+                                          [&](int i, int j, int v) { return acc[i][j][v]; });
+      store_tile<MxF32, C, BM, C::NT / 2>(smem, part + p.N, p.b_rows, p.M, p.N, m0, n0, wm, wn, lane,
+                                          [&](int i, int j, int v) { return acc[i][j + C::NT / 2][v]; });
+    } else {
+      store_tile<MxF32, C, BM, C::NT>(smem, part, p.b_rows, p.M, p.N, m0, n0, wm, wn, lane,
+                                      [&](int i, int j, int v) { return acc[i][j][v]; });
+    }
+  } else if constexpr (GATED) {
+    T* y = reinterpret_cast<T*>(p.y);
+    if (p.gu) {
+      T* gu = reinterpret_cast<T*>(p.gu);
+      store_tile<DT, C, BM, C::NT / 2>(smem, gu, p.ldgu, p.M, p.N, m0, n0, wm, wn, lane,
+                                       [&](int i, int j, int v) { return acc[i][j][v]; });
+      store_tile<DT, C, BM, C::NT / 2>(smem, gu + p.N, p.ldgu, p.M, p.N, m0, n0, wm, wn, lane,
+                                       [&](int i, int j, int v) { return acc[i][j + C::NT / 2][v]; });
+    }
+    with_act(p.act, [&](auto c) {
+#pragma unroll
+      for (int i = 0; i < C::MT; i++)
+#pragma unroll
+        for (int j = 0; j < C::NT / 2; j++)
+#pragma unroll
+          for (int v = 0; v < 16; v++)
+            acc[i][j][v] = act_value<decltype(c)::value, float>(acc[i][j][v]).a * acc[i][j + C::NT / 2][v];
+    });
+    store_tile<DT, C, BM, C::NT / 2>(smem, y, p.ldy, p.M, p.N, m0, n0, wm, wn, lane,
+                                     [&](int i, int j, int v) { return acc[i][j][v]; });
+  } else {
+    if (p.bias) {
+#pragma unroll
+      for (int j = 0; j < C::NT; j++) {
+        const int col = n0 + wn * C::TN + 32 * j + l32;
+        const float b = DT::load(reinterpret_cast<const T*>(p.bias)[col < p.N ? col : p.N - 1]);
+#pragma unroll
+        for (int i = 0; i < C::MT; i++)
+#pragma unroll
+          for (int v = 0; v < 16; v++) acc[i][j][v] += b;
+      }
+    }
+    store_tile<DT, C, BM, C::NT>(smem, reinterpret_cast<T*>(p.y), p.ldy, p.M, p.N, m0, n0, wm, wn, lane,
+                                 [&](int i, int j, int v) { return acc[i][j][v]; });
+  }
+}
+
+// ------------------------------------------------------------------------------ joining split sums
+// Adds the parts in order and finishes each output. A thread takes one output (gated: its g and u).
+template <class DT, bool GATED>
+__global__ __launch_bounds__(256) void k_mx_join(MxGemmParams p) {
+  typedef typename DT::T T;
+  const int64_t n = (int64_t)p.M * p.N, stride = (int64_t)p.M * p.b_rows;
+  for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < n; id += (int64_t)gridDim.x * 256) {
+    const int64_t r = id / p.N, c = id - r * p.N;
+    const float* src = p.part + r * p.b_rows + c;
+    float a = 0.f, b = 0.f;
+    for (int s = 0; s < p.splits; s++) {
+      a += src[s * stride];
+      if (GATED) b += src[s * stride + p.N];
+    }
+    T* y = reinterpret_cast<T*>(p.y) + r * p.ldy + c;
+    if constexpr (GATED) {
+      float h = 0.f;
+      with_act(p.act, [&](auto k) { h = act_value<decltype(k)::value, float>(a).a * b; });
+      *y = DT::store(h);
       if (p.gu) {
-        T* gu = reinterpret_cast<T*>(p.gu) + r * p.ldgu + n0 + l32;
-        gu[0] = DT::store(acc[0][v]);
-        gu[p.N] = DT::store(acc[1][v]);
+        T* gu = reinterpret_cast<T*>(p.gu) + r * p.ldgu + c;
+        gu[0] = DT::store(a);
+        gu[p.N] = DT::store(b);
       }
     } else {
-      y[r * p.ldy] = DT::store(acc[0][v] + bias);
+      if (p.bias) a += DT::load(reinterpret_cast<const T*>(p.bias)[c]);
+      *y = DT::store(a);
     }
   }
 }
@@ -86,22 +410,89 @@ __global__ __launch_bounds__(256) void k_mx_product(MxGemmParams p, int tiles_n)
 
 using namespace dev;
 
-template <class DT>
-static hipError_t launch_product_t(const MxGemmParams& p, bool gated, hipStream_t stream) {
-  const int64_t tn = (p.N + 31) / 32, tm = (p.M + 31) / 32, blocks = (tn * tm + 3) / 4;
+// Compute units of the chip: what a plan spreads a product over.
+constexpr int kCus = 256;
+
+// How a product is cut: tile shape and shares of K.
+struct MxPlan {
+  int bm, bn, splits;
+};
+
+// Rounds of the chip times the time of one: about 8 us of prologue and epilogue, and per stage of 128 codes 0.19 us for
+// 256 x 256 and the time of fewer MFMAs for less. Shares of K cost the writing and reading of the parts.
+static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
+  const int cand[3][2] = {{128, 128}, {128, 256}, {256, 256}};
+  const double stage_us[3] = {0.08, 0.115, 0.19};
+  MxPlan best{0, 0, 1};
+  double best_t = 0;
+  for (int c = 0; c < 3; c++) {
+    // a 128-wide gated tile reaches its up rows' scales from its gate rows' by a 32-bit offset
+    if (gated && c == 0 && N * kq * 4 >= (int64_t)1 << 31) continue;
+    const int bm = cand[c][0], cols = gated ? cand[c][1] / 2 : cand[c][1];
+    const int64_t tiles = ((M + bm - 1) / bm) * ((N + cols - 1) / cols);
+    for (int s = 1; s <= 16; s *= 2) {
+      if (s > 1 && (kq / 2 / s < 4 || tiles * s > kCus)) break;
+      const double rounds = (double)((tiles * s + kCus - 1) / kCus);
+      double t = rounds * (8.0 + stage_us[c] * kq / s);
+      if (s > 1) t += 4.0 + (double)M * N * (gated ? 2 : 1) * 4 * 2 * s / 4e6;
+      if (best.bm == 0 || t < best_t) best = MxPlan{bm, cand[c][1], s}, best_t = t;
+    }
+  }
+  return best;
+}
+
+size_t mx_product_part_bytes(int64_t M, int64_t N, int kq, bool gated) {
+  const MxPlan pl = plan_of(M, N, kq, gated);
+  return pl.splits > 1 ? (size_t)pl.splits * M * N * (gated ? 2 : 1) * 4 : 0;
+}
+
+template <class DT, int BM, int BN, bool GATED, bool SPLIT>
+static hipError_t launch_tile(const MxGemmParams& p, hipStream_t stream) {
+  typedef TileCfg<BM, BN> C;
+  constexpr int COLS = GATED ? BN / 2 : BN;
+  const int64_t blocks = (((int64_t)p.M + BM - 1) / BM) * (((int64_t)p.N + COLS - 1) / COLS) * p.splits;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (gated)
-    k_mx_product<DT, true><<<dim3((unsigned)blocks), 256, 0, stream>>>(p, (int)tn);
-  else
-    k_mx_product<DT, false><<<dim3((unsigned)blocks), 256, 0, stream>>>(p, (int)tn);
+  // once per process and device; a second thread at most repeats the same call
+  static std::atomic<uint64_t> configured;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!bit || !(configured.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mx_tile<DT, BM, BN, GATED, SPLIT>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != hipSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_relaxed);
+  }
+  k_mx_tile<DT, BM, BN, GATED, SPLIT><<<dim3((unsigned)blocks), 512, C::SMEM, stream>>>(p);
   return hipGetLastError();
+}
+
+template <class DT, bool GATED>
+static hipError_t launch_product_t(const MxGemmParams& p0, hipStream_t stream) {
+  MxGemmParams p = p0;
+  const MxPlan pl = plan_of(p.M, p.N, p.kq, GATED);
+  p.splits = pl.splits;
+  if (p.splits > 1) {
+    // the parts are float32 whatever the output's type
+    const hipError_t e = pl.bm == 256   ? launch_tile<MxF32, 256, 256, GATED, true>(p, stream)
+                         : pl.bn == 256 ? launch_tile<MxF32, 128, 256, GATED, true>(p, stream)
+                                        : launch_tile<MxF32, 128, 128, GATED, true>(p, stream);
+    if (e != hipSuccess) return e;
+    const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
+    k_mx_join<DT, GATED><<<dim3((unsigned)(blocks < 4096 ? blocks : 4096)), 256, 0, stream>>>(p);
+    return hipGetLastError();
+  }
+  return pl.bm == 256   ? launch_tile<DT, 256, 256, GATED, false>(p, stream)
+         : pl.bn == 256 ? launch_tile<DT, 128, 256, GATED, false>(p, stream)
+                        : launch_tile<DT, 128, 128, GATED, false>(p, stream);
 }
 
 hipError_t launch_mx_product(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream) {
   switch (dtype) {
-    case SVDQ_F32: return launch_product_t<MxF32>(p, gated, stream);
-    case SVDQ_BF16: return launch_product_t<MxBF16>(p, gated, stream);
-    default: return launch_product_t<MxF16>(p, gated, stream);
+    case SVDQ_F32: return gated ? launch_product_t<MxF32, true>(p, stream) : launch_product_t<MxF32, false>(p, stream);
+    case SVDQ_BF16: return gated ? launch_product_t<MxBF16, true>(p, stream) : launch_product_t<MxBF16, false>(p, stream);
+    default: return gated ? launch_product_t<MxF16, true>(p, stream) : launch_product_t<MxF16, false>(p, stream);
   }
 }
 

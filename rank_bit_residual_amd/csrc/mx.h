@@ -57,6 +57,8 @@ struct MxGemmParams {
   void* gu;  // gated: [M][ldgu] pre-activations (gate, then up), or NULL
   int64_t ldgu;
   int act;
+  int splits;   // shares of K (set by the launcher)
+  float* part;  // [splits][M][b_rows] float32 sums, mx_product_part_bytes of them
 };
 
 struct MxGradParams {
@@ -71,6 +73,8 @@ struct MxGradParams {
 hipError_t launch_mx_quantize(const MxQuantParams& p, int dtype, hipStream_t stream);
 hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t stream);
 hipError_t launch_mx_gated_grad(const MxGradParams& p, int dtype, hipStream_t stream);
+// Bytes of float32 parts that the product's launch writes and reads (0: K is not split).
+size_t mx_product_part_bytes(int64_t M, int64_t N, int kq, bool gated);
 hipError_t launch_mx_product(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream);
 
 }  // namespace svdq

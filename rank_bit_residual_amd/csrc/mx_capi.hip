@@ -54,6 +54,20 @@ int check_matrix(const void* p, int64_t ld, int64_t cols, int dtype, const char*
   return SVDQ_OK;
 }
 
+// The product's workspace: its float32 parts where K is split, else none.
+int check_workspace(const void* ws, size_t bytes, int64_t M, int64_t N, int64_t K, bool gated) {
+  const size_t need = mx_product_part_bytes(M, N, (int)mx_kq(K), gated);
+  if (need && (!ws || bytes < need || !aligned(ws, kAlign)))
+    return set_error(SVDQ_EINVAL, "workspace too small or not 256-byte aligned");
+  return SVDQ_OK;
+}
+
+// Row offsets inside a tile are 32-bit: 2 (kq + 1) KB.
+int check_product_k(int64_t K) {
+  if (K > (int64_t)1 << 27) return set_error(SVDQ_EINVAL, "products take K up to 2^27");
+  return SVDQ_OK;
+}
+
 int check_act(int act) {
   if (act < SVDQ_ACT_SILU || act > SVDQ_ACT_RELU) return set_error(SVDQ_EINVAL, "unknown activation");
   return SVDQ_OK;
@@ -101,14 +115,25 @@ int svdq_mx_dequantize(const void* codes, const void* scales, int64_t rows, int6
   return hip_status(launch_mx_dequantize(p, dtype, (hipStream_t)stream), "mx_dequantize launch");
 }
 
+int svdq_mx_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated, size_t* bytes_out) {
+  clear_error();
+  int st = check_dim(M, "M");
+  if (st || (st = check_dim(gated ? 2 * N : N, "N")) || (st = check_dim(K, "K")) || (st = check_product_k(K))) return st;
+  if (!bytes_out) return set_error(SVDQ_EINVAL, "bytes_out is NULL");
+  *bytes_out = mx_product_part_bytes(M, N, (int)mx_kq(K), gated != 0);
+  return SVDQ_OK;
+}
+
 int svdq_mx_matmul(const void* a_codes, const void* a_scales, int64_t M, const void* b_codes, const void* b_scales,
-                   int64_t N, int64_t K, const void* bias, int dtype, void* y, int64_t ldy, svdq_stream_t stream) {
+                   int64_t N, int64_t K, const void* bias, int dtype, void* y, int64_t ldy, void* workspace,
+                   size_t workspace_bytes, svdq_stream_t stream) {
   int st = begin(dtype);
   if (st || (st = check_dim(M, "M")) || (st = check_dim(N, "N")) || (st = check_dim(K, "K")) ||
       (st = check_tensor(a_codes, a_scales, "a")) || (st = check_tensor(b_codes, b_scales, "b")) ||
       (st = check_matrix(y, ldy, N, dtype, "y")))
     return st;
   if (bias && !aligned(bias, size_of(dtype))) return set_error(SVDQ_EINVAL, "bias misaligned");
+  if ((st = check_product_k(K)) || (st = check_workspace(workspace, workspace_bytes, M, N, K, false))) return st;
   MxGemmParams p{};
   p.a_codes = (const uint8_t*)a_codes;
   p.a_scales = (const uint8_t*)a_scales;
@@ -121,18 +146,20 @@ int svdq_mx_matmul(const void* a_codes, const void* a_scales, int64_t M, const v
   p.bias = bias;
   p.y = y;
   p.ldy = ldy;
+  p.part = (float*)workspace;
   return hip_status(launch_mx_product(p, false, dtype, (hipStream_t)stream), "mx_matmul launch");
 }
 
 int svdq_mx_gated(const void* a_codes, const void* a_scales, int64_t M, const void* w_codes, const void* w_scales,
                   int64_t F, int64_t K, int act, int dtype, void* h, int64_t ldh, void* gu, int64_t ldgu,
-                  svdq_stream_t stream) {
+                  void* workspace, size_t workspace_bytes, svdq_stream_t stream) {
   int st = begin(dtype);
   if (st || (st = check_dim(M, "M")) || (st = check_dim(2 * F, "2F")) || (st = check_dim(K, "K")) || (st = check_act(act)) ||
       (st = check_tensor(a_codes, a_scales, "a")) || (st = check_tensor(w_codes, w_scales, "w")) ||
       (st = check_matrix(h, ldh, F, dtype, "h")))
     return st;
   if (gu && (st = check_matrix(gu, ldgu, 2 * F, dtype, "gu"))) return st;
+  if ((st = check_product_k(K)) || (st = check_workspace(workspace, workspace_bytes, M, F, K, true))) return st;
   MxGemmParams p{};
   p.a_codes = (const uint8_t*)a_codes;
   p.a_scales = (const uint8_t*)a_scales;
@@ -147,6 +174,7 @@ int svdq_mx_gated(const void* a_codes, const void* a_scales, int64_t M, const vo
   p.gu = gu;
   p.ldgu = ldgu;
   p.act = act;
+  p.part = (float*)workspace;
   return hip_status(launch_mx_product(p, true, dtype, (hipStream_t)stream), "mx_gated launch");
 }
 

@@ -166,6 +166,16 @@ def mx_dequantize(t: MxTensor, dtype: torch.dtype = torch.bfloat16, out: torch.T
     return out
 
 
+def _workspace(M: int, N: int, K: int, gated: bool, device) -> tuple:
+    """(tensor, address, bytes) of a product's scratch, from the current stream's memory."""
+    need = ctypes.c_size_t()
+    L.check(L.load().svdq_mx_workspace_bytes(M, N, K, gated, ctypes.byref(need)))
+    if not need.value:
+        return None, None, 0
+    ws = torch.empty(need.value, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), need.value
+
+
 def _operand(a, name: str, dtype):
     """An MxTensor and the output dtype: a matrix is quantised along its rows, its dtype the default."""
     if isinstance(a, torch.Tensor):
@@ -190,8 +200,9 @@ def mx_matmul(a, b: MxTensor, bias: torch.Tensor | None = None, dtype: torch.dty
             raise ValueError(f"bias must be a [{b.rows}] tensor of the output's dtype")
         bias = bias.contiguous()
     y = _output(out, a.rows, b.rows, dtype, device)
+    _keep, *ws = _workspace(a.rows, b.rows, a.cols, False, device)
     _call("svdq_mx_matmul", device, *_parts(a), a.rows, *_parts(b), b.rows, a.cols,
-          None if bias is None else bias.data_ptr(), code, y.data_ptr(), _row_stride(y))
+          None if bias is None else bias.data_ptr(), code, y.data_ptr(), _row_stride(y), *ws)
     return y
 
 
@@ -213,8 +224,9 @@ def mx_gated(x, w: MxTensor, act: str = "silu", dtype: torch.dtype | None = None
     M, F = x.rows, w.rows // 2
     h = _output(out, M, F, dtype, device)
     gu = torch.empty((M, 2 * F), dtype=dtype, device=device) if save else None
+    _keep, *ws = _workspace(M, F, x.cols, True, device)
     _call("svdq_mx_gated", device, *_parts(x), M, *_parts(w), F, x.cols, code, dt, h.data_ptr(), _row_stride(h),
-          None if gu is None else gu.data_ptr(), 2 * F)
+          None if gu is None else gu.data_ptr(), 2 * F, *ws)
     return (h, gu) if save else h
 
 

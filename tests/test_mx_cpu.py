@@ -101,10 +101,12 @@ def test_dequantize_refusals(change, status):
 @pytest.mark.parametrize("change,status", [
     (dict(dtype=F64), EDTYPE), (dict(M=0), EINVAL), (dict(N=0), EINVAL), (dict(K=0), EINVAL), (dict(ac=None), EINVAL),
     (dict(asc=None), EINVAL), (dict(bc=A + 8), EINVAL), (dict(bs=None), EINVAL), (dict(bias=A + 2), EINVAL),
-    (dict(y=None), EINVAL), (dict(y=A + 2), EINVAL), (dict(ldy=7), EINVAL),
+    (dict(y=None), EINVAL), (dict(y=A + 2), EINVAL), (dict(ldy=7), EINVAL), (dict(K=(1 << 27) + 1), EINVAL),
+    (dict(M=256, N=256, K=1 << 16, ldy=256), EINVAL), (dict(M=256, N=256, K=1 << 16, ldy=256, work=A, bytes=1024), EINVAL),
+    (dict(M=256, N=256, K=1 << 16, ldy=256, work=A + 8, bytes=1 << 40), EINVAL),
 ])
 def test_matmul_refusals(change, status):
-    a = dict(ac=A, asc=A, M=4, bc=A, bs=A, N=8, K=40, bias=None, dtype=F32, y=A, ldy=8)
+    a = dict(ac=A, asc=A, M=4, bc=A, bs=A, N=8, K=40, bias=None, dtype=F32, y=A, ldy=8, work=None, bytes=0)
     a.update(change)
     _refused(status, _lib.load().svdq_mx_matmul(*a.values(), None))
 
@@ -115,7 +117,7 @@ def test_matmul_refusals(change, status):
     (dict(ldh=7), EINVAL), (dict(gu=A, ldgu=15), EINVAL), (dict(gu=A + 1, ldgu=16), EINVAL),
 ])
 def test_gated_refusals(change, status):
-    a = dict(ac=A, asc=A, M=4, wc=A, ws=A, F=8, K=40, act=0, dtype=BF16, h=A, ldh=8, gu=None, ldgu=0)
+    a = dict(ac=A, asc=A, M=4, wc=A, ws=A, F=8, K=40, act=0, dtype=BF16, h=A, ldh=8, gu=None, ldgu=0, work=None, bytes=0)
     a.update(change)
     _refused(status, _lib.load().svdq_mx_gated(*a.values(), None))
 
@@ -130,6 +132,16 @@ def test_gated_grad_refusals(change, status):
     a = dict(dh=A, ldh=8, gu=A, ldgu=16, M=4, F=8, act=0, dtype=BF16, codes=A, scales=A, codes_t=A, scales_t=A)
     a.update(change)
     _refused(status, _lib.load().svdq_mx_gated_grad(*a.values(), None))
+
+
+def test_workspace_query():
+    lib, n = _lib.load(), ctypes.c_size_t(7)
+    assert lib.svdq_mx_workspace_bytes(256, 256, 512, 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.svdq_mx_workspace_bytes(256, 256, 1 << 16, 0, ctypes.byref(n)) == 0
+    assert n.value >= 2 * 256 * 256 * 4
+    for bad in ((0, 4, 4, 0), (4, 0, 4, 0), (4, 4, 0, 0), (4, 1 << 30, 4, 1), (4, 4, (1 << 27) + 1, 0)):
+        _refused(EINVAL, lib.svdq_mx_workspace_bytes(*bad, ctypes.byref(n)))
+    _refused(EINVAL, lib.svdq_mx_workspace_bytes(4, 4, 4, 0, None))
 
 
 # ----------------------------------------------------------------------------- binding
