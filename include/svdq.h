@@ -401,6 +401,20 @@ int svdq_mx_gated(const void* a_codes, const void* a_scales, int64_t M, const vo
                   void* workspace, size_t workspace_bytes, svdq_stream_t stream);
 
 /* --------------------------------------------------------------------------------------
+ * svdq_mx_linear, svdq_mx_gated_linear — the two products above of x [M, K] (strides sr, sc in elements)
+ * that is not quantised yet: svdq_mx_quantize along its rows, then the product, with the same results. Few rows
+ * are quantised inside the product's kernel, others into the workspace. x has the outputs' dtype.
+ * workspace: svdq_mx_linear_workspace_bytes. Errors as above.
+ * ------------------------------------------------------------------------------------ */
+int svdq_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t sc, int gated, size_t* bytes_out);
+int svdq_mx_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_t sc, const void* b_codes,
+                   const void* b_scales, int64_t N, const void* bias, int dtype, void* y, int64_t ldy, void* workspace,
+                   size_t workspace_bytes, svdq_stream_t stream);
+int svdq_mx_gated_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_t sc, const void* w_codes,
+                         const void* w_scales, int64_t F, int act, int dtype, void* h, int64_t ldh, void* gu,
+                         int64_t ldgu, void* workspace, size_t workspace_bytes, svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
  * svdq_mx_gated_grad — the gradients of the pre-activations, quantised for the two products
  * behind them in one pass: with d = [dg | du], dg = dh * u * act'(g), du = dh * act(g),
  *   codes / scales:     Q(d)   [M, 2F]  (times the weight quantised along 2F: dx)

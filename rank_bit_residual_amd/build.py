@@ -33,6 +33,7 @@ HIP_SOURCES = {
     "k_ceiling.hip": [],
     "k_mx_quant.hip": ["-ffp-contract=off"],
     "k_mx_gemm.hip": [],
+    "k_mx_decode.hip": [],
     "mx_capi.hip": [],
     "capi.hip": [],
 }

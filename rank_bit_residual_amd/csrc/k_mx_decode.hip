@@ -1,0 +1,194 @@
+// Products of MXFP4 tensors for few rows (decode steps): Y = D(A B^T + bias) and the gated projections, at
+// most 64 rows of A, bound by reading b once.
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 rows of A against 16 rows of b, a stage of 128 codes at a
+// time; lane (i, g) holds block g of row i of either. A block of waves owns 16 or 32 output columns (gated: the
+// gate and up rows of the same 16) and splits K evenly over its waves; every byte of b is used once, so it goes
+// straight into registers, a contiguous kilobyte per 16 rows and stage, several stages of requests in flight. The
+// waves' partial tiles are added in LDS in a fixed order.
+//
+// A may be given unquantised (RAW): lane (i, g) then loads the 32 elements of its own block, takes their
+// maximum and their codes without leaving the lane. That re-quantises x in every block, and costs no launch.
+#include "mx.h"
+#include "mx_device.h"
+
+namespace svdq {
+namespace dev {
+
+template <class DT, int MT, int NT, int WAVES, bool GATED, bool RAW>
+__global__ __launch_bounds__(64 * WAVES) void k_mx_decode(MxGemmParams p) {
+  typedef typename DT::T T;
+  static_assert(!GATED || NT == 2, "a gate tile and an up tile");
+  constexpr int XW = DT::size * 8;  // words of 32 elements of x
+  constexpr int BATCH = RAW ? (DT::size == 4 ? 2 : 4) : (MT >= 2 ? 4 : 8);
+  __shared__ float red[WAVES][MT][NT][4][64];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * (GATED ? 16 : 16 * NT);
+  const int s0 = (int)((int64_t)wave * p.kq / WAVES), s1 = (int)((int64_t)(wave + 1) * p.kq / WAVES);
+
+  const uint8_t *bc[NT], *bs[NT];
+#pragma unroll
+  for (int n = 0; n < NT; n++) {
+    const int64_t col = (int64_t)n0 + i + (GATED ? 0 : 16 * n);
+    int64_t row = (col < p.N ? col : p.N - 1) + (GATED && n ? p.N : 0);
+    bc[n] = p.b_codes + mx_code_tile_offset(row, p.kq) + g * 16;
+    bs[n] = p.b_scales + mx_scale_tiled_index(row, 0, p.kq);
+  }
+  const uint8_t *ac[MT], *as[MT];
+  const T* xr[MT];
+#pragma unroll
+  for (int m = 0; m < MT; m++) {
+    const int64_t row = 16 * m + i < p.M ? 16 * m + i : p.M - 1;
+    if constexpr (RAW) {
+      xr[m] = reinterpret_cast<const T*>(p.x) + row * p.ldx;
+    } else {
+      ac[m] = p.a_codes + mx_code_tile_offset(row, p.kq) + g * 16;
+      as[m] = p.a_scales + mx_scale_tiled_index(row, 0, p.kq);
+    }
+  }
+
+  v4f acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; m++)
+#pragma unroll
+    for (int n = 0; n < NT; n++) acc[m][n] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  struct Step {
+    v4i b[NT];
+    u32 bsc[NT];
+    v4i a[RAW ? 1 : MT];
+    u32 asc[RAW ? 1 : MT];
+    u32 x[RAW ? MT : 1][RAW ? XW : 1];
+  };
+  auto load = [&](Step& q, int s) {
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      q.b[n] = *reinterpret_cast<const v4i*>(bc[n] + (int64_t)s * 1024);
+      q.bsc[n] = *reinterpret_cast<const u32*>(bs[n] + (int64_t)s * 256);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+      if constexpr (RAW) {
+        const int64_t c = (int64_t)s * 128 + 32 * g;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const Vec8<DT> v = load8<DT>(xr[m], c + 8 * e, p.K);
+#pragma unroll
+          for (int k = 0; k < XW / 4; k++) q.x[m][e * (XW / 4) + k] = v.w[k];
+        }
+      } else {
+        q.a[m] = *reinterpret_cast<const v4i*>(ac[m] + (int64_t)s * 1024);
+        q.asc[m] = *reinterpret_cast<const u32*>(as[m] + (int64_t)s * 256);
+      }
+    }
+  };
+  auto step = [&](const Step& q) {
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+      v4i a;
+      u32 sa;
+      if constexpr (RAW) {
+        sa = mx_scale_byte(amax_bits<DT>(q.x[m]));
+#pragma unroll
+        for (int e = 0; e < 4; e++) a[e] = (int)codes8<DT>(q.x[m] + e * (XW / 4), sa);
+      } else {
+        a = q.a[m];
+        sa = q.asc[m] >> (8 * g);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+        acc[m][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            v8i{a[0], a[1], a[2], a[3], 0, 0, 0, 0}, v8i{q.b[n][0], q.b[n][1], q.b[n][2], q.b[n][3], 0, 0, 0, 0}, acc[m][n],
+            4, 4, 0, (int)sa, 0, (int)(q.bsc[n] >> (8 * g)));
+    }
+  };
+  // whole batches, then what is left in halves: a share of K is rarely a multiple of the batch
+  int s = s0;
+  auto batch = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    Step q[N];
+#pragma unroll
+    for (int u = 0; u < N; u++) load(q[u], s + u);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < N; u++) step(q[u]);
+    s += N;
+  };
+  while (s + BATCH <= s1) batch(std::integral_constant<int, BATCH>());
+  if constexpr (BATCH > 4)
+    if (s + 4 <= s1) batch(std::integral_constant<int, 4>());
+  if constexpr (BATCH > 2)
+    if (s + 2 <= s1) batch(std::integral_constant<int, 2>());
+  if (s < s1) batch(std::integral_constant<int, 1>());
+
+#pragma unroll
+  for (int m = 0; m < MT; m++)
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int v = 0; v < 4; v++) red[wave][m][n][v][lane] = acc[m][n][v];
+  __syncthreads();
+  // entry (m, n, v, lane (i, g)) is row 16 m + 4 g + v of column i of tile n
+  constexpr int OUT = MT * (GATED ? 1 : NT) * 256;
+  T* y = reinterpret_cast<T*>(p.y);
+  for (int e = t; e < OUT; e += 64 * WAVES) {
+    const int el = e & 63, v = (e >> 6) & 3, mn = e >> 8;
+    const int m = GATED ? mn : mn / NT, n = GATED ? 0 : mn % NT;
+    const int64_t row = 16 * m + 4 * (el >> 4) + v, col = (int64_t)n0 + 16 * n + (el & 15);
+    if (row >= p.M || col >= p.N) continue;
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; w++) {
+      a += red[w][m][n][v][el];
+      if (GATED) b += red[w][m][NT - 1][v][el];
+    }
+    if constexpr (GATED) {
+      float h = 0.f;
+      with_act(p.act, [&](auto c) { h = act_value<decltype(c)::value, float>(a).a * b; });
+      y[row * p.ldy + col] = DT::store(h);
+      if (p.gu) {
+        T* gu = reinterpret_cast<T*>(p.gu) + row * p.ldgu + col;
+        gu[0] = DT::store(a);
+        gu[p.N] = DT::store(b);
+      }
+    } else {
+      if (p.bias) a += DT::load(reinterpret_cast<const T*>(p.bias)[col]);
+      y[row * p.ldy + col] = DT::store(a);
+    }
+  }
+}
+
+}  // namespace dev
+
+using namespace dev;
+
+template <class DT, int MT, int WAVES, bool RAW>
+static hipError_t launch_rows(const MxGemmParams& p, bool gated, hipStream_t stream) {
+  const int64_t cols16 = ((int64_t)p.N + 15) / 16;
+  if (gated)
+    k_mx_decode<DT, MT, 2, WAVES, true, RAW><<<dim3((unsigned)cols16), 64 * WAVES, 0, stream>>>(p);
+  else if (cols16 >= 512)  // two column tiles per block while that leaves a block for every compute unit
+    k_mx_decode<DT, MT, 2, WAVES, false, RAW><<<dim3((unsigned)((cols16 + 1) / 2)), 64 * WAVES, 0, stream>>>(p);
+  else
+    k_mx_decode<DT, MT, 1, WAVES, false, RAW><<<dim3((unsigned)cols16), 64 * WAVES, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <class DT>
+static hipError_t launch_decode_t(const MxGemmParams& p, bool gated, hipStream_t stream) {
+  if (p.x) return launch_rows<DT, 1, 8, true>(p, gated, stream);
+  if (p.M <= 16) return launch_rows<DT, 1, 8, false>(p, gated, stream);
+  if (p.M <= 32) return launch_rows<DT, 2, 8, false>(p, gated, stream);
+  return launch_rows<DT, 4, 4, false>(p, gated, stream);
+}
+
+hipError_t launch_mx_decode(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream) {
+  switch (dtype) {
+    case SVDQ_F32: return launch_decode_t<MxF32>(p, gated, stream);
+    case SVDQ_BF16: return launch_decode_t<MxBF16>(p, gated, stream);
+    default: return launch_decode_t<MxF16>(p, gated, stream);
+  }
+}
+
+}  // namespace svdq

@@ -24,16 +24,6 @@
 namespace svdq {
 namespace dev {
 
-template <class F>
-__device__ __forceinline__ void with_act(int act, F f) {
-  switch (act) {
-    case SVDQ_ACT_SILU: f(std::integral_constant<int, SVDQ_ACT_SILU>()); break;
-    case SVDQ_ACT_GELU: f(std::integral_constant<int, SVDQ_ACT_GELU>()); break;
-    case SVDQ_ACT_GELU_TANH: f(std::integral_constant<int, SVDQ_ACT_GELU_TANH>()); break;
-    default: f(std::integral_constant<int, SVDQ_ACT_RELU>()); break;
-  }
-}
-
 // ------------------------------------------------------------------------------ tiles
 template <int BM, int BN>
 struct TileCfg {
@@ -424,6 +414,7 @@ static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
   const int cand[3][2] = {{128, 128}, {128, 256}, {256, 256}};
   const double stage_us[3] = {0.08, 0.115, 0.19};
   MxPlan best{0, 0, 1};
+  if (M <= kMxDecodeRows) return best;
   double best_t = 0;
   for (int c = 0; c < 3; c++) {
     // a 128-wide gated tile reaches its up rows' scales from its gate rows' by a 32-bit offset
@@ -489,6 +480,7 @@ static hipError_t launch_product_t(const MxGemmParams& p0, hipStream_t stream) {
 }
 
 hipError_t launch_mx_product(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream) {
+  if (p.M <= kMxDecodeRows) return launch_mx_decode(p, gated, dtype, stream);
   switch (dtype) {
     case SVDQ_F32: return gated ? launch_product_t<MxF32, true>(p, stream) : launch_product_t<MxF32, false>(p, stream);
     case SVDQ_BF16: return gated ? launch_product_t<MxBF16, true>(p, stream) : launch_product_t<MxBF16, false>(p, stream);

@@ -43,7 +43,13 @@ struct MxDequantParams {
   int64_t ldo;
 };
 
+// Rows of A that the decode kernel takes, and those of an unquantised A.
+constexpr int64_t kMxDecodeRows = 64, kMxRawRows = 16;
+
 struct MxGemmParams {
+  // unquantised A (at most kMxRawRows rows): [M][ldx] of the output's dtype, K elements a row, or NULL
+  const void* x;
+  int64_t ldx, K;
   const uint8_t* a_codes;
   const uint8_t* a_scales;
   const uint8_t* b_codes;
@@ -75,6 +81,7 @@ hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t
 hipError_t launch_mx_gated_grad(const MxGradParams& p, int dtype, hipStream_t stream);
 // Bytes of float32 parts that the product's launch writes and reads (0: K is not split).
 size_t mx_product_part_bytes(int64_t M, int64_t N, int kq, bool gated);
+hipError_t launch_mx_decode(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream);
 hipError_t launch_mx_product(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream);
 
 }  // namespace svdq

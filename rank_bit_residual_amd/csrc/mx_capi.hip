@@ -54,11 +54,16 @@ int check_matrix(const void* p, int64_t ld, int64_t cols, int dtype, const char*
   return SVDQ_OK;
 }
 
-// The product's workspace: its float32 parts where K is split, else none.
-int check_workspace(const void* ws, size_t bytes, int64_t M, int64_t N, int64_t K, bool gated) {
-  const size_t need = mx_product_part_bytes(M, N, (int)mx_kq(K), gated);
+int check_workspace(const void* ws, size_t bytes, size_t need) {
   if (need && (!ws || bytes < need || !aligned(ws, kAlign)))
     return set_error(SVDQ_EINVAL, "workspace too small or not 256-byte aligned");
+  return SVDQ_OK;
+}
+
+int check_strided(const void* x, int64_t sr, int64_t sc, int dtype, const char* name) {
+  if (!x) return set_error(SVDQ_EINVAL, std::string(name) + ": NULL buffer");
+  if (!aligned(x, size_of(dtype))) return set_error(SVDQ_EINVAL, std::string(name) + " misaligned");
+  if (sr < 0 || sc < 0) return set_error(SVDQ_EINVAL, "strides must not be negative");
   return SVDQ_OK;
 }
 
@@ -74,6 +79,93 @@ int check_act(int act) {
 }
 
 MxOut out_of(void* codes, void* scales, int64_t K) { return MxOut{(uint8_t*)codes, (uint8_t*)scales, (int)mx_kq(K)}; }
+
+// The product's part of the four calls below: b and everything behind it.
+struct Product {
+  const void *b_codes, *b_scales;
+  int64_t N, K;
+  bool gated;
+  int act, dtype;
+  const void* bias;
+  void* y;
+  int64_t ldy;
+  void* gu;
+  int64_t ldgu;
+};
+
+int check_product(int64_t M, const Product& q) {
+  int st;
+  if ((st = check_dim(M, "M")) || (st = check_dim(q.gated ? 2 * q.N : q.N, q.gated ? "2F" : "N")) || (st = check_dim(q.K, "K")) ||
+      (st = check_product_k(q.K)) || (st = check_tensor(q.b_codes, q.b_scales, q.gated ? "w" : "b")) ||
+      (st = check_matrix(q.y, q.ldy, q.N, q.dtype, q.gated ? "h" : "y")))
+    return st;
+  if (q.gated && (st = check_act(q.act))) return st;
+  if (q.gu && (st = check_matrix(q.gu, q.ldgu, 2 * q.N, q.dtype, "gu"))) return st;
+  if (q.bias && !aligned(q.bias, size_of(q.dtype))) return set_error(SVDQ_EINVAL, "bias misaligned");
+  return SVDQ_OK;
+}
+
+MxGemmParams params_of(int64_t M, const Product& q, void* part) {
+  MxGemmParams p{};
+  p.K = q.K;
+  p.b_codes = (const uint8_t*)q.b_codes;
+  p.b_scales = (const uint8_t*)q.b_scales;
+  p.M = (int)M;
+  p.N = (int)q.N;
+  p.b_rows = (int)(q.gated ? 2 * q.N : q.N);
+  p.kq = (int)mx_kq(q.K);
+  p.bias = q.bias;
+  p.y = q.y;
+  p.ldy = q.ldy;
+  p.gu = q.gu;
+  p.ldgu = q.ldgu;
+  p.act = q.act;
+  p.part = (float*)part;
+  return p;
+}
+
+int product(const void* a_codes, const void* a_scales, int64_t M, const Product& q, void* workspace,
+                   size_t workspace_bytes, svdq_stream_t stream) {
+  int st = begin(q.dtype);
+  if (st || (st = check_product(M, q)) || (st = check_tensor(a_codes, a_scales, "a"))) return st;
+  const size_t need = mx_product_part_bytes(M, q.N, (int)mx_kq(q.K), q.gated);
+  if ((st = check_workspace(workspace, workspace_bytes, need))) return st;
+  MxGemmParams p = params_of(M, q, workspace);
+  p.a_codes = (const uint8_t*)a_codes;
+  p.a_scales = (const uint8_t*)a_scales;
+  return hip_status(launch_mx_product(p, q.gated, q.dtype, (hipStream_t)stream), "MXFP4 product launch");
+}
+
+// Few rows with unit column stride are quantised by the product itself; others into the workspace first.
+bool raw_rows(int64_t M, int64_t sc) { return M <= kMxRawRows && sc == 1; }
+
+// Workspace of an unquantised A: its codes and scales (unless the product quantises it), then the parts.
+size_t linear_bytes(int64_t M, int64_t N, int64_t K, bool gated, int64_t sc) {
+  if (raw_rows(M, sc)) return 0;
+  return (size_t)(mx_code_bytes(M, K) + mx_scale_bytes(M, K)) + mx_product_part_bytes(M, N, (int)mx_kq(K), gated);
+}
+
+int linear(const void* x, int64_t M, int64_t sr, int64_t sc, const Product& q, void* workspace,
+                  size_t workspace_bytes, svdq_stream_t stream) {
+  int st = begin(q.dtype);
+  if (st || (st = check_product(M, q)) || (st = check_strided(x, sr, sc, q.dtype, "x"))) return st;
+  const size_t codes = (size_t)mx_code_bytes(M, q.K), scales = (size_t)mx_scale_bytes(M, q.K);
+  if ((st = check_workspace(workspace, workspace_bytes, linear_bytes(M, q.N, q.K, q.gated, sc)))) return st;
+  uint8_t* ws = (uint8_t*)workspace;
+  hipStream_t s = (hipStream_t)stream;
+  if (raw_rows(M, sc)) {
+    MxGemmParams p = params_of(M, q, nullptr);
+    p.x = x;
+    p.ldx = sr;
+    return hip_status(launch_mx_decode(p, q.gated, q.dtype, s), "MXFP4 product launch");
+  }
+  MxGemmParams p = params_of(M, q, ws + codes + scales);
+  p.a_codes = ws;
+  p.a_scales = ws + codes;
+  MxQuantParams a{x, M, q.K, sr, sc, out_of(ws, ws + codes, q.K), MxOut{}};
+  if ((st = hip_status(launch_mx_quantize(a, q.dtype, s), "mx_quantize launch"))) return st;
+  return hip_status(launch_mx_product(p, q.gated, q.dtype, s), "MXFP4 product launch");
+}
 
 }  // namespace
 }  // namespace svdq
@@ -96,9 +188,7 @@ int svdq_mx_quantize(const void* x, int64_t R, int64_t C, int64_t sr, int64_t sc
                      void* scales, void* codes_t, void* scales_t, svdq_stream_t stream) {
   int st = begin(dtype);
   if (st || (st = check_dim(R, "R")) || (st = check_dim(C, "C"))) return st;
-  if (!x) return set_error(SVDQ_EINVAL, "x: NULL buffer");
-  if (!aligned(x, size_of(dtype))) return set_error(SVDQ_EINVAL, "x misaligned");
-  if (sr < 0 || sc < 0) return set_error(SVDQ_EINVAL, "strides must not be negative");
+  if ((st = check_strided(x, sr, sc, dtype, "x"))) return st;
   if (!codes && !codes_t) return set_error(SVDQ_EINVAL, "nothing to quantise into");
   if ((st = check_out(codes, scales, "codes")) || (st = check_out(codes_t, scales_t, "codes_t"))) return st;
   MxQuantParams p{x, R, C, sr, sc, out_of(codes, scales, C), out_of(codes_t, scales_t, R)};
@@ -127,55 +217,37 @@ int svdq_mx_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated, size_t* 
 int svdq_mx_matmul(const void* a_codes, const void* a_scales, int64_t M, const void* b_codes, const void* b_scales,
                    int64_t N, int64_t K, const void* bias, int dtype, void* y, int64_t ldy, void* workspace,
                    size_t workspace_bytes, svdq_stream_t stream) {
-  int st = begin(dtype);
-  if (st || (st = check_dim(M, "M")) || (st = check_dim(N, "N")) || (st = check_dim(K, "K")) ||
-      (st = check_tensor(a_codes, a_scales, "a")) || (st = check_tensor(b_codes, b_scales, "b")) ||
-      (st = check_matrix(y, ldy, N, dtype, "y")))
-    return st;
-  if (bias && !aligned(bias, size_of(dtype))) return set_error(SVDQ_EINVAL, "bias misaligned");
-  if ((st = check_product_k(K)) || (st = check_workspace(workspace, workspace_bytes, M, N, K, false))) return st;
-  MxGemmParams p{};
-  p.a_codes = (const uint8_t*)a_codes;
-  p.a_scales = (const uint8_t*)a_scales;
-  p.b_codes = (const uint8_t*)b_codes;
-  p.b_scales = (const uint8_t*)b_scales;
-  p.M = (int)M;
-  p.N = (int)N;
-  p.b_rows = (int)N;
-  p.kq = (int)mx_kq(K);
-  p.bias = bias;
-  p.y = y;
-  p.ldy = ldy;
-  p.part = (float*)workspace;
-  return hip_status(launch_mx_product(p, false, dtype, (hipStream_t)stream), "mx_matmul launch");
+  const Product q{b_codes, b_scales, N, K, false, 0, dtype, bias, y, ldy, nullptr, 0};
+  return product(a_codes, a_scales, M, q, workspace, workspace_bytes, stream);
 }
 
 int svdq_mx_gated(const void* a_codes, const void* a_scales, int64_t M, const void* w_codes, const void* w_scales,
                   int64_t F, int64_t K, int act, int dtype, void* h, int64_t ldh, void* gu, int64_t ldgu,
                   void* workspace, size_t workspace_bytes, svdq_stream_t stream) {
-  int st = begin(dtype);
-  if (st || (st = check_dim(M, "M")) || (st = check_dim(2 * F, "2F")) || (st = check_dim(K, "K")) || (st = check_act(act)) ||
-      (st = check_tensor(a_codes, a_scales, "a")) || (st = check_tensor(w_codes, w_scales, "w")) ||
-      (st = check_matrix(h, ldh, F, dtype, "h")))
-    return st;
-  if (gu && (st = check_matrix(gu, ldgu, 2 * F, dtype, "gu"))) return st;
-  if ((st = check_product_k(K)) || (st = check_workspace(workspace, workspace_bytes, M, F, K, true))) return st;
-  MxGemmParams p{};
-  p.a_codes = (const uint8_t*)a_codes;
-  p.a_scales = (const uint8_t*)a_scales;
-  p.b_codes = (const uint8_t*)w_codes;
-  p.b_scales = (const uint8_t*)w_scales;
-  p.M = (int)M;
-  p.N = (int)F;
-  p.b_rows = (int)(2 * F);
-  p.kq = (int)mx_kq(K);
-  p.y = h;
-  p.ldy = ldh;
-  p.gu = gu;
-  p.ldgu = ldgu;
-  p.act = act;
-  p.part = (float*)workspace;
-  return hip_status(launch_mx_product(p, true, dtype, (hipStream_t)stream), "mx_gated launch");
+  const Product q{w_codes, w_scales, F, K, true, act, dtype, nullptr, h, ldh, gu, ldgu};
+  return product(a_codes, a_scales, M, q, workspace, workspace_bytes, stream);
+}
+
+int svdq_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t sc, int gated, size_t* bytes_out) {
+  int st = svdq_mx_workspace_bytes(M, N, K, gated, bytes_out);
+  if (st) return st;
+  if (sc < 0) return set_error(SVDQ_EINVAL, "strides must not be negative");
+  *bytes_out = linear_bytes(M, N, K, gated != 0, sc);
+  return SVDQ_OK;
+}
+
+int svdq_mx_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_t sc, const void* b_codes,
+                   const void* b_scales, int64_t N, const void* bias, int dtype, void* y, int64_t ldy, void* workspace,
+                   size_t workspace_bytes, svdq_stream_t stream) {
+  const Product q{b_codes, b_scales, N, K, false, 0, dtype, bias, y, ldy, nullptr, 0};
+  return linear(x, M, sr, sc, q, workspace, workspace_bytes, stream);
+}
+
+int svdq_mx_gated_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_t sc, const void* w_codes,
+                         const void* w_scales, int64_t F, int act, int dtype, void* h, int64_t ldh, void* gu,
+                         int64_t ldgu, void* workspace, size_t workspace_bytes, svdq_stream_t stream) {
+  const Product q{w_codes, w_scales, F, K, true, act, dtype, nullptr, h, ldh, gu, ldgu};
+  return linear(x, M, sr, sc, q, workspace, workspace_bytes, stream);
 }
 
 int svdq_mx_gated_grad(const void* dh, int64_t ldh, const void* gu, int64_t ldgu, int64_t M, int64_t F, int act,

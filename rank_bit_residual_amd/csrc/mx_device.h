@@ -2,6 +2,8 @@
 // eight codes at a time from packed values, and the gated activations with their derivatives.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 
 #include "../../include/svdq.h"
@@ -24,8 +26,6 @@ struct MxBF16 {
   __device__ static inline u32 pack(float a, float b) { return pack_bf16x2(a, b); }
   // v_cvt_scalef32_pk_fp4_bf16 over four pairs, see fp4_pack8_bf16
   __device__ static inline u32 codes8(const u32* pairs, float scale) { return fp4_pack8_bf16(pairs, scale); }
-  // larger of two non-negative values' bits, in both halves at once
-  static constexpr u32 inf = 0x7F80;
 };
 struct MxF16 {
   typedef uint16_t T;
@@ -42,7 +42,6 @@ struct MxF16 {
     r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(h2, pairs[3]), scale, 3);
     return r;
   }
-  static constexpr u32 inf = 0x7C00;
 };
 
 // Scale byte of a block from the bits of its largest magnitude as float32; 255 (NaN) from
@@ -52,6 +51,87 @@ __device__ inline u32 mx_scale_byte(u32 amax_bits) {
 }
 // 2^e of a scale byte below 255.
 __device__ inline float mx_scale_value(u32 byte) { return pow2f((int)byte - 127); }
+
+// ---- eight elements at a time ------------------------------------------------------------
+// Eight consecutive elements of a row, in registers.
+template <class DT>
+struct Vec8 {
+  u32 w[DT::size * 2];  // 16-bit types: four pairs; float32: eight values' bits
+};
+
+template <class DT>
+__device__ inline Vec8<DT> zero8() {
+  Vec8<DT> v;
+#pragma unroll
+  for (int q = 0; q < DT::size * 2; q++) v.w[q] = 0;
+  return v;
+}
+
+// Elements [c, c + 8) of a row of C elements at src, zeros past its end. A whole vector is loaded
+// at any alignment of its elements (global loads need none on this target).
+template <class DT>
+__device__ inline Vec8<DT> load8(const typename DT::T* src, int64_t c, int64_t C) {
+  Vec8<DT> v = zero8<DT>();
+  if (c + 8 <= C) {
+    __builtin_memcpy(&v, src + c, sizeof v);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; q++) {
+      if (c + q >= C) continue;
+      if constexpr (DT::size == 4)
+        v.w[q] = __float_as_uint(src[c + q]);
+      else
+        v.w[q >> 1] |= (u32)src[c + q] << (16 * (q & 1));
+    }
+  }
+  return v;
+}
+
+template <class DT>
+__device__ inline float elem(const Vec8<DT>& v, int q) {
+  if constexpr (DT::size == 4)
+    return __uint_as_float(v.w[q]);
+  else
+    return DT::load((uint16_t)(v.w[q >> 1] >> (16 * (q & 1))));
+}
+
+typedef uint16_t v2us __attribute__((ext_vector_type(2)));
+
+// Largest magnitude of packed 16-bit values: magnitudes order as their bits do.
+__device__ inline u32 max_pairs(u32 a, u32 b) {
+  return __builtin_bit_cast(u32, __builtin_elementwise_max(__builtin_bit_cast(v2us, a), __builtin_bit_cast(v2us, b)));
+}
+
+// Bits of the largest magnitude of n words of a block's share, as float32.
+template <class DT, int N>
+__device__ inline u32 amax_bits(const u32 (&w)[N]) {
+  if constexpr (DT::size == 4) {
+    u32 m = 0;
+#pragma unroll
+    for (int q = 0; q < N; q++) m = max(m, w[q] & 0x7FFFFFFFu);
+    return m;
+  } else {
+    u32 m = 0;
+#pragma unroll
+    for (int q = 0; q < N; q++) m = max_pairs(m, w[q] & 0x7FFF7FFFu);
+    return __float_as_uint(DT::load((uint16_t)max(m & 0xFFFFu, m >> 16)));
+  }
+}
+
+// The word of eight codes (zeros for a NaN block).
+template <class DT>
+__device__ inline u32 codes8(const u32* w, u32 byte) {
+  if (byte == 255u) return 0;
+  const float s = mx_scale_value(byte);
+  if constexpr (DT::size == 4) {
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; q++) v[q] = __uint_as_float(w[q]);
+    return fp4_pack8(v, s);
+  } else {
+    return DT::codes8(w, s);
+  }
+}
 
 // ---- gated activations ------------------------------------------------------------------
 // act(g) and act'(g), and bounds on the relative error of act and the absolute error of act'
@@ -114,6 +194,16 @@ __device__ inline ActValue<F> act_value(F g) {
     r.abs_d = (float)s * (1.f + fabsf((float)(gc * dw))) * ew;
   }
   return r;
+}
+
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case SVDQ_ACT_SILU: f(std::integral_constant<int, SVDQ_ACT_SILU>()); break;
+    case SVDQ_ACT_GELU: f(std::integral_constant<int, SVDQ_ACT_GELU>()); break;
+    case SVDQ_ACT_GELU_TANH: f(std::integral_constant<int, SVDQ_ACT_GELU_TANH>()); break;
+    default: f(std::integral_constant<int, SVDQ_ACT_RELU>()); break;
+  }
 }
 
 }  // namespace dev

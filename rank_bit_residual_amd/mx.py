@@ -19,7 +19,7 @@ tensors are float32, bfloat16 or float16 on a GPU.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
+import functools
 
 import torch
 
@@ -29,18 +29,37 @@ _DT = {torch.float32: L.SVDQ_F32, torch.bfloat16: L.SVDQ_BF16, torch.float16: L.
 _ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 
-@dataclass(frozen=True, eq=False)
+@functools.lru_cache(maxsize=4096)
+def _bytes(rows: int, cols: int) -> tuple:
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    L.check(L.load().svdq_mx_layout(rows, cols, ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
+
+
 class MxTensor:
     """An MXFP4 tensor on the device: the values Q(x) of a [rows, cols] matrix, blocks along cols.
 
-    codes, scales: uint8 arrays in the layout of svdq_mx_layout (they may be saved and restored
-    with torch; rows past `rows` of the last tiles hold nothing).
+    data: one uint8 array, the codes and behind them the scale bytes, in the layout of svdq_mx_layout. It
+    may be saved and restored with torch; the padding rows of its last tiles hold nothing.
     """
 
-    codes: torch.Tensor
-    scales: torch.Tensor
-    rows: int
-    cols: int
+    __slots__ = ("data", "rows", "cols", "_at")
+
+    def __init__(self, data: torch.Tensor, rows: int, cols: int):
+        code_bytes, scale_bytes = _bytes(rows, cols)
+        if not isinstance(data, torch.Tensor) or data.dtype != torch.uint8 or data.dim() != 1 or not data.is_contiguous():
+            raise TypeError("data must be a contiguous uint8 vector")
+        if data.numel() < code_bytes + scale_bytes:
+            raise ValueError(f"data holds {data.numel()} bytes, a [{rows}, {cols}] tensor needs {code_bytes + scale_bytes}")
+        self.data, self.rows, self.cols, self._at = data, rows, cols, code_bytes
+
+    @classmethod
+    def _empty(cls, rows: int, cols: int, device) -> "MxTensor":
+        t = cls.__new__(cls)
+        code_bytes, scale_bytes = _bytes(rows, cols)
+        t.data = torch.empty(code_bytes + scale_bytes, dtype=torch.uint8, device=device)
+        t.rows, t.cols, t._at = rows, cols, code_bytes
+        return t
 
     @property
     def shape(self) -> tuple:
@@ -48,7 +67,18 @@ class MxTensor:
 
     @property
     def device(self) -> torch.device:
-        return self.codes.device
+        return self.data.device
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self.data[: self._at]
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self.data[self._at: sum(_bytes(self.rows, self.cols))]
+
+    def __repr__(self) -> str:
+        return f"MxTensor([{self.rows}, {self.cols}], device={self.data.device})"
 
 
 def _dtype_code(dtype) -> int:
@@ -63,72 +93,55 @@ def _act_code(act: str) -> int:
     return _ACT[act]
 
 
-def _matrix(t, name: str) -> None:
+def _matrix(t, name: str) -> int:
+    """The dtype code of a nonempty matrix on a GPU."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise RuntimeError("libsvdq device calls need tensors on an AMD GPU (HIP device)")
-    if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
+    if t.dim() != 2 or t.numel() == 0:
         raise ValueError(f"{name} must be a nonempty matrix")
-    _dtype_code(t.dtype)
+    return _dtype_code(t.dtype)
 
 
 def _mx(t, name: str) -> None:
     if not isinstance(t, MxTensor):
         raise TypeError(f"{name}: expected an MxTensor")
-    code_bytes, scale_bytes = _bytes(t.rows, t.cols)
-    for part, need in ((t.codes, code_bytes), (t.scales, scale_bytes)):
-        if not isinstance(part, torch.Tensor) or part.dtype != torch.uint8 or not part.is_contiguous():
-            raise TypeError(f"{name}: codes and scales must be contiguous uint8 tensors")
-        if part.numel() < need:
-            raise ValueError(f"{name}: codes or scales shorter than its shape needs")
-    if not t.codes.is_cuda:
+    if not t.data.is_cuda:
         raise RuntimeError("libsvdq device calls need tensors on an AMD GPU (HIP device)")
-    if t.scales.device != t.codes.device:
-        raise ValueError(f"{name}: codes and scales must be on one device")
 
 
-def _same_device(*ts) -> torch.device:
-    dev = ts[0].device
-    for t in ts[1:]:
-        if t is not None and t.device != dev:
+def _same_device(device, *ts) -> None:
+    for t in ts:
+        if t is not None and t.device != device:
             raise ValueError("all tensors of a call must be on one device")
-    return dev
-
-
-def _bytes(rows: int, cols: int) -> tuple:
-    a, b = ctypes.c_size_t(), ctypes.c_size_t()
-    L.check(L.load().svdq_mx_layout(rows, cols, ctypes.byref(a), ctypes.byref(b)))
-    return a.value, b.value
-
-
-def _empty(rows: int, cols: int, device) -> MxTensor:
-    code_bytes, scale_bytes = _bytes(rows, cols)
-    return MxTensor(torch.empty(code_bytes, dtype=torch.uint8, device=device),
-                    torch.empty(scale_bytes, dtype=torch.uint8, device=device), rows, cols)
 
 
 def _call(name: str, device, *args) -> None:
     """libsvdq's `name` on the current stream of `device`, which is the current device meanwhile."""
-    fn = getattr(L.load(), name)
-    if torch.cuda.current_device() == device.index:
-        L.check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
-    else:
+    index = device.index
+    if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(device):
-            L.check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+            return _call(name, device, *args)
+    status = getattr(L.load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        L.check(status)
 
 
 def _parts(t) -> tuple:
-    return (None, None) if t is None else (t.codes.data_ptr(), t.scales.data_ptr())
+    if t is None:
+        return None, None
+    at = t.data.data_ptr()
+    return at, at + t._at
 
 
-def _output(out, rows: int, cols: int, dtype, device, name: str = "out") -> torch.Tensor:
+def _output(out, rows: int, cols: int, dtype, device) -> torch.Tensor:
     if out is None:
         return torch.empty((rows, cols), dtype=dtype, device=device)
     if not isinstance(out, torch.Tensor) or out.shape != (rows, cols) or out.dtype != dtype or out.device != device:
-        raise ValueError(f"{name} must be a [{rows}, {cols}] {dtype} tensor on {device}")
+        raise ValueError(f"out must be a [{rows}, {cols}] {dtype} tensor on {device}")
     if (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols):
-        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+        raise ValueError("out must have unit column stride and rows that do not overlap")
     return out
 
 
@@ -142,18 +155,32 @@ def _unit_columns(t: torch.Tensor) -> torch.Tensor:
     return t.contiguous()
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(name: str, *sizes) -> int:
+    need = ctypes.c_size_t()
+    L.check(getattr(L.load(), name)(*sizes, ctypes.byref(need)))
+    return need.value
+
+
+def _workspace(need: int, device) -> tuple:
+    """(tensor, address, bytes) of a call's scratch, from the current stream's memory."""
+    if not need:
+        return None, None, 0
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), need
+
+
 def mx_quantize(x: torch.Tensor, axis: int | None = 1):
     """Q(x) of x [R, C] (any strides): with axis=1 the [R, C] MxTensor whose blocks run along the rows of
     x, with axis=0 the [C, R] MxTensor of its transpose, whose blocks run along its columns; with
     axis=None both, from one pass over x. A block with an infinity or a NaN reads as NaN."""
-    _matrix(x, "x")
+    dt = _matrix(x, "x")
     if axis is not None and (isinstance(axis, bool) or axis not in (0, 1)):
         raise ValueError("axis must be 0, 1 or None")
-    R, C = x.shape
-    rows = _empty(R, C, x.device) if axis != 0 else None
-    cols = _empty(C, R, x.device) if axis != 1 else None
-    _call("svdq_mx_quantize", x.device, x.data_ptr(), R, C, x.stride(0), x.stride(1), _DT[x.dtype], *_parts(rows),
-          *_parts(cols))
+    (R, C), device = x.shape, x.device
+    rows = MxTensor._empty(R, C, device) if axis != 0 else None
+    cols = MxTensor._empty(C, R, device) if axis != 1 else None
+    _call("svdq_mx_quantize", device, x.data_ptr(), R, C, *x.stride(), dt, *_parts(rows), *_parts(cols))
     return (rows, cols) if axis is None else (rows if axis == 1 else cols)
 
 
@@ -166,44 +193,59 @@ def mx_dequantize(t: MxTensor, dtype: torch.dtype = torch.bfloat16, out: torch.T
     return out
 
 
-def _workspace(M: int, N: int, K: int, gated: bool, device) -> tuple:
-    """(tensor, address, bytes) of a product's scratch, from the current stream's memory."""
-    need = ctypes.c_size_t()
-    L.check(L.load().svdq_mx_workspace_bytes(M, N, K, gated, ctypes.byref(need)))
-    if not need.value:
-        return None, None, 0
-    ws = torch.empty(need.value, dtype=torch.uint8, device=device)
-    return ws, ws.data_ptr(), need.value
-
-
-def _operand(a, name: str, dtype):
-    """An MxTensor and the output dtype: a matrix is quantised along its rows, its dtype the default."""
-    if isinstance(a, torch.Tensor):
-        return mx_quantize(a), dtype or a.dtype
-    _mx(a, name)
-    return a, dtype or torch.bfloat16
+def _product(a, b, name_a: str, name_b: str, dtype, out, finish, *, gated: bool):
+    """The four products: `finish` gives (arguments between b's rows and the dtype, output columns, gu or None)
+    once a's rows, the dtype and the device are known."""
+    _mx(b, name_b)
+    raw = isinstance(a, torch.Tensor)
+    if raw:
+        _matrix(a, name_a)
+        dtype = dtype or a.dtype
+        if dtype != a.dtype:
+            a, raw = mx_quantize(a), False
+    else:
+        _mx(a, name_a)
+        dtype = dtype or torch.bfloat16
+    code = _dtype_code(dtype)
+    M, K = a.shape
+    if K != b.cols:
+        raise ValueError(f"{name_a} [{M}, {K}] and {name_b} [{b.rows}, {b.cols}] must share their second dimension")
+    device = a.device
+    _same_device(device, b)
+    extra, N, gu = finish(M, dtype, device)
+    y = _output(out, M, N, dtype, device)
+    tail = (code, y.data_ptr(), _row_stride(y)) + ((None if gu is None else gu.data_ptr(), 2 * N) if gated else ())
+    if raw:
+        sr, sc = a.stride()
+        if K == 1:
+            sc = 1
+        ws, *scratch = _workspace(_workspace_bytes("svdq_mx_linear_workspace_bytes", M, N, K, sc, gated), device)
+        _call("svdq_mx_gated_linear" if gated else "svdq_mx_linear", device, a.data_ptr(), M, K, sr, sc, *_parts(b), N,
+              extra, *tail, *scratch)
+    else:
+        ws, *scratch = _workspace(_workspace_bytes("svdq_mx_workspace_bytes", M, N, K, gated), device)
+        _call("svdq_mx_gated" if gated else "svdq_mx_matmul", device, *_parts(a), M, *_parts(b), N, K, extra, *tail,
+              *scratch)
+    return y
 
 
 def mx_matmul(a, b: MxTensor, bias: torch.Tensor | None = None, dtype: torch.dtype | None = None,
               out: torch.Tensor | None = None) -> torch.Tensor:
     """Y = A B^T (+ bias) [M, N] of a [M, K] and b [N, K]: MXFP4 products summed in float32, rounded once.
-    a: an MxTensor, or a matrix, which is quantised along its rows first. dtype: a matrix's own, else
+    a: an MxTensor, or a matrix, which is quantised along its rows. dtype: a matrix's own, else
     bfloat16. bias: [N] of that dtype. For a layer with weight [K, N], b = mx_quantize(weight, axis=0)."""
-    _mx(b, "b")
-    a, dtype = _operand(a, "a", dtype)
-    code = _dtype_code(dtype)
-    if a.cols != b.cols:
-        raise ValueError(f"a [{a.rows}, {a.cols}] and b [{b.rows}, {b.cols}] must share their second dimension")
-    device = _same_device(a, b, bias)
-    if bias is not None:
-        if bias.dim() != 1 or bias.shape[0] != b.rows or bias.dtype != dtype:
+
+    def finish(M, dt, device):
+        if bias is None:
+            return None, b.rows, None
+        if not isinstance(bias, torch.Tensor) or bias.dim() != 1 or bias.shape[0] != b.rows or bias.dtype != dt:
             raise ValueError(f"bias must be a [{b.rows}] tensor of the output's dtype")
-        bias = bias.contiguous()
-    y = _output(out, a.rows, b.rows, dtype, device)
-    _keep, *ws = _workspace(a.rows, b.rows, a.cols, False, device)
-    _call("svdq_mx_matmul", device, *_parts(a), a.rows, *_parts(b), b.rows, a.cols,
-          None if bias is None else bias.data_ptr(), code, y.data_ptr(), _row_stride(y), *ws)
-    return y
+        _same_device(device, bias)
+        held.append(bias.contiguous())
+        return held[0].data_ptr(), b.rows, None
+
+    held = []
+    return _product(a, b, "a", "b", dtype, out, finish, gated=False)
 
 
 def mx_gated(x, w: MxTensor, act: str = "silu", dtype: torch.dtype | None = None, save: bool = False,
@@ -213,20 +255,17 @@ def mx_gated(x, w: MxTensor, act: str = "silu", dtype: torch.dtype | None = None
     the merged weight [K, 2F]. act: "silu", "gelu", "gelu_tanh" or "relu". With save=True also returns the
     pre-activations [M, 2F] (gate, then up), rounded to the dtype, for mx_gated_backward."""
     code = _act_code(act)
-    _mx(w, "w")
-    x, dtype = _operand(x, "x", dtype)
-    dt = _dtype_code(dtype)
-    if w.rows % 2:
-        raise ValueError("w must hold as many up rows as gate rows")
-    if x.cols != w.cols:
-        raise ValueError(f"x [{x.rows}, {x.cols}] and w [{w.rows}, {w.cols}] must share their second dimension")
-    device = _same_device(x, w)
-    M, F = x.rows, w.rows // 2
-    h = _output(out, M, F, dtype, device)
-    gu = torch.empty((M, 2 * F), dtype=dtype, device=device) if save else None
-    _keep, *ws = _workspace(M, F, x.cols, True, device)
-    _call("svdq_mx_gated", device, *_parts(x), M, *_parts(w), F, x.cols, code, dt, h.data_ptr(), _row_stride(h),
-          None if gu is None else gu.data_ptr(), 2 * F, *ws)
+    gu = None
+
+    def finish(M, dt, device):
+        nonlocal gu
+        if w.rows % 2:
+            raise ValueError("w must hold as many up rows as gate rows")
+        if save:
+            gu = torch.empty((M, w.rows), dtype=dt, device=device)
+        return code, w.rows // 2, gu
+
+    h = _product(x, w, "x", "w", dtype, out, finish, gated=True)
     return (h, gu) if save else h
 
 
@@ -234,16 +273,17 @@ def mx_gated_grad(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu"):
     """The gradients d = [dg | du] of a gated block's pre-activations, dg = dh * u * act'(g) and
     du = dh * act(g), from dh [M, F] and gu [M, 2F]: Q(d) [M, 2F] and Q(d^T) [2F, M], from one pass."""
     code = _act_code(act)
-    _matrix(dh, "dh")
+    dt = _matrix(dh, "dh")
     _matrix(gu, "gu")
     M, F = dh.shape
     if gu.shape != (M, 2 * F) or gu.dtype != dh.dtype:
         raise ValueError(f"gu must be a [{M}, {2 * F}] tensor of dh's dtype")
-    device = _same_device(dh, gu)
+    device = dh.device
+    _same_device(device, gu)
     dh, gu = _unit_columns(dh), _unit_columns(gu)
-    rows, cols = _empty(M, 2 * F, device), _empty(2 * F, M, device)
-    _call("svdq_mx_gated_grad", device, dh.data_ptr(), _row_stride(dh), gu.data_ptr(), _row_stride(gu), M, F, code,
-          _DT[dh.dtype], *_parts(rows), *_parts(cols))
+    rows, cols = MxTensor._empty(M, 2 * F, device), MxTensor._empty(2 * F, M, device)
+    _call("svdq_mx_gated_grad", device, dh.data_ptr(), _row_stride(dh), gu.data_ptr(), _row_stride(gu), M, F, code, dt,
+          *_parts(rows), *_parts(cols))
     return rows, cols
 
 
@@ -258,7 +298,7 @@ def mx_gated_backward(dh: torch.Tensor, gu: torch.Tensor, w_rows: MxTensor, x_co
     M, F = dh.shape
     if w_rows.cols != 2 * F or x_cols.cols != M or w_rows.rows != x_cols.rows:
         raise ValueError(f"w_rows must be [K, {2 * F}] and x_cols [K, {M}]")
-    _same_device(dh, w_rows, x_cols)
+    _same_device(dh.device, w_rows, x_cols)
     dtype = dtype or dh.dtype
     _dtype_code(dtype)
     rows, cols = mx_gated_grad(dh, gu, act)

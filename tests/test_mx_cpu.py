@@ -123,6 +123,30 @@ def test_gated_refusals(change, status):
 
 
 @pytest.mark.parametrize("change,status", [
+    (dict(dtype=F64), EDTYPE), (dict(M=0), EINVAL), (dict(N=0), EINVAL), (dict(K=0), EINVAL), (dict(x=None), EINVAL),
+    (dict(x=A + 2), EINVAL), (dict(sr=-1), EINVAL), (dict(sc=-1), EINVAL), (dict(bc=None), EINVAL), (dict(bs=A + 4), EINVAL),
+    (dict(bias=A + 2), EINVAL), (dict(y=None), EINVAL), (dict(ldy=7), EINVAL), (dict(K=(1 << 27) + 1), EINVAL),
+    (dict(M=100), EINVAL), (dict(sc=2), EINVAL), (dict(M=100, work=A, bytes=64), EINVAL),
+    (dict(M=100, work=A + 1, bytes=1 << 40), EINVAL),
+])
+def test_linear_refusals(change, status):
+    a = dict(x=A, M=4, K=40, sr=40, sc=1, bc=A, bs=A, N=8, bias=None, dtype=F32, y=A, ldy=8, work=None, bytes=0)
+    a.update(change)
+    _refused(status, _lib.load().svdq_mx_linear(*a.values(), None))
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=F64), EDTYPE), (dict(M=0), EINVAL), (dict(F=0), EINVAL), (dict(F=1 << 30), EINVAL), (dict(act=4), EINVAL),
+    (dict(x=None), EINVAL), (dict(wc=None), EINVAL), (dict(h=None), EINVAL), (dict(ldh=7), EINVAL),
+    (dict(gu=A, ldgu=15), EINVAL), (dict(M=100), EINVAL), (dict(sc=0), EINVAL),
+])
+def test_gated_linear_refusals(change, status):
+    a = dict(x=A, M=4, K=40, sr=40, sc=1, wc=A, ws=A, F=8, act=0, dtype=BF16, h=A, ldh=8, gu=None, ldgu=0, work=None, bytes=0)
+    a.update(change)
+    _refused(status, _lib.load().svdq_mx_gated_linear(*a.values(), None))
+
+
+@pytest.mark.parametrize("change,status", [
     (dict(dtype=F64), EDTYPE), (dict(M=0), EINVAL), (dict(F=0), EINVAL), (dict(F=1 << 30), EINVAL), (dict(act=9), EINVAL),
     (dict(dh=None), EINVAL), (dict(ldh=7), EINVAL), (dict(gu=None), EINVAL), (dict(ldgu=15), EINVAL), (dict(gu=A + 1), EINVAL),
     (dict(codes=None), EINVAL), (dict(scales_t=A + 1), EINVAL),
@@ -142,12 +166,17 @@ def test_workspace_query():
     for bad in ((0, 4, 4, 0), (4, 0, 4, 0), (4, 4, 0, 0), (4, 1 << 30, 4, 1), (4, 4, (1 << 27) + 1, 0)):
         _refused(EINVAL, lib.svdq_mx_workspace_bytes(*bad, ctypes.byref(n)))
     _refused(EINVAL, lib.svdq_mx_workspace_bytes(4, 4, 4, 0, None))
+    codes, scales = _layout(100, 512)[1:]
+    assert lib.svdq_mx_linear_workspace_bytes(100, 256, 512, 1, 0, ctypes.byref(n)) == 0 and n.value == codes + scales
+    assert lib.svdq_mx_linear_workspace_bytes(1, 256, 512, 1, 1, ctypes.byref(n)) == 0 and n.value == 0
+    _refused(EINVAL, lib.svdq_mx_linear_workspace_bytes(4, 4, 4, -1, 0, ctypes.byref(n)))
+    _refused(EINVAL, lib.svdq_mx_linear_workspace_bytes(4, 0, 4, 1, 0, ctypes.byref(n)))
 
 
 # ----------------------------------------------------------------------------- binding
 def _fake(rows, cols, short=0):
     _, a, b = _layout(rows, cols)
-    return R.MxTensor(torch.zeros(a - short, dtype=torch.uint8), torch.zeros(b, dtype=torch.uint8), rows, cols)
+    return R.MxTensor(torch.zeros(a + b - short, dtype=torch.uint8), rows, cols)
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_types():
@@ -161,7 +190,14 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         with pytest.raises(TypeError):
             call()
     with pytest.raises(ValueError):
-        R.mx_dequantize(_fake(20, 64, short=1))
+        _fake(20, 64, short=1)
+    with pytest.raises(ValueError):
+        R.MxTensor(torch.zeros(1 << 20, dtype=torch.uint8), 0, 4)
+    for data in (torch.zeros(1 << 20), torch.zeros(4, 1 << 20, dtype=torch.uint8), torch.zeros(1 << 21, dtype=torch.uint8)[::2]):
+        with pytest.raises(TypeError):
+            R.MxTensor(data, 4, 4)
+    t = _fake(20, 64)
+    assert t.shape == (20, 64) and t.codes.numel() + t.scales.numel() == t.data.numel() and "20, 64" in repr(t)
     with pytest.raises(ValueError):
         R.mx_gated(x, _fake(8, 64), act="swish")
     with pytest.raises(ValueError):
