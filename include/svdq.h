@@ -420,8 +420,9 @@ int svdq_mx_gated_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_
  *   codes / scales:     Q(d)   [M, 2F]  (times the weight quantised along 2F: dx)
  *   codes_t / scales_t: Q(d^T) [2F, M]  (with the input quantised along M: dw)
  * The codes are those of the formulas in binary64 on the given dh and gu (binary32, and
- * binary64 where that lies too near a border between two codes); a magnitude below 2^-126
- * counts as float32 keeps it. Either pair may be NULL, not both.
+ * binary64 where that lies too near a border between two codes), except that a product
+ * dh * u below 2^-120 or past 2^127 is rounded (or overflows) as float32 does. Either pair may
+ * be NULL, not both.
  * dh: [M, F] row stride ldh >= F; gu: [M, 2F] row stride ldgu >= 2F; both of dtype.
  * Errors: EINVAL, EDTYPE, EHIP.
  * ------------------------------------------------------------------------------------ */

@@ -7,20 +7,35 @@
 // straight into registers, a contiguous kilobyte per 16 rows and stage, several stages of requests in flight. The
 // waves' partial tiles are added in LDS in a fixed order.
 //
-// A may be given unquantised (RAW): lane (i, g) then loads the 32 elements of its own block, takes their
-// maximum and their codes without leaving the lane. That re-quantises x in every block, and costs no launch.
+// A may be given unquantised: every block then quantises x for itself, which costs vector instructions next to the
+// reads of b but no launch. Lane (i, g) loads the 32 elements of its own block and takes their maximum and codes
+// without leaving the lane (X_ROWS); for a single row the 16 lanes of a block share it, two elements each, and
+// broadcast the code words among them (X_ONE), a quarter of the instructions.
 #include "mx.h"
 #include "mx_device.h"
 
 namespace svdq {
 namespace dev {
 
-template <class DT, int MT, int NT, int WAVES, bool GATED, bool RAW>
+enum { A_CODES, X_ROWS, X_ONE };
+
+// Row-of-16 cross-lane moves (DPP): rotation by N lanes, and lane N to all.
+template <int N>
+__device__ inline u32 row_rotate(u32 v) {
+  return (u32)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xF, 0xF, true);
+}
+template <int N>
+__device__ inline u32 row_from(u32 v) {
+  return (u32)__builtin_amdgcn_mov_dpp((int)v, 0x150 + N, 0xF, 0xF, true);
+}
+
+template <class DT, int MT, int NT, int WAVES, bool GATED, int FORM>
 __global__ __launch_bounds__(64 * WAVES) void k_mx_decode(MxGemmParams p) {
   typedef typename DT::T T;
   static_assert(!GATED || NT == 2, "a gate tile and an up tile");
-  constexpr int XW = DT::size * 8;  // words of 32 elements of x
-  constexpr int BATCH = RAW ? (DT::size == 4 ? 2 : 4) : (MT >= 2 ? 4 : 8);
+  constexpr bool RAW = FORM != A_CODES;
+  constexpr int XW = FORM == X_ONE ? DT::size / 2 : DT::size * 8;  // words of x a lane holds of a stage
+  constexpr int BATCH = FORM == X_ROWS ? (DT::size == 4 ? 2 : 4) : (MT >= 2 ? 4 : 8);
   __shared__ float red[WAVES][MT][NT][4][64];
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int i = lane & 15, g = lane >> 4;
@@ -69,7 +84,21 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_decode(MxGemmParams p) {
     }
 #pragma unroll
     for (int m = 0; m < MT; m++) {
-      if constexpr (RAW) {
+      if constexpr (FORM == X_ONE) {
+        const int64_t c = (int64_t)s * 128 + 32 * g + 2 * i;
+        if (c + 2 <= p.K) {
+          __builtin_memcpy(q.x[m], xr[m] + c, sizeof q.x[m]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < XW; k++) q.x[m][k] = 0;
+          if (c < p.K) {
+            if constexpr (DT::size == 4)
+              q.x[m][0] = __float_as_uint(xr[m][c]);
+            else
+              q.x[m][0] = xr[m][c];
+          }
+        }
+      } else if constexpr (FORM == X_ROWS) {
         const int64_t c = (int64_t)s * 128 + 32 * g;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -88,7 +117,21 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_decode(MxGemmParams p) {
     for (int m = 0; m < MT; m++) {
       v4i a;
       u32 sa;
-      if constexpr (RAW) {
+      if constexpr (FORM == X_ONE) {
+        u32 most = amax_bits<DT>(q.x[m]);
+        most = max(most, row_rotate<8>(most));
+        most = max(most, row_rotate<4>(most));
+        most = max(most, row_rotate<2>(most));
+        most = max(most, row_rotate<1>(most));
+        sa = mx_scale_byte(most);
+        u32 w[DT::size * 2] = {};
+        w[0] = q.x[m][0];
+        if constexpr (DT::size == 4) w[1] = q.x[m][1];
+        u32 part = (codes8<DT>(w, sa) & 0xFFu) << (8 * (i & 3));
+        part |= (u32)__builtin_amdgcn_mov_dpp((int)part, 0xB1, 0xF, 0xF, true);  // the quad's four bytes
+        part |= (u32)__builtin_amdgcn_mov_dpp((int)part, 0x4E, 0xF, 0xF, true);
+        a = v4i{(int)row_from<0>(part), (int)row_from<4>(part), (int)row_from<8>(part), (int)row_from<12>(part)};
+      } else if constexpr (FORM == X_ROWS) {
         sa = mx_scale_byte(amax_bits<DT>(q.x[m]));
 #pragma unroll
         for (int e = 0; e < 4; e++) a[e] = (int)codes8<DT>(q.x[m] + e * (XW / 4), sa);
@@ -163,24 +206,24 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_decode(MxGemmParams p) {
 
 using namespace dev;
 
-template <class DT, int MT, int WAVES, bool RAW>
+template <class DT, int MT, int WAVES, int FORM>
 static hipError_t launch_rows(const MxGemmParams& p, bool gated, hipStream_t stream) {
   const int64_t cols16 = ((int64_t)p.N + 15) / 16;
   if (gated)
-    k_mx_decode<DT, MT, 2, WAVES, true, RAW><<<dim3((unsigned)cols16), 64 * WAVES, 0, stream>>>(p);
+    k_mx_decode<DT, MT, 2, WAVES, true, FORM><<<dim3((unsigned)cols16), 64 * WAVES, 0, stream>>>(p);
   else if (cols16 >= 512)  // two column tiles per block while that leaves a block for every compute unit
-    k_mx_decode<DT, MT, 2, WAVES, false, RAW><<<dim3((unsigned)((cols16 + 1) / 2)), 64 * WAVES, 0, stream>>>(p);
+    k_mx_decode<DT, MT, 2, WAVES, false, FORM><<<dim3((unsigned)((cols16 + 1) / 2)), 64 * WAVES, 0, stream>>>(p);
   else
-    k_mx_decode<DT, MT, 1, WAVES, false, RAW><<<dim3((unsigned)cols16), 64 * WAVES, 0, stream>>>(p);
+    k_mx_decode<DT, MT, 1, WAVES, false, FORM><<<dim3((unsigned)cols16), 64 * WAVES, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <class DT>
 static hipError_t launch_decode_t(const MxGemmParams& p, bool gated, hipStream_t stream) {
-  if (p.x) return launch_rows<DT, 1, 8, true>(p, gated, stream);
-  if (p.M <= 16) return launch_rows<DT, 1, 8, false>(p, gated, stream);
-  if (p.M <= 32) return launch_rows<DT, 2, 8, false>(p, gated, stream);
-  return launch_rows<DT, 4, 4, false>(p, gated, stream);
+  if (p.x) return p.M == 1 ? launch_rows<DT, 1, 8, X_ONE>(p, gated, stream) : launch_rows<DT, 1, 8, X_ROWS>(p, gated, stream);
+  if (p.M <= 16) return launch_rows<DT, 1, 8, A_CODES>(p, gated, stream);
+  if (p.M <= 32) return launch_rows<DT, 2, 8, A_CODES>(p, gated, stream);
+  return launch_rows<DT, 4, 4, A_CODES>(p, gated, stream);
 }
 
 hipError_t launch_mx_decode(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream) {

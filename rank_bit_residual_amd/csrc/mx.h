@@ -43,11 +43,18 @@ struct MxDequantParams {
   int64_t ldo;
 };
 
-// Rows of A that the decode kernel takes, and those of an unquantised A.
-constexpr int64_t kMxDecodeRows = 64, kMxRawRows = 16;
+// Rows of A that the decode kernel takes.
+constexpr int64_t kMxDecodeRows = 64;
 
+// Whether the decode kernel quantises A itself: one row, or few rows and few columns to do it again for. Measured on
+// the GPU's clock as one launch against two (quantise, product), K = 4096 unless said: 1 row x 24576 columns 12.3 us
+// against 14.3; 4 x 8192 (K = 8192) 9.3 against 10.3, 8 rows 10.5 against 10.3; 8 x 4096 6.2 against 6.5, 16 rows 7.5 against
+// 6.6; 16 x 1024 (K = 1024) 3.4 against 4.7.
+inline bool mx_raw_rows(int64_t M, int64_t b_rows, int64_t sc) {
+  return sc == 1 && (M == 1 || (M <= 16 && M * b_rows <= 32768));
+}
 struct MxGemmParams {
-  // unquantised A (at most kMxRawRows rows): [M][ldx] of the output's dtype, K elements a row, or NULL
+  // unquantised A (mx_raw_rows): [M][ldx] of the output's dtype, K elements a row, or NULL
   const void* x;
   int64_t ldx, K;
   const uint8_t* a_codes;

@@ -44,13 +44,15 @@ struct MxF16 {
   }
 };
 
-// Scale byte of a block from the bits of its largest magnitude as float32; 255 (NaN) from
-// infinity on.
+// Scale byte e + 127 of a block from the bits of its largest magnitude as float32, with e the smallest with amax <=
+// 6 * 2^e = 1.5 * 2^(e + 2): the exponent field, one more where the fraction is past 1/2, less 2; 0 below 2^-126; 255 (NaN)
+// from infinity on.
 __device__ inline u32 mx_scale_byte(u32 amax_bits) {
-  return amax_bits >= 0x7F800000u ? 255u : (u32)(mx_exponent(__uint_as_float(amax_bits)) + 127);
+  const u32 e = max((amax_bits + 0x3FFFFFu) >> 23, 2u) - 2u;
+  return amax_bits >= 0x7F800000u ? 255u : e;
 }
 // 2^e of a scale byte below 255.
-__device__ inline float mx_scale_value(u32 byte) { return pow2f((int)byte - 127); }
+__device__ inline float mx_scale_value(u32 byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
 
 // ---- eight elements at a time ------------------------------------------------------------
 // Eight consecutive elements of a row, in registers.
@@ -121,22 +123,22 @@ __device__ inline u32 amax_bits(const u32 (&w)[N]) {
 // The word of eight codes (zeros for a NaN block).
 template <class DT>
 __device__ inline u32 codes8(const u32* w, u32 byte) {
-  if (byte == 255u) return 0;
   const float s = mx_scale_value(byte);
+  u32 c;
   if constexpr (DT::size == 4) {
     float v[8];
 #pragma unroll
     for (int q = 0; q < 8; q++) v[q] = __uint_as_float(w[q]);
-    return fp4_pack8(v, s);
+    c = fp4_pack8(v, s);
   } else {
-    return DT::codes8(w, s);
+    c = DT::codes8(w, s);
   }
+  return byte == 255u ? 0u : c;
 }
 
 // ---- gated activations ------------------------------------------------------------------
-// act(g) and act'(g), and bounds on the relative error of act and the absolute error of act'
-// when F is float (unused for double). Where a factor nears the bottom of the float32 range the
-// bound is the value itself.
+// act(g) and act'(g). For float, with ew, abs_d: |error of act| <= ew |act|, |error of act'| <= abs_d, good while
+// tail >= -60 (below that a factor nears the bottom of the float32 range):
 //   silu       g s,  s = 1 / (1 + e^-w), w = g
 //   gelu_tanh  g s with w = 2 sqrt(2 / pi) (g + 0.044715 g^3), which equals
 //              g (1 + tanh(w / 2)) / 2 without its cancellation for negative g
@@ -150,7 +152,7 @@ __device__ inline u32 codes8(const u32* w, u32 byte) {
 template <class F>
 struct ActValue {
   F a, d;
-  float rel_a, abs_d;
+  float ew, abs_d, tail;
 };
 
 __device__ inline float act_exp(float v) { return __expf(v); }
@@ -166,32 +168,32 @@ __device__ inline ActValue<F> act_value(F g) {
   if constexpr (ACT == SVDQ_ACT_RELU) {
     r.a = g < F(0) ? F(0) : g;
     r.d = g > F(0) ? F(1) : (g == g ? F(0) : g);
-    r.rel_a = 0x1p-22f;
-    r.abs_d = 0x1p-22f;
+    r.ew = 0x1p-22f;
+    r.abs_d = (float)r.d * 0x1p-22f;
+    r.tail = 0.f;
   } else if constexpr (ACT == SVDQ_ACT_GELU) {
     const F p = F(0.5) * act_erfc(F(-0.70710678118654752440) * g);
     const F q = g * (F(0.39894228040143267794) * act_exp(F(-0.5) * g * g));
     r.a = g * p;
     r.d = p + q;
-    const float g2 = (float)(g * g);
-    r.rel_a = g < F(-10) ? 1.f : (3.f + g2) * 0x1p-20f;
-    r.abs_d = ((float)p + fabsf((float)q)) * r.rel_a;
+    r.ew = (3.f + (float)(g * g)) * 0x1p-20f;
+    r.abs_d = ((float)p + fabsf((float)q)) * r.ew;
+    r.tail = 6.f * (float)g;
   } else {
     F w = g, dw = F(1), gc = g;
     if constexpr (ACT == SVDQ_ACT_GELU_TANH) {
       // past 30 the sigmoid is 0 or 1 and w' times 1 - s no longer counts, but g^3 could overflow
       gc = g > F(30) ? F(30) : (g < F(-30) ? F(-30) : g);
-      const F c = F(1.59576912160573071176);
-      w = c * (gc + F(0.044715) * (gc * gc * gc));
-      dw = c * (F(1) + F(0.134145) * (gc * gc));
+      const F c = F(1.59576912160573071176), g2 = gc * gc;
+      w = gc * (c + F(1.59576912160573071176 * 0.044715) * g2);
+      dw = c + F(1.59576912160573071176 * 0.134145) * g2;
     }
-    const F s = act_rcp(F(1) + act_exp(-w));
-    const F t = (gc * dw) * (F(1) - s);
+    const F s = act_rcp(F(1) + act_exp(-w)), gw = gc * dw;
     r.a = g * s;
-    r.d = s * (F(1) + t);
-    const float ew = w < F(-60) ? 1.f : (3.f + fabsf((float)w)) * 0x1p-21f;
-    r.rel_a = ew;
-    r.abs_d = (float)s * (1.f + fabsf((float)(gc * dw))) * ew;
+    r.d = s * (F(1) + gw * (F(1) - s));
+    r.ew = (3.f + fabsf((float)w)) * 0x1p-21f;
+    r.abs_d = (float)s * (1.f + fabsf((float)gw)) * r.ew;
+    r.tail = (float)w;
   }
   return r;
 }
