@@ -21,6 +21,10 @@ namespace svdq {
 namespace dev {
 
 constexpr int kTile = 128, kMxBlock = 32;
+#ifndef TWX
+#define TWX 64
+#endif
+constexpr int kGradTw = TWX;
 
 __device__ inline u32 quad_max(u32 v) {
   v = max(v, (u32)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));  // quad_perm [1,0,3,2]
@@ -63,24 +67,28 @@ __device__ inline void put_col(const MxGroup& o, const u32 (&w)[N], u32 lc, u32 
   o.scales[(lc << 2) + kb] = (uint8_t)byte;
 }
 
-// LDS copy of a tile: W words per row. A column reader's lanes are 16 columns x 4 blocks of 32
-// rows; moving a row's 16-word groups by its block's number puts the four blocks on different banks.
+// LDS copy of a tile: W words per row. A column reader's lanes are 16 columns x 4 blocks of 32 rows; moving a row's
+// 16-word groups by its block's number puts the four blocks on different banks (W = 32 has two groups: there the
+// upper blocks' neighbouring rows change places).
 template <int W>
 __device__ inline int tile_word(int row, int word) {
-  return row * W + (word ^ (((row >> 5) & 3) << 4));
+  if constexpr (W == 32)
+    return (row ^ ((row >> 6) & 1)) * W + (word ^ (((row >> 5) & 1) << 4));
+  else
+    return row * W + (word ^ (((row >> 5) & 3) << 4));
 }
 
-// Columns of a 128 x 128 tile of 16-bit values, by four waves: a lane takes a pair of columns, the low halves of its words
+// Columns of a tile of 128 rows of W pairs of 16-bit values, by W / 16 waves: a lane takes a pair of columns, the low halves of its words
 // and then the high halves; a wave's 16 pairs are two 16-column groups, the first of the tile being group0. `left`: columns
 // that exist.
-template <class DT>
+template <class DT, int W>
 __device__ __forceinline__ void pair_cols(const u32* tile, const MxOut& out, int64_t group0, int stage, int wave, int l16,
                                           int kb, int64_t left) {
   const int pr = 16 * wave + l16;
   u32 lo[16], hi[16];
 #pragma unroll
   for (int r = 0; r < 16; r++) {
-    const u32 a = tile[tile_word<kTile / 2>(32 * kb + 2 * r, pr)], b = tile[tile_word<kTile / 2>(32 * kb + 2 * r + 1, pr)];
+    const u32 a = tile[tile_word<W>(32 * kb + 2 * r, pr)], b = tile[tile_word<W>(32 * kb + 2 * r + 1, pr)];
     lo[r] = __builtin_amdgcn_perm(b, a, 0x05040100u);
     hi[r] = __builtin_amdgcn_perm(b, a, 0x07060302u);
   }
@@ -148,7 +156,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantParams p, int tiles_
         put_col<DT>(group_of(p.cols, (int64_t)tc * 8 + 4 * h + wave, tr), w, l16, kb, c < left);
       }
     } else {
-      pair_cols<DT>(tile, p.cols, (int64_t)tc * 8, tr, wave, l16, kb, left);
+      pair_cols<DT, W>(tile, p.cols, (int64_t)tc * 8, tr, wave, l16, kb, left);
     }
   }
 }
@@ -319,38 +327,20 @@ __device__ __forceinline__ void grad8(const GradIn<DT>& x, Vec8<MxBF16>& dg, Vec
   }
 }
 
-// Block: 512 threads, thread t with elements [8 (t % 16), + 8) of rows t / 16 + 32 i of a 128 x 128 tile.
-// PAIR (F a multiple of 32, so that blocks along [dg | du] belong to one side): the tile is one of dh, g and u, and gives a
-// tile of dg and one of du; every input is read once.
-// Else the tile is one of d = [dg | du], each lane's elements from whichever side they lie on. The two that read the
-// same dh and g, one on either side of F, go to blocks 8 apart: neighbours on one XCD, so that the second finds
-// them in its L2.
-// Two blocks per compute unit (128 registers) where that spills next to nothing; float32 inputs and erf take more.
-template <class DT, int ACT, bool PAIR, bool ROWS, bool COLS>
-__global__ __launch_bounds__(512, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 : 4) void k_mx_gated_grad(MxGradParams p, int tiles_c, int pairs) {
-  constexpr int TILE = kTile * kTile / 2;  // words
-  __shared__ __align__(16) u32 tile[COLS ? (PAIR ? 2 : 1) * TILE : 4];
+// A tile of 128 rows of TW columns by 4 TW threads, each with eight elements of rows 32 apart.
+// GRAD_PAIR: columns [c0, c0 + TW) of dh, g and u give a tile of dg and one of du. GRAD_GATE, GRAD_UP, GRAD_MIXED: a tile of
+// d = [dg | du] at j0, all dg, all du, or some of either.
+enum { GRAD_PAIR, GRAD_GATE, GRAD_UP, GRAD_MIXED };
+
+template <class DT, int ACT, int MODE, int TW, bool ROWS, bool COLS>
+__device__ __forceinline__ void grad_tile(const MxGradParams& p, u32* tile, int tr, int tc) {
+  constexpr int LPR = TW / 8, TILE = kTile * TW / 2;  // lanes per row, words of a tile
   typedef typename DT::T T;
-  const int t = threadIdx.x, l16 = t & 15, lr = (t >> 4) & 15, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int half = wave >> 2;
-  const int64_t F = p.F;
-  int tr, tc;
-  if constexpr (PAIR) {
-    tr = blockIdx.x / tiles_c;
-    tc = blockIdx.x - tr * tiles_c;
-  } else {
-    const int64_t id = (int64_t)(blockIdx.x >> 4) * 8 + (blockIdx.x & 7);
-    tr = (int)(id / pairs);
-    const int pair = (int)(id - (int64_t)tr * pairs), side = (blockIdx.x >> 3) & 1, first_up = (int)(F / kTile);
-    tc = side ? first_up + pair : pair;
-    if (side ? tc >= tiles_c : tc >= first_up) return;
-    if (COLS ? tr >= p.cols.kq : (int64_t)tr * kTile >= p.M) return;
-  }
-  const int64_t left_r = p.M - (int64_t)tr * kTile;
-  const int64_t j = (int64_t)tc * kTile + 8 * l16;
-  // this lane's elements: of the gate side, of the up side, or some of either
-  const bool up = !PAIR && j >= F, mixed = !PAIR && !up && j + 8 > F;
-  const int64_t c = up ? j - F : j;
+  const int t = threadIdx.x, lc = t % LPR, lr = (t / LPR) & 15, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int half = wave / (LPR / 4);  // the 16-row half of a pass's 32 rows
+  const int64_t F = p.F, left_r = p.M - (int64_t)tr * kTile;
+  const int64_t j = (int64_t)tc * TW + 8 * lc, c = MODE == GRAD_UP || (MODE == GRAD_MIXED && j >= F) ? j - F : j;
+  const bool mixed = MODE == GRAD_MIXED && j < F && j + 8 > F;
   const int64_t row0 = (int64_t)tr * kTile + 16 * half + lr;
   const T* dhp = reinterpret_cast<const T*>(p.dh) + row0 * p.ldh;
   const T* gp = reinterpret_cast<const T*>(p.gu) + row0 * p.ldgu;
@@ -362,7 +352,7 @@ __global__ __launch_bounds__(512, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 : 4)
     if (!mixed) {
       x.dh = load8<DT>(dr, c, F);
       x.g = load8<DT>(gr, c, F);
-      if (!up) x.u = load8<DT>(gr + F, c, F);
+      if (MODE != GRAD_UP) x.u = load8<DT>(gr + F, c, F);
     } else {
 #pragma unroll
       for (int q = 0; q < 8; q++) {
@@ -381,68 +371,92 @@ __global__ __launch_bounds__(512, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 : 4)
     }
     return x;
   };
-  // du's place in a row of the row tensor: F is a multiple of 32, not of a stage
-  const int up_stage = (int)(F / kTile), up_pos = (int)(F % kTile);
+  // places in a row of the row tensor: the tile's, and du's (F is a multiple of 32, not of a stage)
+  const int64_t up_at = F + (int64_t)tc * TW;
+  const int stage = tc / (kTile / TW), pos = (tc % (kTile / TW)) * TW + 8 * lc;
+  const int up_stage = (int)(up_at / kTile), up_pos = (int)(up_at % kTile) + 8 * lc;
   GradIn<DT> next = load(0);
 #pragma unroll 1
   for (int i = 0; i < 4; i++) {
     const GradIn<DT> x = next;
     if (i < 3) next = load(i + 1);
     const int in = 32 * i + 16 * half;  // the 16-row group's first row in the tile
-    Vec8<MxBF16> dg = zero8<MxBF16>(), du = zero8<MxBF16>();
+    Vec8<MxBF16> d = zero8<MxBF16>(), du = zero8<MxBF16>();
     if (in < left_r) {
-      const int64_t group = (int64_t)tr * 8 + 2 * i + half;
-      const bool live = in + lr < left_r;
-      if constexpr (PAIR) {
-        grad8<DT, ACT, true, true>(x, dg, du);
-        if constexpr (ROWS) {
-          put_row<MxBF16>(group_of(p.rows, group, tc), dg, lr, 8 * l16, live && c < F);
-          put_row<MxBF16>(group_of(p.rows, group, up_stage + tc), du, lr, up_pos + 8 * l16, live && c < F);
-        }
-      } else {
-        if (mixed) {
-          grad8<DT, ACT, true, true>(x, dg, du);
+      if constexpr (MODE == GRAD_UP)
+        grad8<DT, ACT, false, true>(x, du, d);
+      else
+        grad8<DT, ACT, true, MODE != GRAD_GATE>(x, d, du);
+      if constexpr (MODE == GRAD_MIXED) {
 #pragma unroll
-          for (int q = 0; q < 4; q++) {
-            const u32 from_up = (j + 2 * q >= F ? 0xFFFFu : 0u) | (j + 2 * q + 1 >= F ? 0xFFFF0000u : 0u);
-            dg.w[q] = (dg.w[q] & ~from_up) | (du.w[q] & from_up);
-          }
-        } else if (up) {
-          grad8<DT, ACT, false, true>(x, du, dg);  // d is du here
-        } else {
-          grad8<DT, ACT, true, false>(x, dg, du);
+        for (int q = 0; q < 4; q++) {
+          const u32 from_up = (j + 2 * q >= F ? 0xFFFFu : 0u) | (j + 2 * q + 1 >= F ? 0xFFFF0000u : 0u);
+          d.w[q] = (d.w[q] & ~from_up) | (du.w[q] & from_up);
         }
-        if constexpr (ROWS) put_row<MxBF16>(group_of(p.rows, group, tc), dg, lr, 8 * l16, live);
+      }
+      if constexpr (ROWS) {
+        const int64_t group = (int64_t)tr * 8 + 2 * i + half;
+        const bool live = in + lr < left_r && (MODE != GRAD_PAIR || c < F);
+        put_row<MxBF16>(group_of(p.rows, group, stage), d, lr, pos, live);
+        if constexpr (MODE == GRAD_PAIR) put_row<MxBF16>(group_of(p.rows, group, up_stage), du, lr, up_pos, live);
       }
     }
     if constexpr (COLS) {
-      const int at = tile_word<kTile / 2>(in + lr, 4 * l16);
-      *reinterpret_cast<v4i*>(&tile[at]) = v4i{(int)dg.w[0], (int)dg.w[1], (int)dg.w[2], (int)dg.w[3]};
-      if constexpr (PAIR) *reinterpret_cast<v4i*>(&tile[TILE + at]) = v4i{(int)du.w[0], (int)du.w[1], (int)du.w[2], (int)du.w[3]};
-    }
-  }
-  if constexpr (PAIR && ROWS) {
-    // the row tensor's padding past 2 F, zero codes and bytes, by the last column of blocks
-    if (tc == tiles_c - 1) {
-      for (int st = (int)(2 * F / kTile); st < p.rows.kq; st++) {
-        const bool past = (int64_t)st * kTile + 8 * l16 >= 2 * F;
-        for (int i = 0; i < 4; i++) {
-          const int in = 32 * i + 16 * half;
-          if (in < left_r)
-            put_row<MxBF16>(group_of(p.rows, (int64_t)tr * 8 + 2 * i + half, st), zero8<MxBF16>(), lr, 8 * l16, past && in + lr < left_r);
-        }
-      }
+      const int at = tile_word<TW / 2>(in + lr, 4 * lc);
+      *reinterpret_cast<v4i*>(&tile[at]) = v4i{(int)d.w[0], (int)d.w[1], (int)d.w[2], (int)d.w[3]};
+      if constexpr (MODE == GRAD_PAIR) *reinterpret_cast<v4i*>(&tile[TILE + at]) = v4i{(int)du.w[0], (int)du.w[1], (int)du.w[2], (int)du.w[3]};
     }
   }
   if constexpr (COLS) {
     __syncthreads();
-    const int kb = (t & 63) >> 4;
-    const int64_t col0 = (int64_t)tc * kTile;
-    if constexpr (PAIR)  // four waves for each side
-      pair_cols<MxBF16>(tile + half * TILE, p.cols, (int64_t)tc * 8 + (half ? F / 16 : 0), tr, wave & 3, l16, kb, F - col0);
+    const int kb = (t & 63) >> 4, l16 = t & 15, w = wave % (TW / 32);
+    const int64_t col0 = (int64_t)tc * TW;
+    if constexpr (MODE == GRAD_PAIR)  // half of the waves for each side
+      pair_cols<MxBF16, TW / 2>(tile + half * TILE, p.cols, (col0 + (half ? F : 0)) / 16, tr, w, l16, kb, F - col0);
     else if (half == 0)
-      pair_cols<MxBF16>(tile, p.cols, (int64_t)tc * 8, tr, wave, l16, kb, 2 * F - col0);
+      pair_cols<MxBF16, TW / 2>(tile, p.cols, col0 / 16, tr, w, l16, kb, 2 * F - col0);
   }
+}
+
+// F a multiple of 32, so that blocks along d = [dg | du] belong to one side: every input is read once.
+// Two blocks of 512 threads (or four of 256) per compute unit, 128 registers, where that spills next to nothing; float32
+// inputs and erf take more.
+template <class DT, int ACT, int TW, bool ROWS, bool COLS>
+__global__ __launch_bounds__(4 * TW, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 : 4) void k_mx_gated_grad(MxGradParams p, int tiles_c) {
+  __shared__ __align__(16) u32 tile[COLS ? kTile * TW : 4];
+  const int tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+  grad_tile<DT, ACT, GRAD_PAIR, TW, ROWS, COLS>(p, tile, tr, tc);
+  if constexpr (ROWS) {
+    // the row tensor's padding past 2 F, zero codes and bytes, by the last column of blocks
+    if (tc == tiles_c - 1) {
+      const int l16 = threadIdx.x & 15, lr = threadIdx.x >> 4;
+      for (int st = (int)(2 * p.F / kTile); st < p.rows.kq; st++) {
+        const bool past = (int64_t)st * kTile + 8 * l16 >= 2 * p.F;
+        for (int r = lr; r < kTile; r += TW / 4) {
+          const int64_t row = (int64_t)tr * kTile + r;
+          put_row<MxBF16>(group_of(p.rows, row >> 4, st), zero8<MxBF16>(), row & 15, 8 * l16, past && row < p.M);
+        }
+      }
+    }
+  }
+}
+
+// Any F: tiles of d itself. The two that read the same dh and g, one on either side of F, go to blocks 8 apart:
+// neighbours on one XCD, so that the second finds them in its L2.
+template <class DT, int ACT, int TW, bool ROWS, bool COLS>
+__global__ __launch_bounds__(4 * TW, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 : 4) void k_mx_gated_grad_any(MxGradParams p, int tiles_c, int pairs) {
+  __shared__ __align__(16) u32 tile[COLS ? kTile * TW / 2 : 4];
+  const int64_t id = (int64_t)(blockIdx.x >> 4) * 8 + (blockIdx.x & 7);
+  const int tr = (int)(id / pairs), pair = (int)(id - (int64_t)tr * pairs), side = (blockIdx.x >> 3) & 1;
+  const int first_up = (int)(p.F / TW), tc = side ? first_up + pair : pair;
+  if (side ? tc >= tiles_c : tc >= first_up) return;
+  if (COLS ? tr >= p.cols.kq : (int64_t)tr * kTile >= p.M) return;
+  if (side == 0)
+    grad_tile<DT, ACT, GRAD_GATE, TW, ROWS, COLS>(p, tile, tr, tc);
+  else if (pair != 0)
+    grad_tile<DT, ACT, GRAD_UP, TW, ROWS, COLS>(p, tile, tr, tc);
+  else
+    grad_tile<DT, ACT, GRAD_MIXED, TW, ROWS, COLS>(p, tile, tr, tc);
 }
 
 }  // namespace dev
@@ -492,29 +506,29 @@ hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t
   });
 }
 
-template <class DT, int ACT, bool ROWS, bool COLS>
+template <class DT, int ACT, int TW, bool ROWS, bool COLS>
 static hipError_t launch_grad_t(const MxGradParams& p, hipStream_t stream) {
   const int64_t tr = COLS ? p.cols.kq : tiles_of(p.M);
   // Measured at 4096 rows, bf16, silu, both directions: @@PAIR@@ us for F = 12288 as pairs, @@ANY@@ us for F = 12300.
   if (p.F % kMxBlock == 0) {
-    const int64_t tc = tiles_of(p.F);
+    const int64_t tc = (p.F + TW - 1) / TW;
     if (tc * tr > 0x7FFFFFFF) return hipErrorInvalidValue;
-    k_mx_gated_grad<DT, ACT, true, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 512, 0, stream>>>(p, (int)tc, 0);
+    k_mx_gated_grad<DT, ACT, TW, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 4 * TW, 0, stream>>>(p, (int)tc);
     return hipGetLastError();
   }
   // tiles of [0, 2F), with the row tensor's padding; those that begin below F, and those from the one that holds F on
-  const int64_t tc = ROWS ? p.rows.kq : tiles_of(2 * p.F);
-  const int64_t below = p.F / kTile, pairs = tc - below > below ? tc - below : below;
+  const int64_t tc = ROWS ? (int64_t)p.rows.kq * (kTile / TW) : (2 * p.F + TW - 1) / TW;
+  const int64_t below = p.F / TW, pairs = tc - below > below ? tc - below : below;
   const int64_t blocks = (pairs * tr + 7) / 8 * 16;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  k_mx_gated_grad<DT, ACT, false, ROWS, COLS><<<dim3((unsigned)blocks), 512, 0, stream>>>(p, (int)tc, (int)pairs);
+  k_mx_gated_grad_any<DT, ACT, TW, ROWS, COLS><<<dim3((unsigned)blocks), 4 * TW, 0, stream>>>(p, (int)tc, (int)pairs);
   return hipGetLastError();
 }
 
 template <class DT, int ACT>
 static hipError_t launch_grad_act(const MxGradParams& p, hipStream_t stream) {
-  if (p.rows.codes && p.cols.codes) return launch_grad_t<DT, ACT, true, true>(p, stream);
-  return p.rows.codes ? launch_grad_t<DT, ACT, true, false>(p, stream) : launch_grad_t<DT, ACT, false, true>(p, stream);
+  if (p.rows.codes && p.cols.codes) return launch_grad_t<DT, ACT, kGradTw, true, true>(p, stream);
+  return p.rows.codes ? launch_grad_t<DT, ACT, kGradTw, true, false>(p, stream) : launch_grad_t<DT, ACT, kGradTw, false, true>(p, stream);
 }
 
 hipError_t launch_mx_gated_grad(const MxGradParams& p, int dtype, hipStream_t stream) {
