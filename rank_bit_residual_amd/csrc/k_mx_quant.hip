@@ -21,10 +21,7 @@ namespace svdq {
 namespace dev {
 
 constexpr int kTile = 128, kMxBlock = 32;
-#ifndef TWX
-#define TWX 64
-#endif
-constexpr int kGradTw = TWX;
+constexpr int kGradCols = 64, kGradFew = 1024;
 
 __device__ inline u32 quad_max(u32 v) {
   v = max(v, (u32)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));  // quad_perm [1,0,3,2]
@@ -83,7 +80,7 @@ __device__ inline int tile_word(int row, int word) {
 // that exist.
 template <class DT, int W>
 __device__ __forceinline__ void pair_cols(const u32* tile, const MxOut& out, int64_t group0, int stage, int wave, int l16,
-                                          int kb, int64_t left) {
+                                          int kb, int at_kb, int64_t left) {
   const int pr = 16 * wave + l16;
   u32 lo[16], hi[16];
 #pragma unroll
@@ -93,8 +90,8 @@ __device__ __forceinline__ void pair_cols(const u32* tile, const MxOut& out, int
     hi[r] = __builtin_amdgcn_perm(b, a, 0x07060302u);
   }
   const MxGroup o = group_of(out, group0 + 2 * wave + (l16 >> 3), stage);
-  put_col<DT>(o, lo, (2 * pr) & 15, kb, 2 * pr < left);
-  put_col<DT>(o, hi, (2 * pr + 1) & 15, kb, 2 * pr + 1 < left);
+  put_col<DT>(o, lo, (2 * pr) & 15, at_kb, 2 * pr < left);
+  put_col<DT>(o, hi, (2 * pr + 1) & 15, at_kb, 2 * pr + 1 < left);
 }
 
 // ------------------------------------------------------------------------------ quantise
@@ -156,7 +153,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantParams p, int tiles_
         put_col<DT>(group_of(p.cols, (int64_t)tc * 8 + 4 * h + wave, tr), w, l16, kb, c < left);
       }
     } else {
-      pair_cols<DT, W>(tile, p.cols, (int64_t)tc * 8, tr, wave, l16, kb, left);
+      pair_cols<DT, W>(tile, p.cols, (int64_t)tc * 8, tr, wave, l16, kb, kb, left);
     }
   }
 }
@@ -217,17 +214,13 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantParams p, int st
 // zero, with the lowest bit set if anything was cut off. That lies on the same side of every border as v does.
 // A settled v lies on no border, so its bit is simply set; and the tile's copy in LDS takes half the room.
 //
-// Instructions bound this kernel as much as memory does (about 45 for each pair dg, du): eight elements are
-// tested together, by the bits in which any of their ends differ and by their least tail (see ActValue).
-struct Settled {
-  u32 differ = 0;
-  float tail = 0.f;
-  __device__ inline void add(float v, float err) {
-    const float a = fabsf(v);
-    differ |= __float_as_uint(a - err) ^ __float_as_uint(a + err);
-  }
-  __device__ inline bool open() const { return (differ >= 1u << 21) | (tail < -60.f); }
-};
+// Instructions bound this kernel as much as memory does (about 45 for each pair dg, du): two elements are
+// tested together, by the bits in which any of their ends differ, and eight by their least tail (see ActValue).
+constexpr u32 kOpen = 1u << 21;
+__device__ __forceinline__ u32 ends_differ(float v, float err) {
+  const float a = fabsf(v);
+  return __float_as_uint(a - err) ^ __float_as_uint(a + err);
+}
 
 // The 16 bits for a binary64 gradient (from infinity on, any of those mark a block).
 __device__ inline u32 to_odd16(double v) {
@@ -280,68 +273,60 @@ struct GradIn {
   Vec8<DT> dh, g, u;
 };
 
-template <int ACT>
-__device__ __forceinline__ float grad_gate(const ActValue<float>& r, float dh, float u, Settled& s) {
-  const float a = dh * u, v = a * r.d;
-  s.add(v, fabsf(a) * r.abs_d);
-  return v;
-}
-template <int ACT>
-__device__ __forceinline__ float grad_up(const ActValue<float>& r, float dh, Settled& s) {
-  const float v = dh * r.a;
-  s.add(v, fabsf(v) * r.ew);
-  return v;
-}
-
 // Eight elements of dg and / or du (whichever of GATE and UP) in those 16 bits.
 template <class DT, int ACT, bool GATE, bool UP>
 __device__ __forceinline__ void grad8(const GradIn<DT>& x, Vec8<MxBF16>& dg, Vec8<MxBF16>& du) {
-  Settled s;
+  u32 differ[4];
+  float tail = 0.f;
 #pragma unroll
-  for (int q = 0; q < 8; q += 2) {
+  for (int h = 0; h < 4; h++) {
     float vg[2], vu[2];
+    differ[h] = 0;
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-      const float dh = elem<DT>(x.dh, q + k);
-      const ActValue<float> r = act_value<ACT, float>(elem<DT>(x.g, q + k));
-      s.tail = r.tail < s.tail ? r.tail : s.tail;
-      if (GATE) vg[k] = grad_gate<ACT>(r, dh, elem<DT>(x.u, q + k), s);
-      if (UP) vu[k] = grad_up<ACT>(r, dh, s);
+      const float dh = elem<DT>(x.dh, 2 * h + k);
+      const ActValue<float> r = act_value<ACT, float>(elem<DT>(x.g, 2 * h + k));
+      tail = r.tail < tail ? r.tail : tail;
+      if (GATE) {
+        const float a = dh * elem<DT>(x.u, 2 * h + k);
+        vg[k] = a * r.d;
+        differ[h] |= ends_differ(vg[k], fabsf(a) * r.abs_d);
+      }
+      if (UP) {
+        vu[k] = dh * r.a;
+        differ[h] |= ends_differ(vu[k], fabsf(vu[k]) * r.ew);
+      }
     }
-    if (GATE) dg.w[q / 2] = odd_pair(vg[0], vg[1]);
-    if (UP) du.w[q / 2] = odd_pair(vu[0], vu[1]);
+    if (GATE) dg.w[h] = odd_pair(vg[0], vg[1]);
+    if (UP) du.w[h] = odd_pair(vu[0], vu[1]);
   }
-  if (!s.open()) return;
+  const bool far = tail < -60.f;
+  if (!((differ[0] >= kOpen) | (differ[1] >= kOpen) | (differ[2] >= kOpen) | (differ[3] >= kOpen) | far)) return;
 #pragma unroll 1
   for (int q = 0; q < 8; q++) {
-    const float dh = pick<DT>(x.dh, q), g = pick<DT>(x.g, q), u = pick<DT>(x.u, q);
-    const ActValue<float> r = act_value<ACT, float>(g);
-    Settled one;
-    one.tail = r.tail;
-    if (GATE) grad_gate<ACT>(r, dh, u, one);
-    if (UP) grad_up<ACT>(r, dh, one);
-    if (!one.open()) continue;
-    const ActValue<double> e = act_value<ACT, double>((double)g);
-    if (GATE) set16(dg, q, to_odd16(((double)dh * (double)u) * e.d));
-    if (UP) set16(du, q, to_odd16((double)dh * e.a));
+    if (get_at(differ, q >> 1) < kOpen && !far) continue;
+    const double dh = (double)pick<DT>(x.dh, q);
+    const ActValue<double> e = act_value<ACT, double>((double)pick<DT>(x.g, q));
+    if (GATE) set16(dg, q, to_odd16((dh * (double)pick<DT>(x.u, q)) * e.d));
+    if (UP) set16(du, q, to_odd16(dh * e.a));
   }
 }
 
-// A tile of 128 rows of TW columns by 4 TW threads, each with eight elements of rows 32 apart.
+// A tile of 32 NP rows of TW columns by 4 TW threads, each with eight elements of NP rows 32 apart.
 // GRAD_PAIR: columns [c0, c0 + TW) of dh, g and u give a tile of dg and one of du. GRAD_GATE, GRAD_UP, GRAD_MIXED: a tile of
 // d = [dg | du] at j0, all dg, all du, or some of either.
 enum { GRAD_PAIR, GRAD_GATE, GRAD_UP, GRAD_MIXED };
 
-template <class DT, int ACT, int MODE, int TW, bool ROWS, bool COLS>
+template <class DT, int ACT, int MODE, int TW, int NP, bool ROWS, bool COLS>
 __device__ __forceinline__ void grad_tile(const MxGradParams& p, u32* tile, int tr, int tc) {
-  constexpr int LPR = TW / 8, TILE = kTile * TW / 2;  // lanes per row, words of a tile
+  constexpr int LPR = TW / 8, TH = 32 * NP, TILE = TH * TW / 2;  // lanes per row, words of a tile
   typedef typename DT::T T;
   const int t = threadIdx.x, lc = t % LPR, lr = (t / LPR) & 15, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int half = wave / (LPR / 4);  // the 16-row half of a pass's 32 rows
-  const int64_t F = p.F, left_r = p.M - (int64_t)tr * kTile;
+  const int64_t F = p.F, left_r = p.M - (int64_t)tr * TH;
   const int64_t j = (int64_t)tc * TW + 8 * lc, c = MODE == GRAD_UP || (MODE == GRAD_MIXED && j >= F) ? j - F : j;
   const bool mixed = MODE == GRAD_MIXED && j < F && j + 8 > F;
-  const int64_t row0 = (int64_t)tr * kTile + 16 * half + lr;
+  const int64_t row0 = (int64_t)tr * TH + 16 * half + lr;
   const T* dhp = reinterpret_cast<const T*>(p.dh) + row0 * p.ldh;
   const T* gp = reinterpret_cast<const T*>(p.gu) + row0 * p.ldgu;
   auto load = [&](int i) {
@@ -377,9 +362,9 @@ __device__ __forceinline__ void grad_tile(const MxGradParams& p, u32* tile, int 
   const int up_stage = (int)(up_at / kTile), up_pos = (int)(up_at % kTile) + 8 * lc;
   GradIn<DT> next = load(0);
 #pragma unroll 1
-  for (int i = 0; i < 4; i++) {
+  for (int i = 0; i < NP; i++) {
     const GradIn<DT> x = next;
-    if (i < 3) next = load(i + 1);
+    if (i + 1 < NP) next = load(i + 1);
     const int in = 32 * i + 16 * half;  // the 16-row group's first row in the tile
     Vec8<MxBF16> d = zero8<MxBF16>(), du = zero8<MxBF16>();
     if (in < left_r) {
@@ -395,7 +380,7 @@ __device__ __forceinline__ void grad_tile(const MxGradParams& p, u32* tile, int 
         }
       }
       if constexpr (ROWS) {
-        const int64_t group = (int64_t)tr * 8 + 2 * i + half;
+        const int64_t group = (int64_t)tr * (2 * NP) + 2 * i + half;
         const bool live = in + lr < left_r && (MODE != GRAD_PAIR || c < F);
         put_row<MxBF16>(group_of(p.rows, group, stage), d, lr, pos, live);
         if constexpr (MODE == GRAD_PAIR) put_row<MxBF16>(group_of(p.rows, group, up_stage), du, lr, up_pos, live);
@@ -409,31 +394,34 @@ __device__ __forceinline__ void grad_tile(const MxGradParams& p, u32* tile, int 
   }
   if constexpr (COLS) {
     __syncthreads();
-    const int kb = (t & 63) >> 4, l16 = t & 15, w = wave % (TW / 32);
     const int64_t col0 = (int64_t)tc * TW;
-    if constexpr (MODE == GRAD_PAIR)  // half of the waves for each side
-      pair_cols<MxBF16, TW / 2>(tile + half * TILE, p.cols, (col0 + (half ? F : 0)) / 16, tr, w, l16, kb, F - col0);
-    else if (half == 0)
-      pair_cols<MxBF16, TW / 2>(tile, p.cols, col0 / 16, tr, w, l16, kb, 2 * F - col0);
+    const int stage_c = tr / (kTile / TH), kb0 = tr % (kTile / TH) * NP;
+    const int l16 = t & 15;
+    // sixteen lanes take 16 pairs of columns of one block of 32 rows
+    int s16 = t >> 4;
+    const int kb = s16 % NP, w = s16 / NP % (TW / 32), side = s16 / NP / (TW / 32);
+    if (side < (MODE == GRAD_PAIR ? 2 : 1))
+      pair_cols<MxBF16, TW / 2>(tile + side * TILE, p.cols, (col0 + (side ? F : 0)) / 16, stage_c, w, l16, kb, kb0 + kb,
+                                (MODE == GRAD_PAIR ? F : 2 * F) - col0);
   }
 }
 
 // F a multiple of 32, so that blocks along d = [dg | du] belong to one side: every input is read once.
 // Two blocks of 512 threads (or four of 256) per compute unit, 128 registers, where that spills next to nothing; float32
 // inputs and erf take more.
-template <class DT, int ACT, int TW, bool ROWS, bool COLS>
+template <class DT, int ACT, int TW, int NP, bool ROWS, bool COLS>
 __global__ __launch_bounds__(4 * TW, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 : 4) void k_mx_gated_grad(MxGradParams p, int tiles_c) {
-  __shared__ __align__(16) u32 tile[COLS ? kTile * TW : 4];
+  __shared__ __align__(16) u32 tile[COLS ? 32 * NP * TW : 4];
   const int tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
-  grad_tile<DT, ACT, GRAD_PAIR, TW, ROWS, COLS>(p, tile, tr, tc);
+  grad_tile<DT, ACT, GRAD_PAIR, TW, NP, ROWS, COLS>(p, tile, tr, tc);
   if constexpr (ROWS) {
     // the row tensor's padding past 2 F, zero codes and bytes, by the last column of blocks
     if (tc == tiles_c - 1) {
       const int l16 = threadIdx.x & 15, lr = threadIdx.x >> 4;
       for (int st = (int)(2 * p.F / kTile); st < p.rows.kq; st++) {
         const bool past = (int64_t)st * kTile + 8 * l16 >= 2 * p.F;
-        for (int r = lr; r < kTile; r += TW / 4) {
-          const int64_t row = (int64_t)tr * kTile + r;
+        for (int r = lr; r < 32 * NP; r += TW / 4) {
+          const int64_t row = (int64_t)tr * (32 * NP) + r;
           put_row<MxBF16>(group_of(p.rows, row >> 4, st), zero8<MxBF16>(), row & 15, 8 * l16, past && row < p.M);
         }
       }
@@ -443,20 +431,20 @@ __global__ __launch_bounds__(4 * TW, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 :
 
 // Any F: tiles of d itself. The two that read the same dh and g, one on either side of F, go to blocks 8 apart:
 // neighbours on one XCD, so that the second finds them in its L2.
-template <class DT, int ACT, int TW, bool ROWS, bool COLS>
+template <class DT, int ACT, int TW, int NP, bool ROWS, bool COLS>
 __global__ __launch_bounds__(4 * TW, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 : 4) void k_mx_gated_grad_any(MxGradParams p, int tiles_c, int pairs) {
-  __shared__ __align__(16) u32 tile[COLS ? kTile * TW / 2 : 4];
+  __shared__ __align__(16) u32 tile[COLS ? 16 * NP * TW : 4];
   const int64_t id = (int64_t)(blockIdx.x >> 4) * 8 + (blockIdx.x & 7);
   const int tr = (int)(id / pairs), pair = (int)(id - (int64_t)tr * pairs), side = (blockIdx.x >> 3) & 1;
   const int first_up = (int)(p.F / TW), tc = side ? first_up + pair : pair;
   if (side ? tc >= tiles_c : tc >= first_up) return;
-  if (COLS ? tr >= p.cols.kq : (int64_t)tr * kTile >= p.M) return;
+  if (COLS ? tr >= p.cols.kq * (4 / NP) : (int64_t)tr * (32 * NP) >= p.M) return;
   if (side == 0)
-    grad_tile<DT, ACT, GRAD_GATE, TW, ROWS, COLS>(p, tile, tr, tc);
+    grad_tile<DT, ACT, GRAD_GATE, TW, NP, ROWS, COLS>(p, tile, tr, tc);
   else if (pair != 0)
-    grad_tile<DT, ACT, GRAD_UP, TW, ROWS, COLS>(p, tile, tr, tc);
+    grad_tile<DT, ACT, GRAD_UP, TW, NP, ROWS, COLS>(p, tile, tr, tc);
   else
-    grad_tile<DT, ACT, GRAD_MIXED, TW, ROWS, COLS>(p, tile, tr, tc);
+    grad_tile<DT, ACT, GRAD_MIXED, TW, NP, ROWS, COLS>(p, tile, tr, tc);
 }
 
 }  // namespace dev
@@ -506,14 +494,15 @@ hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t
   });
 }
 
-template <class DT, int ACT, int TW, bool ROWS, bool COLS>
+template <class DT, int ACT, int NP, bool ROWS, bool COLS>
 static hipError_t launch_grad_t(const MxGradParams& p, hipStream_t stream) {
-  const int64_t tr = COLS ? p.cols.kq : tiles_of(p.M);
+  constexpr int TW = kGradCols, TH = 32 * NP;
+  const int64_t tr = COLS ? (int64_t)p.cols.kq * (kTile / TH) : (p.M + TH - 1) / TH;
   // Measured at 4096 rows, bf16, silu, both directions: @@PAIR@@ us for F = 12288 as pairs, @@ANY@@ us for F = 12300.
   if (p.F % kMxBlock == 0) {
     const int64_t tc = (p.F + TW - 1) / TW;
     if (tc * tr > 0x7FFFFFFF) return hipErrorInvalidValue;
-    k_mx_gated_grad<DT, ACT, TW, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 4 * TW, 0, stream>>>(p, (int)tc);
+    k_mx_gated_grad<DT, ACT, TW, NP, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 4 * TW, 0, stream>>>(p, (int)tc);
     return hipGetLastError();
   }
   // tiles of [0, 2F), with the row tensor's padding; those that begin below F, and those from the one that holds F on
@@ -521,14 +510,22 @@ static hipError_t launch_grad_t(const MxGradParams& p, hipStream_t stream) {
   const int64_t below = p.F / TW, pairs = tc - below > below ? tc - below : below;
   const int64_t blocks = (pairs * tr + 7) / 8 * 16;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  k_mx_gated_grad_any<DT, ACT, TW, ROWS, COLS><<<dim3((unsigned)blocks), 4 * TW, 0, stream>>>(p, (int)tc, (int)pairs);
+  k_mx_gated_grad_any<DT, ACT, TW, NP, ROWS, COLS><<<dim3((unsigned)blocks), 4 * TW, 0, stream>>>(p, (int)tc, (int)pairs);
   return hipGetLastError();
 }
 
+template <class DT, int ACT, int NP>
+static hipError_t launch_grad_np(const MxGradParams& p, hipStream_t stream) {
+  if (p.rows.codes && p.cols.codes) return launch_grad_t<DT, ACT, NP, true, true>(p, stream);
+  return p.rows.codes ? launch_grad_t<DT, ACT, NP, true, false>(p, stream) : launch_grad_t<DT, ACT, NP, false, true>(p, stream);
+}
+
+// Tiles of 128 rows fill whole 64-byte rows of the transpose's codes; where they would leave the chip with less than
+// @@NB@@ blocks per compute unit, tiles of 32 rows, whose loads all wait at once.
 template <class DT, int ACT>
 static hipError_t launch_grad_act(const MxGradParams& p, hipStream_t stream) {
-  if (p.rows.codes && p.cols.codes) return launch_grad_t<DT, ACT, kGradTw, true, true>(p, stream);
-  return p.rows.codes ? launch_grad_t<DT, ACT, kGradTw, true, false>(p, stream) : launch_grad_t<DT, ACT, kGradTw, false, true>(p, stream);
+  const int64_t blocks = tiles_of(p.M) * ((p.F + kGradCols - 1) / kGradCols);
+  return blocks < kGradFew ? launch_grad_np<DT, ACT, 1>(p, stream) : launch_grad_np<DT, ACT, 4>(p, stream);
 }
 
 hipError_t launch_mx_gated_grad(const MxGradParams& p, int dtype, hipStream_t stream) {
