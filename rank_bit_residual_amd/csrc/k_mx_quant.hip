@@ -21,7 +21,6 @@ namespace svdq {
 namespace dev {
 
 constexpr int kTile = 128, kMxBlock = 32;
-constexpr int kGradCols = 64, kGradFew = 1024;
 
 __device__ inline u32 quad_max(u32 v) {
   v = max(v, (u32)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));  // quad_perm [1,0,3,2]
@@ -64,53 +63,48 @@ __device__ inline void put_col(const MxGroup& o, const u32 (&w)[N], u32 lc, u32 
   o.scales[(lc << 2) + kb] = (uint8_t)byte;
 }
 
-// LDS copy of a tile: W words per row. A column reader's lanes are 16 columns x 4 blocks of 32 rows; moving a row's
-// 16-word groups by its block's number puts the four blocks on different banks (W = 32 has two groups: there the
-// upper blocks' neighbouring rows change places).
-template <int W>
-__device__ inline int tile_word(int row, int word) {
-  if constexpr (W == 32)
-    return (row ^ ((row >> 6) & 1)) * W + (word ^ (((row >> 5) & 1) << 4));
-  else
-    return row * W + (word ^ (((row >> 5) & 3) << 4));
-}
-
-// Columns of a tile of 128 rows of W pairs of 16-bit values, by W / 16 waves: a lane takes a pair of columns, the low halves of its words
-// and then the high halves; a wave's 16 pairs are two 16-column groups, the first of the tile being group0. `left`: columns
-// that exist.
-template <class DT, int W>
-__device__ __forceinline__ void pair_cols(const u32* tile, const MxOut& out, int64_t group0, int stage, int wave, int l16,
-                                          int kb, int at_kb, int64_t left) {
-  const int pr = 16 * wave + l16;
+// Pair of columns `pr` of 32 rows of 16-bit values in LDS (W words a row from `rows`, the pair at word `at`): the low halves
+// of a lane's words, then the high halves. The tile's first 16-column group is group0; the rows are block kb of `stage`; `left` columns exist.
+template <class DT>
+__device__ __forceinline__ void pair_cols(const u32* rows, int W, int at, int pr, const MxOut& out, int64_t group0, int stage,
+                                          int kb, int64_t left) {
   u32 lo[16], hi[16];
 #pragma unroll
   for (int r = 0; r < 16; r++) {
-    const u32 a = tile[tile_word<W>(32 * kb + 2 * r, pr)], b = tile[tile_word<W>(32 * kb + 2 * r + 1, pr)];
+    const u32 a = rows[2 * r * W + at], b = rows[(2 * r + 1) * W + at];
     lo[r] = __builtin_amdgcn_perm(b, a, 0x05040100u);
     hi[r] = __builtin_amdgcn_perm(b, a, 0x07060302u);
   }
-  const MxGroup o = group_of(out, group0 + 2 * wave + (l16 >> 3), stage);
-  put_col<DT>(o, lo, (2 * pr) & 15, at_kb, 2 * pr < left);
-  put_col<DT>(o, hi, (2 * pr + 1) & 15, at_kb, 2 * pr + 1 < left);
+  const MxGroup o = group_of(out, group0 + (pr >> 3), stage);
+  put_col<DT>(o, lo, (2 * pr) & 15, kb, 2 * pr < left);
+  put_col<DT>(o, hi, (2 * pr + 1) & 15, kb, 2 * pr + 1 < left);
 }
 
 // ------------------------------------------------------------------------------ quantise
-// Block: 256 threads; thread t holds elements [8 (t % 16), + 8) of rows t / 16 + 16 i.
-template <class DT, bool ROWS, bool COLS>
+// Block: 256 threads, a tile of 16 NP rows of 128 columns; thread t holds elements [8 (t % 16), + 8) of rows t / 16 + 16 i.
+//
+// The tile's LDS copy has W words per row. A column reader's lanes are 16 columns x 4 blocks of 32 rows; moving a
+// row's 16-word groups by its block's number (tile_word) puts the four blocks on different banks.
+template <int W>
+__device__ inline int tile_word(int row, int word) {
+  return row * W + (word ^ (((row >> 5) & 3) << 4));
+}
+
+template <class DT, int NP, bool ROWS, bool COLS>
 __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantParams p, int tiles_c) {
-  constexpr int W = kTile * DT::size / 4;  // words per tile row
-  __shared__ __align__(16) u32 tile[COLS ? kTile * W : 4];
+  constexpr int TH = 16 * NP, W = kTile * DT::size / 4;  // tile rows, words per tile row
+  __shared__ __align__(16) u32 tile[COLS ? TH * W : 4];
   typedef typename DT::T T;
   const int t = threadIdx.x, l16 = t & 15, lr = t >> 4;
   const int tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
   const int64_t c0 = (int64_t)tc * kTile + 8 * l16;
-  const T* x = reinterpret_cast<const T*>(p.x) + ((int64_t)tr * kTile + lr) * p.sr + c0 * p.sc;
+  const T* x = reinterpret_cast<const T*>(p.x) + ((int64_t)tr * TH + lr) * p.sr + c0 * p.sc;
   // rows and elements of this thread's part that exist
-  const int64_t left_r = p.R - (int64_t)tr * kTile, left_c = p.C - c0;
+  const int64_t left_r = p.R - (int64_t)tr * TH, left_c = p.C - c0;
 
-  Vec8<DT> v[8];
+  Vec8<DT> v[NP];
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
+  for (int i = 0; i < NP; i++) {
     v[i] = zero8<DT>();
     if (lr + 16 * i >= left_r) continue;
     const T* src = x + (int64_t)(16 * i) * p.sr;
@@ -129,9 +123,9 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantParams p, int tiles_
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    if (!COLS && 16 * i >= left_r) break;  // few rows: nothing but latency
-    if constexpr (ROWS) put_row<DT>(group_of(p.rows, (int64_t)tr * 8 + i, tc), v[i], lr, 8 * l16, lr + 16 * i < left_r);
+  for (int i = 0; i < NP; i++) {
+    if (!COLS && 16 * i >= left_r) break;
+    if constexpr (ROWS) put_row<DT>(group_of(p.rows, (int64_t)tr * NP + i, tc), v[i], lr, 8 * l16, lr + 16 * i < left_r);
     if constexpr (COLS) {
 #pragma unroll
       for (int h = 0; h < DT::size / 2; h++)
@@ -141,19 +135,24 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantParams p, int tiles_
   }
   if constexpr (COLS) {
     __syncthreads();
-    const int kb = (t & 63) >> 4, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    // sixteen lanes take 16 columns, or 16 pairs of them, of one block of 32 rows
+    constexpr int KB = TH / 32, PER = kTile / TH;  // blocks in the tile, tiles in a stage
+    constexpr int GROUPS = W / 16, AT_ONCE = 16 / KB;
+    const int s16 = t >> 4, kb = s16 % KB, stage = tr / PER, at_kb = tr % PER * KB + kb;
+    const u32* rows = tile + 32 * kb * W;
     const int64_t left = p.C - (int64_t)tc * kTile;
-    if constexpr (DT::size == 4) {
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int c = 16 * (4 * h + wave) + l16;
-        u32 w[32];
+    for (int h = 0; h < (GROUPS + AT_ONCE - 1) / AT_ONCE; h++) {
+      const int w = s16 / KB + AT_ONCE * h, c = 16 * w + l16, at = c ^ (kb << 4);  // a block's rows share their move
+      if (w >= GROUPS) continue;
+      if constexpr (DT::size == 4) {
+        u32 e[32];
 #pragma unroll
-        for (int r = 0; r < 32; r++) w[r] = tile[tile_word<W>(32 * kb + r, c)];
-        put_col<DT>(group_of(p.cols, (int64_t)tc * 8 + 4 * h + wave, tr), w, l16, kb, c < left);
+        for (int r = 0; r < 32; r++) e[r] = rows[r * W + at];
+        put_col<DT>(group_of(p.cols, (int64_t)tc * 8 + w, stage), e, l16, at_kb, c < left);
+      } else {
+        pair_cols<DT>(rows, W, at, c, p.cols, (int64_t)tc * 8, stage, at_kb, left);
       }
-    } else {
-      pair_cols<DT, W>(tile, p.cols, (int64_t)tc * 8, tr, wave, l16, kb, kb, left);
     }
   }
 }
@@ -312,29 +311,28 @@ __device__ __forceinline__ void grad8(const GradIn<DT>& x, Vec8<MxBF16>& dg, Vec
   }
 }
 
-// A tile of 32 NP rows of TW columns by 4 TW threads, each with eight elements of NP rows 32 apart.
-// GRAD_PAIR: columns [c0, c0 + TW) of dh, g and u give a tile of dg and one of du. GRAD_GATE, GRAD_UP, GRAD_MIXED: a tile of
+// A tile of 32 rows (one block of the transpose) of 64 columns by 256 threads, thread t with elements [8 (t % 8), + 8) of row
+// t / 8. Many small blocks hide each other's loads: tiles of 128 rows, whose columns' codes fill whole 64-byte rows, were
+// no faster at 4096 x 12288 (103 us against 105) and twice as slow at 515 x 2731 (24 us against 11.7).
+// GRAD_PAIR: columns [c0, c0 + 64) of dh, g and u give a tile of dg and one of du. GRAD_GATE, GRAD_UP, GRAD_MIXED: a tile of
 // d = [dg | du] at j0, all dg, all du, or some of either.
+constexpr int kGradRows = 32, kGradCols = 64;
 enum { GRAD_PAIR, GRAD_GATE, GRAD_UP, GRAD_MIXED };
 
-template <class DT, int ACT, int MODE, int TW, int NP, bool ROWS, bool COLS>
+template <class DT, int ACT, int MODE, bool ROWS, bool COLS>
 __device__ __forceinline__ void grad_tile(const MxGradParams& p, u32* tile, int tr, int tc) {
-  constexpr int LPR = TW / 8, TH = 32 * NP, TILE = TH * TW / 2;  // lanes per row, words of a tile
+  constexpr int LPR = kGradCols / 8, W = kGradCols / 2, TILE = kGradRows * W;  // lanes and words per row, words of a tile
   typedef typename DT::T T;
-  const int t = threadIdx.x, lc = t % LPR, lr = (t / LPR) & 15, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int half = wave / (LPR / 4);  // the 16-row half of a pass's 32 rows
-  const int64_t F = p.F, left_r = p.M - (int64_t)tr * TH;
-  const int64_t j = (int64_t)tc * TW + 8 * lc, c = MODE == GRAD_UP || (MODE == GRAD_MIXED && j >= F) ? j - F : j;
-  const bool mixed = MODE == GRAD_MIXED && j < F && j + 8 > F;
-  const int64_t row0 = (int64_t)tr * TH + 16 * half + lr;
-  const T* dhp = reinterpret_cast<const T*>(p.dh) + row0 * p.ldh;
-  const T* gp = reinterpret_cast<const T*>(p.gu) + row0 * p.ldgu;
-  auto load = [&](int i) {
+  const int t = threadIdx.x, lc = t % LPR, lr = t / LPR;
+  const int half = __builtin_amdgcn_readfirstlane(t >> 7);  // the 16-row half
+  const int64_t F = p.F, row = (int64_t)tr * kGradRows + lr;
+  const int64_t j = (int64_t)tc * kGradCols + 8 * lc, c = MODE == GRAD_UP || (MODE == GRAD_MIXED && j >= F) ? j - F : j;
+  Vec8<MxBF16> d = zero8<MxBF16>(), du = zero8<MxBF16>();
+  if (row < p.M) {
     GradIn<DT> x{zero8<DT>(), zero8<DT>(), zero8<DT>()};
-    if (32 * i + 16 * half + lr >= left_r) return x;
-    const T* dr = dhp + (int64_t)(32 * i) * p.ldh;
-    const T* gr = gp + (int64_t)(32 * i) * p.ldgu;
-    if (!mixed) {
+    const T* dr = reinterpret_cast<const T*>(p.dh) + row * p.ldh;
+    const T* gr = reinterpret_cast<const T*>(p.gu) + row * p.ldgu;
+    if (MODE != GRAD_MIXED || j >= F || j + 8 <= F) {
       x.dh = load8<DT>(dr, c, F);
       x.g = load8<DT>(gr, c, F);
       if (MODE != GRAD_UP) x.u = load8<DT>(gr + F, c, F);
@@ -354,74 +352,55 @@ __device__ __forceinline__ void grad_tile(const MxGradParams& p, u32* tile, int 
         }
       }
     }
-    return x;
-  };
-  // places in a row of the row tensor: the tile's, and du's (F is a multiple of 32, not of a stage)
-  const int64_t up_at = F + (int64_t)tc * TW;
-  const int stage = tc / (kTile / TW), pos = (tc % (kTile / TW)) * TW + 8 * lc;
-  const int up_stage = (int)(up_at / kTile), up_pos = (int)(up_at % kTile) + 8 * lc;
-  GradIn<DT> next = load(0);
-#pragma unroll 1
-  for (int i = 0; i < NP; i++) {
-    const GradIn<DT> x = next;
-    if (i + 1 < NP) next = load(i + 1);
-    const int in = 32 * i + 16 * half;  // the 16-row group's first row in the tile
-    Vec8<MxBF16> d = zero8<MxBF16>(), du = zero8<MxBF16>();
-    if (in < left_r) {
-      if constexpr (MODE == GRAD_UP)
-        grad8<DT, ACT, false, true>(x, du, d);
-      else
-        grad8<DT, ACT, true, MODE != GRAD_GATE>(x, d, du);
-      if constexpr (MODE == GRAD_MIXED) {
+    if constexpr (MODE == GRAD_UP)
+      grad8<DT, ACT, false, true>(x, du, d);
+    else
+      grad8<DT, ACT, true, MODE != GRAD_GATE>(x, d, du);
+    if constexpr (MODE == GRAD_MIXED) {
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const u32 from_up = (j + 2 * q >= F ? 0xFFFFu : 0u) | (j + 2 * q + 1 >= F ? 0xFFFF0000u : 0u);
-          d.w[q] = (d.w[q] & ~from_up) | (du.w[q] & from_up);
-        }
+      for (int q = 0; q < 4; q++) {
+        const u32 from_up = (j + 2 * q >= F ? 0xFFFFu : 0u) | (j + 2 * q + 1 >= F ? 0xFFFF0000u : 0u);
+        d.w[q] = (d.w[q] & ~from_up) | (du.w[q] & from_up);
       }
-      if constexpr (ROWS) {
-        const int64_t group = (int64_t)tr * (2 * NP) + 2 * i + half;
-        const bool live = in + lr < left_r && (MODE != GRAD_PAIR || c < F);
-        put_row<MxBF16>(group_of(p.rows, group, stage), d, lr, pos, live);
-        if constexpr (MODE == GRAD_PAIR) put_row<MxBF16>(group_of(p.rows, group, up_stage), du, lr, up_pos, live);
-      }
-    }
-    if constexpr (COLS) {
-      const int at = tile_word<TW / 2>(in + lr, 4 * lc);
-      *reinterpret_cast<v4i*>(&tile[at]) = v4i{(int)d.w[0], (int)d.w[1], (int)d.w[2], (int)d.w[3]};
-      if constexpr (MODE == GRAD_PAIR) *reinterpret_cast<v4i*>(&tile[TILE + at]) = v4i{(int)du.w[0], (int)du.w[1], (int)du.w[2], (int)du.w[3]};
     }
   }
+  if constexpr (ROWS) {
+    // places in a row of the row tensor: the tile's, and du's (F is a multiple of 32, not of a stage)
+    constexpr int PER = kTile / kGradCols;
+    const int64_t group = (int64_t)tr * 2 + half, up_at = F + (int64_t)tc * kGradCols;
+    const bool live = row < p.M && (MODE != GRAD_PAIR || c < F);
+    put_row<MxBF16>(group_of(p.rows, group, tc / PER), d, lr & 15, (tc % PER) * kGradCols + 8 * lc, live);
+    if constexpr (MODE == GRAD_PAIR)
+      put_row<MxBF16>(group_of(p.rows, group, up_at / kTile), du, lr & 15, (u32)(up_at % kTile) + 8 * lc, live);
+  }
   if constexpr (COLS) {
+    // two copies of 32 rows; a reader's lanes are 16 pairs of columns of one of them
+    *reinterpret_cast<v4i*>(&tile[lr * W + 4 * lc]) = v4i{(int)d.w[0], (int)d.w[1], (int)d.w[2], (int)d.w[3]};
+    if constexpr (MODE == GRAD_PAIR)
+      *reinterpret_cast<v4i*>(&tile[TILE + lr * W + 4 * lc]) = v4i{(int)du.w[0], (int)du.w[1], (int)du.w[2], (int)du.w[3]};
     __syncthreads();
-    const int64_t col0 = (int64_t)tc * TW;
-    const int stage_c = tr / (kTile / TH), kb0 = tr % (kTile / TH) * NP;
-    const int l16 = t & 15;
-    // sixteen lanes take 16 pairs of columns of one block of 32 rows
-    int s16 = t >> 4;
-    const int kb = s16 % NP, w = s16 / NP % (TW / 32), side = s16 / NP / (TW / 32);
+    const int64_t col0 = (int64_t)tc * kGradCols;
+    const int side = t >> 5, pr = t & 31;
     if (side < (MODE == GRAD_PAIR ? 2 : 1))
-      pair_cols<MxBF16, TW / 2>(tile + side * TILE, p.cols, (col0 + (side ? F : 0)) / 16, stage_c, w, l16, kb, kb0 + kb,
-                                (MODE == GRAD_PAIR ? F : 2 * F) - col0);
+      pair_cols<MxBF16>(tile + side * TILE, W, pr, pr, p.cols, (col0 + (side ? F : 0)) / 16, tr / (kTile / kGradRows),
+                        tr % (kTile / kGradRows), (MODE == GRAD_PAIR ? F : 2 * F) - col0);
   }
 }
 
 // F a multiple of 32, so that blocks along d = [dg | du] belong to one side: every input is read once.
-// Two blocks of 512 threads (or four of 256) per compute unit, 128 registers, where that spills next to nothing; float32
-// inputs and erf take more.
-template <class DT, int ACT, int TW, int NP, bool ROWS, bool COLS>
-__global__ __launch_bounds__(4 * TW, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 : 4) void k_mx_gated_grad(MxGradParams p, int tiles_c) {
-  __shared__ __align__(16) u32 tile[COLS ? 32 * NP * TW : 4];
+template <class DT, int ACT, bool ROWS, bool COLS>
+__global__ __launch_bounds__(256) void k_mx_gated_grad(MxGradParams p, int tiles_c) {
+  __shared__ __align__(16) u32 tile[COLS ? kGradRows * kGradCols : 4];
   const int tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
-  grad_tile<DT, ACT, GRAD_PAIR, TW, NP, ROWS, COLS>(p, tile, tr, tc);
+  grad_tile<DT, ACT, GRAD_PAIR, ROWS, COLS>(p, tile, tr, tc);
   if constexpr (ROWS) {
     // the row tensor's padding past 2 F, zero codes and bytes, by the last column of blocks
     if (tc == tiles_c - 1) {
-      const int l16 = threadIdx.x & 15, lr = threadIdx.x >> 4;
+      const int l16 = threadIdx.x & 15;
       for (int st = (int)(2 * p.F / kTile); st < p.rows.kq; st++) {
         const bool past = (int64_t)st * kTile + 8 * l16 >= 2 * p.F;
-        for (int r = lr; r < 32 * NP; r += TW / 4) {
-          const int64_t row = (int64_t)tr * (32 * NP) + r;
+        for (int r = threadIdx.x >> 4; r < kGradRows; r += 16) {
+          const int64_t row = (int64_t)tr * kGradRows + r;
           put_row<MxBF16>(group_of(p.rows, row >> 4, st), zero8<MxBF16>(), row & 15, 8 * l16, past && row < p.M);
         }
       }
@@ -431,20 +410,20 @@ __global__ __launch_bounds__(4 * TW, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 :
 
 // Any F: tiles of d itself. The two that read the same dh and g, one on either side of F, go to blocks 8 apart:
 // neighbours on one XCD, so that the second finds them in its L2.
-template <class DT, int ACT, int TW, int NP, bool ROWS, bool COLS>
-__global__ __launch_bounds__(4 * TW, DT::size == 4 || ACT == SVDQ_ACT_GELU ? 2 : 4) void k_mx_gated_grad_any(MxGradParams p, int tiles_c, int pairs) {
-  __shared__ __align__(16) u32 tile[COLS ? 16 * NP * TW : 4];
+template <class DT, int ACT, bool ROWS, bool COLS>
+__global__ __launch_bounds__(256) void k_mx_gated_grad_any(MxGradParams p, int tiles_c, int pairs) {
+  __shared__ __align__(16) u32 tile[COLS ? kGradRows * kGradCols / 2 : 4];
   const int64_t id = (int64_t)(blockIdx.x >> 4) * 8 + (blockIdx.x & 7);
   const int tr = (int)(id / pairs), pair = (int)(id - (int64_t)tr * pairs), side = (blockIdx.x >> 3) & 1;
-  const int first_up = (int)(p.F / TW), tc = side ? first_up + pair : pair;
+  const int first_up = (int)(p.F / kGradCols), tc = side ? first_up + pair : pair;
   if (side ? tc >= tiles_c : tc >= first_up) return;
-  if (COLS ? tr >= p.cols.kq * (4 / NP) : (int64_t)tr * (32 * NP) >= p.M) return;
+  if (COLS ? tr >= p.cols.kq * (kTile / kGradRows) : (int64_t)tr * kGradRows >= p.M) return;
   if (side == 0)
-    grad_tile<DT, ACT, GRAD_GATE, TW, NP, ROWS, COLS>(p, tile, tr, tc);
+    grad_tile<DT, ACT, GRAD_GATE, ROWS, COLS>(p, tile, tr, tc);
   else if (pair != 0)
-    grad_tile<DT, ACT, GRAD_UP, TW, NP, ROWS, COLS>(p, tile, tr, tc);
+    grad_tile<DT, ACT, GRAD_UP, ROWS, COLS>(p, tile, tr, tc);
   else
-    grad_tile<DT, ACT, GRAD_MIXED, TW, NP, ROWS, COLS>(p, tile, tr, tc);
+    grad_tile<DT, ACT, GRAD_MIXED, ROWS, COLS>(p, tile, tr, tc);
 }
 
 }  // namespace dev
@@ -463,25 +442,33 @@ static hipError_t with_dtype(int dtype, Fn f) {
 
 static int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 
+template <class DT, int NP, bool ROWS, bool COLS>
+static hipError_t launch_quant(const MxQuantParams& p, hipStream_t stream) {
+  constexpr int TH = 16 * NP;
+  // a direction that is written covers its padding too
+  const int64_t tc = ROWS ? p.rows.kq : tiles_of(p.C), tr = COLS ? (int64_t)p.cols.kq * (kTile / TH) : (p.R + TH - 1) / TH;
+  if (tc * tr > 0x7FFFFFFF) return hipErrorInvalidValue;
+  k_mx_quantize<DT, NP, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 256, 0, stream>>>(p, (int)tc);
+  return hipGetLastError();
+}
+
+// Tiles of 128 rows, whose columns' codes fill whole 64-byte rows, while they fill the chip, else of 32 rows. Measured,
+// bf16, both directions: 8192 x 12288 59 us (80 with tiles of 32 x 64), 2048 x 4096 7.9 us with 32 rows against 8.7, 777 x
+// 5003 6.2 against 8.4.
+constexpr int64_t kFewTiles = 768;
+
 hipError_t launch_mx_quantize(const MxQuantParams& p0, int dtype, hipStream_t stream) {
   MxQuantParams p = p0;
   if (p.sc != 1 && p.sr == 1) {  // columns are contiguous: the transpose's rows
     const MxQuantParams q = p;
     p.R = q.C, p.C = q.R, p.sr = q.sc, p.sc = q.sr, p.rows = q.cols, p.cols = q.rows;
   }
-  // a direction that is written covers its padding too
-  const int64_t tc = p.rows.codes ? p.rows.kq : tiles_of(p.C), tr = p.cols.codes ? p.cols.kq : tiles_of(p.R);
-  if (tc * tr > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const bool few = tiles_of(p.R) * tiles_of(p.C) < kFewTiles;
   return with_dtype(dtype, [&](auto d) {
     typedef decltype(d) DT;
-    const dim3 grid((unsigned)(tc * tr));
-    if (p.rows.codes && p.cols.codes)
-      k_mx_quantize<DT, true, true><<<grid, 256, 0, stream>>>(p, (int)tc);
-    else if (p.rows.codes)
-      k_mx_quantize<DT, true, false><<<grid, 256, 0, stream>>>(p, (int)tc);
-    else
-      k_mx_quantize<DT, false, true><<<grid, 256, 0, stream>>>(p, (int)tc);
-    return hipGetLastError();
+    if (p.rows.codes && p.cols.codes) return few ? launch_quant<DT, 2, true, true>(p, stream) : launch_quant<DT, 8, true, true>(p, stream);
+    if (p.rows.codes) return few ? launch_quant<DT, 2, true, false>(p, stream) : launch_quant<DT, 8, true, false>(p, stream);
+    return few ? launch_quant<DT, 2, false, true>(p, stream) : launch_quant<DT, 8, false, true>(p, stream);
   });
 }
 
@@ -494,38 +481,29 @@ hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t
   });
 }
 
-template <class DT, int ACT, int NP, bool ROWS, bool COLS>
+template <class DT, int ACT, bool ROWS, bool COLS>
 static hipError_t launch_grad_t(const MxGradParams& p, hipStream_t stream) {
-  constexpr int TW = kGradCols, TH = 32 * NP;
-  const int64_t tr = COLS ? (int64_t)p.cols.kq * (kTile / TH) : (p.M + TH - 1) / TH;
-  // Measured at 4096 rows, bf16, silu, both directions: @@PAIR@@ us for F = 12288 as pairs, @@ANY@@ us for F = 12300.
+  const int64_t tr = COLS ? (int64_t)p.cols.kq * (kTile / kGradRows) : (p.M + kGradRows - 1) / kGradRows;
+  // Measured at 4096 rows, bf16, silu, both directions: 106 us for F = 12288 as pairs, 152 us for F = 12300.
   if (p.F % kMxBlock == 0) {
-    const int64_t tc = (p.F + TW - 1) / TW;
+    const int64_t tc = (p.F + kGradCols - 1) / kGradCols;
     if (tc * tr > 0x7FFFFFFF) return hipErrorInvalidValue;
-    k_mx_gated_grad<DT, ACT, TW, NP, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 4 * TW, 0, stream>>>(p, (int)tc);
+    k_mx_gated_grad<DT, ACT, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 256, 0, stream>>>(p, (int)tc);
     return hipGetLastError();
   }
   // tiles of [0, 2F), with the row tensor's padding; those that begin below F, and those from the one that holds F on
-  const int64_t tc = ROWS ? (int64_t)p.rows.kq * (kTile / TW) : (2 * p.F + TW - 1) / TW;
-  const int64_t below = p.F / TW, pairs = tc - below > below ? tc - below : below;
+  const int64_t tc = ROWS ? (int64_t)p.rows.kq * (kTile / kGradCols) : (2 * p.F + kGradCols - 1) / kGradCols;
+  const int64_t below = p.F / kGradCols, pairs = tc - below > below ? tc - below : below;
   const int64_t blocks = (pairs * tr + 7) / 8 * 16;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  k_mx_gated_grad_any<DT, ACT, TW, NP, ROWS, COLS><<<dim3((unsigned)blocks), 4 * TW, 0, stream>>>(p, (int)tc, (int)pairs);
+  k_mx_gated_grad_any<DT, ACT, ROWS, COLS><<<dim3((unsigned)blocks), 256, 0, stream>>>(p, (int)tc, (int)pairs);
   return hipGetLastError();
 }
 
-template <class DT, int ACT, int NP>
-static hipError_t launch_grad_np(const MxGradParams& p, hipStream_t stream) {
-  if (p.rows.codes && p.cols.codes) return launch_grad_t<DT, ACT, NP, true, true>(p, stream);
-  return p.rows.codes ? launch_grad_t<DT, ACT, NP, true, false>(p, stream) : launch_grad_t<DT, ACT, NP, false, true>(p, stream);
-}
-
-// Tiles of 128 rows fill whole 64-byte rows of the transpose's codes; where they would leave the chip with less than
-// @@NB@@ blocks per compute unit, tiles of 32 rows, whose loads all wait at once.
 template <class DT, int ACT>
 static hipError_t launch_grad_act(const MxGradParams& p, hipStream_t stream) {
-  const int64_t blocks = tiles_of(p.M) * ((p.F + kGradCols - 1) / kGradCols);
-  return blocks < kGradFew ? launch_grad_np<DT, ACT, 1>(p, stream) : launch_grad_np<DT, ACT, 4>(p, stream);
+  if (p.rows.codes && p.cols.codes) return launch_grad_t<DT, ACT, true, true>(p, stream);
+  return p.rows.codes ? launch_grad_t<DT, ACT, true, false>(p, stream) : launch_grad_t<DT, ACT, false, true>(p, stream);
 }
 
 hipError_t launch_mx_gated_grad(const MxGradParams& p, int dtype, hipStream_t stream) {
