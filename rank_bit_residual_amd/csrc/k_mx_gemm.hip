@@ -120,15 +120,13 @@ __global__ __launch_bounds__(512) void k_mx_tile(MxGemmParams p) {
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int l32 = lane & 31, g = lane >> 5;
 
-  // ---- tile order: blocks i, i + 8, ... share an XCD, whose blocks walk groups of 4 row tiles column by column
+  // ---- tile order: blocks i, i + 8, ... share an XCD and its L2, so each XCD takes a run of (share of K, tile): few shares,
+  // and within one groups of 4 row tiles walked column by column
   const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + COLS - 1) / COLS;
-  const int ntiles = tiles_m * tiles_n;
-  int split = 0, tid = blockIdx.x;
-  if (SPLIT) {
-    split = blockIdx.x / ntiles;
-    tid = blockIdx.x - split * ntiles;
-  }
-  if ((ntiles & 7) == 0) tid = (tid & 7) * (ntiles >> 3) + (tid >> 3);
+  const int ntiles = tiles_m * tiles_n, all = SPLIT ? ntiles * p.splits : ntiles;
+  const int run = (blockIdx.x & 7) * ((all + 7) >> 3) + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= (all + 7) >> 3 || run >= all) return;
+  const int split = SPLIT ? run / ntiles : 0, tid = SPLIT ? run - split * ntiles : run;
   const int GM = 4;
   const int group = tid / (GM * tiles_n), gm0 = group * GM;
   const int gsz = (tiles_m - gm0) < GM ? (tiles_m - gm0) : GM;
@@ -366,32 +364,39 @@ __global__ __launch_bounds__(512) void k_mx_tile(MxGemmParams p) {
 }
 
 // ------------------------------------------------------------------------------ joining split sums
-// Adds the parts in order and finishes each output. A thread takes one output (gated: its g and u).
-template <class DT, bool GATED>
+// Adds the parts in order and finishes the outputs, V neighbouring ones per thread (gated: their g and u).
+template <class DT, bool GATED, int V>
 __global__ __launch_bounds__(256) void k_mx_join(MxGemmParams p) {
   typedef typename DT::T T;
-  const int64_t n = (int64_t)p.M * p.N, stride = (int64_t)p.M * p.b_rows;
-  for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < n; id += (int64_t)gridDim.x * 256) {
-    const int64_t r = id / p.N, c = id - r * p.N;
+  typedef float vec __attribute__((ext_vector_type(V), aligned(V == 4 ? 16 : 4)));
+  const int c = (blockIdx.x * 256 + threadIdx.x) * V;
+  if (c >= p.N) return;
+  const int64_t stride = (int64_t)p.M * p.b_rows;
+  for (int64_t r = blockIdx.y; r < p.M; r += gridDim.y) {
     const float* src = p.part + r * p.b_rows + c;
-    float a = 0.f, b = 0.f;
-    for (int s = 0; s < p.splits; s++) {
-      a += src[s * stride];
-      if (GATED) b += src[s * stride + p.N];
+    vec a = *reinterpret_cast<const vec*>(src), b = a;
+    if (GATED) b = *reinterpret_cast<const vec*>(src + p.N);
+    for (int s = 1; s < p.splits; s++) {
+      a += *reinterpret_cast<const vec*>(src + s * stride);
+      if (GATED) b += *reinterpret_cast<const vec*>(src + s * stride + p.N);
     }
     T* y = reinterpret_cast<T*>(p.y) + r * p.ldy + c;
     if constexpr (GATED) {
-      float h = 0.f;
-      with_act(p.act, [&](auto k) { h = act_value<decltype(k)::value, float>(a).a * b; });
-      *y = DT::store(h);
       if (p.gu) {
         T* gu = reinterpret_cast<T*>(p.gu) + r * p.ldgu + c;
-        gu[0] = DT::store(a);
-        gu[p.N] = DT::store(b);
+#pragma unroll
+        for (int k = 0; k < V; k++) {
+          gu[k] = DT::store(a[k]);
+          gu[p.N + k] = DT::store(b[k]);
+        }
       }
+      with_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int k = 0; k < V; k++) y[k] = DT::store(act_value<decltype(act)::value, float>(a[k]).a * b[k]);
+      });
     } else {
-      if (p.bias) a += DT::load(reinterpret_cast<const T*>(p.bias)[c]);
-      *y = DT::store(a);
+#pragma unroll
+      for (int k = 0; k < V; k++) y[k] = DT::store(a[k] + (p.bias ? DT::load(reinterpret_cast<const T*>(p.bias)[c + k]) : 0.f));
     }
   }
 }
@@ -403,34 +408,51 @@ using namespace dev;
 // Compute units of the chip: what a plan spreads a product over.
 constexpr int kCus = 256;
 
-// How a product is cut: tile shape and shares of K.
+// How a product is cut: tile shape (bm 0: the kernel for few rows) and shares of K.
 struct MxPlan {
   int bm, bn, splits;
 };
 
-// Rounds of the chip times the time of one: about 8 us of prologue and epilogue, and per stage of 128 codes 0.19 us for
-// 256 x 256 and the time of fewer MFMAs for less. Shares of K cost the writing and reading of the parts.
+// The form with the least estimated time in us, from the times measured on this chip (K = 4096 is kq = 32 stages of 128):
+//   few rows  per 64 rows (k_mx_decode): b is read again for each 64; with b's elements in millions, 2.7 us at 17, 6.2 at
+//             67, 9.3 at 100, 0.6 at 2.5; a wave's stages come after one another, 0.33 us each
+//   128 x 128 two blocks per compute unit; 13 us for up to 256 tiles at kq = 32, 21 for 64 stages, 114 us for 3072 tiles
+//   128 x 256 one block: 16.5 us for 32 tiles to 21 for 256, 109 us for 1536
+//   256 x 256 one block: 23.5 us for 64 tiles, 29 for 192, 35 for 256, 94 for 768; 231 us for 1024 at kq = 64
+// Shares of K add the joining launch and the parts' way through memory at 4 TB/s.
 static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
-  const int cand[3][2] = {{128, 128}, {128, 256}, {256, 256}};
-  const double stage_us[3] = {0.08, 0.115, 0.19};
+  const double b_rows = (double)N * (gated ? 2 : 1), millions = b_rows * kq * 128 * 1e-6;
   MxPlan best{0, 0, 1};
-  if (M <= kMxDecodeRows) return best;
-  double best_t = 0;
+  double few = 0.25 * millions;
+  if (few > 0.9 + 0.11 * millions) few = 0.9 + 0.11 * millions;
+  double best_t = 3.2 + (double)((M + 63) / 64) * few;
+  const double in_turn = 3.0 + 0.33 * kq / (M <= 32 ? 8 : 4);
+  if (best_t < in_turn) best_t = in_turn;
+  const int cand[3][2] = {{128, 128}, {128, 256}, {256, 256}};
   for (int c = 0; c < 3; c++) {
     // a 128-wide gated tile reaches its up rows' scales from its gate rows' by a 32-bit offset
     if (gated && c == 0 && N * kq * 4 >= (int64_t)1 << 31) continue;
     const int bm = cand[c][0], cols = gated ? cand[c][1] / 2 : cand[c][1];
     const int64_t tiles = ((M + bm - 1) / bm) * ((N + cols - 1) / cols);
-    for (int s = 1; s <= 16; s *= 2) {
+    for (int s = 1; s <= 64; s *= 2) {
       if (s > 1 && (kq / 2 / s < 4 || tiles * s > kCus)) break;
-      const double rounds = (double)((tiles * s + kCus - 1) / kCus);
-      double t = rounds * (8.0 + stage_us[c] * kq / s);
-      if (s > 1) t += 4.0 + (double)M * N * (gated ? 2 : 1) * 4 * 2 * s / 4e6;
-      if (best.bm == 0 || t < best_t) best = MxPlan{bm, cand[c][1], s}, best_t = t;
+      const double rounds = (double)(tiles * s) / kCus, st = (double)kq / s;
+      const double whole = (double)((tiles * s) / kCus), rest = rounds - whole;
+      double t;
+      if (c == 0)
+        t = 4 + 0.29 * st * (rounds > 1 ? rounds : 1);
+      else if (c == 1)
+        t = (whole + (rest > 0)) * (4 + 0.45 * st);
+      else
+        t = whole * (6 + 0.8 * st) + (rest > 0 ? 6 + st * (0.5 + 0.3 * rest) : 0);
+      if (s > 1) t += 3.0 + (double)M * b_rows * 4 * 2 * s / 4e6;
+      if (t < best_t) best = MxPlan{bm, cand[c][1], s}, best_t = t;
     }
   }
   return best;
 }
+
+bool mx_product_decodes(int64_t M, int64_t N, int kq, bool gated) { return plan_of(M, N, kq, gated).bm == 0; }
 
 size_t mx_product_part_bytes(int64_t M, int64_t N, int kq, bool gated) {
   const MxPlan pl = plan_of(M, N, kq, gated);
@@ -441,7 +463,8 @@ template <class DT, int BM, int BN, bool GATED, bool SPLIT>
 static hipError_t launch_tile(const MxGemmParams& p, hipStream_t stream) {
   typedef TileCfg<BM, BN> C;
   constexpr int COLS = GATED ? BN / 2 : BN;
-  const int64_t blocks = (((int64_t)p.M + BM - 1) / BM) * (((int64_t)p.N + COLS - 1) / COLS) * p.splits;
+  const int64_t tiles = (((int64_t)p.M + BM - 1) / BM) * (((int64_t)p.N + COLS - 1) / COLS) * p.splits;
+  const int64_t blocks = (tiles + 7) / 8 * 8;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   // once per process and device; a second thread at most repeats the same call
   static std::atomic<uint64_t> configured;
@@ -460,9 +483,8 @@ static hipError_t launch_tile(const MxGemmParams& p, hipStream_t stream) {
 }
 
 template <class DT, bool GATED>
-static hipError_t launch_product_t(const MxGemmParams& p0, hipStream_t stream) {
+static hipError_t launch_product_t(const MxGemmParams& p0, const MxPlan& pl, hipStream_t stream) {
   MxGemmParams p = p0;
-  const MxPlan pl = plan_of(p.M, p.N, p.kq, GATED);
   p.splits = pl.splits;
   if (p.splits > 1) {
     // the parts are float32 whatever the output's type
@@ -470,8 +492,11 @@ static hipError_t launch_product_t(const MxGemmParams& p0, hipStream_t stream) {
                          : pl.bn == 256 ? launch_tile<MxF32, 128, 256, GATED, true>(p, stream)
                                         : launch_tile<MxF32, 128, 128, GATED, true>(p, stream);
     if (e != hipSuccess) return e;
-    const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
-    k_mx_join<DT, GATED><<<dim3((unsigned)(blocks < 4096 ? blocks : 4096)), 256, 0, stream>>>(p);
+    const unsigned rows = p.M < 65535 ? p.M : 65535;
+    if (p.N % 4 == 0)
+      k_mx_join<DT, GATED, 4><<<dim3((unsigned)((p.N / 4 + 255) / 256), rows), 256, 0, stream>>>(p);
+    else
+      k_mx_join<DT, GATED, 1><<<dim3((unsigned)((p.N + 255) / 256), rows), 256, 0, stream>>>(p);
     return hipGetLastError();
   }
   return pl.bm == 256   ? launch_tile<DT, 256, 256, GATED, false>(p, stream)
@@ -480,11 +505,12 @@ static hipError_t launch_product_t(const MxGemmParams& p0, hipStream_t stream) {
 }
 
 hipError_t launch_mx_product(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream) {
-  if (p.M <= kMxDecodeRows) return launch_mx_decode(p, gated, dtype, stream);
+  const MxPlan pl = plan_of(p.M, p.N, p.kq, gated);
+  if (pl.bm == 0) return launch_mx_decode(p, gated, dtype, stream);
   switch (dtype) {
-    case SVDQ_F32: return gated ? launch_product_t<MxF32, true>(p, stream) : launch_product_t<MxF32, false>(p, stream);
-    case SVDQ_BF16: return gated ? launch_product_t<MxBF16, true>(p, stream) : launch_product_t<MxBF16, false>(p, stream);
-    default: return gated ? launch_product_t<MxF16, true>(p, stream) : launch_product_t<MxF16, false>(p, stream);
+    case SVDQ_F32: return gated ? launch_product_t<MxF32, true>(p, pl, stream) : launch_product_t<MxF32, false>(p, pl, stream);
+    case SVDQ_BF16: return gated ? launch_product_t<MxBF16, true>(p, pl, stream) : launch_product_t<MxBF16, false>(p, pl, stream);
+    default: return gated ? launch_product_t<MxF16, true>(p, pl, stream) : launch_product_t<MxF16, false>(p, pl, stream);
   }
 }
 

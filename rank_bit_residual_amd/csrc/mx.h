@@ -43,9 +43,6 @@ struct MxDequantParams {
   int64_t ldo;
 };
 
-// Rows of A that the decode kernel takes.
-constexpr int64_t kMxDecodeRows = 64;
-
 // Whether the decode kernel quantises A itself: one row, or few rows and few columns to do it again for. Measured on
 // the GPU's clock as one launch against two (quantise, product), K = 4096 unless said: 1 row x 24576 columns 12.3 us
 // against 14.3; 4 x 8192 (K = 8192) 9.3 against 10.3, 8 rows 10.5 against 10.3; 8 x 4096 6.2 against 6.5, 16 rows 7.5 against
@@ -86,6 +83,8 @@ struct MxGradParams {
 hipError_t launch_mx_quantize(const MxQuantParams& p, int dtype, hipStream_t stream);
 hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t stream);
 hipError_t launch_mx_gated_grad(const MxGradParams& p, int dtype, hipStream_t stream);
+// Whether the product's launch is the kernel for few rows (the only one that takes an unquantised A).
+bool mx_product_decodes(int64_t M, int64_t N, int kq, bool gated);
 // Bytes of float32 parts that the product's launch writes and reads (0: K is not split).
 size_t mx_product_part_bytes(int64_t M, int64_t N, int kq, bool gated);
 hipError_t launch_mx_decode(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream);

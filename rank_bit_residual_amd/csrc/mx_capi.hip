@@ -136,9 +136,14 @@ int product(const void* a_codes, const void* a_scales, int64_t M, const Product&
   return hip_status(launch_mx_product(p, q.gated, q.dtype, (hipStream_t)stream), "MXFP4 product launch");
 }
 
+// Whether the product quantises its rows itself.
+bool raw_rows(int64_t M, int64_t N, int64_t K, bool gated, int64_t sc) {
+  return mx_raw_rows(M, gated ? 2 * N : N, sc) && mx_product_decodes(M, N, (int)mx_kq(K), gated);
+}
+
 // Workspace of an unquantised A: its codes and scales (unless the product quantises it), then the parts.
 size_t linear_bytes(int64_t M, int64_t N, int64_t K, bool gated, int64_t sc) {
-  if (mx_raw_rows(M, gated ? 2 * N : N, sc)) return 0;
+  if (raw_rows(M, N, K, gated, sc)) return 0;
   return (size_t)(mx_code_bytes(M, K) + mx_scale_bytes(M, K)) + mx_product_part_bytes(M, N, (int)mx_kq(K), gated);
 }
 
@@ -150,7 +155,7 @@ int linear(const void* x, int64_t M, int64_t sr, int64_t sc, const Product& q, v
   if ((st = check_workspace(workspace, workspace_bytes, linear_bytes(M, q.N, q.K, q.gated, sc)))) return st;
   uint8_t* ws = (uint8_t*)workspace;
   hipStream_t s = (hipStream_t)stream;
-  if (mx_raw_rows(M, q.gated ? 2 * q.N : q.N, sc)) {
+  if (raw_rows(M, q.N, q.K, q.gated, sc)) {
     MxGemmParams p = params_of(M, q, nullptr);
     p.x = x;
     p.ldx = sr;
