@@ -414,8 +414,9 @@ struct MxPlan {
 };
 
 // The form with the least estimated time in us, from the times measured on this chip (K = 4096 is kq = 32 stages of 128):
-//   few rows  per 64 rows (k_mx_decode): b is read again for each 64; with b's elements in millions, 2.7 us at 17, 6.2 at
-//             67, 9.3 at 100, 0.6 at 2.5; a wave's stages come after one another, 0.33 us each
+//   few rows  (k_mx_decode) b is read again for each 64 rows; with b's elements in millions, up to 32 rows 2.5 us at 1, 3.3
+//             to 4 at 17, 7.9 at 67; 64 rows 3.2, 5.2 and 10.1, 128 rows 3.2, 9.0 and 17.8; a wave's stages come after one
+//             another, 0.33 us each
 //   128 x 128 two blocks per compute unit; 13 us for up to 256 tiles at kq = 32, 21 for 64 stages, 114 us for 3072 tiles
 //   128 x 256 one block: 16.5 us for 32 tiles to 21 for 256, 109 us for 1536
 //   256 x 256 one block: 23.5 us for 64 tiles, 29 for 192, 35 for 256, 94 for 768; 231 us for 1024 at kq = 64
@@ -424,8 +425,9 @@ static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
   const double b_rows = (double)N * (gated ? 2 : 1), millions = b_rows * kq * 128 * 1e-6;
   MxPlan best{0, 0, 1};
   double few = 0.25 * millions;
-  if (few > 0.9 + 0.11 * millions) few = 0.9 + 0.11 * millions;
-  double best_t = 3.2 + (double)((M + 63) / 64) * few;
+  if (few > 1.6 + 0.11 * millions) few = 1.6 + 0.11 * millions;
+  double best_t = M <= 32 ? 2.2 + 0.082 * millions : 3.0 + (double)((M + 63) / 64) * few;
+  if (M > 64 * 65535) best_t = 1e30;  // past the grid's second dimension
   const double in_turn = 3.0 + 0.33 * kq / (M <= 32 ? 8 : 4);
   if (best_t < in_turn) best_t = in_turn;
   const int cand[3][2] = {{128, 128}, {128, 256}, {256, 256}};

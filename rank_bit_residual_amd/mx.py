@@ -55,8 +55,8 @@ class MxTensor:
 
     @classmethod
     def _empty(cls, rows: int, cols: int, device) -> "MxTensor":
-        t = cls.__new__(cls)
         code_bytes, scale_bytes = _bytes(rows, cols)
+        t = cls.__new__(cls)
         t.data = torch.empty(code_bytes + scale_bytes, dtype=torch.uint8, device=device)
         t.rows, t.cols, t._at = rows, cols, code_bytes
         return t
@@ -117,13 +117,14 @@ def _same_device(device, *ts) -> None:
             raise ValueError("all tensors of a call must be on one device")
 
 
-def _call(name: str, device, *args) -> None:
-    """libsvdq's `name` on the current stream of `device`, which is the current device meanwhile."""
-    index = device.index
-    if torch._C._cuda_getDevice() != index:
-        with torch.cuda.device(device):
-            return _call(name, device, *args)
-    status = getattr(L.load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+def _call(fn, index: int, *args) -> None:
+    """A libsvdq call on the current stream of device `index`, which is the current device meanwhile."""
+    # the stream's handle and the device's index as torch's own wrappers read them, without their objects
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status:
         L.check(status)
 
@@ -137,7 +138,7 @@ def _parts(t) -> tuple:
 
 def _output(out, rows: int, cols: int, dtype, device) -> torch.Tensor:
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device)
+        return torch.empty(rows, cols, dtype=dtype, device=device)
     if not isinstance(out, torch.Tensor) or out.shape != (rows, cols) or out.dtype != dtype or out.device != device:
         raise ValueError(f"out must be a [{rows}, {cols}] {dtype} tensor on {device}")
     if (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols):
@@ -146,7 +147,8 @@ def _output(out, rows: int, cols: int, dtype, device) -> torch.Tensor:
 
 
 def _row_stride(t: torch.Tensor) -> int:
-    return max(t.stride(0), t.shape[1])  # a single row may have any stride
+    n = t.stride(0)
+    return n if n >= t.shape[1] else t.shape[1]  # a single row may have any stride
 
 
 def _unit_columns(t: torch.Tensor) -> torch.Tensor:
@@ -177,10 +179,10 @@ def mx_quantize(x: torch.Tensor, axis: int | None = 1):
     dt = _matrix(x, "x")
     if axis is not None and (isinstance(axis, bool) or axis not in (0, 1)):
         raise ValueError("axis must be 0, 1 or None")
-    (R, C), device = x.shape, x.device
+    (R, C), (sr, sc), device = x.shape, x.stride(), x.device
     rows = MxTensor._empty(R, C, device) if axis != 0 else None
     cols = MxTensor._empty(C, R, device) if axis != 1 else None
-    _call("svdq_mx_quantize", device, x.data_ptr(), R, C, *x.stride(), dt, *_parts(rows), *_parts(cols))
+    _call(L.load().svdq_mx_quantize, device.index, x.data_ptr(), R, C, sr, sc, dt, *_parts(rows), *_parts(cols))
     return (rows, cols) if axis is None else (rows if axis == 1 else cols)
 
 
@@ -189,7 +191,7 @@ def mx_dequantize(t: MxTensor, dtype: torch.dtype = torch.bfloat16, out: torch.T
     _mx(t, "t")
     code = _dtype_code(dtype)
     out = _output(out, t.rows, t.cols, dtype, t.device)
-    _call("svdq_mx_dequantize", t.device, *_parts(t), t.rows, t.cols, code, out.data_ptr(), _row_stride(out))
+    _call(L.load().svdq_mx_dequantize, out.device.index, *_parts(t), t.rows, t.cols, code, out.data_ptr(), _row_stride(out))
     return out
 
 
@@ -212,6 +214,7 @@ def _product(a, b, name_a: str, name_b: str, dtype, out, finish, *, gated: bool)
         raise ValueError(f"{name_a} [{M}, {K}] and {name_b} [{b.rows}, {b.cols}] must share their second dimension")
     device = a.device
     _same_device(device, b)
+    lib = L.load()
     extra, N, gu = finish(M, dtype, device)
     y = _output(out, M, N, dtype, device)
     tail = (code, y.data_ptr(), _row_stride(y)) + ((None if gu is None else gu.data_ptr(), 2 * N) if gated else ())
@@ -220,11 +223,11 @@ def _product(a, b, name_a: str, name_b: str, dtype, out, finish, *, gated: bool)
         if K == 1:
             sc = 1
         ws, *scratch = _workspace(_workspace_bytes("svdq_mx_linear_workspace_bytes", M, N, K, sc, gated), device)
-        _call("svdq_mx_gated_linear" if gated else "svdq_mx_linear", device, a.data_ptr(), M, K, sr, sc, *_parts(b), N,
+        _call(lib.svdq_mx_gated_linear if gated else lib.svdq_mx_linear, device.index, a.data_ptr(), M, K, sr, sc, *_parts(b), N,
               extra, *tail, *scratch)
     else:
         ws, *scratch = _workspace(_workspace_bytes("svdq_mx_workspace_bytes", M, N, K, gated), device)
-        _call("svdq_mx_gated" if gated else "svdq_mx_matmul", device, *_parts(a), M, *_parts(b), N, K, extra, *tail,
+        _call(lib.svdq_mx_gated if gated else lib.svdq_mx_matmul, device.index, *_parts(a), M, *_parts(b), N, K, extra, *tail,
               *scratch)
     return y
 
@@ -282,7 +285,7 @@ def mx_gated_grad(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu"):
     _same_device(device, gu)
     dh, gu = _unit_columns(dh), _unit_columns(gu)
     rows, cols = MxTensor._empty(M, 2 * F, device), MxTensor._empty(2 * F, M, device)
-    _call("svdq_mx_gated_grad", device, dh.data_ptr(), _row_stride(dh), gu.data_ptr(), _row_stride(gu), M, F, code, dt,
+    _call(L.load().svdq_mx_gated_grad, device.index, dh.data_ptr(), _row_stride(dh), gu.data_ptr(), _row_stride(gu), M, F, code, dt,
           *_parts(rows), *_parts(cols))
     return rows, cols
 
