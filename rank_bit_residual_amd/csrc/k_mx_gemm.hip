@@ -374,11 +374,22 @@ __global__ __launch_bounds__(256) void k_mx_join(MxGemmParams p) {
   const int64_t stride = (int64_t)p.M * p.b_rows;
   for (int64_t r = blockIdx.y; r < p.M; r += gridDim.y) {
     const float* src = p.part + r * p.b_rows + c;
-    vec a = *reinterpret_cast<const vec*>(src), b = a;
-    if (GATED) b = *reinterpret_cast<const vec*>(src + p.N);
-    for (int s = 1; s < p.splits; s++) {
-      a += *reinterpret_cast<const vec*>(src + s * stride);
-      if (GATED) b += *reinterpret_cast<const vec*>(src + s * stride + p.N);
+    vec a = {}, b = {};
+    // four parts requested at a time, added in order
+    for (int s = 0; s < p.splits; s += 4) {
+      vec x[4], z[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const int at = s + k < p.splits ? s + k : p.splits - 1;
+        x[k] = *reinterpret_cast<const vec*>(src + at * stride);
+        if (GATED) z[k] = *reinterpret_cast<const vec*>(src + at * stride + p.N);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        if (s + k >= p.splits) continue;
+        a += x[k];
+        if (GATED) b += z[k];
+      }
     }
     T* y = reinterpret_cast<T*>(p.y) + r * p.ldy + c;
     if constexpr (GATED) {
