@@ -202,6 +202,115 @@ def test_matmul_into_a_view(M, K, N):
     assert (big == 3.0).all()
 
 
+# ----------------------------------------------------------------------------- every form of the product
+GRID = [0, 0.5, 1, 1.5, 2, 3, 4, 6]
+
+
+def _on_grid(gen, rows, cols):
+    """Values that are their own Q: codes of a block whose largest is 6, signs included."""
+    x = torch.tensor(GRID, device=dev())[torch.randint(0, 8, (rows, cols), generator=gen, device=dev())]
+    x[:, ::32] = 6.0
+    return x * (1 - 2 * torch.randint(0, 2, (rows, cols), generator=gen, device=dev()))
+
+
+def _gen(seed):
+    g = torch.Generator(device=dev())
+    g.manual_seed(seed)
+    return g
+
+
+# rows of A from one to many, K long enough to be shared out, tiles of each shape, last tiles of a row or a column
+@pytest.mark.parametrize("M,K,N", [(1, 1024, 8200), (1, 4097, 100), (3, 4097, 100), (16, 65536, 20), (17, 520, 9000),
+                                   (40, 512, 9001), (64, 65536, 64), (70, 8192, 8192), (97, 40000, 300), (130, 40000, 301),
+                                   (200, 1030, 3000), (300, 4096, 5000), (513, 4096, 12290), (2000, 1030, 4090),
+                                   (1030, 4096, 12300)])
+def test_every_form_of_the_product(M, K, N):
+    """Sums of multiples of 1/4 below 2^22 (65536 * 36): one value in float32 whatever the order."""
+    gen = _gen(M + K + N)
+    a, b = _on_grid(gen, M, K), _on_grid(gen, N, K)
+    ref = a.double() @ b.double().t().contiguous()
+    bq = R.mx_quantize(b)
+    for x in (a, R.mx_quantize(a)):
+        y = R.mx_matmul(x, bq, dtype=torch.float32)
+        assert torch.equal(y.double(), ref)
+    bias = torch.randint(-8, 8, (N,), generator=gen, device=dev()).to(torch.bfloat16)
+    y = R.mx_matmul(a.to(torch.bfloat16), bq, bias=bias)
+    assert torch.equal(y, (ref + bias.double()).float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("save", [False, True])
+@pytest.mark.parametrize("M,K,F", [(1, 4096, 600), (1, 1023, 9000), (5, 520, 333), (33, 33000, 40), (130, 33000, 151), (200, 1030, 3001),
+                                   (300, 4096, 6000), (500, 2048, 12290), (1500, 512, 2050)])
+def test_every_form_of_the_gated_product(M, K, F, save):
+    gen = _gen(M + K + F)
+    x, w = _on_grid(gen, M, K) / 64, _on_grid(gen, 2 * F, K) / 64
+    gu = x.double() @ w.double().t().contiguous()
+    wq = R.mx_quantize(w)
+    for a in (x, R.mx_quantize(x)):
+        got = R.mx_gated(a, wq, act="silu", dtype=torch.float32, save=save)
+        h = got[0] if save else got
+        if save:
+            assert torch.equal(got[1].double(), gu)  # exact sums, as above
+        g, u = gu[:, :F], gu[:, F:]
+        ref = g / (1 + torch.exp(-g)) * u
+        # the float32 activation's relative error (3 + |g|) 2^-21, the product's and the store's 2^-24 each
+        bound = ((3 + g.abs()) * 2.0**-21 + 2.0**-23) * ref.abs() + 1e-37
+        assert ((h.double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M", [1, 3, 20, 200])
+def test_unquantised_rows_at_any_place(dtype, M):
+    """Rows that start off every vector's alignment, with any row stride and with strided columns."""
+    gen = _gen(M)
+    big = _on_grid(gen, 2 * M + 1, 700).to(TD[dtype])
+    b = R.mx_quantize(_on_grid(gen, 50, 333))
+    w = R.mx_quantize(_on_grid(gen, 24, 333))
+    for x in (big[1:M + 1, 1:334], big[::2, 3:336][:M], big[:M, :666:2], big[:1, 5:338].expand(M, 333)):
+        c = x.contiguous().clone()
+        assert torch.equal(R.mx_matmul(x, b), R.mx_matmul(c, b))
+        assert torch.equal(R.mx_gated(x, w), R.mx_gated(c, w))
+
+
+# ----------------------------------------------------------------------------- far offsets
+def test_offsets_past_32_bits():
+    """A tensor of 4.6 GB of codes from 18 GB of values in {-3 .. 3}, which are their own Q along either axis (a block's
+    largest of 3 is 6 halves): values back, and products with its last rows."""
+    rows, cols = 140_000, 65_536
+    gen = _gen(77)
+    x = torch.randint(-3, 4, (rows, cols), generator=gen, device=dev(), dtype=torch.int8).to(torch.bfloat16)
+    x[:, ::32] = 3
+    x[::32] = 3
+    r, c = R.mx_quantize(x, axis=None)
+    assert r.data.numel() > 2**32
+    assert torch.equal(R.mx_dequantize(r), x)
+    back = R.mx_dequantize(c)
+    assert all(torch.equal(back[k:k + 8192], x[:, k:k + 8192].t()) for k in range(0, cols, 8192))
+    del back
+    for M in (1, 40, 200):
+        a = torch.randint(-3, 4, (M, cols), generator=gen, device=dev(), dtype=torch.int8).to(torch.bfloat16)
+        a[:, ::32] = 3
+        y = R.mx_matmul(R.mx_quantize(a), r, dtype=torch.float32)
+        for part in (slice(0, 300), slice(rows - 300, rows)):
+            assert torch.equal(y[:, part], a.float() @ x[part].float().t().contiguous())
+        g = R.mx_gated(R.mx_quantize(a), r, act="relu", dtype=torch.float32)
+        up = slice(rows - 300, rows)
+        gate = slice(rows // 2 - 300, rows // 2)
+        ref = (a.float() @ x[gate].float().t().contiguous()).relu() * (a.float() @ x[up].float().t().contiguous())
+        assert torch.equal(g[:, -300:], ref)  # two exact factors, one rounding
+
+
+def test_gated_grad_offsets_past_32_bits():
+    M, F = 70_016, 32_768
+    gen = _gen(78)
+    dh = torch.randn(M, F, generator=gen, device=dev(), dtype=torch.bfloat16)
+    gu = torch.randn(M, 2 * F, generator=gen, device=dev(), dtype=torch.bfloat16)
+    rows, cols = R.mx_gated_grad(dh, gu)
+    want_r, want_c = R.mx_gated_grad(dh[-128:].clone(), gu[-128:].clone())
+    assert torch.equal(R.mx_dequantize(rows)[-128:], R.mx_dequantize(want_r))
+    assert torch.equal(R.mx_dequantize(cols)[:, -128:], R.mx_dequantize(want_c))
+
+
 # ----------------------------------------------------------------------------- gated block
 REL_ACT = 2.0**-18  # the float32 activation: (3 + |w|) 2^-21 with |w| below 5 where it counts
 
