@@ -355,12 +355,13 @@ typedef enum {
   SVDQ_ACT_RELU = 3       /* max(g, 0) */
 } svdq_act;
 
-/* Bytes of the two arrays of a rows x K tensor. Errors: EINVAL. */
+/* Bytes of the two arrays of a rows x K tensor (multiples of 256, so that they may share one
+ * buffer). Errors: EINVAL. */
 int svdq_mx_layout(int64_t rows, int64_t K, size_t* code_bytes, size_t* scale_bytes);
 
 /* --------------------------------------------------------------------------------------
- * svdq_mx_quantize — Q(x) and / or Q(x^T) of x [R, C] (strides sr, sc in elements, any sign
- * of neither: >= 0) in one pass. codes / scales: the R x C tensor (blocks along C); codes_t /
+ * svdq_mx_quantize — Q(x) and / or Q(x^T) of x [R, C] (strides sr, sc >= 0 in elements) in one
+ * pass. codes / scales: the R x C tensor (blocks along C); codes_t /
  * scales_t: the C x R tensor (blocks along R), as the other operand order or a backward
  * product wants it. Either pair may be NULL, not both.
  * Errors: EINVAL (shape, strides, alignment, nothing to do), EDTYPE, EHIP.
@@ -428,6 +429,19 @@ int svdq_mx_gated_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_
  * ------------------------------------------------------------------------------------ */
 int svdq_mx_gated_grad(const void* dh, int64_t ldh, const void* gu, int64_t ldgu, int64_t M, int64_t F, int act,
                        int dtype, void* codes, void* scales, void* codes_t, void* scales_t, svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_mx_gated_backward — the backward pass of svdq_mx_gated in one call: svdq_mx_gated_grad into the workspace,
+ * then dx = Q(d) Q(w)^T [M, K] and dw = Q(x^T) Q(d^T)^T [K, 2F] by svdq_mx_matmul, with the same results.
+ * w_codes / w_scales: the merged weight [K, 2F] quantised along its rows; x_codes / x_scales: x^T, [K, M],
+ * the input quantised along its columns. dtype: of dh and gu; out_dtype: of dx and dw. M and 2F are at most
+ * 2^27. workspace: svdq_mx_gated_backward_workspace_bytes, 256-byte aligned. Errors: EINVAL, EDTYPE, EHIP.
+ * ------------------------------------------------------------------------------------ */
+int svdq_mx_gated_backward_workspace_bytes(int64_t M, int64_t F, int64_t K, size_t* bytes_out);
+int svdq_mx_gated_backward(const void* dh, int64_t ldh, const void* gu, int64_t ldgu, int64_t M, int64_t F, int act,
+                           int dtype, const void* w_codes, const void* w_scales, const void* x_codes,
+                           const void* x_scales, int64_t K, int out_dtype, void* dx, int64_t lddx, void* dw,
+                           int64_t lddw, void* workspace, size_t workspace_bytes, svdq_stream_t stream);
 
 /* --------------------------------------------------------------------------------------
  * Kernel timing (profiling aid; not on any page). Between svdq_profile_begin and

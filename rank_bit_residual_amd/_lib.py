@@ -63,6 +63,9 @@ SIGNATURES = {
                                      c_vp, c_i64, c_vp, c_sz, c_vp]),
     "svdq_mx_gated_grad": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_vp, c_vp, c_vp, c_vp,
                                    c_vp]),
+    "svdq_mx_gated_backward_workspace_bytes": (c_int, [c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)]),
+    "svdq_mx_gated_backward": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_vp, c_vp, c_vp, c_vp,
+                                       c_i64, c_int, c_vp, c_i64, c_vp, c_i64, c_vp, c_sz, c_vp]),
 }
 NSTAGES = 4
 STAGE_NAMES = ("amax", "act_quant_down", "down_reduce", "gemm")

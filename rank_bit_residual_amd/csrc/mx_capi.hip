@@ -95,7 +95,7 @@ struct Product {
 
 int check_product(int64_t M, const Product& q) {
   int st;
-  if ((st = check_dim(M, "M")) || (st = check_dim(q.gated ? 2 * q.N : q.N, q.gated ? "2F" : "N")) || (st = check_dim(q.K, "K")) ||
+  if ((st = check_dim(M, "M")) || (st = check_dim(q.N, q.gated ? "F" : "N")) || (q.gated && (st = check_dim(2 * q.N, "2F"))) || (st = check_dim(q.K, "K")) ||
       (st = check_product_k(q.K)) || (st = check_tensor(q.b_codes, q.b_scales, q.gated ? "w" : "b")) ||
       (st = check_matrix(q.y, q.ldy, q.N, q.dtype, q.gated ? "h" : "y")))
     return st;
@@ -210,7 +210,7 @@ int svdq_mx_dequantize(const void* codes, const void* scales, int64_t rows, int6
 int svdq_mx_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated, size_t* bytes_out) {
   clear_error();
   int st = check_dim(M, "M");
-  if (st || (st = check_dim(gated ? 2 * N : N, "N")) || (st = check_dim(K, "K")) || (st = check_product_k(K))) return st;
+  if (st || (st = check_dim(N, "N")) || (st = check_dim(gated ? 2 * N : N, "N")) || (st = check_dim(K, "K")) || (st = check_product_k(K))) return st;
   if (!bytes_out) return set_error(SVDQ_EINVAL, "bytes_out is NULL");
   *bytes_out = mx_product_part_bytes(M, N, (int)mx_kq(K), gated != 0);
   return SVDQ_OK;
@@ -252,10 +252,66 @@ int svdq_mx_gated_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_
   return linear(x, M, sr, sc, q, workspace, workspace_bytes, stream);
 }
 
+// d in both directions, then the larger of the two products' parts (they run one after the other).
+static size_t backward_bytes(int64_t M, int64_t F, int64_t K, size_t at[5]) {
+  size_t o = 0;
+  const int64_t size[4] = {mx_code_bytes(M, 2 * F), mx_scale_bytes(M, 2 * F), mx_code_bytes(2 * F, M), mx_scale_bytes(2 * F, M)};
+  for (int i = 0; i < 4; i++) {
+    at[i] = o;
+    o += (size_t)size[i];
+  }
+  at[4] = o;
+  const size_t dx = mx_product_part_bytes(M, K, (int)mx_kq(2 * F), false), dw = mx_product_part_bytes(K, 2 * F, (int)mx_kq(M), false);
+  return o + (dx > dw ? dx : dw);
+}
+
+int svdq_mx_gated_backward_workspace_bytes(int64_t M, int64_t F, int64_t K, size_t* bytes_out) {
+  clear_error();
+  int st = check_dim(M, "M");
+  if (st || (st = check_dim(F, "F")) || (st = check_dim(2 * F, "2F")) || (st = check_dim(K, "K")) ||
+      (st = check_product_k(2 * F)) || (st = check_product_k(M)))
+    return st;
+  if (!bytes_out) return set_error(SVDQ_EINVAL, "bytes_out is NULL");
+  size_t at[5];
+  *bytes_out = backward_bytes(M, F, K, at);
+  return SVDQ_OK;
+}
+
+int svdq_mx_gated_backward(const void* dh, int64_t ldh, const void* gu, int64_t ldgu, int64_t M, int64_t F, int act,
+                           int dtype, const void* w_codes, const void* w_scales, const void* x_codes, const void* x_scales,
+                           int64_t K, int out_dtype, void* dx, int64_t lddx, void* dw, int64_t lddw, void* workspace,
+                           size_t workspace_bytes, svdq_stream_t stream) {
+  int st = begin(dtype);
+  if (st || (st = begin(out_dtype)) || (st = check_dim(F, "F")) || (st = check_act(act)) ||
+      (st = check_matrix(dh, ldh, F, dtype, "dh")) || (st = check_matrix(gu, ldgu, 2 * F, dtype, "gu")))
+    return st;
+  Product q_dx{w_codes, w_scales, K, 2 * F, false, 0, out_dtype, nullptr, dx, lddx, nullptr, 0};
+  Product q_dw{nullptr, nullptr, 2 * F, M, false, 0, out_dtype, nullptr, dw, lddw, nullptr, 0};
+  size_t at[5];
+  if ((st = check_product(M, q_dx)) || (st = check_dim(M, "M")) || (st = check_product_k(M)) ||
+      (st = check_tensor(x_codes, x_scales, "x")) || (st = check_matrix(dw, lddw, 2 * F, out_dtype, "dw")) ||
+      (st = check_workspace(workspace, workspace_bytes, backward_bytes(M, F, K, at))))
+    return st;
+  uint8_t* ws = (uint8_t*)workspace;
+  hipStream_t s = (hipStream_t)stream;
+  const MxGradParams p{dh, gu, M, F, ldh, ldgu, act, out_of(ws + at[0], ws + at[1], 2 * F), out_of(ws + at[2], ws + at[3], M)};
+  if ((st = hip_status(launch_mx_gated_grad(p, dtype, s), "mx_gated_grad launch"))) return st;
+  MxGemmParams a = params_of(M, q_dx, ws + at[4]);
+  a.a_codes = ws + at[0];
+  a.a_scales = ws + at[1];
+  if ((st = hip_status(launch_mx_product(a, false, out_dtype, s), "MXFP4 product launch"))) return st;
+  q_dw.b_codes = ws + at[2];
+  q_dw.b_scales = ws + at[3];
+  MxGemmParams b = params_of(K, q_dw, ws + at[4]);
+  b.a_codes = (const uint8_t*)x_codes;
+  b.a_scales = (const uint8_t*)x_scales;
+  return hip_status(launch_mx_product(b, false, out_dtype, s), "MXFP4 product launch");
+}
+
 int svdq_mx_gated_grad(const void* dh, int64_t ldh, const void* gu, int64_t ldgu, int64_t M, int64_t F, int act,
                        int dtype, void* codes, void* scales, void* codes_t, void* scales_t, svdq_stream_t stream) {
   int st = begin(dtype);
-  if (st || (st = check_dim(M, "M")) || (st = check_dim(2 * F, "2F")) || (st = check_act(act)) ||
+  if (st || (st = check_dim(M, "M")) || (st = check_dim(F, "F")) || (st = check_dim(2 * F, "2F")) || (st = check_act(act)) ||
       (st = check_matrix(dh, ldh, F, dtype, "dh")) || (st = check_matrix(gu, ldgu, 2 * F, dtype, "gu")))
     return st;
   if (!codes && !codes_t) return set_error(SVDQ_EINVAL, "nothing to quantise into");

@@ -272,10 +272,8 @@ def mx_gated(x, w: MxTensor, act: str = "silu", dtype: torch.dtype | None = None
     return (h, gu) if save else h
 
 
-def mx_gated_grad(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu"):
-    """The gradients d = [dg | du] of a gated block's pre-activations, dg = dh * u * act'(g) and
-    du = dh * act(g), from dh [M, F] and gu [M, 2F]: Q(d) [M, 2F] and Q(d^T) [2F, M], from one pass."""
-    code = _act_code(act)
+def _pre_activations(dh, gu) -> tuple:
+    """(dtype code, M, F, device, dh, gu) of a backward call's gradient and saved pre-activations."""
     dt = _matrix(dh, "dh")
     _matrix(gu, "gu")
     M, F = dh.shape
@@ -283,7 +281,14 @@ def mx_gated_grad(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu"):
         raise ValueError(f"gu must be a [{M}, {2 * F}] tensor of dh's dtype")
     device = dh.device
     _same_device(device, gu)
-    dh, gu = _unit_columns(dh), _unit_columns(gu)
+    return dt, M, F, device, _unit_columns(dh), _unit_columns(gu)
+
+
+def mx_gated_grad(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu"):
+    """The gradients d = [dg | du] of a gated block's pre-activations, dg = dh * u * act'(g) and
+    du = dh * act(g), from dh [M, F] and gu [M, 2F]: Q(d) [M, 2F] and Q(d^T) [2F, M], from one pass."""
+    code = _act_code(act)
+    dt, M, F, device, dh, gu = _pre_activations(dh, gu)
     rows, cols = MxTensor._empty(M, 2 * F, device), MxTensor._empty(2 * F, M, device)
     _call(L.load().svdq_mx_gated_grad, device.index, dh.data_ptr(), _row_stride(dh), gu.data_ptr(), _row_stride(gu), M, F, code, dt,
           *_parts(rows), *_parts(cols))
@@ -295,14 +300,19 @@ def mx_gated_backward(dh: torch.Tensor, gu: torch.Tensor, w_rows: MxTensor, x_co
     """(dx [M, K], dw [K, 2F]) of h = mx_gated(x, w): dx = Q(d) Q(w)^T and dw = Q(x^T) Q(d^T)^T with the d of
     mx_gated_grad. w_rows: the merged weight [K, 2F] quantised along its rows (axis=1); x_cols: the input
     quantised along its columns (axis=0), [K, M]. dtype: of the gradients, dh's by default."""
+    code = _act_code(act)
     _mx(w_rows, "w_rows")
     _mx(x_cols, "x_cols")
-    _matrix(dh, "dh")
-    M, F = dh.shape
-    if w_rows.cols != 2 * F or x_cols.cols != M or w_rows.rows != x_cols.rows:
+    dt, M, F, device, dh, gu = _pre_activations(dh, gu)
+    K = w_rows.rows
+    if w_rows.cols != 2 * F or x_cols.cols != M or x_cols.rows != K:
         raise ValueError(f"w_rows must be [K, {2 * F}] and x_cols [K, {M}]")
-    _same_device(dh.device, w_rows, x_cols)
+    _same_device(device, w_rows, x_cols)
     dtype = dtype or dh.dtype
-    _dtype_code(dtype)
-    rows, cols = mx_gated_grad(dh, gu, act)
-    return mx_matmul(rows, w_rows, dtype=dtype), mx_matmul(x_cols, cols, dtype=dtype)
+    out = _dtype_code(dtype)
+    dx = torch.empty(M, K, dtype=dtype, device=device)
+    dw = torch.empty(K, 2 * F, dtype=dtype, device=device)
+    ws, *scratch = _workspace(_workspace_bytes("svdq_mx_gated_backward_workspace_bytes", M, F, K), device)
+    _call(L.load().svdq_mx_gated_backward, device.index, dh.data_ptr(), _row_stride(dh), gu.data_ptr(), _row_stride(gu), M,
+          F, code, dt, *_parts(w_rows), *_parts(x_cols), K, out, dx.data_ptr(), K, dw.data_ptr(), 2 * F, *scratch)
+    return dx, dw

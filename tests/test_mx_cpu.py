@@ -158,6 +158,32 @@ def test_gated_grad_refusals(change, status):
     _refused(status, _lib.load().svdq_mx_gated_grad(*a.values(), None))
 
 
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=F64), EDTYPE), (dict(out=F64), EDTYPE), (dict(M=0), EINVAL), (dict(F=0), EINVAL), (dict(F=1 << 30), EINVAL),
+    (dict(F=1 << 62), EINVAL), (dict(K=0), EINVAL), (dict(act=7), EINVAL), (dict(dh=None), EINVAL), (dict(ldh=7), EINVAL),
+    (dict(gu=None), EINVAL), (dict(ldgu=15), EINVAL), (dict(wc=None), EINVAL), (dict(ws=A + 4), EINVAL), (dict(xc=A + 16), EINVAL),
+    (dict(xs=None), EINVAL), (dict(dx=None), EINVAL), (dict(lddx=39), EINVAL), (dict(dw=A + 1), EINVAL), (dict(lddw=15), EINVAL),
+    (dict(work=None), EINVAL), (dict(work=A + 8), EINVAL), (dict(bytes=4096), EINVAL), (dict(M=(1 << 27) + 1), EINVAL),
+    (dict(F=1 << 27, ldh=1 << 27, ldgu=1 << 28, lddw=1 << 28), EINVAL),
+])
+def test_gated_backward_refusals(change, status):
+    a = dict(dh=A, ldh=8, gu=A, ldgu=16, M=4, F=8, act=0, dtype=BF16, wc=A, ws=A, xc=A, xs=A, K=40, out=F32, dx=A, lddx=40, dw=A,
+             lddw=16, work=A, bytes=1 << 50)
+    a.update(change)
+    _refused(status, _lib.load().svdq_mx_gated_backward(*a.values(), None))
+
+
+def test_backward_workspace_query():
+    lib, n = _lib.load(), ctypes.c_size_t()
+    d = sum(_layout(100, 2 * 96)[1:]) + sum(_layout(2 * 96, 100)[1:])
+    assert lib.svdq_mx_gated_backward_workspace_bytes(100, 96, 512, ctypes.byref(n)) == 0 and n.value == d
+    assert lib.svdq_mx_gated_backward_workspace_bytes(1 << 16, 64, 128, ctypes.byref(n)) == 0
+    assert n.value > sum(_layout(1 << 16, 128)[1:]) + sum(_layout(128, 1 << 16)[1:])  # dw's sum over many rows is shared out
+    for bad in ((0, 4, 4), (4, 0, 4), (4, 4, 0), (4, 1 << 29, 4), ((1 << 27) + 1, 4, 4), (4, 1 << 27, 4), (4, 1 << 62, 4)):
+        _refused(EINVAL, lib.svdq_mx_gated_backward_workspace_bytes(*bad, ctypes.byref(n)))
+    _refused(EINVAL, lib.svdq_mx_gated_backward_workspace_bytes(4, 4, 4, None))
+
+
 def test_workspace_query():
     lib, n = _lib.load(), ctypes.c_size_t(7)
     assert lib.svdq_mx_workspace_bytes(256, 256, 512, 0, ctypes.byref(n)) == 0 and n.value == 0

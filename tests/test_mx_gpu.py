@@ -124,6 +124,19 @@ def test_infinities_and_nan_poison_their_block_alone(dtype):
         assert np.flatnonzero(bad).tolist() == [1, 2, 50, 51]
 
 
+def test_nan_blocks_in_tiles():
+    """The tiled product: rows of A and of b with a NaN block give NaN rows and columns, nothing else."""
+    gen = _gen(4)
+    a, b = _on_grid(gen, 2000, 512), _on_grid(gen, 4096, 512)
+    ref = a @ b.t().contiguous()
+    a[7, 100], a[1999, 511], b[3, 0], b[4095, 300] = float("nan"), float("inf"), float("-inf"), float("nan")
+    y = R.mx_matmul(a, R.mx_quantize(b))
+    bad = torch.zeros(2000, 4096, dtype=torch.bool, device=a.device)
+    bad[[7, 1999]] = True
+    bad[:, [3, 4095]] = True
+    assert torch.equal(y.isnan(), bad) and torch.equal(y[~bad], ref[~bad])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (5, 33), (64, 128), (70, 300)])
 def test_dequantize(dtype, rows, cols):
@@ -420,6 +433,21 @@ def test_training_step_together(dtype, M, K, F):
     for got, a, b in ((dx, X.values(d), X.values(_np(w))), (dw, X.values(_np(x).T), X.values(d.T))):
         ref = a @ b.T
         assert (np.abs(_np(got) - ref) <= _matmul_bound(a, b, ref, dtype)).all()
+
+
+@pytest.mark.parametrize("M,K,F", [(1, 64, 17), (40, 300, 96), (2000, 520, 700), (40_000, 128, 48)])
+def test_backward_is_its_parts(M, K, F):
+    """The one call against the gradients and the two products one by one, in both output types."""
+    gen = _gen(M)
+    dh = torch.randn(M, F, generator=gen, device=dev()).to(torch.bfloat16)
+    gu = torch.randn(M, 2 * F, generator=gen, device=dev()).to(torch.bfloat16)
+    w = R.mx_quantize(torch.randn(K, 2 * F, generator=gen, device=dev()))
+    x = R.mx_quantize(torch.randn(M, K, generator=gen, device=dev()), axis=0)
+    rows, cols = R.mx_gated_grad(dh, gu, act="gelu")
+    for dtype in (torch.bfloat16, torch.float32):
+        dx, dw = R.mx_gated_backward(dh, gu, w, x, act="gelu", dtype=dtype)
+        assert torch.equal(dx, R.mx_matmul(rows, w, dtype=dtype))
+        assert torch.equal(dw, R.mx_matmul(x, cols, dtype=dtype))
 
 
 def test_gradients_against_differences():
