@@ -146,15 +146,15 @@ def _output(out, rows: int, cols: int, dtype, device) -> torch.Tensor:
     return out
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    n = t.stride(0)
-    return n if n >= t.shape[1] else t.shape[1]  # a single row may have any stride
-
-
-def _unit_columns(t: torch.Tensor) -> torch.Tensor:
-    if (t.shape[1] == 1 or t.stride(1) == 1) and (t.shape[0] == 1 or t.stride(0) >= t.shape[1]):
-        return t
-    return t.contiguous()
+def _rows(t: torch.Tensor) -> tuple:
+    """(t or a copy of it with unit column stride and rows that do not overlap, its row stride)."""
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if step == 1 or cols == 1:
+        if ld >= cols:
+            return t, ld
+        if rows == 1:
+            return t, cols  # a single row may have any stride
+    return t.contiguous(), cols
 
 
 @functools.lru_cache(maxsize=4096)
@@ -162,14 +162,6 @@ def _workspace_bytes(name: str, *sizes) -> int:
     need = ctypes.c_size_t()
     L.check(getattr(L.load(), name)(*sizes, ctypes.byref(need)))
     return need.value
-
-
-def _workspace(need: int, device) -> tuple:
-    """(tensor, address, bytes) of a call's scratch, from the current stream's memory."""
-    if not need:
-        return None, None, 0
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    return ws, ws.data_ptr(), need
 
 
 def mx_quantize(x: torch.Tensor, axis: int | None = 1):
@@ -190,46 +182,59 @@ def mx_dequantize(t: MxTensor, dtype: torch.dtype = torch.bfloat16, out: torch.T
     """The values of an MxTensor as a [rows, cols] tensor (exact in float32 and bfloat16)."""
     _mx(t, "t")
     code = _dtype_code(dtype)
-    out = _output(out, t.rows, t.cols, dtype, t.device)
-    _call(L.load().svdq_mx_dequantize, out.device.index, *_parts(t), t.rows, t.cols, code, out.data_ptr(), _row_stride(out))
+    device = t.data.device
+    out = _output(out, t.rows, t.cols, dtype, device)
+    _call(L.load().svdq_mx_dequantize, device.index, *_parts(t), t.rows, t.cols, code, out.data_ptr(), _rows(out)[1])
     return out
 
 
-def _product(a, b, name_a: str, name_b: str, dtype, out, finish, *, gated: bool):
-    """The four products: `finish` gives (arguments between b's rows and the dtype, output columns, gu or None)
-    once a's rows, the dtype and the device are known."""
-    _mx(b, name_b)
+def _product(a, b, names, dtype, out, bias=None, act=None, save=False) -> tuple:
+    """(y or h, gu or None) of the four product calls: gated with an activation's code in `act`."""
+    _mx(b, names[1])
     raw = isinstance(a, torch.Tensor)
     if raw:
-        _matrix(a, name_a)
-        dtype = dtype or a.dtype
-        if dtype != a.dtype:
+        _matrix(a, names[0])
+        if dtype is None:
+            dtype = a.dtype
+        elif dtype != a.dtype:
             a, raw = mx_quantize(a), False
     else:
-        _mx(a, name_a)
+        _mx(a, names[0])
         dtype = dtype or torch.bfloat16
     code = _dtype_code(dtype)
-    M, K = a.shape
+    (M, K), device, gated = a.shape, a.device, act is not None
     if K != b.cols:
-        raise ValueError(f"{name_a} [{M}, {K}] and {name_b} [{b.rows}, {b.cols}] must share their second dimension")
-    device = a.device
-    _same_device(device, b)
-    lib = L.load()
-    extra, N, gu = finish(M, dtype, device)
+        raise ValueError(f"{names[0]} [{M}, {K}] and {names[1]} [{b.rows}, {b.cols}] must share their second dimension")
+    _same_device(device, b, bias)
+    N, extra, gu, at_gu = b.rows, act, None, None
+    if gated:
+        if N % 2:
+            raise ValueError(f"{names[1]} must hold as many up rows as gate rows")
+        N //= 2
+        if save:
+            gu = torch.empty(M, 2 * N, dtype=dtype, device=device)
+            at_gu = gu.data_ptr()
+    elif bias is not None:
+        if bias.dim() != 1 or bias.shape[0] != N or bias.dtype != dtype:
+            raise ValueError(f"bias must be a [{N}] tensor of the output's dtype")
+        bias = bias.contiguous()
+        extra = bias.data_ptr()
     y = _output(out, M, N, dtype, device)
-    tail = (code, y.data_ptr(), _row_stride(y)) + ((None if gu is None else gu.data_ptr(), 2 * N) if gated else ())
     if raw:
         sr, sc = a.stride()
-        if K == 1:
-            sc = 1
-        ws, *scratch = _workspace(_workspace_bytes("svdq_mx_linear_workspace_bytes", M, N, K, sc, gated), device)
-        _call(lib.svdq_mx_gated_linear if gated else lib.svdq_mx_linear, device.index, a.data_ptr(), M, K, sr, sc, *_parts(b), N,
-              extra, *tail, *scratch)
+        need = _workspace_bytes("svdq_mx_linear_workspace_bytes", M, N, K, 1 if K == 1 else sc, gated)
     else:
-        ws, *scratch = _workspace(_workspace_bytes("svdq_mx_workspace_bytes", M, N, K, gated), device)
-        _call(lib.svdq_mx_gated if gated else lib.svdq_mx_matmul, device.index, *_parts(a), M, *_parts(b), N, K, extra, *tail,
-              *scratch)
-    return y
+        need = _workspace_bytes("svdq_mx_workspace_bytes", M, N, K, gated)
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    tail = (y.data_ptr(), _rows(y)[1]) + ((at_gu, 2 * N) if gated else ()) + (ws.data_ptr() if need else None, need)
+    lib = L.load()
+    if raw:
+        _call(lib.svdq_mx_gated_linear if gated else lib.svdq_mx_linear, device.index, a.data_ptr(), M, K, sr,
+              1 if K == 1 else sc, *_parts(b), N, extra, code, *tail)
+    else:
+        _call(lib.svdq_mx_gated if gated else lib.svdq_mx_matmul, device.index, *_parts(a), M, *_parts(b), N, K, extra, code,
+              *tail)
+    return y, gu
 
 
 def mx_matmul(a, b: MxTensor, bias: torch.Tensor | None = None, dtype: torch.dtype | None = None,
@@ -237,18 +242,9 @@ def mx_matmul(a, b: MxTensor, bias: torch.Tensor | None = None, dtype: torch.dty
     """Y = A B^T (+ bias) [M, N] of a [M, K] and b [N, K]: MXFP4 products summed in float32, rounded once.
     a: an MxTensor, or a matrix, which is quantised along its rows. dtype: a matrix's own, else
     bfloat16. bias: [N] of that dtype. For a layer with weight [K, N], b = mx_quantize(weight, axis=0)."""
-
-    def finish(M, dt, device):
-        if bias is None:
-            return None, b.rows, None
-        if not isinstance(bias, torch.Tensor) or bias.dim() != 1 or bias.shape[0] != b.rows or bias.dtype != dt:
-            raise ValueError(f"bias must be a [{b.rows}] tensor of the output's dtype")
-        _same_device(device, bias)
-        held.append(bias.contiguous())
-        return held[0].data_ptr(), b.rows, None
-
-    held = []
-    return _product(a, b, "a", "b", dtype, out, finish, gated=False)
+    if bias is not None and not isinstance(bias, torch.Tensor):
+        raise TypeError("bias: expected a torch.Tensor")
+    return _product(a, b, ("a", "b"), dtype, out, bias=bias)[0]
 
 
 def mx_gated(x, w: MxTensor, act: str = "silu", dtype: torch.dtype | None = None, save: bool = False,
@@ -257,23 +253,13 @@ def mx_gated(x, w: MxTensor, act: str = "silu", dtype: torch.dtype | None = None
     [M, K], as in mx_matmul. w: [2F, K], the F gate rows, then the F up rows: mx_quantize(weight, axis=0) of
     the merged weight [K, 2F]. act: "silu", "gelu", "gelu_tanh" or "relu". With save=True also returns the
     pre-activations [M, 2F] (gate, then up), rounded to the dtype, for mx_gated_backward."""
-    code = _act_code(act)
-    gu = None
-
-    def finish(M, dt, device):
-        nonlocal gu
-        if w.rows % 2:
-            raise ValueError("w must hold as many up rows as gate rows")
-        if save:
-            gu = torch.empty((M, w.rows), dtype=dt, device=device)
-        return code, w.rows // 2, gu
-
-    h = _product(x, w, "x", "w", dtype, out, finish, gated=True)
+    h, gu = _product(x, w, ("x", "w"), dtype, out, act=_act_code(act), save=save)
     return (h, gu) if save else h
 
 
 def _pre_activations(dh, gu) -> tuple:
-    """(dtype code, M, F, device, dh, gu) of a backward call's gradient and saved pre-activations."""
+    """(dtype code, M, F, device, dh, its row stride, gu, its row stride) of a backward call's gradient and saved
+    pre-activations."""
     dt = _matrix(dh, "dh")
     _matrix(gu, "gu")
     M, F = dh.shape
@@ -281,17 +267,17 @@ def _pre_activations(dh, gu) -> tuple:
         raise ValueError(f"gu must be a [{M}, {2 * F}] tensor of dh's dtype")
     device = dh.device
     _same_device(device, gu)
-    return dt, M, F, device, _unit_columns(dh), _unit_columns(gu)
+    return dt, M, F, device, *_rows(dh), *_rows(gu)
 
 
 def mx_gated_grad(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu"):
     """The gradients d = [dg | du] of a gated block's pre-activations, dg = dh * u * act'(g) and
     du = dh * act(g), from dh [M, F] and gu [M, 2F]: Q(d) [M, 2F] and Q(d^T) [2F, M], from one pass."""
     code = _act_code(act)
-    dt, M, F, device, dh, gu = _pre_activations(dh, gu)
+    dt, M, F, device, dh, ldh, gu, ldgu = _pre_activations(dh, gu)
     rows, cols = MxTensor._empty(M, 2 * F, device), MxTensor._empty(2 * F, M, device)
-    _call(L.load().svdq_mx_gated_grad, device.index, dh.data_ptr(), _row_stride(dh), gu.data_ptr(), _row_stride(gu), M, F, code, dt,
-          *_parts(rows), *_parts(cols))
+    _call(L.load().svdq_mx_gated_grad, device.index, dh.data_ptr(), ldh, gu.data_ptr(), ldgu, M, F, code, dt, *_parts(rows),
+          *_parts(cols))
     return rows, cols
 
 
@@ -303,7 +289,7 @@ def mx_gated_backward(dh: torch.Tensor, gu: torch.Tensor, w_rows: MxTensor, x_co
     code = _act_code(act)
     _mx(w_rows, "w_rows")
     _mx(x_cols, "x_cols")
-    dt, M, F, device, dh, gu = _pre_activations(dh, gu)
+    dt, M, F, device, dh, ldh, gu, ldgu = _pre_activations(dh, gu)
     K = w_rows.rows
     if w_rows.cols != 2 * F or x_cols.cols != M or x_cols.rows != K:
         raise ValueError(f"w_rows must be [K, {2 * F}] and x_cols [K, {M}]")
@@ -312,7 +298,8 @@ def mx_gated_backward(dh: torch.Tensor, gu: torch.Tensor, w_rows: MxTensor, x_co
     out = _dtype_code(dtype)
     dx = torch.empty(M, K, dtype=dtype, device=device)
     dw = torch.empty(K, 2 * F, dtype=dtype, device=device)
-    ws, *scratch = _workspace(_workspace_bytes("svdq_mx_gated_backward_workspace_bytes", M, F, K), device)
-    _call(L.load().svdq_mx_gated_backward, device.index, dh.data_ptr(), _row_stride(dh), gu.data_ptr(), _row_stride(gu), M,
-          F, code, dt, *_parts(w_rows), *_parts(x_cols), K, out, dx.data_ptr(), K, dw.data_ptr(), 2 * F, *scratch)
+    need = _workspace_bytes("svdq_mx_gated_backward_workspace_bytes", M, F, K)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    _call(L.load().svdq_mx_gated_backward, device.index, dh.data_ptr(), ldh, gu.data_ptr(), ldgu, M, F, code, dt,
+          *_parts(w_rows), *_parts(x_cols), K, out, dx.data_ptr(), K, dw.data_ptr(), 2 * F, ws.data_ptr(), need)
     return dx, dw
