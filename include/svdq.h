@@ -344,8 +344,10 @@ int svdq_calibrate_scale(const void* x, int64_t B, int64_t M, int64_t ldx, const
  * padding rows are neither written nor read.
  *
  * dtype is SVDQ_F32, SVDQ_BF16 or SVDQ_F16 (the other calls of this header take no SVDQ_F16).
- * Sizes are 1 .. 2^30, and the arrays' sizes are what memory holds: offsets are 64-bit. The
- * calls keep no state; two calls on two streams are independent when their workspaces are.
+ * Sizes are 1 .. 2^30, and the arrays' sizes are what memory holds: offsets are 64-bit. (EINVAL where a
+ * launch would hold 2^32 threads, which takes 2^26 rows or 2^35 elements at least.) Outputs and the
+ * workspace must not overlap the inputs or each other. The calls keep no state; two calls on two streams
+ * are independent when their outputs and workspaces are.
  * ------------------------------------------------------------------------------------ */
 enum { SVDQ_F16 = 3 };
 typedef enum {
@@ -421,9 +423,9 @@ int svdq_mx_gated_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_
  *   codes / scales:     Q(d)   [M, 2F]  (times the weight quantised along 2F: dx)
  *   codes_t / scales_t: Q(d^T) [2F, M]  (with the input quantised along M: dw)
  * The codes are those of the formulas in binary64 on the given dh and gu (binary32, and
- * binary64 where that lies too near a border between two codes), except that a product
- * dh * u below 2^-120 or past 2^127 is rounded (or overflows) as float32 does. Either pair may
- * be NULL, not both.
+ * binary64 where that lies too near a border between two codes), except that dh * u and the gradients
+ * themselves are rounded as float32 does below a magnitude of 2^-120, and are infinite from 2^128 on.
+ * Either pair may be NULL, not both.
  * dh: [M, F] row stride ldh >= F; gu: [M, 2F] row stride ldgu >= 2F; both of dtype.
  * Errors: EINVAL, EDTYPE, EHIP.
  * ------------------------------------------------------------------------------------ */

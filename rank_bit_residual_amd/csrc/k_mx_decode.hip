@@ -211,12 +211,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_decode(MxGemmParams p) {
 
 using namespace dev;
 
-static unsigned runs(int64_t blocks) { return (unsigned)((blocks + 7) / 8 * 8); }
-
 template <class DT, int MT, int NT, int WAVES, bool GATED, int FORM>
 static hipError_t launch_rows(const MxGemmParams& p, hipStream_t stream) {
   const int64_t cols = GATED ? 16 : 16 * NT;
-  const dim3 grid(runs((p.N + cols - 1) / cols), (unsigned)((p.M + 16 * MT - 1) / (16 * MT)));
+  const int64_t blocks = ((p.N + cols - 1) / cols + 7) / 8 * 8;  // whole runs for each XCD
+  if (!mx_fits_grid(blocks, 64 * WAVES)) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, (unsigned)((p.M + 16 * MT - 1) / (16 * MT)));
   k_mx_decode<DT, MT, NT, WAVES, GATED, FORM><<<grid, 64 * WAVES, 0, stream>>>(p);
   return hipGetLastError();
 }

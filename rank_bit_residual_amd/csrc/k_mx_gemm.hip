@@ -478,7 +478,7 @@ static hipError_t launch_tile(const MxGemmParams& p, hipStream_t stream) {
   constexpr int COLS = GATED ? BN / 2 : BN;
   const int64_t tiles = (((int64_t)p.M + BM - 1) / BM) * (((int64_t)p.N + COLS - 1) / COLS) * p.splits;
   const int64_t blocks = (tiles + 7) / 8 * 8;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!mx_fits_grid(blocks, 64 * C::NWV)) return hipErrorInvalidConfiguration;
   // once per process and device; a second thread at most repeats the same call
   static std::atomic<uint64_t> configured;
   int dev = 0;

@@ -447,7 +447,7 @@ static hipError_t launch_quant(const MxQuantParams& p, hipStream_t stream) {
   constexpr int TH = 16 * NP;
   // a direction that is written covers its padding too
   const int64_t tc = ROWS ? p.rows.kq : tiles_of(p.C), tr = COLS ? (int64_t)p.cols.kq * (kTile / TH) : (p.R + TH - 1) / TH;
-  if (tc * tr > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!mx_fits_grid(tc * tr, 256)) return hipErrorInvalidConfiguration;
   k_mx_quantize<DT, NP, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 256, 0, stream>>>(p, (int)tc);
   return hipGetLastError();
 }
@@ -474,7 +474,7 @@ hipError_t launch_mx_quantize(const MxQuantParams& p0, int dtype, hipStream_t st
 
 hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t stream) {
   const int64_t st = tiles_of(p.K), blocks = (p.rows + 63) / 64 * st;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!mx_fits_grid(blocks, 256)) return hipErrorInvalidConfiguration;
   return with_dtype(dtype, [&](auto d) {
     k_mx_dequantize<decltype(d)><<<dim3((unsigned)blocks), 256, 0, stream>>>(p, (int)st);
     return hipGetLastError();
@@ -487,7 +487,7 @@ static hipError_t launch_grad_t(const MxGradParams& p, hipStream_t stream) {
   // Measured at 4096 rows, bf16, silu, both directions: 106 us for F = 12288 as pairs, 152 us for F = 12300.
   if (p.F % kMxBlock == 0) {
     const int64_t tc = (p.F + kGradCols - 1) / kGradCols;
-    if (tc * tr > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!mx_fits_grid(tc * tr, 256)) return hipErrorInvalidConfiguration;
     k_mx_gated_grad<DT, ACT, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 256, 0, stream>>>(p, (int)tc);
     return hipGetLastError();
   }
@@ -495,7 +495,7 @@ static hipError_t launch_grad_t(const MxGradParams& p, hipStream_t stream) {
   const int64_t tc = ROWS ? (int64_t)p.rows.kq * (kTile / kGradCols) : (2 * p.F + kGradCols - 1) / kGradCols;
   const int64_t below = p.F / kGradCols, pairs = tc - below > below ? tc - below : below;
   const int64_t blocks = (pairs * tr + 7) / 8 * 16;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!mx_fits_grid(blocks, 256)) return hipErrorInvalidConfiguration;
   k_mx_gated_grad_any<DT, ACT, ROWS, COLS><<<dim3((unsigned)blocks), 256, 0, stream>>>(p, (int)tc, (int)pairs);
   return hipGetLastError();
 }

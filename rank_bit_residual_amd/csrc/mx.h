@@ -80,6 +80,10 @@ struct MxGradParams {
   MxOut cols;  // 2F x M: the transpose
 };
 
+// A launch holds fewer than 2^32 threads along a dimension of its grid; a call past that is refused
+// (hipErrorInvalidConfiguration) before anything runs.
+inline bool mx_fits_grid(int64_t blocks, int threads) { return blocks < (int64_t)0x100000000 / threads; }
+
 hipError_t launch_mx_quantize(const MxQuantParams& p, int dtype, hipStream_t stream);
 hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t stream);
 hipError_t launch_mx_gated_grad(const MxGradParams& p, int dtype, hipStream_t stream);

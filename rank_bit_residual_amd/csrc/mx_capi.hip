@@ -14,6 +14,7 @@ constexpr int64_t kMaxMxDim = (int64_t)1 << 30;
 
 int hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return SVDQ_OK;
+  if (e == hipErrorInvalidConfiguration) return set_error(SVDQ_EINVAL, std::string(what) + ": more threads than a launch holds");
   return set_error(SVDQ_EHIP, std::string(what) + ": " + hipGetErrorString(e));
 }
 

@@ -136,13 +136,27 @@ def _parts(t) -> tuple:
     return at, at + t._at
 
 
-def _output(out, rows: int, cols: int, dtype, device) -> torch.Tensor:
+def _overlap(out: torch.Tensor, t: torch.Tensor) -> bool:
+    """Whether an element of t may lie in out (a checked output)."""
+    size, other = out.element_size(), t.element_size()
+    a, b = out.data_ptr(), t.data_ptr()
+    ld, cols = out.stride(0) * size, out.shape[1] * size
+    if a + (out.shape[0] - 1) * ld + cols <= b or b + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * other <= a:
+        return False
+    # columns beside the output's in the rows of one buffer
+    beside = t.dim() == 2 and t.stride(1) == 1 and t.stride(0) * other == ld
+    return not (beside and cols <= (b - a) % ld and (b - a) % ld + t.shape[1] * other <= ld)
+
+
+def _output(out, rows: int, cols: int, dtype, device, *inputs) -> torch.Tensor:
     if out is None:
         return torch.empty(rows, cols, dtype=dtype, device=device)
     if not isinstance(out, torch.Tensor) or out.shape != (rows, cols) or out.dtype != dtype or out.device != device:
         raise ValueError(f"out must be a [{rows}, {cols}] {dtype} tensor on {device}")
     if (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols):
         raise ValueError("out must have unit column stride and rows that do not overlap")
+    if any(t is not None and _overlap(out, t) for t in inputs):
+        raise ValueError("out must not overlap an input")
     return out
 
 
@@ -183,7 +197,7 @@ def mx_dequantize(t: MxTensor, dtype: torch.dtype = torch.bfloat16, out: torch.T
     _mx(t, "t")
     code = _dtype_code(dtype)
     device = t.data.device
-    out = _output(out, t.rows, t.cols, dtype, device)
+    out = _output(out, t.rows, t.cols, dtype, device, t.data)
     _call(L.load().svdq_mx_dequantize, device.index, *_parts(t), t.rows, t.cols, code, out.data_ptr(), _rows(out)[1])
     return out
 
@@ -219,7 +233,7 @@ def _product(a, b, names, dtype, out, bias=None, act=None, save=False) -> tuple:
             raise ValueError(f"bias must be a [{N}] tensor of the output's dtype")
         bias = bias.contiguous()
         extra = bias.data_ptr()
-    y = _output(out, M, N, dtype, device)
+    y = _output(out, M, N, dtype, device, a if raw else a.data, b.data, bias)
     if raw:
         sr, sc = a.stride()
         need = _workspace_bytes("svdq_mx_linear_workspace_bytes", M, N, K, 1 if K == 1 else sc, gated)

@@ -199,7 +199,43 @@ def test_workspace_query():
     _refused(EINVAL, lib.svdq_mx_linear_workspace_bytes(4, 0, 4, 1, 0, ctypes.byref(n)))
 
 
+def test_launches_past_the_grid_are_refused():
+    """2^32 threads along a dimension of a grid: refused before anything is launched."""
+    lib, big = _lib.load(), 1 << 30
+    _refused(EINVAL, lib.svdq_mx_quantize(A, big, 4, 4, 1, BF16, A, A, None, None, None))
+    _refused(EINVAL, lib.svdq_mx_quantize(A, 4, big, 1, 4, BF16, None, None, A, A, None))
+    _refused(EINVAL, lib.svdq_mx_dequantize(A, A, big, 4, BF16, A, 4, None))
+    _refused(EINVAL, lib.svdq_mx_gated_grad(A, 1, A, 2, big, 1, 0, BF16, A, A, A, A, None))
+    _refused(EINVAL, lib.svdq_mx_gated_grad(A, 32, A, 64, big, 32, 0, BF16, A, A, A, A, None))
+    _refused(EINVAL, lib.svdq_mx_matmul(A, A, big, A, A, 4, 64, None, BF16, A, 4, None, 0, None))
+    _refused(EINVAL, lib.svdq_mx_matmul(A, A, 1, A, A, big, 64, None, BF16, A, big, None, 0, None))
+
+
 # ----------------------------------------------------------------------------- binding
+@pytest.mark.parametrize("out,x,want", [
+    ((0, 4, 8, 8), (32, 4, 8, 8), False),  # (offset, rows, columns, row stride)
+    ((0, 4, 8, 8), (31, 4, 8, 8), True),
+    ((40, 4, 8, 8), (8, 4, 8, 8), False),
+    ((40, 4, 8, 8), (9, 4, 8, 8), True),
+    ((0, 4, 8, 8), (0, 4, 8, 8), True),
+    ((0, 4, 8, 16), (8, 4, 8, 16), False),  # beside it in one buffer
+    ((8, 4, 8, 16), (0, 4, 8, 16), False),
+    ((0, 4, 8, 16), (7, 4, 8, 16), True),
+    ((0, 4, 8, 16), (8, 4, 9, 16), True),
+    ((8, 4, 8, 16), (24, 2, 8, 16), True),
+    ((0, 4, 8, 16), (10, 4, 4, 12), True),  # other strides: taken to overlap
+    ((5, 1, 8, 8), (12, 1, 1, 1), True),
+    ((5, 1, 8, 8), (13, 1, 1, 1), False),
+])
+def test_overlap(out, x, want):
+    from rank_bit_residual_amd import mx
+
+    buf = torch.zeros(200)
+    out, x = (torch.as_strided(buf, (r, c), (ld, 1), at) for at, r, c, ld in (out, x))
+    assert mx._overlap(out, x) is want
+    assert not mx._overlap(out, torch.zeros(4, 8)) and not mx._overlap(out, torch.zeros(8))
+
+
 def _fake(rows, cols, short=0):
     _, a, b = _layout(rows, cols)
     return R.MxTensor(torch.zeros(a + b - short, dtype=torch.uint8), rows, cols)

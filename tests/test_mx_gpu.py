@@ -4,6 +4,8 @@ Codes, scale bytes and dequantised values must be equal. Products: every term is
 sum of K terms in any order is off by at most K steps of 2^-23 of the sum of the terms' sizes (a matrix
 core may cut off instead of rounding); the output adds half a step of its type.
 """
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -559,6 +561,46 @@ def test_captured_and_replayed(M):
             assert all(torch.equal(a, b) for a, b in zip(want, out)), k
 
 
+FIRST_CALL = """
+import torch, rank_bit_residual_amd as R
+g = torch.Generator(device="cuda").manual_seed(3)
+x, w = (torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16) for s in ((100, 512), (512, 192)))
+dh = torch.randn(100, 96, generator=g, device="cuda", dtype=torch.bfloat16)
+def step():
+    xr, xc = R.mx_quantize(x, axis=None)
+    wr, wc = R.mx_quantize(w, axis=None)
+    h, gu = R.mx_gated(xr, wc, save=True)
+    return h, *R.mx_gated_backward(dh, gu, wr, xc), R.mx_matmul(x[:1], wc)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+for k in range(3):
+    x.mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, step())), k
+print("same")
+"""
+
+
+def test_first_call_of_a_process_captured():
+    import subprocess
+    import sys
+
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=100,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+def test_output_beside_the_input():
+    """Input and output as columns of one buffer."""
+    buf = torch.randn(100, 64 + 40, device=dev(), dtype=torch.bfloat16)
+    b = R.mx_quantize(torch.randn(40, 64, device=dev()))
+    want = R.mx_matmul(buf[:, :64], b)
+    assert torch.equal(R.mx_matmul(buf[:, :64], b, out=buf[:, 64:]), want) and torch.equal(buf[:, 64:], want)
+
+
 # ----------------------------------------------------------------------------- refusals that need device tensors
 def test_binding_refusals():
     d = dev()
@@ -579,6 +621,9 @@ def test_binding_refusals():
                  lambda: R.mx_matmul(x, t, out=torch.zeros(4, 4, device=d).t()),
                  lambda: R.mx_matmul(x, t, out=torch.zeros(1, 4, device=d).expand(4, 4)),
                  lambda: R.mx_matmul(x, t, out=torch.zeros(4, 4, device=d, dtype=torch.bfloat16)),
+                 lambda: R.mx_matmul(x, R.mx_quantize(torch.randn(64, 64, device=d)), out=x),
+                 lambda: R.mx_dequantize(t, torch.bfloat16, out=t.data[:512].view(torch.bfloat16).view(4, 64)),
+                 lambda: R.mx_matmul(x, R.MxTensor(torch.zeros(1 << 14, dtype=torch.uint8, device=d)[16:], 4, 64)),
                  lambda: R.mx_gated(x, R.mx_quantize(x[:3])), lambda: R.mx_gated(x[:, :60], t),
                  lambda: R.mx_gated(x, t, act="tanh"), lambda: R.mx_gated_grad(x, x),
                  lambda: R.mx_gated_grad(x, torch.zeros(4, 128, device=d, dtype=torch.float16)),
