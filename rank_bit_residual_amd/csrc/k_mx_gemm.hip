@@ -430,6 +430,8 @@ struct MxPlan {
 //             another, 0.33 us each
 //   128 x 128 two blocks per compute unit; 13 us for up to 256 tiles at kq = 32, 21 for 64 stages, 114 us for 3072 tiles
 //   128 x 256 one block: 16.5 us for 32 tiles to 21 for 256, 109 us for 1536
+//             shares of K run 7 % faster a stage (an XCD's blocks read the same one): 1024 x 65536 x 1024 in 8 shares 48 us, 52 with
+//             operands from HBM; 128 x 128 in 4 shares 51 and 62, in 8 shares 51 and 57
 //   256 x 256 one block: 23.5 us for 64 tiles, 29 for 192, 35 for 256, 94 for 768; 231 us for 1024 at kq = 64
 // Shares of K add the joining launch and the parts' way through memory at 4 TB/s.
 static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
@@ -455,7 +457,7 @@ static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
       if (c == 0)
         t = 4 + 0.29 * st * (rounds > 1 ? rounds : 1);
       else if (c == 1)
-        t = (whole + (rest > 0)) * (4 + 0.45 * st);
+        t = (whole + (rest > 0)) * (4 + (s > 1 ? 0.42 : 0.45) * st);
       else
         t = whole * (6 + 0.8 * st) + (rest > 0 ? 6 + st * (0.5 + 0.3 * rest) : 0);
       if (s > 1) t += 3.0 + (double)M * b_rows * 4 * 2 * s / 4e6;
