@@ -1,6 +1,6 @@
 // Products of MXFP4 tensors for few rows (decode steps): Y = D(A B^T + bias) and the gated projections, bound by
-// reading b once for each 64 rows of A. 16 rows against 8192 x 8192 take 7.7 us (35.7 MB at 4.6 TB/s), one row against
-// 24576 x 4096 12.3 us, quantised on the way.
+// reading b once for each 64 rows of A. 16 rows against 8192 x 8192 take 8.0 us (35.7 MB at 4.5 TB/s), one row against
+// 24576 x 4096 10.7 us (53.5 MB at 5.0 TB/s), quantised on the way.
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 rows of A against 16 rows of b, a stage of 128 codes at a
 // time; lane (i, g) holds block g of row i of either. A block of waves owns 16 or 32 output columns (gated: the

@@ -44,9 +44,9 @@ struct MxDequantParams {
 };
 
 // Whether the decode kernel quantises A itself: one row, or few rows and few columns to do it again for. Measured on
-// the GPU's clock as one launch against two (quantise, product), K = 4096 unless said: 1 row x 24576 columns 12.3 us
-// against 14.3; 4 x 8192 (K = 8192) 9.3 against 10.3, 8 rows 10.5 against 10.3; 8 x 4096 6.2 against 6.5, 16 rows 7.5 against
-// 6.6; 16 x 1024 (K = 1024) 3.4 against 4.7.
+// the GPU's clock as one launch against two (quantise, product), K = 4096 unless said: 1 row x 24576 columns 10.7 us
+// against 14.0; 4 x 8192 (K = 8192) 8.9 against 10.2, 8 rows 10.4 against 10.2; 8 x 4096 6.1 against 6.4, 16 rows 6.4 against
+// 6.5; 16 x 1024 (K = 1024) 3.4 against 4.8.
 inline bool mx_raw_rows(int64_t M, int64_t b_rows, int64_t sc) {
   return sc == 1 && (M == 1 || (M <= 16 && M * b_rows <= 32768));
 }
