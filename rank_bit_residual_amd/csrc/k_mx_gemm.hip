@@ -375,17 +375,17 @@ __global__ __launch_bounds__(256) void k_mx_join(MxGemmParams p) {
   for (int64_t r = blockIdx.y; r < p.M; r += gridDim.y) {
     const float* src = p.part + r * p.b_rows + c;
     vec a = {}, b = {};
-    // four parts requested at a time, added in order
-    for (int s = 0; s < p.splits; s += 4) {
-      vec x[4], z[4];
+    // eight parts requested at a time, added in order (64 x 64 outputs of 64 parts, with the product's kernel: 13.9 us, 16.9 with four)
+    for (int s = 0; s < p.splits; s += 8) {
+      vec x[8], z[8];
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
+      for (int k = 0; k < 8; k++) {
         const int at = s + k < p.splits ? s + k : p.splits - 1;
         x[k] = *reinterpret_cast<const vec*>(src + at * stride);
         if (GATED) z[k] = *reinterpret_cast<const vec*>(src + at * stride + p.N);
       }
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
+      for (int k = 0; k < 8; k++) {
         if (s + k >= p.splits) continue;
         a += x[k];
         if (GATED) b += z[k];
