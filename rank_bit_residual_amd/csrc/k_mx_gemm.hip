@@ -428,7 +428,7 @@ struct MxPlan {
 //   few rows  (k_mx_decode) b is read again for each 64 rows; with b's elements in millions, up to 32 rows 2.5 us at 1, 3.3
 //             to 4 at 17, 7.9 at 67; 64 rows 3.2, 5.2 and 10.1, 128 rows 3.2, 9.0 and 17.8; a wave's stages come after one
 //             another, 0.33 us each
-//   128 x 128 two blocks per compute unit; 13 us for up to 256 tiles at kq = 32, 21 for 64 stages, 114 us for 3072 tiles
+//   128 x 128 two blocks per compute unit; 13 us for up to 256 tiles at kq = 32, 21 for 64 stages, 114 us for 12 tiles a unit
 //   128 x 256 one block: 16.5 us for 32 tiles to 21 for 256, 109 us for 1536
 //             shares of K run 7 % faster a stage (an XCD's blocks read the same one): 1024 x 65536 x 1024 in 8 shares 48 us, 52 with
 //             operands from HBM; 128 x 128 in 4 shares 51 and 62, in 8 shares 51 and 57
