@@ -427,17 +427,20 @@ struct MxPlan {
 // The form with the least estimated time in us, from the times measured on this chip (K = 4096 is kq = 32 stages of 128):
 //   few rows  (k_mx_decode) b is read again for each 64 rows; with b's elements in millions, up to 32 rows 2.5 us at 1, 3.3
 //             to 4 at 17, 7.9 at 67; 64 rows 3.2, 5.2 and 10.1, 128 rows 3.2, 9.0 and 17.8; a wave's stages come after one
-//             another, 0.33 us each
+//             another, 0.33 us each. Small b, many rows, us for each 64 of them: 0.29 (1000 columns, K = 512), 0.46 (1000, 1024),
+//             0.79 (1500, 1536), 1.9 (5000, 768)
 //   128 x 128 two blocks per compute unit; 13 us for up to 256 tiles at kq = 32, 21 for 64 stages, 114 us for 12 tiles a unit
 //   128 x 256 one block: 16.5 us for 32 tiles to 21 for 256, 109 us for 1536
 //             shares of K run 7 % faster a stage (an XCD's blocks read the same one): 1024 x 65536 x 1024 in 8 shares 48 us, 52 with
 //             operands from HBM; 128 x 128 in 4 shares 51 and 62, in 8 shares 51 and 57
 //   256 x 256 one block: 23.5 us for 64 tiles, 29 for 192, 35 for 256, 94 for 768; 231 us for 1024 at kq = 64
+// A gated product's tiles leave as one to three arrays: 500 x 300 x 2*700 5.4 us, 7.7 with g and u (few rows 5.7 and 6.1); 2048 x 2048 x
+// 2*8192 39.9 us on 256 x 256 against 45.4 on 128 x 128.
 // Shares of K add the joining launch and the parts' way through memory at 4 TB/s.
 static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
   const double b_rows = (double)N * (gated ? 2 : 1), millions = b_rows * kq * 128 * 1e-6;
   MxPlan best{0, 0, 1};
-  double few = 0.25 * millions;
+  double few = 0.25 * millions + 0.17e-3 * b_rows;
   if (few > 1.6 + 0.11 * millions) few = 1.6 + 0.11 * millions;
   double best_t = M <= 32 ? 2.2 + 0.082 * millions : 3.0 + (double)((M + 63) / 64) * few;
   if (M > 64 * 65535) best_t = 1e30;  // past the grid's second dimension
@@ -460,6 +463,7 @@ static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
         t = (whole + (rest > 0)) * (4 + (s > 1 ? 0.42 : 0.45) * st);
       else
         t = whole * (6 + 0.8 * st) + (rest > 0 ? 6 + st * (0.5 + 0.3 * rest) : 0);
+      if (gated && s == 1) t += c == 0 ? 2 : (c == 1 ? 3 : 2) * (whole + (rest > 0));
       if (s > 1) t += 3.0 + (double)M * b_rows * 4 * 2 * s / 4e6;
       if (t < best_t) best = MxPlan{bm, cand[c][1], s}, best_t = t;
     }
