@@ -238,7 +238,7 @@ def _gen(seed):
 @pytest.mark.parametrize("M,K,N", [(1, 1024, 8200), (1, 4097, 100), (3, 4097, 100), (16, 65536, 20), (17, 520, 9000),
                                    (40, 512, 9001), (64, 65536, 64), (70, 8192, 8192), (97, 40000, 300), (130, 40000, 301),
                                    (200, 1030, 3000), (300, 4096, 5000), (513, 4096, 12290), (2000, 1030, 4090),
-                                   (1030, 4096, 12300)])
+                                   (1030, 4096, 12300), (1, 32768, 1300), (33, 128, 8192), (300, 128, 20000), (700, 65536, 1300)])
 def test_every_form_of_the_product(M, K, N):
     """Sums of multiples of 1/4 below 2^22 (65536 * 36): one value in float32 whatever the order."""
     gen = _gen(M + K + N)
@@ -255,7 +255,8 @@ def test_every_form_of_the_product(M, K, N):
 
 @pytest.mark.parametrize("save", [False, True])
 @pytest.mark.parametrize("M,K,F", [(1, 4096, 600), (1, 1023, 9000), (5, 520, 333), (33, 33000, 40), (130, 33000, 151), (200, 1030, 3001),
-                                   (300, 4096, 6000), (500, 2048, 12290), (1500, 512, 2050)])
+                                   (300, 4096, 6000), (500, 2048, 12290), (1500, 512, 2050), (1, 65536, 300), (100, 128, 4096),
+                                   (400, 1024, 8192), (700, 65536, 700), (3000, 1024, 2500)])
 def test_every_form_of_the_gated_product(M, K, F, save):
     gen = _gen(M + K + F)
     x, w = _on_grid(gen, M, K) / 64, _on_grid(gen, 2 * F, K) / 64
