@@ -166,8 +166,9 @@ template <int ACT, class F>
 __device__ inline ActValue<F> act_value(F g) {
   ActValue<F> r;
   if constexpr (ACT == SVDQ_ACT_RELU) {
-    r.a = g < F(0) ? F(0) : g;
-    r.d = g > F(0) ? F(1) : (g == g ? F(0) : g);
+    const F none = g == g ? F(0) : g;  // +0 for either zero, NaN for a NaN
+    r.a = g > F(0) ? g : none;
+    r.d = g > F(0) ? F(1) : none;
     r.ew = 0x1p-22f;
     r.abs_d = (float)r.d * 0x1p-22f;
     r.tail = 0.f;

@@ -421,6 +421,19 @@ def test_gated_grad_not_finite():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_relu_of_a_negative_zero(dtype):
+    """max(-0, 0) is +0: the gradients are zeros with dh's sign, codes and all."""
+    dh = np.where(np.arange(96 * 40).reshape(40, 96) % 3 == 0, -1.5, 1.5)
+    gu = np.full((40, 192), -0.0)
+    gu[:, 96:] = 2.0
+    d, z = _gpu(dh, dtype), _gpu(gu, dtype)
+    want = np.concatenate([dh * 2.0 * 0.0, dh * 0.0], axis=1)
+    rows, cols = R.mx_gated_grad(d, z, act="relu")
+    _check_tensor(rows, want)
+    _check_tensor(cols, want.T)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M,K,F", [(5, 40, 33), (70, 256, 64), (130, 300, 100)])
 def test_training_step_together(dtype, M, K, F):
     """The operators as a training step uses them, against the formulas on the same inputs."""
