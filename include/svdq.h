@@ -424,7 +424,8 @@ int svdq_mx_gated_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_
  *   codes_t / scales_t: Q(d^T) [2F, M]  (with the input quantised along M: dw)
  * The codes are those of the formulas in binary64 on the given dh and gu (binary32, and
  * binary64 where that lies too near a border between two codes), except that dh * u and the gradients
- * themselves are rounded as float32 does below a magnitude of 2^-120, and are infinite from 2^128 on.
+ * themselves are rounded as float32 does below a magnitude of 2^-120, and that a gradient (not dh * u) is
+ * infinite from 2^128 on.
  * Either pair may be NULL, not both.
  * dh: [M, F] row stride ldh >= F; gu: [M, 2F] row stride ldgu >= 2F; both of dtype.
  * Errors: EINVAL, EDTYPE, EHIP.

@@ -220,6 +220,12 @@ __device__ __forceinline__ u32 ends_differ(float v, float err) {
   const float a = fabsf(v);
   return __float_as_uint(a - err) ^ __float_as_uint(a + err);
 }
+// The same where v may be a NaN although the formula's value is finite (an infinite dh * u times a derivative of 0): never
+// settled, since the larger of a NaN and 0 is 0.
+__device__ __forceinline__ u32 ends_differ_or_nan(float v, float err) {
+  const float a = fabsf(v);
+  return __float_as_uint(a - err) ^ __float_as_uint(fmaxf(a + err, 0.f));
+}
 
 // The 16 bits for a binary64 gradient (from infinity on, any of those mark a block).
 __device__ inline u32 to_odd16(double v) {
@@ -289,7 +295,7 @@ __device__ __forceinline__ void grad8(const GradIn<DT>& x, Vec8<MxBF16>& dg, Vec
       if (GATE) {
         const float a = dh * elem<DT>(x.u, 2 * h + k);
         vg[k] = a * r.d;
-        differ[h] |= ends_differ(vg[k], fabsf(a) * r.abs_d);
+        differ[h] |= ends_differ_or_nan(vg[k], fabsf(a) * r.abs_d);
       }
       if (UP) {
         vu[k] = dh * r.a;

@@ -433,6 +433,32 @@ def test_relu_of_a_negative_zero(dtype):
     _check_tensor(cols, want.T)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", X.ACTS)
+@pytest.mark.parametrize("F", [64, 70])
+def test_gated_grad_of_an_overflowing_product(dtype, act, F):
+    """dh * u past the float32 range where act' brings the gradient back: below relu's zero, beside the zeros of the
+    other derivatives, and far out on their tails. The formula's gradient is finite there, and small or zero."""
+    rng = np.random.default_rng(F)
+    dh = rng.standard_normal((40, F))
+    gu = rng.standard_normal((40, 2 * F))
+    big = np.zeros((40, F), bool)
+    big[2, 7] = big[9, 33:40] = big[33, F - 1] = big[39, 0] = True
+    big[:, 50] = True
+    dh[big] = 1.5e30 * rng.choice([-1, 1], big.sum())
+    gu[:, F:][big] = 1e10
+    root = {"silu": -1.2784645427610738, "gelu": -0.7517915246935645, "gelu_tanh": -0.7524614220710163, "relu": -0.0}[act]
+    gu[:, :F][big] = root - rng.integers(0, 5, big.sum()) * 2.0**-23
+    far = {"silu": -55.0, "gelu": -9.0, "gelu_tanh": -8.0, "relu": -1.0}[act]
+    gu[:, 5], dh[:, 5], gu[:, F + 5] = far, 1.5e30, 1e10
+    d, z = _gpu(dh, dtype), _gpu(gu, dtype)
+    want = X.gated_grad(_np(d), _np(z), act)
+    assert np.abs(want).max() < 2.0**127
+    rows, cols = R.mx_gated_grad(d, z, act=act)
+    _check_tensor(rows, want)
+    _check_tensor(cols, want.T)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M,K,F", [(5, 40, 33), (70, 256, 64), (130, 300, 100)])
 def test_training_step_together(dtype, M, K, F):
