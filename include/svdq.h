@@ -381,6 +381,12 @@ int svdq_mx_dequantize(const void* codes, const void* scales, int64_t rows, int6
  * in time need one each. Errors: EINVAL. */
 int svdq_mx_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated, size_t* bytes_out);
 
+/* The form that these calls take (host query, a measurement aid): form[0] x form[1] is the tile of a block, rows of a by
+ * rows of b (gated: half gate rows, half up rows); form[2] the shares of K over blocks (1: one kernel, no
+ * workspace); form[3] the shares of K over the waves of a block (1: the tile kernel, more: the kernel for few
+ * rows). Errors: EINVAL. */
+int svdq_mx_product_form(int64_t M, int64_t N, int64_t K, int gated, int form[4]);
+
 /* --------------------------------------------------------------------------------------
  * svdq_mx_matmul — Y = D( A B^T + bias ) of two MXFP4 tensors a [M, K] and b [N, K]: block-scaled
  * FP4 matrix cores, float32 sums, one rounding to dtype. bias: [N] of dtype, or NULL.

@@ -52,6 +52,7 @@ SIGNATURES = {
     "svdq_mx_quantize": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "svdq_mx_dequantize": (c_int, [c_vp, c_vp, c_i64, c_i64, c_int, c_vp, c_i64, c_vp]),
     "svdq_mx_workspace_bytes": (c_int, [c_i64, c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]),
+    "svdq_mx_product_form": (c_int, [c_i64, c_i64, c_i64, c_int, ctypes.POINTER(c_int)]),
     "svdq_mx_matmul": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_vp, c_i64, c_vp, c_sz,
                                c_vp]),
     "svdq_mx_gated": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_vp, c_i64, c_vp, c_i64,

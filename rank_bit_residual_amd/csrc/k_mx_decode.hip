@@ -221,27 +221,44 @@ static hipError_t launch_rows(const MxGemmParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Column tiles and waves of a block: one tile and eight waves up to 8191 columns (a block for every compute unit matters
-// most), two tiles for 8192, and past that, for up to 32 rows, one tile and four waves, so that all blocks are on the chip
-// at once. 16 rows, K = 4096, 12288 columns: 6.6 us against 7.9 with
-// two tiles and eight waves; 64 rows 11.2 against 10.8.
+// Column tiles and waves of a block (MxForm: bn = 16 column tiles, waves). A gated block has a gate tile and an up tile.
+// Others, by the column tiles there are on 256 compute units; measured on the GPU's clock, us:
+//   up to 256    one tile, eight waves: a block for every compute unit matters most. 8192 x 4096 at one row 5.8, 6.2 with two
+//   257 to 512   two tiles, so that a compute unit's blocks are one: 8192 x 5120 at 16 rows 7.7 against 8.7, 8192 x 8192 8.9
+//                against 9.7 (1024 x 6000 3.4 both)
+//   more         past 16 rows two tiles, so that a's operands serve twice: 8192 x 16384 at 32 rows 17.2, 22.7 with one tile,
+//                at 64 rows 23.4 and 34.6. Up to 16 rows one tile; with four waves below 64 stages, so that more blocks run at
+//                once (1024 x 16384 at one row 3.9, 4.5 with eight waves, 4096 x 12288 7.6 and 8.5, 7168 x 12288 10.9 and
+//                11.9), with eight from there on, where the waves' own chains of stages count (8192 x 16384 16.4, 21.1 with
+//                four, 16384 x 16384 28.9 and 31.0, 28672 x 9216 32.0 and 31.8)
+MxForm mx_decode_form(int64_t M, int64_t N, int kq, bool gated) {
+  const int bm = M <= 16 ? 16 : (M <= 32 ? 32 : 64);
+  if (gated) return MxForm{bm, 32, 1, 8};
+  const int64_t tiles = (N + 15) / 16;
+  if (tiles <= 256) return MxForm{bm, 16, 1, 8};
+  if (tiles <= 512 || bm > 16) return MxForm{bm, 32, 1, 8};
+  return MxForm{bm, 16, 1, kq < 64 ? 4 : 8};
+}
+
 template <class DT, int MT, int FORM>
 static hipError_t launch_cols(const MxGemmParams& p, bool gated, hipStream_t stream) {
   if (gated) return launch_rows<DT, MT, 2, 8, true, FORM>(p, stream);
-  const int64_t cols16 = ((int64_t)p.N + 15) / 16;
-  if (cols16 < 512) return launch_rows<DT, MT, 1, 8, false, FORM>(p, stream);
-  if constexpr (MT <= 2) {
-    if (cols16 > 512) return launch_rows<DT, MT, 1, 4, false, FORM>(p, stream);
+  const MxForm f = mx_decode_form(p.M, p.N, p.kq, false);
+  if (f.bn == 32) return launch_rows<DT, MT, 2, 8, false, FORM>(p, stream);
+  if constexpr (MT == 1) {
+    if (f.waves == 4) return launch_rows<DT, MT, 1, 4, false, FORM>(p, stream);
   }
-  return launch_rows<DT, MT, 2, 8, false, FORM>(p, stream);
+  return launch_rows<DT, MT, 1, 8, false, FORM>(p, stream);
 }
 
 template <class DT>
 static hipError_t launch_decode_t(const MxGemmParams& p, bool gated, hipStream_t stream) {
   if (p.x) return p.M == 1 ? launch_cols<DT, 1, X_ONE>(p, gated, stream) : launch_cols<DT, 1, X_ROWS>(p, gated, stream);
-  if (p.M <= 16) return launch_cols<DT, 1, A_CODES>(p, gated, stream);
-  if (p.M <= 32) return launch_cols<DT, 2, A_CODES>(p, gated, stream);
-  return launch_cols<DT, 4, A_CODES>(p, gated, stream);
+  switch (mx_decode_form(p.M, p.N, p.kq, gated).bm) {
+    case 16: return launch_cols<DT, 1, A_CODES>(p, gated, stream);
+    case 32: return launch_cols<DT, 2, A_CODES>(p, gated, stream);
+    default: return launch_cols<DT, 4, A_CODES>(p, gated, stream);
+  }
 }
 
 hipError_t launch_mx_decode(const MxGemmParams& p, bool gated, int dtype, hipStream_t stream) {

@@ -471,6 +471,11 @@ static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
   return best;
 }
 
+MxForm mx_product_form(int64_t M, int64_t N, int kq, bool gated) {
+  const MxPlan pl = plan_of(M, N, kq, gated);
+  return pl.bm ? MxForm{pl.bm, pl.bn, pl.splits, 1} : mx_decode_form(M, N, kq, gated);
+}
+
 bool mx_product_decodes(int64_t M, int64_t N, int kq, bool gated) { return plan_of(M, N, kq, gated).bm == 0; }
 
 size_t mx_product_part_bytes(int64_t M, int64_t N, int kq, bool gated) {

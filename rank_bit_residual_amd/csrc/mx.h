@@ -87,7 +87,16 @@ inline bool mx_fits_grid(int64_t blocks, int threads) { return blocks < (int64_t
 hipError_t launch_mx_quantize(const MxQuantParams& p, int dtype, hipStream_t stream);
 hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t stream);
 hipError_t launch_mx_gated_grad(const MxGradParams& p, int dtype, hipStream_t stream);
-// Whether the product's launch is the kernel for few rows (the only one that takes an unquantised A).
+// How a product is cut: output tiles of bm x bn (rows of a by rows of b: a gated tile holds half gate rows, half up rows),
+// K in `splits` shares over blocks, which a second kernel joins, and in `waves` shares over the waves of a block, which are
+// joined in LDS (1: the tile kernels).
+struct MxForm {
+  int bm, bn, splits, waves;
+};
+MxForm mx_product_form(int64_t M, int64_t N, int kq, bool gated);
+// The block shape of the kernel for few rows.
+MxForm mx_decode_form(int64_t M, int64_t N, int kq, bool gated);
+// Whether the product's launch is that kernel (the only one that takes an unquantised A).
 bool mx_product_decodes(int64_t M, int64_t N, int kq, bool gated);
 // Bytes of float32 parts that the product's launch writes and reads (0: K is not split).
 size_t mx_product_part_bytes(int64_t M, int64_t N, int kq, bool gated);

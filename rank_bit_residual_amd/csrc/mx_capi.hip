@@ -217,6 +217,19 @@ int svdq_mx_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated, size_t* 
   return SVDQ_OK;
 }
 
+int svdq_mx_product_form(int64_t M, int64_t N, int64_t K, int gated, int form[4]) {
+  size_t bytes;
+  const int st = svdq_mx_workspace_bytes(M, N, K, gated, &bytes);
+  if (st) return st;
+  if (!form) return set_error(SVDQ_EINVAL, "form is NULL");
+  const MxForm f = mx_product_form(M, N, (int)mx_kq(K), gated != 0);
+  form[0] = f.bm;
+  form[1] = f.bn;
+  form[2] = f.splits;
+  form[3] = f.waves;
+  return SVDQ_OK;
+}
+
 int svdq_mx_matmul(const void* a_codes, const void* a_scales, int64_t M, const void* b_codes, const void* b_scales,
                    int64_t N, int64_t K, const void* bias, int dtype, void* y, int64_t ldy, void* workspace,
                    size_t workspace_bytes, svdq_stream_t stream) {

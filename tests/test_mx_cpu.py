@@ -211,6 +211,34 @@ def test_launches_past_the_grid_are_refused():
     _refused(EINVAL, lib.svdq_mx_matmul(A, A, 1, A, A, big, 64, None, BF16, A, big, None, 0, None))
 
 
+def _form(M, N, K, gated=0):
+    got = (ctypes.c_int * 4)()
+    assert _lib.load().svdq_mx_product_form(M, N, K, gated, got) == 0
+    return tuple(got)
+
+
+def test_product_form_query():
+    lib, got = _lib.load(), (ctypes.c_int * 4)()
+    for bad in ((0, 4, 4, 0), (4, 0, 4, 0), (4, 4, 0, 0), (4, 1 << 30, 4, 1), (4, 4, (1 << 27) + 1, 0)):
+        _refused(EINVAL, lib.svdq_mx_product_form(*bad, got))
+    _refused(EINVAL, lib.svdq_mx_product_form(4, 4, 4, 0, None))
+    n = ctypes.c_size_t()
+    for M, N, K, gated in ((1, 100, 512, 0), (300, 5000, 4096, 1), (1024, 1024, 65536, 0), (130, 151, 33000, 1)):
+        bm, bn, splits, waves = _form(M, N, K, gated)
+        assert lib.svdq_mx_workspace_bytes(M, N, K, gated, ctypes.byref(n)) == 0
+        assert n.value == (splits * M * N * (2 if gated else 1) * 4 if splits > 1 else 0)
+        assert (waves == 1) == (bm >= 128) and bn % 16 == 0
+
+
+@pytest.mark.parametrize("M", [1, 16, 32, 64])
+@pytest.mark.parametrize("K", [512, 8192])
+def test_few_row_blocks_change_with_the_tiles_a_compute_unit_gets(M, K):
+    """The block shape is one over each range of column tiles: up to 256, to 512, and more; no width has its own."""
+    for widths in ((16, 1000, 4080, 4096), (4097, 5000, 8000, 8176, 8177, 8192), (8193, 8208, 9000, 16384, 16400)):
+        forms = {f for f in (_form(M, n, K) for n in widths) if f[3] > 1}
+        assert len(forms) <= 1, forms
+
+
 # ----------------------------------------------------------------------------- binding
 @pytest.mark.parametrize("out,x,want", [
     ((0, 4, 8, 8), (32, 4, 8, 8), False),  # (offset, rows, columns, row stride)

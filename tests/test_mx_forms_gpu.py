@@ -1,0 +1,63 @@
+"""Every kernel form of the MXFP4 products on an MI355X, with the form asserted before it is run.
+
+Operands are codes of blocks whose largest is 6, so they are their own Q, and every partial sum is a multiple of 1/4 below
+2^22 (36 K <= 2^22): one value in float32, whatever the order of the sum and the form of the product.
+"""
+import ctypes
+
+import pytest
+import torch
+
+import rank_bit_residual_amd as R
+from rank_bit_residual_amd import _lib
+
+pytestmark = pytest.mark.gpu
+
+TD = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+GRID = [0, 0.5, 1, 1.5, 2, 3, 4, 6]
+
+
+def _form(M, N, K, gated=False):
+    got = (ctypes.c_int * 4)()
+    _lib.check(_lib.load().svdq_mx_product_form(M, N, K, gated, got))
+    return tuple(got)
+
+
+def _gen(seed):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _on_grid(gen, rows, cols):
+    x = torch.tensor(GRID, device="cuda")[torch.randint(0, 8, (rows, cols), generator=gen, device="cuda")]
+    x[:, ::32] = 6.0
+    return x * (1 - 2 * torch.randint(0, 2, (rows, cols), generator=gen, device="cuda"))
+
+
+def _product(a, b):
+    return a.double() @ b.double().t().contiguous()
+
+
+# ----------------------------------------------------------------------------- few rows
+# one-tile blocks of eight waves, two-tile blocks, and past 512 column tiles four waves or eight
+@pytest.mark.parametrize("M,N,K,form", [
+    (1, 4096, 1000, (16, 16, 1, 8)), (16, 4097, 1000, (16, 32, 1, 8)), (1, 8176, 1000, (16, 32, 1, 8)),
+    (4, 8177, 1000, (16, 32, 1, 8)), (16, 8192, 1000, (16, 32, 1, 8)), (1, 8192, 8000, (16, 32, 1, 8)),
+    (1, 8193, 1000, (16, 16, 1, 4)), (16, 16400, 1000, (16, 16, 1, 4)), (4, 8193, 1000, (16, 16, 1, 4)),
+    (1, 8193, 8000, (16, 16, 1, 8)), (16, 8208, 8000, (16, 16, 1, 8)),
+    (17, 300, 1000, (32, 16, 1, 8)), (32, 4112, 1000, (32, 32, 1, 8)), (32, 8193, 1000, (32, 32, 1, 8)),
+    (33, 300, 1000, (64, 16, 1, 8)), (64, 4112, 512, (64, 32, 1, 8)), (70, 300, 1000, (64, 16, 1, 8)),
+])
+def test_few_row_forms(M, N, K, form):
+    assert _form(M, N, K) == form
+    gen = _gen(M + N + K)
+    a, b = _on_grid(gen, M, K), _on_grid(gen, N, K)
+    ref = _product(a, b)
+    bq, aq = R.mx_quantize(b), R.mx_quantize(a)
+    bias = torch.randint(-8, 8, (N,), generator=gen, device="cuda").float()
+    for dtype in TD.values():
+        want = ref.float().to(dtype)
+        assert torch.equal(R.mx_matmul(aq, bq, dtype=dtype), want)
+        assert torch.equal(R.mx_matmul(a.to(dtype), bq), want)
+        assert torch.equal(R.mx_matmul(a.to(dtype), bq, bias=bias.to(dtype)), (ref + bias.double()).float().to(dtype))
