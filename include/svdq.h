@@ -413,9 +413,12 @@ int svdq_mx_gated(const void* a_codes, const void* a_scales, int64_t M, const vo
  * svdq_mx_linear, svdq_mx_gated_linear — the two products above of x [M, K] (strides sr, sc in elements)
  * that is not quantised yet: svdq_mx_quantize along its rows, then the product, with the same results. Few rows
  * are quantised inside the product's kernel, others into the workspace. x has the outputs' dtype.
- * workspace: svdq_mx_linear_workspace_bytes. Errors as above.
+ * workspace: svdq_mx_linear_workspace_bytes_of, or svdq_mx_linear_workspace_bytes, which is enough for every
+ * dtype. Errors as above.
  * ------------------------------------------------------------------------------------ */
 int svdq_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t sc, int gated, size_t* bytes_out);
+int svdq_mx_linear_workspace_bytes_of(int64_t M, int64_t N, int64_t K, int64_t sc, int gated, int dtype,
+                                      size_t* bytes_out);
 int svdq_mx_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_t sc, const void* b_codes,
                    const void* b_scales, int64_t N, const void* bias, int dtype, void* y, int64_t ldy, void* workspace,
                    size_t workspace_bytes, svdq_stream_t stream);

@@ -58,6 +58,7 @@ SIGNATURES = {
     "svdq_mx_gated": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_vp, c_i64, c_vp, c_i64,
                               c_vp, c_sz, c_vp]),
     "svdq_mx_linear_workspace_bytes": (c_int, [c_i64, c_i64, c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]),
+    "svdq_mx_linear_workspace_bytes_of": (c_int, [c_i64, c_i64, c_i64, c_i64, c_int, c_int, ctypes.POINTER(c_sz)]),
     "svdq_mx_linear": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_int, c_vp, c_i64, c_vp,
                                c_sz, c_vp]),
     "svdq_mx_gated_linear": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_int, c_int, c_vp, c_i64,

@@ -43,12 +43,18 @@ struct MxDequantParams {
   int64_t ldo;
 };
 
-// Whether the decode kernel quantises A itself: one row, or few rows and few columns to do it again for. Measured on
-// the GPU's clock as one launch against two (quantise, product), K = 4096 unless said: 1 row x 24576 columns 10.7 us
-// against 14.0; 4 x 8192 (K = 8192) 8.9 against 10.2, 8 rows 10.4 against 10.2; 8 x 4096 6.1 against 6.4, 16 rows 6.4 against
-// 6.5; 16 x 1024 (K = 1024) 3.4 against 4.8.
-inline bool mx_raw_rows(int64_t M, int64_t b_rows, int64_t sc) {
-  return sc == 1 && (M == 1 || (M <= 16 && M * b_rows <= 32768));
+// Whether the decode kernel quantises A itself: always for one row; for a few, where doing it again in every block is
+// shorter than a launch of its own (1.9 us). A block's share costs 0.035 us (M + 4) for each 128-code stage of a wave in 16-bit
+// types, twice that in float32. Measured as one launch against two (quantise, product), us on the GPU's clock:
+//   16-bit   K = 2048, 16 rows x 1024 columns 4.2 and 4.8; K = 4096, 8 rows 5.6 and 5.6, 16 rows 6.8 and 5.7; K = 8192, 2 rows 6.6 and
+//            6.4, 16 rows 11.3 and 6.9; K = 65536, 16 rows 77 and 27
+//   float32  K = 1024, 16 rows 4.0 and 4.6; K = 2048, 8 rows 4.7 and 4.7; K = 4096, 4 rows 6.3 and 5.5, 16 rows 11.2 and 5.7
+// Past 4096 rows of b a part of it hides behind the reading of b (16-bit, 4 rows x 8192: K = 8192 10.0 and 11.0, K = 16384 17.4 and 16.8),
+// up to 32768 rows of a times b, where the second reading of x counts.
+inline bool mx_raw_rows(int64_t M, int64_t b_rows, int64_t K, int64_t sc, int dtype_bytes) {
+  if (sc != 1 || M == 1) return sc == 1;
+  const int64_t most = dtype_bytes == 2 && b_rows > 4096 ? 200000 : 110000;
+  return M <= 16 && M * b_rows <= 32768 && (M + 4) * K * dtype_bytes <= most;
 }
 struct MxGemmParams {
   // unquantised A (mx_raw_rows): [M][ldx] of the output's dtype, K elements a row, or NULL

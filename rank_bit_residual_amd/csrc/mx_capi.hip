@@ -21,13 +21,17 @@ int hip_status(hipError_t e, const char* what) {
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 int64_t size_of(int dtype) { return dtype == SVDQ_F32 ? 4 : 2; }
 
+int check_mx_dtype(int dtype) {
+  if (dtype != SVDQ_F32 && dtype != SVDQ_BF16 && dtype != SVDQ_F16)
+    return set_error(SVDQ_EDTYPE, "dtype must be SVDQ_F32, SVDQ_BF16 or SVDQ_F16");
+  return SVDQ_OK;
+}
+
 // Common start of a device call: a clean error state and a dtype these calls take.
 int begin(int dtype) {
   clear_error();
   (void)hipGetLastError();  // an error that an earlier, unrelated HIP call left
-  if (dtype != SVDQ_F32 && dtype != SVDQ_BF16 && dtype != SVDQ_F16)
-    return set_error(SVDQ_EDTYPE, "dtype must be SVDQ_F32, SVDQ_BF16 or SVDQ_F16");
-  return SVDQ_OK;
+  return check_mx_dtype(dtype);
 }
 
 int check_dim(int64_t v, const char* name) {
@@ -138,13 +142,13 @@ int product(const void* a_codes, const void* a_scales, int64_t M, const Product&
 }
 
 // Whether the product quantises its rows itself.
-bool raw_rows(int64_t M, int64_t N, int64_t K, bool gated, int64_t sc) {
-  return mx_raw_rows(M, gated ? 2 * N : N, sc) && mx_product_decodes(M, N, (int)mx_kq(K), gated);
+bool raw_rows(int64_t M, int64_t N, int64_t K, bool gated, int64_t sc, int64_t dtype_bytes) {
+  return mx_raw_rows(M, gated ? 2 * N : N, K, sc, (int)dtype_bytes) && mx_product_decodes(M, N, (int)mx_kq(K), gated);
 }
 
 // Workspace of an unquantised A: its codes and scales (unless the product quantises it), then the parts.
-size_t linear_bytes(int64_t M, int64_t N, int64_t K, bool gated, int64_t sc) {
-  if (raw_rows(M, N, K, gated, sc)) return 0;
+size_t linear_bytes(int64_t M, int64_t N, int64_t K, bool gated, int64_t sc, int64_t dtype_bytes) {
+  if (raw_rows(M, N, K, gated, sc, dtype_bytes)) return 0;
   return (size_t)(mx_code_bytes(M, K) + mx_scale_bytes(M, K)) + mx_product_part_bytes(M, N, (int)mx_kq(K), gated);
 }
 
@@ -153,10 +157,10 @@ int linear(const void* x, int64_t M, int64_t sr, int64_t sc, const Product& q, v
   int st = begin(q.dtype);
   if (st || (st = check_product(M, q)) || (st = check_strided(x, sr, sc, q.dtype, "x"))) return st;
   const size_t codes = (size_t)mx_code_bytes(M, q.K), scales = (size_t)mx_scale_bytes(M, q.K);
-  if ((st = check_workspace(workspace, workspace_bytes, linear_bytes(M, q.N, q.K, q.gated, sc)))) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, linear_bytes(M, q.N, q.K, q.gated, sc, size_of(q.dtype))))) return st;
   uint8_t* ws = (uint8_t*)workspace;
   hipStream_t s = (hipStream_t)stream;
-  if (raw_rows(M, q.N, q.K, q.gated, sc)) {
+  if (raw_rows(M, q.N, q.K, q.gated, sc, size_of(q.dtype))) {
     MxGemmParams p = params_of(M, q, nullptr);
     p.x = x;
     p.ldx = sr;
@@ -245,10 +249,15 @@ int svdq_mx_gated(const void* a_codes, const void* a_scales, int64_t M, const vo
 }
 
 int svdq_mx_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t sc, int gated, size_t* bytes_out) {
+  // the widest type is quantised inside the product least often
+  return svdq_mx_linear_workspace_bytes_of(M, N, K, sc, gated, SVDQ_F32, bytes_out);
+}
+
+int svdq_mx_linear_workspace_bytes_of(int64_t M, int64_t N, int64_t K, int64_t sc, int gated, int dtype, size_t* bytes_out) {
   int st = svdq_mx_workspace_bytes(M, N, K, gated, bytes_out);
-  if (st) return st;
+  if (st || (st = check_mx_dtype(dtype))) return st;
   if (sc < 0) return set_error(SVDQ_EINVAL, "strides must not be negative");
-  *bytes_out = linear_bytes(M, N, K, gated != 0, sc);
+  *bytes_out = linear_bytes(M, N, K, gated != 0, sc, size_of(dtype));
   return SVDQ_OK;
 }
 

@@ -236,7 +236,7 @@ def _product(a, b, names, dtype, out, bias=None, act=None, save=False) -> tuple:
     y = _output(out, M, N, dtype, device, a if raw else a.data, b.data, bias)
     if raw:
         sr, sc = a.stride()
-        need = _workspace_bytes("svdq_mx_linear_workspace_bytes", M, N, K, 1 if K == 1 else sc, gated)
+        need = _workspace_bytes("svdq_mx_linear_workspace_bytes_of", M, N, K, 1 if K == 1 else sc, gated, code)
     else:
         need = _workspace_bytes("svdq_mx_workspace_bytes", M, N, K, gated)
     ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None

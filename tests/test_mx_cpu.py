@@ -211,6 +211,34 @@ def test_launches_past_the_grid_are_refused():
     _refused(EINVAL, lib.svdq_mx_matmul(A, A, 1, A, A, big, 64, None, BF16, A, big, None, 0, None))
 
 
+def _linear_workspace(M, N, K, gated=0, dtype=None, sc=1):
+    n, lib = ctypes.c_size_t(), _lib.load()
+    if dtype is None:
+        assert lib.svdq_mx_linear_workspace_bytes(M, N, K, sc, gated, ctypes.byref(n)) == 0
+    else:
+        assert lib.svdq_mx_linear_workspace_bytes_of(M, N, K, sc, gated, dtype, ctypes.byref(n)) == 0
+    return n.value
+
+
+def test_long_rows_are_quantised_before_the_product():
+    """A few rows are quantised inside the product (no workspace) while K is short, one row always, many never."""
+    for gated in (0, 1):
+        for M in (2, 4, 8, 16):
+            for dtype in (BF16, F16, F32):
+                fused = [_linear_workspace(M, 64, K, gated, dtype) == 0 for K in (64, 512, 1024, 16384, 28672, 1 << 17)]
+                assert fused == [True, True, True, False, False, False]
+            assert _linear_workspace(M, 64, 4096, gated, F32) >= _linear_workspace(M, 64, 4096, gated, BF16)
+            for K in (64, 2048, 4096, 16384):
+                widest = max(_linear_workspace(M, 64, K, gated, d) for d in (F32, BF16, F16))
+                assert _linear_workspace(M, 64, K, gated) == widest
+        for K in (64, 4096):
+            assert _linear_workspace(1, 8192, K, gated, F32) == _linear_workspace(1, 8192, K, gated, BF16) == 0
+            assert _linear_workspace(1, 64, K, gated, F32, sc=2) > 0 and _linear_workspace(17, 64, K, gated, BF16) > 0
+    n = ctypes.c_size_t()
+    _refused(EDTYPE, _lib.load().svdq_mx_linear_workspace_bytes_of(4, 4, 4, 1, 0, F64, ctypes.byref(n)))
+    _refused(EINVAL, _lib.load().svdq_mx_linear_workspace_bytes_of(4, 4, 4, -1, 0, F32, ctypes.byref(n)))
+
+
 def _form(M, N, K, gated=0):
     got = (ctypes.c_int * 4)()
     assert _lib.load().svdq_mx_product_form(M, N, K, gated, got) == 0

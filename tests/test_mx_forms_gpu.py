@@ -61,3 +61,23 @@ def test_few_row_forms(M, N, K, form):
         assert torch.equal(R.mx_matmul(aq, bq, dtype=dtype), want)
         assert torch.equal(R.mx_matmul(a.to(dtype), bq), want)
         assert torch.equal(R.mx_matmul(a.to(dtype), bq, bias=bias.to(dtype)), (ref + bias.double()).float().to(dtype))
+
+
+def _fused(M, N, K, dtype, gated=False):
+    n = ctypes.c_size_t()
+    code = {torch.float32: _lib.SVDQ_F32, torch.bfloat16: _lib.SVDQ_BF16, torch.float16: _lib.SVDQ_F16}[dtype]
+    _lib.check(_lib.load().svdq_mx_linear_workspace_bytes_of(M, N, K, 1, gated, code, ctypes.byref(n)))
+    return n.value == 0
+
+
+# rows quantised inside the product and before it, on either side of each type's border
+@pytest.mark.parametrize("M,N,K,fused", [(2, 64, 1000, "f32 bf16 f16"), (16, 200, 2048, "bf16 f16"), (8, 40, 4096, "bf16 f16"),
+                                         (16, 40, 4096, ""), (2, 33, 28672, ""), (4, 8000, 8192, "bf16 f16"), (1, 33, 8192, "f32 bf16 f16")])
+def test_quantised_inside_the_product_or_before(M, N, K, fused):
+    gen = _gen(M + N + K)
+    a, b = _on_grid(gen, M, K), _on_grid(gen, N, K)
+    ref = _product(a, b)
+    bq = R.mx_quantize(b)
+    for name, dtype in TD.items():
+        assert _fused(M, N, K, dtype) == (name in fused.split())
+        assert torch.equal(R.mx_matmul(a.to(dtype), bq), ref.float().to(dtype))
