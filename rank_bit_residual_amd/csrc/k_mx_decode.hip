@@ -227,7 +227,8 @@ static hipError_t launch_rows(const MxGemmParams& p, hipStream_t stream) {
 //   257 to 512   two tiles, so that a compute unit's blocks are one: 8192 x 5120 at 16 rows 7.7 against 8.7, 8192 x 8192 8.9
 //                against 9.7 (1024 x 6000 3.4 both)
 //   more         past 16 rows two tiles, so that a's operands serve twice: 8192 x 16384 at 32 rows 17.2, 22.7 with one tile,
-//                at 64 rows 23.4 and 34.6. Up to 16 rows one tile; with four waves below 64 stages, so that more blocks run at
+//                at 64 rows 23.4 and 34.6. Up to 16 rows, or 32 rows of up to eight stages (1024 x 12288 at 32 rows 4.2, with two
+//                tiles 4.4), one tile; with four waves below 64 stages, so that more blocks run at
 //                once (1024 x 16384 at one row 3.9, 4.5 with eight waves, 4096 x 12288 7.6 and 8.5, 7168 x 12288 10.9 and
 //                11.9), with eight from there on, where the waves' own chains of stages count (8192 x 16384 16.4, 21.1 with
 //                four, 16384 x 16384 28.9 and 31.0, 28672 x 9216 32.0 and 31.8)
@@ -236,7 +237,7 @@ MxForm mx_decode_form(int64_t M, int64_t N, int kq, bool gated) {
   if (gated) return MxForm{bm, 32, 1, 8};
   const int64_t tiles = (N + 15) / 16;
   if (tiles <= 256) return MxForm{bm, 16, 1, 8};
-  if (tiles <= 512 || bm > 16) return MxForm{bm, 32, 1, 8};
+  if (tiles <= 512 || bm > (kq <= 8 ? 32 : 16)) return MxForm{bm, 32, 1, 8};
   return MxForm{bm, 16, 1, kq < 64 ? 4 : 8};
 }
 
@@ -245,7 +246,7 @@ static hipError_t launch_cols(const MxGemmParams& p, bool gated, hipStream_t str
   if (gated) return launch_rows<DT, MT, 2, 8, true, FORM>(p, stream);
   const MxForm f = mx_decode_form(p.M, p.N, p.kq, false);
   if (f.bn == 32) return launch_rows<DT, MT, 2, 8, false, FORM>(p, stream);
-  if constexpr (MT == 1) {
+  if constexpr (MT <= 2) {
     if (f.waves == 4) return launch_rows<DT, MT, 1, 4, false, FORM>(p, stream);
   }
   return launch_rows<DT, MT, 1, 8, false, FORM>(p, stream);

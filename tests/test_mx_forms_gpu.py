@@ -46,7 +46,7 @@ def _product(a, b):
     (4, 8177, 1000, (16, 32, 1, 8)), (16, 8192, 1000, (16, 32, 1, 8)), (1, 8192, 8000, (16, 32, 1, 8)),
     (1, 8193, 1000, (16, 16, 1, 4)), (16, 16400, 1000, (16, 16, 1, 4)), (4, 8193, 1000, (16, 16, 1, 4)),
     (1, 8193, 8000, (16, 16, 1, 8)), (16, 8208, 8000, (16, 16, 1, 8)),
-    (17, 300, 1000, (32, 16, 1, 8)), (32, 4112, 1000, (32, 32, 1, 8)), (32, 8193, 1000, (32, 32, 1, 8)),
+    (17, 300, 1000, (32, 16, 1, 8)), (32, 4112, 1000, (32, 32, 1, 8)), (32, 8193, 1100, (32, 32, 1, 8)), (20, 8193, 1000, (32, 16, 1, 4)),
     (33, 300, 1000, (64, 16, 1, 8)), (64, 4112, 512, (64, 32, 1, 8)), (70, 300, 1000, (64, 16, 1, 8)),
 ])
 def test_few_row_forms(M, N, K, form):
