@@ -426,9 +426,12 @@ struct MxPlan {
 
 // The form with the least estimated time in us, from the times measured on this chip (K = 4096 is kq = 32 stages of 128):
 //   few rows  (k_mx_decode) b is read again for each 64 rows; with b's elements in millions, up to 32 rows 2.5 us at 1, 3.3
-//             to 4 at 17, 7.9 at 67; 64 rows 3.2, 5.2 and 10.1, 128 rows 3.2, 9.0 and 17.8; a wave's stages come after one
-//             another, 0.33 us each. Small b, many rows, us for each 64 of them: 0.29 (1000 columns, K = 512), 0.46 (1000, 1024),
-//             0.79 (1500, 1536), 1.9 (5000, 768)
+//             to 4 at 17, 7.9 at 67; 64 rows 3.2, 5.2 and 10.1, 128 rows 3.2, 9.0 and 17.8. Small b, many rows, us for each 64
+//             of them: 0.29 (1000 columns, K = 512), 0.46 (1000, 1024), 0.79 (1500, 1536), 1.9 (5000, 768).
+//             No less than b's bytes from memory: 5.4 TB/s at one row, 9 % slower for every ten rows (143 MB 28 us at one row, 32
+//             at 16, 35 at 32, 44 at 64; 570 MB 98, 113, 123 and 160). No less than its blocks: 512 x 82944 7.6 us at one row, 1024 x
+//             131072 49 at 64. No less than a wave's stages one after another, 0.25 us each at one row, 0.35 at 16, 0.47 at 32,
+//             0.73 at 64 (28672 x 1024: 10.0, 12.7, 16.1, 23.4 us), 0.31 to 0.47 gated at one row
 //   128 x 128 two blocks per compute unit; 13 us for up to 256 tiles at kq = 32, 21 for 64 stages, 114 us for 12 tiles a unit
 //   128 x 256 one block: 16.5 us for 32 tiles to 21 for 256, 109 us for 1536
 //             shares of K run 7 % faster a stage (an XCD's blocks read the same one): 1024 x 65536 x 1024 in 8 shares 48 us, 52 with
@@ -437,15 +440,21 @@ struct MxPlan {
 // A gated product's tiles leave as one to three arrays: 500 x 300 x 2*700 5.4 us, 7.7 with g and u (few rows 5.7 and 6.1); 2048 x 2048 x
 // 2*8192 39.9 us on 256 x 256 against 45.4 on 128 x 128.
 // Shares of K add the joining launch and the parts' way through memory at 4 TB/s.
+// Against few rows, tiles take no less than b's bytes from memory at 5 TB/s, and, for one row, a launch more, as the few-row kernel
+// quantises that itself. One row, the best tiles and the few-row kernel, us: 28672 x 8192 32.6 and 25.3; 16384 x 16384 34.8 and
+// 29.4; 65536 x 4096 37.5 and 27.7; 4096 x 128256 55 and 49; 28672 x 1024 13.5 and 10.0; 65536 x 256 12.7 and 14.7.
 static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
-  const double b_rows = (double)N * (gated ? 2 : 1), millions = b_rows * kq * 128 * 1e-6;
-  MxPlan best{0, 0, 1};
+  const double b_rows = (double)N * (gated ? 2 : 1), millions = b_rows * kq * 128 * 1e-6, mb = millions * 17 / 32;
   double few = 0.25 * millions + 0.17e-3 * b_rows;
   if (few > 1.6 + 0.11 * millions) few = 1.6 + 0.11 * millions;
-  double best_t = M <= 32 ? 2.2 + 0.082 * millions : 3.0 + (double)((M + 63) / 64) * few;
-  if (M > 64 * 65535) best_t = 1e30;  // past the grid's second dimension
-  const double in_turn = 3.0 + 0.33 * kq / (M <= 32 ? 8 : 4);
-  if (best_t < in_turn) best_t = in_turn;
+  double few_t = M <= 32 ? 2.2 + 0.082 * millions : 3.0 + (double)((M + 63) / 64) * few;
+  const double rows = M <= 32 ? (double)M : 64.0;  // past 32 rows a block computes 64
+  const double bytes = 2.0 + mb / 5.4 * (1 + 0.009 * rows), blocks = 2.0 + b_rows * (M <= 32 ? 0.08e-3 : 0.36e-3);
+  const double in_turn = 2.4 + kq / 8.0 * ((gated ? 0.36 : 0.24) + 0.0075 * rows);
+  for (double least : {bytes, blocks, in_turn})
+    if (few_t < least) few_t = least;
+  MxPlan best{0, 0, 1};
+  double best_t = 1e30;
   const int cand[3][2] = {{128, 128}, {128, 256}, {256, 256}};
   for (int c = 0; c < 3; c++) {
     // a 128-wide gated tile reaches its up rows' scales from its gate rows' by a 32-bit offset
@@ -468,7 +477,10 @@ static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
       if (t < best_t) best = MxPlan{bm, cand[c][1], s}, best_t = t;
     }
   }
-  return best;
+  if (M > 64 * 65535) return best;  // past the few-row grid's second dimension
+  const double least = 4 + mb / 5.0 + (best.splits > 1 ? 5.0 + (double)M * b_rows * 4 * 2 * best.splits / 4e6 : 0);
+  if (best_t < least) best_t = least;
+  return few_t <= best_t + (M == 1 ? 2.0 : 0.0) ? MxPlan{0, 0, 1} : best;
 }
 
 MxForm mx_product_form(int64_t M, int64_t N, int kq, bool gated) {

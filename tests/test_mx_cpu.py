@@ -267,6 +267,17 @@ def test_few_row_blocks_change_with_the_tiles_a_compute_unit_gets(M, K):
         assert len(forms) <= 1, forms
 
 
+
+@pytest.mark.parametrize("N,K,gated", [(12288, 4096, 1), (28672, 8192, 1), (8192, 28672, 0), (1024, 28672, 0), (128256, 4096, 0),
+                                       (16384, 16384, 0), (4096, 65536, 0), (140000, 65536, 0), (72000, 65536, 1)])
+def test_one_row_is_one_launch(N, K, gated):
+    """However large the weight: its bytes take as long in any form, and tiles would need two or three launches."""
+    bm, _, splits, waves = _form(1, N, K, gated)
+    assert bm == 16 and splits == 1 and waves > 1
+    for dtype in (F32, BF16, F16):
+        assert _linear_workspace(1, N, K, gated, dtype) == 0
+
+
 # ----------------------------------------------------------------------------- binding
 @pytest.mark.parametrize("out,x,want", [
     ((0, 4, 8, 8), (32, 4, 8, 8), False),  # (offset, rows, columns, row stride)

@@ -72,7 +72,8 @@ def _fused(M, N, K, dtype, gated=False):
 
 # rows quantised inside the product and before it, on either side of each type's border
 @pytest.mark.parametrize("M,N,K,fused", [(2, 64, 1000, "f32 bf16 f16"), (16, 200, 2048, "bf16 f16"), (8, 40, 4096, "bf16 f16"),
-                                         (16, 40, 4096, ""), (2, 33, 28672, ""), (4, 8000, 8192, "bf16 f16"), (1, 33, 8192, "f32 bf16 f16")])
+                                         (16, 40, 4096, ""), (2, 33, 28672, ""), (4, 8000, 8192, "bf16 f16"), (1, 33, 8192, "f32 bf16 f16"),
+                                         (1, 33, 28672, "f32 bf16 f16")])
 def test_quantised_inside_the_product_or_before(M, N, K, fused):
     gen = _gen(M + N + K)
     a, b = _on_grid(gen, M, K), _on_grid(gen, N, K)
@@ -81,3 +82,24 @@ def test_quantised_inside_the_product_or_before(M, N, K, fused):
     for name, dtype in TD.items():
         assert _fused(M, N, K, dtype) == (name in fused.split())
         assert torch.equal(R.mx_matmul(a.to(dtype), bq), ref.float().to(dtype))
+
+
+def test_few_rows_of_a_tensor_past_32_bits():
+    """Few rows against 4.6 GB of codes, in the few-row kernel's own addressing: the first and the last columns."""
+    rows, cols = 140_000, 65_536
+    assert all(_form(M, rows, cols)[3] > 1 and _form(M, rows // 2, cols, True)[3] > 1 for M in (1, 4))
+    gen = _gen(79)
+    x = torch.randint(-3, 4, (rows, cols), generator=gen, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    x[:, ::32] = 3
+    r = R.mx_quantize(x)
+    assert r.data.numel() > 2**32
+    for M in (1, 4):
+        a = torch.randint(-3, 4, (M, cols), generator=gen, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+        a[:, ::32] = 3
+        y = R.mx_matmul(a.float(), r)
+        for part in (slice(0, 300), slice(rows - 300, rows)):
+            assert torch.equal(y[:, part], a.float() @ x[part].float().t().contiguous())
+        g = R.mx_gated(a.float(), r, act="relu")
+        gate, up = slice(rows // 2 - 300, rows // 2), slice(rows - 300, rows)
+        ref = (a.float() @ x[gate].float().t().contiguous()).relu() * (a.float() @ x[up].float().t().contiguous())
+        assert torch.equal(g[:, -300:], ref)
