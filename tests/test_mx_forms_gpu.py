@@ -294,3 +294,34 @@ def test_first_call_of_a_process_captured():
     r = subprocess.run([sys.executable, "-c", FIRST_TILES], capture_output=True, text=True, timeout=100,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+# ----------------------------------------------------------------------------- ends of the range
+@pytest.mark.parametrize("e", [-127, -126, -125, -124, -60, 100, 124])
+def test_values_at_the_ends_of_the_range(e):
+    """Blocks of the lowest scale bytes (0 stands for 2^-127, a float32 subnormal) and of high ones, read back along both axes."""
+    gen = _gen(e + 200)
+    x = _on_grid(gen, 70, 96)
+    x[::32] = 6.0
+    want = x.double() * 2.0**e
+    assert torch.equal(want.float().double(), want)
+    rows, cols = R.mx_quantize(want.float(), axis=None)
+    bytes_of = lambda t: t.scales.view(-1, 64, 4)[0, :32, :3]  # noqa: E731
+    assert (bytes_of(rows) == e + 127).all()
+    for dtype in TD.values():
+        assert torch.equal(R.mx_dequantize(rows, dtype), want.to(dtype))
+        back = R.mx_dequantize(cols, dtype)
+        assert torch.equal(back[:, :64], want.t()[:, :64].to(dtype))
+
+
+@pytest.mark.parametrize("e,f", [(-127, 100), (-127, 0), (-127, -8), (-126, 2), (-125, -1), (-120, -10), (100, 10), (-60, -60)])
+@pytest.mark.parametrize("M,N,K", [(3, 64, 160), (300, 2500, 160), (129, 300, 9000)])
+def test_products_at_the_ends_of_the_range(M, N, K, e, f):
+    """Terms down to 2^-140 and their sums, subnormal float32 numbers among them, are exact in every kernel."""
+    gen = _gen(M + K)
+    a, b = _on_grid(gen, M, K).double(), _on_grid(gen, N, K).double()
+    ref = a @ b.t().contiguous() * 2.0 ** (e + f)
+    y = R.mx_matmul((a * 2.0**e).float(), R.mx_quantize((b * 2.0**f).float()))
+    assert torch.equal(y.double(), ref)
+    assert torch.equal(R.mx_matmul(R.mx_quantize((a * 2.0**e).float()), R.mx_quantize((b * 2.0**f).float()), dtype=torch.bfloat16),
+                       ref.float().to(torch.bfloat16))
