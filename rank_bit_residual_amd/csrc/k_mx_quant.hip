@@ -232,8 +232,8 @@ __device__ inline u32 to_odd16(double v) {
   const float f = (float)v;
   u32 u = __float_as_uint(f);
   const double d = (double)f;
-  if (!(fabsf(f) < __builtin_inff()) || d == v) return (u >> 16) | ((u & 0xFFFFu) ? 1u : 0u);
-  if (fabs(d) > fabs(v)) u -= 1;  // toward zero (f is not zero then)
+  if (!(fabs(v) < 0x1p128) || d == v) return (u >> 16) | ((u & 0xFFFFu) ? 1u : 0u);
+  if (fabs(d) > fabs(v)) u -= 1;  // toward zero (f is not zero then; it may be the infinity above the largest float)
   return (u >> 16) | (v < 0 ? 0x8001u : 1u);
 }
 

@@ -459,6 +459,25 @@ def test_gated_grad_of_an_overflowing_product(dtype, act, F):
     _check_tensor(cols, want.T)
 
 
+@pytest.mark.parametrize("F", [64, 70])
+def test_gated_grad_just_below_infinity(F):
+    """Gradients between the largest float32 and 2^128, which float32 would round up to infinity, are finite; from 2^128
+    on a block is NaN."""
+    dh, gu = np.ones((33, F)), np.ones((33, 2 * F))
+    dh[3, 5], gu[3, F + 5] = (2 - 2.0**-22) * 2.0**64, (1 + 2.0**-23) * 2.0**63  # (2 - 2^-44 (1 + ..)) 2^127
+    dh[7, 9], gu[7, F + 9] = -(2 - 2.0**-22) * 2.0**63, (1 + 2.0**-23) * 2.0**64
+    dh[20, 40], gu[20, F + 40] = 2.0**64, 2.0**64
+    d, z = _gpu(dh, "f32"), _gpu(gu, "f32")
+    want = X.gated_grad(_np(d), _np(z), "relu")
+    high = np.abs(want[[3, 7], [5, 9]])
+    with np.errstate(over="ignore"):
+        assert (high < 2.0**128).all() and np.isinf(high.astype(np.float32)).all() and want[20, 40] == 2.0**128
+    want[20, 40] = np.inf
+    rows, cols = R.mx_gated_grad(d, z, act="relu")
+    _check_tensor(rows, want)
+    _check_tensor(cols, want.T)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M,K,F", [(5, 40, 33), (70, 256, 64), (130, 300, 100)])
 def test_training_step_together(dtype, M, K, F):
