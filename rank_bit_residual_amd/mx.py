@@ -143,8 +143,8 @@ def _overlap(out: torch.Tensor, t: torch.Tensor) -> bool:
     ld, cols = out.stride(0) * size, out.shape[1] * size
     if a + (out.shape[0] - 1) * ld + cols <= b or b + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * other <= a:
         return False
-    # columns beside the output's in the rows of one buffer
-    beside = t.dim() == 2 and t.stride(1) == 1 and t.stride(0) * other == ld
+    # columns beside the output's in the rows of one buffer (whose rows do not overlap: a single row's stride may be anything)
+    beside = t.dim() == 2 and t.stride(1) == 1 and t.stride(0) * other == ld >= cols
     return not (beside and cols <= (b - a) % ld and (b - a) % ld + t.shape[1] * other <= ld)
 
 

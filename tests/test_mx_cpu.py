@@ -303,6 +303,18 @@ def test_overlap(out, x, want):
     assert not mx._overlap(out, torch.zeros(4, 8)) and not mx._overlap(out, torch.zeros(8))
 
 
+def test_overlap_of_an_output_row_without_a_stride():
+    """A row may have any row stride, 0 too (a view made by expand)."""
+    from rank_bit_residual_amd import mx
+
+    buf = torch.zeros(200)
+    out = torch.as_strided(buf, (1, 8), (0, 1), 5)
+    for at, want in ((0, True), (12, True), (13, False)):
+        assert mx._overlap(out, torch.as_strided(buf, (1, 8), (0, 1), at)) is want
+        assert mx._overlap(out, torch.as_strided(buf, (3, 8), (0, 1), at)) is want
+        assert mx._overlap(out, torch.as_strided(buf, (2, 8), (8, 1), at)) is want
+
+
 def _fake(rows, cols, short=0):
     _, a, b = _layout(rows, cols)
     return R.MxTensor(torch.zeros(a + b - short, dtype=torch.uint8), rows, cols)
