@@ -211,10 +211,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_decode(MxGemmParams p) {
 
 using namespace dev;
 
+// Blocks over N columns, `cols` a block, in whole runs for each XCD.
+static int64_t decode_blocks(int64_t N, int64_t cols) { return ((N + cols - 1) / cols + 7) / 8 * 8; }
+
 template <class DT, int MT, int NT, int WAVES, bool GATED, int FORM>
 static hipError_t launch_rows(const MxGemmParams& p, hipStream_t stream) {
-  const int64_t cols = GATED ? 16 : 16 * NT;
-  const int64_t blocks = ((p.N + cols - 1) / cols + 7) / 8 * 8;  // whole runs for each XCD
+  const int64_t blocks = decode_blocks(p.N, GATED ? 16 : 16 * NT);
   if (!mx_fits_grid(blocks, 64 * WAVES)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks, (unsigned)((p.M + 16 * MT - 1) / (16 * MT)));
   k_mx_decode<DT, MT, NT, WAVES, GATED, FORM><<<grid, 64 * WAVES, 0, stream>>>(p);
@@ -239,6 +241,11 @@ MxForm mx_decode_form(int64_t M, int64_t N, int kq, bool gated) {
   if (tiles <= 256) return MxForm{bm, 16, 1, 8};
   if (tiles <= 512 || bm > (kq <= 8 ? 32 : 16)) return MxForm{bm, 32, 1, 8};
   return MxForm{bm, 16, 1, kq < 64 ? 4 : 8};
+}
+
+bool mx_decode_fits(int64_t M, int64_t N, int kq, bool gated) {
+  const MxForm f = mx_decode_form(M, N, kq, gated);
+  return mx_fits_grid(decode_blocks(N, gated ? f.bn / 2 : f.bn), 64 * f.waves);
 }
 
 template <class DT, int MT, int FORM>

@@ -15,6 +15,7 @@
 // the same output columns: a lane ends with g and u of its outputs in registers, and the activation and the
 // product are its epilogue.
 #include <atomic>
+#include <initializer_list>
 #include <type_traits>
 
 #include "mx.h"
@@ -495,12 +496,21 @@ size_t mx_product_part_bytes(int64_t M, int64_t N, int kq, bool gated) {
   return pl.splits > 1 ? (size_t)pl.splits * M * N * (gated ? 2 : 1) * 4 : 0;
 }
 
+// Blocks of bm x cols output tiles in `splits` shares of K, in whole runs for each XCD.
+static int64_t tile_blocks(int64_t M, int64_t N, int64_t bm, int64_t cols, int64_t splits) {
+  return ((M + bm - 1) / bm * ((N + cols - 1) / cols) * splits + 7) / 8 * 8;
+}
+
+bool mx_product_fits(int64_t M, int64_t N, int kq, bool gated) {
+  const MxPlan pl = plan_of(M, N, kq, gated);
+  if (pl.bm == 0) return mx_decode_fits(M, N, kq, gated);
+  return mx_fits_grid(tile_blocks(M, N, pl.bm, gated ? pl.bn / 2 : pl.bn, pl.splits), 512);
+}
+
 template <class DT, int BM, int BN, bool GATED, bool SPLIT>
 static hipError_t launch_tile(const MxGemmParams& p, hipStream_t stream) {
   typedef TileCfg<BM, BN> C;
-  constexpr int COLS = GATED ? BN / 2 : BN;
-  const int64_t tiles = (((int64_t)p.M + BM - 1) / BM) * (((int64_t)p.N + COLS - 1) / COLS) * p.splits;
-  const int64_t blocks = (tiles + 7) / 8 * 8;
+  const int64_t blocks = tile_blocks(p.M, p.N, BM, GATED ? BN / 2 : BN, p.splits);
   if (!mx_fits_grid(blocks, 64 * C::NWV)) return hipErrorInvalidConfiguration;
   // once per process and device; a second thread at most repeats the same call
   static std::atomic<uint64_t> configured;

@@ -448,33 +448,48 @@ static hipError_t with_dtype(int dtype, Fn f) {
 
 static int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 
-template <class DT, int NP, bool ROWS, bool COLS>
-static hipError_t launch_quant(const MxQuantParams& p, hipStream_t stream) {
-  constexpr int TH = 16 * NP;
-  // a direction that is written covers its padding too
-  const int64_t tc = ROWS ? p.rows.kq : tiles_of(p.C), tr = COLS ? (int64_t)p.cols.kq * (kTile / TH) : (p.R + TH - 1) / TH;
-  if (!mx_fits_grid(tc * tr, 256)) return hipErrorInvalidConfiguration;
-  k_mx_quantize<DT, NP, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 256, 0, stream>>>(p, (int)tc);
-  return hipGetLastError();
-}
-
 // Tiles of 128 rows, whose columns' codes fill whole 64-byte rows, while they fill the chip, else of 32 rows. Measured,
 // bf16, both directions: 8192 x 12288 59 us (80 with tiles of 32 x 64), 2048 x 4096 7.9 us with 32 rows against 8.7, 777 x
 // 5003 6.2 against 8.4.
 constexpr int64_t kFewTiles = 768;
 
-hipError_t launch_mx_quantize(const MxQuantParams& p0, int dtype, hipStream_t stream) {
-  MxQuantParams p = p0;
+struct QuantGrid {
+  MxQuantParams p;
+  bool few;
+  int64_t tc, blocks;
+};
+static QuantGrid quant_grid(const MxQuantParams& p0) {
+  QuantGrid g{p0, false, 0, 0};
+  MxQuantParams& p = g.p;
   if (p.sc != 1 && p.sr == 1) {  // columns are contiguous: the transpose's rows
     const MxQuantParams q = p;
     p.R = q.C, p.C = q.R, p.sr = q.sc, p.sc = q.sr, p.rows = q.cols, p.cols = q.rows;
   }
-  const bool few = tiles_of(p.R) * tiles_of(p.C) < kFewTiles;
+  g.few = tiles_of(p.R) * tiles_of(p.C) < kFewTiles;
+  const int64_t th = g.few ? 32 : kTile;
+  // a direction that is written covers its padding too
+  g.tc = p.rows.codes ? p.rows.kq : tiles_of(p.C);
+  g.blocks = g.tc * (p.cols.codes ? (int64_t)p.cols.kq * (kTile / th) : (p.R + th - 1) / th);
+  return g;
+}
+
+bool mx_quantize_fits(const MxQuantParams& p) { return mx_fits_grid(quant_grid(p).blocks, 256); }
+
+template <class DT, int NP, bool ROWS, bool COLS>
+static hipError_t launch_quant(const QuantGrid& g, hipStream_t stream) {
+  k_mx_quantize<DT, NP, ROWS, COLS><<<dim3((unsigned)g.blocks), 256, 0, stream>>>(g.p, (int)g.tc);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_quantize(const MxQuantParams& p, int dtype, hipStream_t stream) {
+  const QuantGrid g = quant_grid(p);
+  if (!mx_fits_grid(g.blocks, 256)) return hipErrorInvalidConfiguration;
   return with_dtype(dtype, [&](auto d) {
     typedef decltype(d) DT;
-    if (p.rows.codes && p.cols.codes) return few ? launch_quant<DT, 2, true, true>(p, stream) : launch_quant<DT, 8, true, true>(p, stream);
-    if (p.rows.codes) return few ? launch_quant<DT, 2, true, false>(p, stream) : launch_quant<DT, 8, true, false>(p, stream);
-    return few ? launch_quant<DT, 2, false, true>(p, stream) : launch_quant<DT, 8, false, true>(p, stream);
+    if (g.p.rows.codes && g.p.cols.codes)
+      return g.few ? launch_quant<DT, 2, true, true>(g, stream) : launch_quant<DT, 8, true, true>(g, stream);
+    if (g.p.rows.codes) return g.few ? launch_quant<DT, 2, true, false>(g, stream) : launch_quant<DT, 8, true, false>(g, stream);
+    return g.few ? launch_quant<DT, 2, false, true>(g, stream) : launch_quant<DT, 8, false, true>(g, stream);
   });
 }
 
@@ -487,22 +502,37 @@ hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t
   });
 }
 
+// Measured at 4096 rows, bf16, silu, both directions: 106 us for F = 12288 as pairs, 152 us for F = 12300.
+struct GradGrid {
+  bool pairs;  // dg's and du's tiles of the same columns in one block
+  int64_t tc, across, blocks;
+};
+static GradGrid grad_grid(const MxGradParams& p) {
+  GradGrid g{p.F % kMxBlock == 0, 0, 0, 0};
+  const int64_t tr = p.cols.codes ? (int64_t)p.cols.kq * (kTile / kGradRows) : (p.M + kGradRows - 1) / kGradRows;
+  if (g.pairs) {
+    g.tc = (p.F + kGradCols - 1) / kGradCols;
+    g.blocks = g.tc * tr;
+  } else {
+    // tiles of [0, 2F), with the row tensor's padding; those that begin below F, and those from the one that holds F on
+    g.tc = p.rows.codes ? (int64_t)p.rows.kq * (kTile / kGradCols) : (2 * p.F + kGradCols - 1) / kGradCols;
+    const int64_t below = p.F / kGradCols;
+    g.across = g.tc - below > below ? g.tc - below : below;
+    g.blocks = (g.across * tr + 7) / 8 * 16;
+  }
+  return g;
+}
+
+bool mx_gated_grad_fits(const MxGradParams& p) { return mx_fits_grid(grad_grid(p).blocks, 256); }
+
 template <class DT, int ACT, bool ROWS, bool COLS>
 static hipError_t launch_grad_t(const MxGradParams& p, hipStream_t stream) {
-  const int64_t tr = COLS ? (int64_t)p.cols.kq * (kTile / kGradRows) : (p.M + kGradRows - 1) / kGradRows;
-  // Measured at 4096 rows, bf16, silu, both directions: 106 us for F = 12288 as pairs, 152 us for F = 12300.
-  if (p.F % kMxBlock == 0) {
-    const int64_t tc = (p.F + kGradCols - 1) / kGradCols;
-    if (!mx_fits_grid(tc * tr, 256)) return hipErrorInvalidConfiguration;
-    k_mx_gated_grad<DT, ACT, ROWS, COLS><<<dim3((unsigned)(tc * tr)), 256, 0, stream>>>(p, (int)tc);
-    return hipGetLastError();
-  }
-  // tiles of [0, 2F), with the row tensor's padding; those that begin below F, and those from the one that holds F on
-  const int64_t tc = ROWS ? (int64_t)p.rows.kq * (kTile / kGradCols) : (2 * p.F + kGradCols - 1) / kGradCols;
-  const int64_t below = p.F / kGradCols, pairs = tc - below > below ? tc - below : below;
-  const int64_t blocks = (pairs * tr + 7) / 8 * 16;
-  if (!mx_fits_grid(blocks, 256)) return hipErrorInvalidConfiguration;
-  k_mx_gated_grad_any<DT, ACT, ROWS, COLS><<<dim3((unsigned)blocks), 256, 0, stream>>>(p, (int)tc, (int)pairs);
+  const GradGrid g = grad_grid(p);
+  if (!mx_fits_grid(g.blocks, 256)) return hipErrorInvalidConfiguration;
+  if (g.pairs)
+    k_mx_gated_grad<DT, ACT, ROWS, COLS><<<dim3((unsigned)g.blocks), 256, 0, stream>>>(p, (int)g.tc);
+  else
+    k_mx_gated_grad_any<DT, ACT, ROWS, COLS><<<dim3((unsigned)g.blocks), 256, 0, stream>>>(p, (int)g.tc, (int)g.across);
   return hipGetLastError();
 }
 

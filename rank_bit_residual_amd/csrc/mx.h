@@ -86,10 +86,14 @@ struct MxGradParams {
   MxOut cols;  // 2F x M: the transpose
 };
 
-// A launch holds fewer than 2^32 threads along a dimension of its grid; a call past that is refused
-// (hipErrorInvalidConfiguration) before anything runs.
+// A launch holds fewer than 2^32 threads along a dimension of its grid; a launcher refuses more
+// (hipErrorInvalidConfiguration). A call of several launches asks mx_*_fits of each before the first, so that a refused call
+// has run nothing.
 inline bool mx_fits_grid(int64_t blocks, int threads) { return blocks < (int64_t)0x100000000 / threads; }
 
+bool mx_quantize_fits(const MxQuantParams& p);
+bool mx_gated_grad_fits(const MxGradParams& p);
+bool mx_product_fits(int64_t M, int64_t N, int kq, bool gated);
 hipError_t launch_mx_quantize(const MxQuantParams& p, int dtype, hipStream_t stream);
 hipError_t launch_mx_dequantize(const MxDequantParams& p, int dtype, hipStream_t stream);
 hipError_t launch_mx_gated_grad(const MxGradParams& p, int dtype, hipStream_t stream);
@@ -100,8 +104,9 @@ struct MxForm {
   int bm, bn, splits, waves;
 };
 MxForm mx_product_form(int64_t M, int64_t N, int kq, bool gated);
-// The block shape of the kernel for few rows.
+// The block shape of the kernel for few rows, and whether its grid fits.
 MxForm mx_decode_form(int64_t M, int64_t N, int kq, bool gated);
+bool mx_decode_fits(int64_t M, int64_t N, int kq, bool gated);
 // Whether the product's launch is that kernel (the only one that takes an unquantised A).
 bool mx_product_decodes(int64_t M, int64_t N, int kq, bool gated);
 // Bytes of float32 parts that the product's launch writes and reads (0: K is not split).

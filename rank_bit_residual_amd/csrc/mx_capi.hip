@@ -72,6 +72,11 @@ int check_strided(const void* x, int64_t sr, int64_t sc, int dtype, const char* 
   return SVDQ_OK;
 }
 
+// For calls of several launches, before the first.
+int check_grid(bool fits, const char* what) {
+  return fits ? SVDQ_OK : hip_status(hipErrorInvalidConfiguration, what);
+}
+
 // Row offsets inside a tile are 32-bit: 2 (kq + 1) KB.
 int check_product_k(int64_t K) {
   if (K > (int64_t)1 << 27) return set_error(SVDQ_EINVAL, "products take K up to 2^27");
@@ -170,6 +175,9 @@ int linear(const void* x, int64_t M, int64_t sr, int64_t sc, const Product& q, v
   p.a_codes = ws;
   p.a_scales = ws + codes;
   MxQuantParams a{x, M, q.K, sr, sc, out_of(ws, ws + codes, q.K), MxOut{}};
+  if ((st = check_grid(mx_quantize_fits(a), "mx_quantize launch")) ||
+      (st = check_grid(mx_product_fits(M, q.N, (int)mx_kq(q.K), q.gated), "MXFP4 product launch")))
+    return st;
   if ((st = hip_status(launch_mx_quantize(a, q.dtype, s), "mx_quantize launch"))) return st;
   return hip_status(launch_mx_product(p, q.gated, q.dtype, s), "MXFP4 product launch");
 }
@@ -318,6 +326,10 @@ int svdq_mx_gated_backward(const void* dh, int64_t ldh, const void* gu, int64_t 
   uint8_t* ws = (uint8_t*)workspace;
   hipStream_t s = (hipStream_t)stream;
   const MxGradParams p{dh, gu, M, F, ldh, ldgu, act, out_of(ws + at[0], ws + at[1], 2 * F), out_of(ws + at[2], ws + at[3], M)};
+  if ((st = check_grid(mx_gated_grad_fits(p), "mx_gated_grad launch")) ||
+      (st = check_grid(mx_product_fits(M, K, (int)mx_kq(2 * F), false), "launch of the product for dx")) ||
+      (st = check_grid(mx_product_fits(K, 2 * F, (int)mx_kq(M), false), "launch of the product for dw")))
+    return st;
   if ((st = hip_status(launch_mx_gated_grad(p, dtype, s), "mx_gated_grad launch"))) return st;
   MxGemmParams a = params_of(M, q_dx, ws + at[4]);
   a.a_codes = ws + at[0];

@@ -211,6 +211,20 @@ def test_launches_past_the_grid_are_refused():
     _refused(EINVAL, lib.svdq_mx_matmul(A, A, 1, A, A, big, 64, None, BF16, A, big, None, 0, None))
 
 
+def test_calls_of_several_launches_are_refused_whole():
+    """Every launch's grid is checked before the first one: where only the last does not fit, nothing runs. (Without a GPU a
+    launch that was tried would give EHIP.)"""
+    lib, room = _lib.load(), 1 << 60
+    M, N = 1 << 24, 1 << 17  # 2^24 tiles of 256 x 256
+    _refused(EINVAL, lib.svdq_mx_linear(A, M, 64, 64, 1, A, A, N, None, BF16, A, N, A, room, None))
+    _refused(EINVAL, lib.svdq_mx_gated_linear(A, M, 64, 64, 1, A, A, N // 2, 0, BF16, A, N // 2, None, 0, A, room, None))
+    # dx [M, K] does not fit, then dw [K, 2F] does not
+    F, K = 64, 1 << 17
+    _refused(EINVAL, lib.svdq_mx_gated_backward(A, F, A, 2 * F, M, F, 0, BF16, A, A, A, A, K, BF16, A, K, A, 2 * F, A, room, None))
+    F, K, M = 1 << 20, 1 << 24, 32
+    _refused(EINVAL, lib.svdq_mx_gated_backward(A, F, A, 2 * F, M, F, 0, BF16, A, A, A, A, K, BF16, A, K, A, 2 * F, A, room, None))
+
+
 def _linear_workspace(M, N, K, gated=0, dtype=None, sc=1):
     n, lib = ctypes.c_size_t(), _lib.load()
     if dtype is None:
