@@ -14,7 +14,8 @@ training (the quantisers pass gradients straight through):
     dx, dw = mx_gated_backward(dh, gu, w_rows, x_cols, act="silu")
 
 and in serving `h = mx_gated(x, w_cols)`, with w_cols kept. Every arithmetic step runs in libsvdq;
-tensors are float32, bfloat16 or float16 on a GPU.
+tensors are float32, bfloat16 or float16 on a GPU. The calls record no autograd graph: a training step runs them
+under torch.no_grad() or inside a torch.autograd.Function, and an input that requires grad is refused elsewhere.
 """
 from __future__ import annotations
 
@@ -101,7 +102,15 @@ def _matrix(t, name: str) -> int:
         raise RuntimeError("libsvdq device calls need tensors on an AMD GPU (HIP device)")
     if t.dim() != 2 or t.numel() == 0:
         raise ValueError(f"{name} must be a nonempty matrix")
+    _no_graph(t, name)
     return _dtype_code(t.dtype)
+
+
+def _no_graph(t: torch.Tensor, name: str) -> None:
+    """Refuses an input whose gradient would be lost in silence."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError(f"{name} requires grad, and this call records no graph: detach it, or call under torch.no_grad() or in a "
+                           "torch.autograd.Function (mx_gated_backward is the backward pass of mx_gated)")
 
 
 def _mx(t, name: str) -> None:
@@ -155,6 +164,7 @@ def _output(out, rows: int, cols: int, dtype, device, *inputs) -> torch.Tensor:
         raise ValueError(f"out must be a [{rows}, {cols}] {dtype} tensor on {device}")
     if (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols):
         raise ValueError("out must have unit column stride and rows that do not overlap")
+    _no_graph(out, "out")
     if any(t is not None and _overlap(out, t) for t in inputs):
         raise ValueError("out must not overlap an input")
     return out
@@ -231,6 +241,7 @@ def _product(a, b, names, dtype, out, bias=None, act=None, save=False) -> tuple:
     elif bias is not None:
         if bias.dim() != 1 or bias.shape[0] != N or bias.dtype != dtype:
             raise ValueError(f"bias must be a [{N}] tensor of the output's dtype")
+        _no_graph(bias, "bias")
         bias = bias.contiguous()
         extra = bias.data_ptr()
     y = _output(out, M, N, dtype, device, a if raw else a.data, b.data, bias)

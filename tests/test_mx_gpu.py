@@ -691,6 +691,47 @@ def test_binding_refusals():
             call()
 
 
+def test_inputs_that_require_grad():
+    """Refused where autograd would lose their gradient; taken under no_grad, in inference mode and in a Function."""
+    d = dev()
+    x, w = torch.randn(40, 64, device=d, requires_grad=True), torch.randn(64, 96, device=d, requires_grad=True)
+    bias, out = torch.zeros(96, device=d, requires_grad=True), torch.zeros(40, 96, device=d)
+    with torch.no_grad():
+        xr, xc = R.mx_quantize(x, axis=None)
+        wr, wc = R.mx_quantize(w, axis=None)
+        h, gu = R.mx_gated(x, wc, save=True)
+        dh = torch.randn_like(h)
+        want = R.mx_gated_backward(dh, gu, wr, xc)
+        y = R.mx_matmul(x, wc, bias=bias, out=out)
+    assert not h.requires_grad and not y.requires_grad
+    with torch.inference_mode():
+        assert torch.equal(R.mx_gated(x, wc), h)
+    assert torch.equal(R.mx_gated(x.detach(), wc), h)
+    leaf = dh.clone().requires_grad_()
+    for call in (lambda: R.mx_quantize(w), lambda: R.mx_matmul(x, wc), lambda: R.mx_matmul(x, wc, dtype=torch.bfloat16),
+                 lambda: R.mx_matmul(xr, wc, bias=bias, dtype=torch.float32), lambda: R.mx_gated(x, wc),
+                 lambda: R.mx_gated_grad(leaf, gu), lambda: R.mx_gated_backward(leaf, gu, wr, xc),
+                 lambda: R.mx_dequantize(xr, torch.float32, out=x)):
+        with pytest.raises(RuntimeError, match="requires grad"):
+            call()
+
+    class Gated(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w):
+            xr, ctx.x = R.mx_quantize(x, axis=None)
+            ctx.w, wc = R.mx_quantize(w, axis=None)
+            h, gu = R.mx_gated(xr, wc, dtype=x.dtype, save=True)
+            ctx.save_for_backward(gu)
+            return h
+
+        @staticmethod
+        def backward(ctx, dh):
+            return R.mx_gated_backward(dh, ctx.saved_tensors[0], ctx.w, ctx.x)
+
+    Gated.apply(x, w).backward(dh)
+    assert torch.equal(x.grad, want[0]) and torch.equal(w.grad, want[1])
+
+
 def test_float64_oracle_matches_the_library_rule():
     """The operators' codes are those of quantize_activations with a unit scale."""
     x = _gpu(_wide(np.random.default_rng(4), 20, 300), "bf16")
