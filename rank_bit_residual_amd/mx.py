@@ -188,13 +188,17 @@ def _workspace_bytes(name: str, *sizes) -> int:
     return need.value
 
 
+def _check_axis(axis) -> None:
+    if axis is not None and (isinstance(axis, bool) or axis not in (0, 1)):
+        raise ValueError("axis must be 0, 1 or None")
+
+
 def mx_quantize(x: torch.Tensor, axis: int | None = 1):
     """Q(x) of x [R, C] (any strides): with axis=1 the [R, C] MxTensor whose blocks run along the rows of
     x, with axis=0 the [C, R] MxTensor of its transpose, whose blocks run along its columns; with
     axis=None both, from one pass over x. A block with an infinity or a NaN reads as NaN."""
     dt = _matrix(x, "x")
-    if axis is not None and (isinstance(axis, bool) or axis not in (0, 1)):
-        raise ValueError("axis must be 0, 1 or None")
+    _check_axis(axis)
     (R, C), (sr, sc), device = x.shape, x.stride(), x.device
     rows = MxTensor._empty(R, C, device) if axis != 0 else None
     cols = MxTensor._empty(C, R, device) if axis != 1 else None
@@ -295,15 +299,18 @@ def _pre_activations(dh, gu) -> tuple:
     return dt, M, F, device, *_rows(dh), *_rows(gu)
 
 
-def mx_gated_grad(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu"):
+def mx_gated_grad(dh: torch.Tensor, gu: torch.Tensor, act: str = "silu", axis: int | None = None):
     """The gradients d = [dg | du] of a gated block's pre-activations, dg = dh * u * act'(g) and
-    du = dh * act(g), from dh [M, F] and gu [M, 2F]: Q(d) [M, 2F] and Q(d^T) [2F, M], from one pass."""
+    du = dh * act(g), from dh [M, F] and gu [M, 2F]: Q(d) [M, 2F] and Q(d^T) [2F, M], from one pass; with axis=1
+    Q(d) alone (all that dx needs), with axis=0 Q(d^T) alone (all that dw needs)."""
     code = _act_code(act)
+    _check_axis(axis)
     dt, M, F, device, dh, ldh, gu, ldgu = _pre_activations(dh, gu)
-    rows, cols = MxTensor._empty(M, 2 * F, device), MxTensor._empty(2 * F, M, device)
+    rows = MxTensor._empty(M, 2 * F, device) if axis != 0 else None
+    cols = MxTensor._empty(2 * F, M, device) if axis != 1 else None
     _call(L.load().svdq_mx_gated_grad, device.index, dh.data_ptr(), ldh, gu.data_ptr(), ldgu, M, F, code, dt, *_parts(rows),
           *_parts(cols))
-    return rows, cols
+    return (rows, cols) if axis is None else (rows if axis == 1 else cols)
 
 
 def mx_gated_backward(dh: torch.Tensor, gu: torch.Tensor, w_rows: MxTensor, x_cols: MxTensor, act: str = "silu",

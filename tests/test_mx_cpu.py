@@ -357,3 +357,12 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         R.mx_gated(x, _fake(8, 64), act="swish")
     with pytest.raises(ValueError):
         R.mx_gated_grad(x, x, act="tanh")
+
+
+@pytest.mark.parametrize("axis", [2, -1, True, "rows"])
+def test_axes_are_refused(axis):
+    x = torch.zeros(4, 64)
+    with pytest.raises((ValueError, RuntimeError)):
+        R.mx_quantize(x, axis=axis)
+    with pytest.raises(ValueError):
+        R.mx_gated_grad(x, torch.zeros(4, 128), axis=axis)

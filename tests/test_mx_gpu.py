@@ -370,6 +370,18 @@ def test_gated_grad(dtype, act, M, F):
 
 
 @pytest.mark.parametrize("act", X.ACTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,F", [(1, 1), (1, 96), (33, 31), (130, 64), (70, 129), (129, 260), (40, 32), (300, 416)])
+def test_gated_grad_in_one_direction(dtype, act, M, F):
+    """Each direction alone: the same codes and scale bytes as both from one pass, padding and all."""
+    rng = np.random.default_rng(M + F)
+    dh, gu = _gpu(rng.standard_normal((M, F)), dtype), _gpu(2 * rng.standard_normal((M, 2 * F)), dtype)
+    want = X.gated_grad(_np(dh), _np(gu), act)
+    _check_tensor(R.mx_gated_grad(dh, gu, act=act, axis=1), want)
+    _check_tensor(R.mx_gated_grad(dh, gu, act=act, axis=0), want.T)
+
+
+@pytest.mark.parametrize("act", X.ACTS)
 def test_gated_grad_far_pre_activations(act):
     """Pre-activations at both ends, where a sigmoid or its complement has few digits in float32, and around
     the zero of act', in blocks of their own so that each decides its block's scale."""
