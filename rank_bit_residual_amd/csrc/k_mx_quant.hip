@@ -220,12 +220,6 @@ __device__ __forceinline__ u32 ends_differ(float v, float err) {
   const float a = fabsf(v);
   return __float_as_uint(a - err) ^ __float_as_uint(a + err);
 }
-// The same where v may be a NaN although the formula's value is finite (an infinite dh * u times a derivative of 0): never
-// settled, since the larger of a NaN and 0 is 0.
-__device__ __forceinline__ u32 ends_differ_or_nan(float v, float err) {
-  const float a = fabsf(v);
-  return __float_as_uint(a - err) ^ __float_as_uint(fmaxf(a + err, 0.f));
-}
 
 // The 16 bits for a binary64 gradient (from infinity on, any of those mark a block).
 __device__ inline u32 to_odd16(double v) {
@@ -282,7 +276,7 @@ struct GradIn {
 template <class DT, int ACT, bool GATE, bool UP>
 __device__ __forceinline__ void grad8(const GradIn<DT>& x, Vec8<MxBF16>& dg, Vec8<MxBF16>& du) {
   u32 differ[4];
-  float tail = 0.f;
+  float tail = 0.f, reach = 0.f;
 #pragma unroll
   for (int h = 0; h < 4; h++) {
     float vg[2], vu[2];
@@ -294,8 +288,9 @@ __device__ __forceinline__ void grad8(const GradIn<DT>& x, Vec8<MxBF16>& dg, Vec
       tail = r.tail < tail ? r.tail : tail;
       if (GATE) {
         const float a = dh * elem<DT>(x.u, 2 * h + k);
+        if (DT::wide) reach += fabsf(a);
         vg[k] = a * r.d;
-        differ[h] |= ends_differ_or_nan(vg[k], fabsf(a) * r.abs_d);
+        differ[h] |= ends_differ(vg[k], fabsf(a) * r.abs_d);
       }
       if (UP) {
         vu[k] = dh * r.a;
@@ -305,7 +300,8 @@ __device__ __forceinline__ void grad8(const GradIn<DT>& x, Vec8<MxBF16>& dg, Vec
     if (GATE) dg.w[h] = odd_pair(vg[0], vg[1]);
     if (UP) du.w[h] = odd_pair(vu[0], vu[1]);
   }
-  const bool far = tail < -60.f;
+  // an infinite dh * u: times a derivative of 0 it is a NaN, whose two ends agree, though the formula's value may be finite
+  const bool far = tail < -60.f || !(reach < __builtin_inff());
   if (!((differ[0] >= kOpen) | (differ[1] >= kOpen) | (differ[2] >= kOpen) | (differ[3] >= kOpen) | far)) return;
 #pragma unroll 1
   for (int q = 0; q < 8; q++) {

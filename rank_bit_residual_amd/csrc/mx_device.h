@@ -11,16 +11,19 @@
 namespace svdq {
 namespace dev {
 
-// Storage types: `pair` is two 16-bit values in one word (the lower index in the low half).
+// Storage types: `pair` is two 16-bit values in one word (the lower index in the low half); wide: a product of two values may
+// pass the float32 range.
 struct MxF32 {
   typedef float T;
   static constexpr int size = 4;
+  static constexpr bool wide = true;
   __device__ static inline float load(T v) { return v; }
   __device__ static inline T store(float v) { return v; }
 };
 struct MxBF16 {
   typedef uint16_t T;
   static constexpr int size = 2;
+  static constexpr bool wide = true;
   __device__ static inline float load(T v) { return __uint_as_float((u32)v << 16); }
   __device__ static inline T store(float v) { return (T)pack_bf16x2(v, v); }
   __device__ static inline u32 pack(float a, float b) { return pack_bf16x2(a, b); }
@@ -30,6 +33,7 @@ struct MxBF16 {
 struct MxF16 {
   typedef uint16_t T;
   static constexpr int size = 2;
+  static constexpr bool wide = false;
   __device__ static inline float load(T v) { return (float)__builtin_bit_cast(_Float16, v); }
   __device__ static inline T store(float v) { return __builtin_bit_cast(T, (_Float16)v); }
   __device__ static inline u32 pack(float a, float b) { return (u32)store(a) | ((u32)store(b) << 16); }
