@@ -25,6 +25,7 @@ import functools
 import torch
 
 from . import _lib as L
+from .api import _check_int
 
 _DT = {torch.float32: L.SVDQ_F32, torch.bfloat16: L.SVDQ_BF16, torch.float16: L.SVDQ_F16}
 _ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
@@ -47,6 +48,8 @@ class MxTensor:
     __slots__ = ("data", "rows", "cols", "_at")
 
     def __init__(self, data: torch.Tensor, rows: int, cols: int):
+        _check_int("rows", rows)
+        _check_int("cols", cols)
         code_bytes, scale_bytes = _bytes(rows, cols)
         if not isinstance(data, torch.Tensor) or data.dtype != torch.uint8 or data.dim() != 1 or not data.is_contiguous():
             raise TypeError("data must be a contiguous uint8 vector")

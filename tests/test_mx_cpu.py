@@ -366,3 +366,11 @@ def test_axes_are_refused(axis):
         R.mx_quantize(x, axis=axis)
     with pytest.raises(ValueError):
         R.mx_gated_grad(x, torch.zeros(4, 128), axis=axis)
+
+
+@pytest.mark.parametrize("rows,cols", [(4.0, 64), (4, 64.0), (True, 64), ("4", 64), (None, 4)])
+def test_tensor_sizes_are_whole_numbers(rows, cols):
+    data = torch.zeros(1 << 16, dtype=torch.uint8)
+    assert R.MxTensor(data, 4, 64).shape == (4, 64) and R.MxTensor(data, 1, 64).shape == (1, 64)
+    with pytest.raises(ValueError, match="int"):
+        R.MxTensor(data, rows, cols)
