@@ -402,6 +402,9 @@ int svdq_mx_matmul(const void* a_codes, const void* a_scales, int64_t M, const v
  * svdq_mx_gated — the gated projections of a feed-forward block in one kernel:
  *   [g | u] = A W^T,  h = D( act(g) * u )
  * a [M, K]; w [2F, K]: the F gate rows, then the F up rows. act is applied to the float32 sums.
+ * act is computed in float32 for every output type, within (3 + |w|) 2^-21 of its value for silu (w = g) and
+ * gelu_tanh (w = 2 sqrt(2 / pi) (g + 0.044715 g^3)) and (3 + g^2) 2^-20 for gelu, down to where a factor nears the
+ * bottom of the range (w = -60, g = -10: |act| < 2^-70), below which it may be 0; relu is exact.
  * h: [M, F], row stride ldh >= F. gu: NULL, or [M, 2F] (row stride ldgu >= 2F) receiving
  * D(g) | D(u) for svdq_mx_gated_grad. K and workspace as above. Errors: EINVAL, EDTYPE, EHIP.
  * ------------------------------------------------------------------------------------ */

@@ -224,16 +224,16 @@ static hipError_t launch_rows(const MxGemmParams& p, hipStream_t stream) {
 }
 
 // Column tiles and waves of a block (MxForm: bn = 16 column tiles, waves). A gated block has a gate tile and an up tile.
-// Others, by the column tiles there are on 256 compute units; measured on the GPU's clock, us:
+// Others, by the column tiles there are on 256 compute units; measured at K x N on the GPU's clock, us:
 //   up to 256    one tile, eight waves: a block for every compute unit matters most. 8192 x 4096 at one row 5.8, 6.2 with two
 //   257 to 512   two tiles, so that a compute unit's blocks are one: 8192 x 5120 at 16 rows 7.7 against 8.7, 8192 x 8192 8.9
 //                against 9.7 (1024 x 6000 3.4 both)
 //   more         past 16 rows two tiles, so that a's operands serve twice: 8192 x 16384 at 32 rows 17.2, 22.7 with one tile,
-//                at 64 rows 23.4 and 34.6. Up to 16 rows, or 32 rows of up to eight stages (1024 x 12288 at 32 rows 4.2, with two
-//                tiles 4.4), one tile; with four waves below 64 stages, so that more blocks run at
-//                once (1024 x 16384 at one row 3.9, 4.5 with eight waves, 4096 x 12288 7.6 and 8.5, 7168 x 12288 10.9 and
-//                11.9), with eight from there on, where the waves' own chains of stages count (8192 x 16384 16.4, 21.1 with
-//                four, 16384 x 16384 28.9 and 31.0, 28672 x 9216 32.0 and 31.8)
+//                at 64 rows 23.4 and 34.6. Up to 16 rows, or 32 rows of up to eight stages (1024 x 12288 at 32 rows 4.2,
+//                with two tiles 4.4), one tile. Four waves below 64 stages, so that more blocks run at once (1024 x 16384
+//                at one row 3.9, 4.5 with eight waves, 4096 x 12288 7.6 and 8.5, 7168 x 12288 10.9 and 11.9); eight from
+//                there on, where the waves' own chains of stages count (8192 x 16384 16.4, 21.1 with four, 16384 x 16384
+//                28.9 and 31.0, 28672 x 9216 32.0 and 31.8)
 MxForm mx_decode_form(int64_t M, int64_t N, int kq, bool gated) {
   const int bm = M <= 16 ? 16 : (M <= 32 ? 32 : 64);
   if (gated) return MxForm{bm, 32, 1, 8};

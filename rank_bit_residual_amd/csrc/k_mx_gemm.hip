@@ -442,7 +442,7 @@ struct MxPlan {
 // 2*8192 39.9 us on 256 x 256 against 45.4 on 128 x 128.
 // Shares of K add the joining launch and the parts' way through memory at 4 TB/s.
 // Against few rows, tiles take no less than b's bytes from memory at 5 TB/s, and, for one row, a launch more, as the few-row kernel
-// quantises that itself. One row, the best tiles and the few-row kernel, us: 28672 x 8192 32.6 and 25.3; 16384 x 16384 34.8 and
+// quantises that itself. One row at K x N, the best tiles and the few-row kernel, us: 28672 x 8192 32.6 and 25.3; 16384 x 16384 34.8 and
 // 29.4; 65536 x 4096 37.5 and 27.7; 4096 x 128256 55 and 49; 28672 x 1024 13.5 and 10.0; 65536 x 256 12.7 and 14.7.
 static MxPlan plan_of(int64_t M, int64_t N, int kq, bool gated) {
   const double b_rows = (double)N * (gated ? 2 : 1), millions = b_rows * kq * 128 * 1e-6, mb = millions * 17 / 32;
