@@ -343,7 +343,7 @@ int svdq_calibrate_scale(const void* x, int64_t B, int64_t M, int64_t ldx, const
  * of 64 rows x 4 blocks (rows rounded up to 64). The padding along K is written as zeros; the
  * padding rows are neither written nor read.
  *
- * dtype is SVDQ_F32, SVDQ_BF16 or SVDQ_F16 (the other calls of this header take no SVDQ_F16).
+ * dtype is SVDQ_F32, SVDQ_BF16 or SVDQ_F16 (svdq_i8_* and svdq_layer_norm* take it too, the other calls of this header do not).
  * Sizes are 1 .. 2^30, and the arrays' sizes are what memory holds: offsets are 64-bit. (EINVAL where a
  * launch would hold 2^32 threads, which takes 2^26 rows or 2^35 elements at least.) Outputs and the
  * workspace must not overlap the inputs or each other. The calls keep no state; two calls on two streams
@@ -457,6 +457,107 @@ int svdq_mx_gated_backward(const void* dh, int64_t ldh, const void* gu, int64_t 
                            int dtype, const void* w_codes, const void* w_scales, const void* x_codes,
                            const void* x_scales, int64_t K, int out_dtype, void* dx, int64_t lddx, void* dw,
                            int64_t lddw, void* workspace, size_t workspace_bytes, svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
+ * 8-bit tensors with a scale for each row, made on the device. An 8-bit tensor of rows x K holds Q(x) of a matrix whose
+ * products sum over K: for each row a float32 scale s, float32(max|x| / 127) and 2^-126 at least (0 for a row of zeros), and
+ * codes in [-127, 127], the integers nearest to x / s, ties to even. The quotient is the real one: a code never depends on
+ * how a division was rounded. A row with an infinity or a NaN has the scale NaN and codes 0 and reads as NaN, and so does
+ * every output that it enters.
+ *
+ * Two caller-owned device arrays, both 256-byte aligned, of svdq_i8_layout's sizes: the codes as int8 in 1 KB tiles of 16 rows
+ * x 64 codes (code k of row r at ((r / 16) kq + k / 64) 1024 + (r % 16) 64 + k % 64 with kq = 2 ceil(K / 128); rows rounded up
+ * to 16), the scales as float32 [rows] (rounded up to 64). The padding along K is written as zeros; the padding rows are
+ * neither written nor used.
+ *
+ * Types, sizes, overlap and streams are as for the MXFP4 tensors above; a workspace is device scratch of any contents, 256-byte
+ * aligned, NULL where its query gives 0, one for each of the calls that may overlap in time. Integer sums are exact; K is at
+ * most 2^26 in products. Equal calls give equal bits.
+ * ------------------------------------------------------------------------------------ */
+/* Bytes of the two arrays of a rows x K tensor (multiples of 256, so that they may share one buffer). Errors: EINVAL. */
+int svdq_i8_layout(int64_t rows, int64_t K, size_t* code_bytes, size_t* scale_bytes);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_i8_quantize — Q(x) and / or Q(x^T) of x [R, C] (strides sr, sc >= 0 in elements). codes / scales: the R x C tensor (a
+ * scale for each row); codes_t / scales_t: the C x R tensor (a scale for each column). Either pair may be NULL, not both.
+ * workspace: svdq_i8_quantize_workspace_bytes, with rows and cols whether the pairs are given.
+ * Errors: EINVAL (shape, strides, alignment, workspace, nothing to do), EDTYPE, EHIP.
+ * ------------------------------------------------------------------------------------ */
+int svdq_i8_quantize_workspace_bytes(int64_t R, int64_t C, int64_t sr, int64_t sc, int rows, int cols, size_t* bytes_out);
+int svdq_i8_quantize(const void* x, int64_t R, int64_t C, int64_t sr, int64_t sc, int dtype, void* codes, void* scales,
+                     void* codes_t, void* scales_t, void* workspace, size_t workspace_bytes, svdq_stream_t stream);
+
+/* svdq_i8_dequantize — float32(code * s) of a rows x K tensor, rounded to dtype, out [rows, K] with row stride ldo. Errors as
+ * above. */
+int svdq_i8_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, int dtype, void* out, int64_t ldo,
+                       svdq_stream_t stream);
+
+/* Workspace of svdq_i8_matmul, and the form that a product takes (host queries; form as in svdq_mx_product_form).
+ * Errors: EINVAL. */
+int svdq_i8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes_out);
+int svdq_i8_product_form(int64_t M, int64_t N, int64_t K, int form[4]);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_i8_matmul — y = D( (sum_k a[m, k] b[n, k]) sa[m] sb[n] + bias[n] ) of two 8-bit tensors a [M, K] and b [N, K]: the sum is
+ * exact, the scales and the bias enter in float32 (at most three roundings of 2^-24 each of the product, one of the sum with the bias;
+ * in binary64 where a scale lies outside [2^-60, 2^40], or K is shared out), one rounding to dtype. bias: [N] of dtype, or NULL.
+ * y: [M, N] of dtype, row stride ldy >= N. workspace: svdq_i8_workspace_bytes.
+ * Errors: EINVAL (shape, stride, alignment, workspace), EDTYPE, EHIP.
+ * ------------------------------------------------------------------------------------ */
+int svdq_i8_matmul(const void* a_codes, const void* a_scales, int64_t M, const void* b_codes, const void* b_scales, int64_t N,
+                   int64_t K, const void* bias, int dtype, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                   svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_i8_linear — that product of x [M, K] (strides sr, sc in elements) that is not quantised yet: svdq_i8_quantize along its
+ * rows, then the product, with the same results. Few rows are quantised inside the product's kernel, others into the workspace.
+ * x has the output's dtype. workspace: svdq_i8_linear_workspace_bytes. Errors as above.
+ * ------------------------------------------------------------------------------------ */
+int svdq_i8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t sr, int64_t sc, int dtype, size_t* bytes_out);
+int svdq_i8_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_t sc, const void* b_codes, const void* b_scales, int64_t N,
+                   const void* bias, int dtype, void* y, int64_t ldy, void* workspace, size_t workspace_bytes, svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_i8_backward — the backward pass of y = Q(x) Q(w^T)^T + b with w [K, N] in one call: Q(dy) and Q(dy^T) of dy [M, N] (row
+ * stride lddy >= N, of dtype) into the workspace, then dx = Q(dy) Q(w)^T [M, K] and dw = Q(x^T) Q(dy^T)^T [K, N] by
+ * svdq_i8_matmul, with the same results, and db [N] = the sums of dy's columns (summed in float32 over up to 256 strips of
+ * rows, the strips in binary64), unless db is NULL. w_codes / w_scales: w quantised along its rows; x_codes / x_scales: x^T,
+ * [K, M], the input quantised along its columns. out_dtype: of dx, dw and db. M and N are at most 2^26.
+ * workspace: svdq_i8_backward_workspace_bytes. Errors: EINVAL, EDTYPE, EHIP.
+ * ------------------------------------------------------------------------------------ */
+int svdq_i8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes_out);
+int svdq_i8_backward(const void* dy, int64_t lddy, int64_t M, int64_t N, int dtype, const void* w_codes, const void* w_scales,
+                     const void* x_codes, const void* x_scales, int64_t K, int out_dtype, void* dx, int64_t lddx, void* dw,
+                     int64_t lddw, void* db, void* workspace, size_t workspace_bytes, svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_layer_norm, _i8, _mx — y = (x - mean) / sqrt(var + eps) * weight + bias of each row of x [M, K] (row stride ldx >= K, of
+ * dtype), with mean = sum x / K and var = sum (x - mean)^2 / K. All of it is computed in binary64 and rounded to float32 once;
+ * svdq_layer_norm rounds on to dtype (y, row stride ldy >= K), _i8 and _mx write the 8-bit or MXFP4 tensor of the float32
+ * values (the arrays of svdq_i8_layout or svdq_mx_layout for M x K), ready for a product. weight, bias: [K] of param_dtype,
+ * dtype or SVDQ_F32; both NULL, or bias alone. eps: finite, >= 0. mean, rstd: float32 [M] receiving mean and 1 / sqrt(var + eps), or
+ * both NULL. A row with an infinity or a NaN is NaN throughout. Errors: EINVAL, EDTYPE, EHIP.
+ * ------------------------------------------------------------------------------------ */
+int svdq_layer_norm(const void* x, int64_t ldx, int64_t M, int64_t K, const void* weight, const void* bias, int param_dtype,
+                    double eps, int dtype, void* y, int64_t ldy, float* mean, float* rstd, svdq_stream_t stream);
+int svdq_layer_norm_i8(const void* x, int64_t ldx, int64_t M, int64_t K, const void* weight, const void* bias, int param_dtype,
+                       double eps, int dtype, void* codes, void* scales, float* mean, float* rstd, svdq_stream_t stream);
+int svdq_layer_norm_mx(const void* x, int64_t ldx, int64_t M, int64_t K, const void* weight, const void* bias, int param_dtype,
+                       double eps, int dtype, void* codes, void* scales, float* mean, float* rstd, svdq_stream_t stream);
+
+/* --------------------------------------------------------------------------------------
+ * svdq_layer_norm_backward — the backward pass, with xh = (x - mean) rstd and g = dy weight (dy without one):
+ *   dx = rstd (g - mean over the row of g - xh times the mean over the row of g xh),
+ *   dweight = sum over the rows of dy xh, dbias = sum over the rows of dy,
+ * in float32, rounded once. dy, x, dx: [M, K] of dtype with row strides >= K; mean, rstd: as the forward call left them;
+ * weight: [K] of param_dtype (dtype or SVDQ_F32) or NULL; dweight, dbias: [K] of param_dtype, given with a weight and NULL
+ * without. workspace: svdq_layer_norm_backward_workspace_bytes, params whether a weight is given.
+ * Errors: EINVAL, EDTYPE, EHIP.
+ * ------------------------------------------------------------------------------------ */
+int svdq_layer_norm_backward_workspace_bytes(int64_t M, int64_t K, int params, size_t* bytes_out);
+int svdq_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* mean, const float* rstd, int64_t M,
+                             int64_t K, const void* weight, int param_dtype, int dtype, void* dx, int64_t lddx, void* dweight,
+                             void* dbias, void* workspace, size_t workspace_bytes, svdq_stream_t stream);
 
 /* --------------------------------------------------------------------------------------
  * Kernel timing (profiling aid; not on any page). Between svdq_profile_begin and

@@ -68,13 +68,35 @@ SIGNATURES = {
     "svdq_mx_gated_backward_workspace_bytes": (c_int, [c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)]),
     "svdq_mx_gated_backward": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_vp, c_vp, c_vp, c_vp,
                                        c_i64, c_int, c_vp, c_i64, c_vp, c_i64, c_vp, c_sz, c_vp]),
+    "svdq_i8_layout": (c_int, [c_i64, c_i64, ctypes.POINTER(c_sz), ctypes.POINTER(c_sz)]),
+    "svdq_i8_quantize_workspace_bytes": (c_int, [c_i64, c_i64, c_i64, c_i64, c_int, c_int, ctypes.POINTER(c_sz)]),
+    "svdq_i8_quantize": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "svdq_i8_dequantize": (c_int, [c_vp, c_vp, c_i64, c_i64, c_int, c_vp, c_i64, c_vp]),
+    "svdq_i8_workspace_bytes": (c_int, [c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)]),
+    "svdq_i8_product_form": (c_int, [c_i64, c_i64, c_i64, ctypes.POINTER(c_int)]),
+    "svdq_i8_matmul": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_vp, c_i64, c_vp, c_sz, c_vp]),
+    "svdq_i8_linear_workspace_bytes": (c_int, [c_i64, c_i64, c_i64, c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]),
+    "svdq_i8_linear": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_int, c_vp, c_i64, c_vp, c_sz,
+                               c_vp]),
+    "svdq_i8_backward_workspace_bytes": (c_int, [c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)]),
+    "svdq_i8_backward": (c_int, [c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp, c_vp, c_i64, c_int, c_vp, c_i64, c_vp,
+                                 c_i64, c_vp, c_vp, c_sz, c_vp]),
+    "svdq_layer_norm": (c_int, [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_int, ctypes.c_double, c_int, c_vp, c_i64, c_vp,
+                                c_vp, c_vp]),
+    "svdq_layer_norm_i8": (c_int, [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_int, ctypes.c_double, c_int, c_vp, c_vp, c_vp,
+                                   c_vp, c_vp]),
+    "svdq_layer_norm_mx": (c_int, [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_int, ctypes.c_double, c_int, c_vp, c_vp, c_vp,
+                                   c_vp, c_vp]),
+    "svdq_layer_norm_backward_workspace_bytes": (c_int, [c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]),
+    "svdq_layer_norm_backward": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_int, c_vp, c_i64,
+                                         c_vp, c_vp, c_vp, c_sz, c_vp]),
 }
 NSTAGES = 4
 STAGE_NAMES = ("amax", "act_quant_down", "down_reduce", "gemm")
 
 SVDQ_OK, SVDQ_EINVAL, SVDQ_EDTYPE, SVDQ_EUNSUPPORTED, SVDQ_EHIP = 0, 1, 2, 3, 4
 SVDQ_F32, SVDQ_BF16, SVDQ_F64 = 0, 1, 2
-SVDQ_F16 = 3  # svdq_mx_* only
+SVDQ_F16 = 3  # svdq_mx_*, svdq_i8_* and svdq_layer_norm* only
 SVDQ_FMT_INT, SVDQ_FMT_MX = 0, 1
 SEC_SCALE, SEC_RCODES, SEC_RSCALES, SEC_L1T, SEC_L2T, SEC_RECIP, SEC_GLOBAL, SEC_END = 0, 1, 2, 3, 4, 5, 6, 7
 NSEC = 8

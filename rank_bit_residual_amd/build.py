@@ -35,6 +35,11 @@ HIP_SOURCES = {
     "k_mx_gemm.hip": [],
     "k_mx_decode.hip": [],
     "mx_capi.hip": [],
+    "k_i8_quant.hip": ["-ffp-contract=off"],
+    "k_i8_gemm.hip": [],
+    "k_i8_decode.hip": ["-ffp-contract=off"],
+    "k_norm.hip": ["-ffp-contract=off"],
+    "i8_capi.hip": [],
     "capi.hip": [],
 }
 CXX = os.environ.get("CXX", "g++")

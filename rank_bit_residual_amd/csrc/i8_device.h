@@ -1,0 +1,105 @@
+// Device helpers of the 8-bit tensor and layer norm kernels: reductions over a wave and a block, and the codes of values.
+#pragma once
+
+#include "mx_device.h"
+
+namespace svdq {
+namespace dev {
+
+// ---- reductions ---------------------------------------------------------------------------
+// Lane exchanges within a row of 16 (DPP): lanes 1, 2, 4 (mirrored halves) and 8 (mirrored row) apart.
+template <int CTRL>
+__device__ inline u32 dpp(u32 v) {
+  return (u32)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kQuad1 = 0xB1, kQuad2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+template <int CTRL>
+__device__ inline double dpp(double v) {
+  const u64 u = __builtin_bit_cast(u64, v);
+  return __builtin_bit_cast(double, (u64)dpp<CTRL>((u32)u) | ((u64)dpp<CTRL>((u32)(u >> 32)) << 32));
+}
+template <int CTRL>
+__device__ inline float dpp(float v) {
+  return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+__device__ inline u32 lane_of(u32 v, int lane) { return (u32)__builtin_amdgcn_readlane((int)v, lane); }
+__device__ inline float lane_of(float v, int lane) { return __uint_as_float(lane_of(__float_as_uint(v), lane)); }
+__device__ inline double lane_of(double v, int lane) {
+  const u64 u = __builtin_bit_cast(u64, v);
+  return __builtin_bit_cast(double, (u64)lane_of((u32)u, lane) | ((u64)lane_of((u32)(u >> 32), lane) << 32));
+}
+
+// Over all 64 lanes of a wave (all of them active), the same value in every lane.
+template <class V>
+__device__ inline V wave_sum(V v) {
+  v += dpp<kQuad1>(v);
+  v += dpp<kQuad2>(v);
+  v += dpp<kHalfMirror>(v);
+  v += dpp<kMirror>(v);
+  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
+__device__ inline u32 wave_umax(u32 v) {
+  v = max(v, dpp<kQuad1>(v));
+  v = max(v, dpp<kQuad2>(v));
+  v = max(v, dpp<kHalfMirror>(v));
+  v = max(v, dpp<kMirror>(v));
+  return max(max(lane_of(v, 0), lane_of(v, 16)), max(lane_of(v, 32), lane_of(v, 48)));
+}
+
+// ---- 8-bit codes --------------------------------------------------------------------------
+// A row's scale from the bits of its largest magnitude: float32(max / 127), 2^-126 at least (so that every step below is
+// exact), 0 for a row of zeros, NaN if the row holds an infinity or a NaN.
+struct Scale8 {
+  float s;  // as stored
+  float r;  // float32(1 / s); 0 where every code is 0
+};
+__device__ inline Scale8 scale8(u32 amax_bits) {
+  if (amax_bits >= 0x7F800000u) return {__uint_as_float(0x7FC00000u), 0.f};
+  if (amax_bits == 0) return {0.f, 0.f};
+  const float s = fmaxf(__uint_as_float(amax_bits) / 127.0f, 0x1p-126f);
+  return {s, 1.0f / s};
+}
+
+// The nearest integer to x / s, ties to even, in the low byte.
+// x r differs from x / s by less than 127 * 2^-24 + 2^-24 < 2^-16.9, so adding 1.5 * 2^23 to it (one rounding, to an integer)
+// gives that integer unless x r lies within 2^-16 of a border, and how far it lies from the integer says which. There the
+// remainder x - k s decides, which one fma gives exactly: it is at most s / 2 (1 + 2^-15) in size and a multiple of the
+// smaller unit of x and s.
+constexpr float kMagic8 = 12582912.f, kSure8 = 0.5f - 0x1p-16f;
+__device__ inline float code8_fast(float x, float r, float& far) {
+  const float u = __builtin_fmaf(x, r, kMagic8);
+  far = fmaxf(far, fabsf(__builtin_fmaf(x, r, kMagic8 - u)));
+  return u;
+}
+__device__ inline float code8_sure(float x, float s, float r) {
+  const float u = __builtin_fmaf(x, r, kMagic8);
+  const float k = u - kMagic8, rem = __builtin_fmaf(-k, s, x), half = 0.5f * s, size = fabsf(rem);
+  const bool odd = __float_as_uint(u) & 1u;
+  if (size > half || (size == half && odd)) return u + (rem > 0.f ? 1.f : -1.f);
+  return u;
+}
+__device__ inline u32 bytes4(float a, float b, float c, float d) {
+  const u32 lo = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x0C0C0400u);
+  const u32 hi = __builtin_amdgcn_perm(__float_as_uint(d), __float_as_uint(c), 0x04000C0Cu);
+  return lo | hi;
+}
+
+// Eight codes of v[0..7], in order.
+__device__ inline v2u codes8x8(const float (&v)[8], const Scale8& q) {
+  float u[8], far = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; k++) u[k] = code8_fast(v[k], q.r, far);
+  if (far > kSure8) {
+    asm volatile("");  // rarely taken: keep it a branch
+#pragma unroll
+    for (int k = 0; k < 8; k++) u[k] = code8_sure(v[k], q.s, q.r);
+  }
+  const v2u c = {bytes4(u[0], u[1], u[2], u[3]), bytes4(u[4], u[5], u[6], u[7])};
+  return q.r == 0.f ? v2u{0, 0} : c;
+}
+
+// Where code k of row r lies.
+__device__ inline int64_t i8_at(int64_t r, int64_t k, int kq) { return (((r >> 4) * kq + (k >> 6)) << 10) + ((r & 15) << 6) + (k & 63); }
+
+}  // namespace dev
+}  // namespace svdq

@@ -1,0 +1,226 @@
+// Products of 8-bit tensors for few rows (decode steps), bound by reading b once for each 64 rows of A.
+//
+// v_mfma_i32_16x16x64_i8 takes 16 rows of A against 16 rows of b, a stage of 64 codes at a time; lane (i, g) holds codes
+// [16 g, 16 g + 16) of row i of either. A block of waves owns 16 NT output columns and splits K evenly over its waves; every byte of
+// b is used once, so it goes straight into registers, a contiguous kilobyte per 16 rows and stage, several stages of requests in
+// flight. The waves' partial tiles are added in LDS (exact: K is at most 2^17 here).
+//
+// A may be given unquantised (RAW): every block then takes the maxima of x's rows for itself and lays its codes in LDS, which costs
+// vector instructions next to the reads of b but no launch. Its first reads of b are on their way meanwhile.
+#include "i8.h"
+#include "i8_device.h"
+
+namespace svdq {
+namespace dev {
+
+template <class DT, int MT, int NT, int WAVES, bool RAW>
+__global__ __launch_bounds__(64 * WAVES) void k_i8_decode(I8GemmParams p) {
+  typedef typename DT::T T;
+  constexpr int BATCH = MT * NT >= 4 ? 4 : 8;
+  __shared__ int red[WAVES][MT][NT][4][64];
+  __shared__ float row_scale[16];
+  __shared__ u32 row_max[WAVES][16];
+  extern __shared__ __align__(16) uint8_t xcodes[];  // RAW: [M][64 kq]
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  // blocks i, i + 8, ... share an XCD: each takes a run of columns
+  const int run = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  const int64_t n0 = (int64_t)run * 16 * NT;
+  const int m0 = blockIdx.y * 16 * MT;
+  if (n0 >= p.N) return;
+  const int s0 = (int)((int64_t)wave * p.kq / WAVES), s1 = (int)((int64_t)(wave + 1) * p.kq / WAVES);
+
+  const uint8_t* bc[NT];
+#pragma unroll
+  for (int n = 0; n < NT; n++) {
+    const int64_t row = n0 + 16 * n + i;
+    bc[n] = p.b_codes + i8_at(row < p.N ? row : p.N - 1, 16 * g, p.kq);
+  }
+  const uint8_t* ac[MT];
+  if constexpr (!RAW) {
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+      const int row = m0 + 16 * m + i;
+      ac[m] = p.a_codes + i8_at(row < p.M ? row : p.M - 1, 16 * g, p.kq);
+    }
+  }
+
+  v4i acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; m++)
+#pragma unroll
+    for (int n = 0; n < NT; n++) acc[m][n] = v4i{0, 0, 0, 0};
+
+  struct Step {
+    v4i b[NT], a[RAW ? 1 : MT];
+  };
+  auto load = [&](Step& q, int s) {
+#pragma unroll
+    for (int n = 0; n < NT; n++) q.b[n] = *reinterpret_cast<const v4i*>(bc[n] + (int64_t)s * 1024);
+    if constexpr (!RAW) {
+#pragma unroll
+      for (int m = 0; m < MT; m++) q.a[m] = *reinterpret_cast<const v4i*>(ac[m] + (int64_t)s * 1024);
+    }
+  };
+  // RAW: rows past M repeat the last
+  const uint8_t* xrow = xcodes + (int64_t)(i < p.M ? i : p.M - 1) * p.kq * 64 + 16 * g;
+  auto step = [&](const Step& q, int s) {
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+      v4i a;
+      if constexpr (RAW)
+        a = *reinterpret_cast<const v4i*>(xrow + s * 64);
+      else
+        a = q.a[m];
+#pragma unroll
+      for (int n = 0; n < NT; n++) acc[m][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, q.b[n], acc[m][n], 0, 0, 0);
+    }
+  };
+
+  int s = s0;
+  Step ahead[RAW ? BATCH : 1];
+  if constexpr (RAW) {
+    // the first batch of b, requested before x is looked at (a repeated stage is loaded, not used)
+#pragma unroll
+    for (int u = 0; u < BATCH; u++) load(ahead[u], s0 + u < p.kq ? s0 + u : p.kq - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    // a wave takes the stages of its share of every row
+    const T* x = reinterpret_cast<const T*>(p.x);
+    for (int m = 0; m < p.M; m++) {
+      u32 most = 0;
+      for (int64_t c = (int64_t)s0 * 64 + 8 * lane; c < (int64_t)s1 * 64; c += 512)
+        most = max(most, amax_bits<DT>(load8<DT>(x + m * p.ldx, c, p.K).w));
+      most = wave_umax(most);
+      if (lane == 0) row_max[wave][m] = most;
+    }
+    lds_barrier();
+    for (int m = 0; m < p.M; m++) {
+      u32 most = 0;
+#pragma unroll
+      for (int w = 0; w < WAVES; w++) most = max(most, row_max[w][m]);
+      const Scale8 q = scale8(most);
+      if (t == 0) row_scale[m] = q.s;
+      for (int64_t c = (int64_t)s0 * 64 + 8 * lane; c < (int64_t)s1 * 64; c += 512) {
+        const Vec8<DT> v = load8<DT>(x + m * p.ldx, c, p.K);
+        float e[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) e[k] = elem<DT>(v, k);
+        *reinterpret_cast<v2u*>(xcodes + (int64_t)m * p.kq * 64 + c) = codes8x8(e, q);
+      }
+    }
+    // a wave reads the codes that it wrote itself
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    const int n = s1 - s0 < BATCH ? s1 - s0 : BATCH;
+#pragma unroll
+    for (int u = 0; u < BATCH; u++)
+      if (u < n) step(ahead[u], s0 + u);
+    s += n;
+  }
+  // whole batches, then what is left in halves: a share of K is rarely a multiple of the batch
+  auto batch = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    Step q[N];
+#pragma unroll
+    for (int u = 0; u < N; u++) load(q[u], s + u);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < N; u++) step(q[u], s + u);
+    s += N;
+  };
+  while (s + BATCH <= s1) batch(std::integral_constant<int, BATCH>());
+  if constexpr (BATCH > 4)
+    if (s + 4 <= s1) batch(std::integral_constant<int, 4>());
+  if (s + 2 <= s1) batch(std::integral_constant<int, 2>());
+  if (s < s1) batch(std::integral_constant<int, 1>());
+
+#pragma unroll
+  for (int m = 0; m < MT; m++)
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int v = 0; v < 4; v++) red[wave][m][n][v][lane] = acc[m][n][v];
+  __syncthreads();
+  // entry (m, n, v, lane (i, g)) is row 16 m + 4 g + v of column i of tile n
+  T* y = reinterpret_cast<T*>(p.y);
+  for (int e = t; e < MT * NT * 256; e += 64 * WAVES) {
+    const int el = e & 63, v = (e >> 6) & 3, m = (e >> 8) / NT, n = (e >> 8) % NT;
+    const int64_t row = (int64_t)m0 + 16 * m + 4 * (el >> 4) + v, col = n0 + 16 * n + (el & 15);
+    if (row >= p.M || col >= p.N) continue;
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; w++) sum += red[w][m][n][v][el];
+    const double sa = RAW ? row_scale[row] : p.a_scales[row];
+    const double bz = p.bias ? DT::load(reinterpret_cast<const T*>(p.bias)[col]) : 0.f;
+    y[row * p.ldy + col] = DT::store((float)((double)sum * sa * (double)p.b_scales[col] + bz));
+  }
+}
+
+}  // namespace dev
+
+using namespace dev;
+
+// Blocks over N columns, `cols` a block, in whole runs for each XCD.
+static int64_t decode_blocks(int64_t N, int64_t cols) { return ((N + cols - 1) / cols + 7) / 8 * 8; }
+
+constexpr int kRawBytes = 64 * 1024;  // of LDS for the codes of unquantised rows
+
+bool i8_raw_rows(int64_t M, int64_t N, int64_t K, int64_t sc, int dtype_bytes) {
+  (void)N;
+  return sc == 1 && M <= 4 && M * i8_kq(K) * 64 <= kRawBytes && M * K * dtype_bytes <= 65536;
+}
+
+template <class DT, int MT, int NT, int WAVES, bool RAW>
+static hipError_t launch_rows(const I8GemmParams& p, hipStream_t stream) {
+  const int64_t blocks = decode_blocks(p.N, 16 * NT);
+  if (!mx_fits_grid(blocks, 64 * WAVES)) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, (unsigned)((p.M + 16 * MT - 1) / (16 * MT)));
+  const unsigned lds = RAW ? (unsigned)(p.M * p.kq * 64) : 0;
+  if (RAW) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_i8_decode<DT, MT, NT, WAVES, RAW>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kRawBytes);
+    if (e != hipSuccess) return e;
+  }
+  k_i8_decode<DT, MT, NT, WAVES, RAW><<<grid, 64 * WAVES, lds, stream>>>(p);
+  return hipGetLastError();
+}
+
+MxForm i8_decode_form(int64_t M, int64_t N, int kq) {
+  (void)kq;
+  const int bm = M <= 16 ? 16 : (M <= 32 ? 32 : 64);
+  return MxForm{bm, (N + 15) / 16 <= 512 && bm < 64 ? 16 : 32, 1, 8};
+}
+
+bool i8_decode_fits(int64_t M, int64_t N, int kq) {
+  const MxForm f = i8_decode_form(M, N, kq);
+  return mx_fits_grid(decode_blocks(N, f.bn), 64 * f.waves);
+}
+
+template <class DT, int MT, bool RAW>
+static hipError_t launch_cols(const I8GemmParams& p, const MxForm& f, hipStream_t stream) {
+  if (f.bn == 32) return launch_rows<DT, MT, 2, 8, RAW>(p, stream);
+  if constexpr (MT <= 2) return launch_rows<DT, MT, 1, 8, RAW>(p, stream);
+  return hipErrorInvalidConfiguration;
+}
+
+template <class DT>
+static hipError_t launch_decode_t(const I8GemmParams& p, hipStream_t stream) {
+  const MxForm f = i8_decode_form(p.M, p.N, p.kq);
+  if (p.x) return launch_cols<DT, 1, true>(p, f, stream);
+  switch (f.bm) {
+    case 16: return launch_cols<DT, 1, false>(p, f, stream);
+    case 32: return launch_cols<DT, 2, false>(p, f, stream);
+    default: return launch_cols<DT, 4, false>(p, f, stream);
+  }
+}
+
+hipError_t launch_i8_decode(const I8GemmParams& p, int dtype, hipStream_t stream) {
+  switch (dtype) {
+    case SVDQ_F32: return launch_decode_t<MxF32>(p, stream);
+    case SVDQ_BF16: return launch_decode_t<MxBF16>(p, stream);
+    default: return launch_decode_t<MxF16>(p, stream);
+  }
+}
+
+}  // namespace svdq

@@ -1,0 +1,406 @@
+// Products of 8-bit tensors on gfx950: y[m, n] = D( (sum_k a[m, k] b[n, k]) sa[m] sb[n] + bias[n] ).
+//
+// v_mfma_i32_32x32x32_i8 takes 16 K-consecutive codes per lane and sums in int32, so the sum is exact up to K = 2^17
+// (2^17 * 127^2 < 2^31); a longer K is cut into shares, whose sums are joined in 64 bits. The scales and the bias enter once, in the
+// epilogue: float32 of the sum, times float32(sa sb), plus the bias with one rounding (fma), then the output's own.
+//
+// Tiles (k_i8_tile): a BM x BN output tile per block of WM x WN waves. K advances in stages of 64 codes (64 bytes per row), which
+// land in a ring of LDS buffers through direct global->LDS loads issued DIST stages ahead; a wave waits on its own loads, one
+// barrier per stage publishes them, and a stage's operands are read from LDS under the previous slice's MFMAs. Both operands
+// come in 1 KB tiles of 16 rows, one contiguous kilobyte per wave-wide load. LDS rows are 64 bytes; chunk c of row r sits at
+// c ^ ((r >> 2) & 3), so that 16 consecutive rows' 16-byte reads meet distinct banks.
+#include <atomic>
+#include <type_traits>
+
+#include "i8.h"
+#include "i8_device.h"
+#include "tile_store.h"
+
+namespace svdq {
+namespace dev {
+
+template <int BM_, int BN_, int WM_, int WN_, int DIST_>
+struct I8Cfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NWV = WM * WN;
+  static constexpr int TM = BM / WM, TN = BN / WN;  // per-wave tile
+  static constexpr int MT = TM / 32, NT = TN / 32;
+  static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;
+  static constexpr int A_PER_WAVE = A_BYTES / 1024 / NWV, B_PER_WAVE = B_BYTES / 1024 / NWV;
+  static_assert(A_PER_WAVE * NWV * 1024 == A_BYTES && B_PER_WAVE * NWV * 1024 == B_BYTES, "whole wave-wide loads");
+  static_assert(TM % 32 == 0 && TN % 32 == 0, "wave tiles are whole MFMA tiles");
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int LPS = A_PER_WAVE + B_PER_WAVE;  // loads per stage and wave
+  static constexpr int DIST = DIST_, NS = DIST + 2;    // stages in flight ahead, ring depth
+  static_assert(DIST % 2 == 0, "the loop takes two stages a turn");
+  static constexpr int SMEM = NS * STAGE;
+  static constexpr int ALL = SMEM + (BM + BN) * 4;  // behind the ring: the scales of the tile's rows and columns
+};
+
+// Whether a scale may enter a float32 product with another such scale and an int32 without leaving the normal range.
+__device__ inline bool tame(float s) { return s == 0.f || (s >= 0x1p-60f && s <= 0x1p40f); }
+
+// y from a sum and its scales: in float32 where they are tame, else in binary64 (an infinite product of scales would make a NaN
+// of a zero sum, a vanished one a zero of a large sum). Which of them depends on the output's own scales alone.
+__device__ inline float scaled(int sum, float sa, float sb, float bias) { return __builtin_fmaf((float)sum, sa * sb, bias); }
+__device__ inline float scaled_far(int sum, float sa, float sb, float bias) {
+  if (tame(sa) && tame(sb)) return scaled(sum, sa, sb, bias);
+  return (float)((double)sum * (double)sa * (double)sb + (double)bias);
+}
+
+// Block: tile `tid` of tiles_m x tiles_n, stages [s0, s0 + nst) of K (an even number, at least two). SPLIT: the block's share of K,
+// as int32 sums into its part of p.part; else the finished output.
+template <class DT, class C, bool SPLIT>
+__global__ __launch_bounds__(64 * C::NWV) void k_i8_tile(I8GemmParams p) {
+  typedef typename DT::T T;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int l32 = lane & 31, g = lane >> 5;
+
+  // ---- tile order: blocks i, i + 8, ... share an XCD and its L2, so each XCD takes a run of (share of K, tile): few shares,
+  // and within one groups of 4 row tiles walked column by column
+  const int tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN;
+  const int ntiles = tiles_m * tiles_n, all = SPLIT ? ntiles * p.splits : ntiles;
+  const int run = (blockIdx.x & 7) * ((all + 7) >> 3) + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= (all + 7) >> 3 || run >= all) return;
+  const int split = SPLIT ? run / ntiles : 0, tid = SPLIT ? run - split * ntiles : run;
+  const int GM = 4;
+  const int group = tid / (GM * tiles_n), gm0 = group * GM;
+  const int gsz = (tiles_m - gm0) < GM ? (tiles_m - gm0) : GM;
+  const int in_g = tid - group * GM * tiles_n;
+  const int m0 = (gm0 + in_g % gsz) * C::BM, n0 = (in_g / gsz) * C::BN;
+  int s0 = 0, nst = p.kq;
+  if (SPLIT) {
+    const int pairs = p.kq / 2;
+    s0 = (int)((int64_t)pairs * split / p.splits) * 2;
+    nst = (int)((int64_t)pairs * (split + 1) / p.splits) * 2 - s0;
+  }
+
+  // ---- sources of this wave's loads: one buffer resource each, based at the 1 KB tile of its first row, so that offsets
+  // within it stay below 1024 (kq + 1) whatever the arrays' sizes; rows past the end repeat the last
+  auto a_row = [&](int rr) { return m0 + rr < p.M ? m0 + rr : p.M - 1; };
+  auto b_row = [&](int rr) { return n0 + rr < p.N ? n0 + rr : p.N - 1; };
+  const int64_t a_end = (int64_t)((p.M + 15) >> 4) * p.kq << 10, b_end = (int64_t)((p.N + 15) >> 4) * p.kq << 10;
+  const uint8_t *a_base[C::A_PER_WAVE], *b_base[C::B_PER_WAVE];
+  int a_rec[C::A_PER_WAVE], b_rec[C::B_PER_WAVE], a_off[C::A_PER_WAVE], b_off[C::B_PER_WAVE];
+  const int lr = lane >> 2, chunk = (lane & 3) ^ ((lr >> 2) & 3);
+#pragma unroll
+  for (int j = 0; j < C::A_PER_WAVE; j++) {
+    const int rr = 16 * (wave + C::NWV * j);
+    const int64_t at = ((int64_t)(a_row(rr) >> 4) * p.kq + s0) << 10;
+    a_base[j] = p.a_codes + at;
+    a_rec[j] = records(a_end - at);
+    a_off[j] = ((a_row(rr + lr) & 15) << 6) + chunk * 16;
+  }
+#pragma unroll
+  for (int j = 0; j < C::B_PER_WAVE; j++) {
+    const int rr = 16 * (wave + C::NWV * j);
+    const int64_t at = ((int64_t)(b_row(rr) >> 4) * p.kq + s0) << 10;
+    b_base[j] = p.b_codes + at;
+    b_rec[j] = records(b_end - at);
+    b_off[j] = ((b_row(rr + lr) & 15) << 6) + chunk * 16;
+  }
+  if constexpr (!SPLIT) {
+    // 64 scales a load; they are older than any stage's loads, so the first stage's wait covers them
+    for (int q = wave; q < (C::BM + C::BN) / 64; q += C::NWV) {
+      const bool isb = q >= C::BM / 64;
+      const int first = isb ? n0 : m0, row = isb ? b_row(64 * q - C::BM + lane) : a_row(64 * q + lane);
+      const float* src = (isb ? p.b_scales : p.a_scales) + first;
+      buffer_to_lds4(reinterpret_cast<const uint8_t*>(src), records((int64_t)((isb ? p.N : p.M) - first) * 4), smem + C::SMEM + q * 256,
+                     (row - first) * 4, 0);
+    }
+  }
+  auto issue = [&](int st) {
+    uint8_t* base = smem + (st % C::NS) * C::STAGE;
+#pragma unroll
+    for (int j = 0; j < C::A_PER_WAVE; j++)
+      buffer_to_lds16(a_base[j], a_rec[j], base + (wave + C::NWV * j) * 1024, a_off[j], st * 1024);
+#pragma unroll
+    for (int j = 0; j < C::B_PER_WAVE; j++)
+      buffer_to_lds16(b_base[j], b_rec[j], base + C::A_BYTES + (wave + C::NWV * j) * 1024, b_off[j], st * 1024);
+  };
+
+  v16i acc[C::MT][C::NT];
+#pragma unroll
+  for (int i = 0; i < C::MT; i++)
+#pragma unroll
+    for (int j = 0; j < C::NT; j++)
+#pragma unroll
+      for (int v = 0; v < 16; v++) acc[i][j][v] = 0;
+
+  struct Frag {
+    v4i a[C::MT], b[C::NT];
+  };
+  // a 32-code slice's operands: rows 32 apart share the swizzle
+  int fa_off[2], fb_off[2];
+#pragma unroll
+  for (int ks = 0; ks < 2; ks++) {
+    fa_off[ks] = lds_swizzle(wm * C::TM + l32, 2 * ks + g);
+    fb_off[ks] = C::A_BYTES + lds_swizzle(wn * C::TN + l32, 2 * ks + g);
+  }
+  auto read_frag = [&](const uint8_t* base, int ks, Frag& f) {
+#pragma unroll
+    for (int i = 0; i < C::MT; i++) f.a[i] = *reinterpret_cast<const v4i*>(base + fa_off[ks] + 2048 * i);
+#pragma unroll
+    for (int j = 0; j < C::NT; j++) f.b[j] = *reinterpret_cast<const v4i*>(base + fb_off[ks] + 2048 * j);
+  };
+  auto mma = [&](const Frag& f) {
+#pragma unroll
+    for (int i = 0; i < C::MT; i++)
+#pragma unroll
+      for (int j = 0; j < C::NT; j++) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+  };
+
+  // ---- pipeline. Stage s + DIST is issued at the top of iteration s; slice 1 of stage s is read under slice 0's MFMAs; then the
+  // wave waits for its own loads of stage s + 1, one barrier publishes every wave's, and stage s + 1's slice 0 is read under slice
+  // 1's MFMAs. The same barrier makes refilling buffer (s + 1 + DIST) % NS = (s - 1) % NS safe in iteration s + 1: every
+  // wave's reads of stage s - 1 were consumed before it.
+  constexpr int NR = C::MT + C::NT, NM = C::MT * C::NT;
+  constexpr int P1 = NM - 1 < NR ? NM - 1 : NR;
+  const int first = nst < C::DIST ? nst : C::DIST;
+  for (int s = 0; s < first; s++) issue(s);
+  wait_stage_upto<C::LPS, C::DIST - 1>(first - 1);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frag fa, fb, f1;
+  read_frag(smem, 0, fa);
+
+  // `ahead`: stages issued after s + 1 (a constant in the steady state), or -1: s is the last
+  auto stage = [&](int s, Frag& cur0, Frag& nxt0, auto ahead) {
+    const uint8_t* base = smem + (s % C::NS) * C::STAGE;
+    read_frag(base, 1, f1);
+    mma(cur0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+    for (int q = 0; q < P1; q++) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+    if constexpr (NR > P1) __builtin_amdgcn_sched_group_barrier(0x100, NR - P1, 0);
+    if constexpr (NM - 1 > P1) __builtin_amdgcn_sched_group_barrier(0x008, NM - 1 - P1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    constexpr bool steady = !std::is_same<decltype(ahead), int>::value;
+    if (steady || ahead >= 0) {
+      if constexpr (steady)
+        wait_vmcnt<C::LPS * decltype(ahead)::value>();
+      else
+        wait_stage_upto<C::LPS, C::DIST - 1>(ahead);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      read_frag(smem + ((s + 1) % C::NS) * C::STAGE, 0, nxt0);
+    }
+    mma(f1);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+    for (int q = 0; q < NR; q++) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (q < NM - 1) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, NM - 1 > NR ? NM - 1 - NR : 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  typedef std::integral_constant<int, C::DIST - 1> Steady;
+  int s = 0;
+  for (; s < nst - C::DIST; s += 2) {
+    issue(s + C::DIST);
+    stage(s, fa, fb, Steady());
+    issue(s + 1 + C::DIST);
+    stage(s + 1, fb, fa, Steady());
+  }
+  for (; s < nst; s += 2) {
+    stage(s, fa, fb, nst - 2 - s);
+    stage(s + 1, fb, fa, nst - 3 - s);
+  }
+
+  // ---- epilogue
+  if constexpr (SPLIT) {
+    store_tile<MxF32, C, C::BM, C::NT>(smem, reinterpret_cast<float*>(p.part) + (int64_t)split * p.M * p.N, p.N, p.M, p.N, m0, n0,
+                                       wm, wn, lane, [&](int i, int j, int v) { return __int_as_float(acc[i][j][v]); });
+  } else {
+    const float* scales = reinterpret_cast<const float*>(smem + C::SMEM);
+    float sb[C::NT], bz[C::NT];
+    bool far = false;
+#pragma unroll
+    for (int j = 0; j < C::NT; j++) {
+      const int cc = wn * C::TN + 32 * j + l32;
+      sb[j] = scales[C::BM + cc];
+      bz[j] = p.bias ? DT::load(reinterpret_cast<const T*>(p.bias)[b_row(cc)]) : 0.f;
+      far |= !tame(sb[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < C::MT; i++) {
+      // entry v of the lane lies in row 8 (v / 4) + 4 g + v % 4
+      v4f sa[4];
+      bool any = far;
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        sa[q] = *reinterpret_cast<const v4f*>(scales + wm * C::TM + 32 * i + 8 * q + 4 * g);
+#pragma unroll
+        for (int e = 0; e < 4; e++) any |= !tame(sa[q][e]);
+      }
+      if (__builtin_amdgcn_ballot_w64(any)) {
+#pragma unroll
+        for (int j = 0; j < C::NT; j++)
+#pragma unroll
+          for (int v = 0; v < 16; v++) {
+            acc[i][j][v] = __float_as_int(scaled_far(acc[i][j][v], sa[v >> 2][v & 3], sb[j], bz[j]));
+            __builtin_amdgcn_sched_barrier(0);  // rarely taken: one at a time, in few registers
+          }
+      } else {
+#pragma unroll
+        for (int j = 0; j < C::NT; j++)
+#pragma unroll
+          for (int v = 0; v < 16; v++)
+            acc[i][j][v] = __float_as_int(scaled(acc[i][j][v], sa[v >> 2][v & 3], sb[j], bz[j]));
+      }
+    }
+    store_tile<DT, C, C::BM, C::NT>(smem, reinterpret_cast<T*>(p.y), p.ldy, p.M, p.N, m0, n0, wm, wn, lane,
+                                    [&](int i, int j, int v) { return __int_as_float(acc[i][j][v]); });
+  }
+}
+
+// ------------------------------------------------------------------------------ joining split sums
+// Adds the parts in 64 bits and finishes the outputs, V neighbouring ones per thread.
+template <class DT, int V>
+__global__ __launch_bounds__(256) void k_i8_join(I8GemmParams p) {
+  typedef typename DT::T T;
+  typedef int vec __attribute__((ext_vector_type(V), aligned(V == 4 ? 16 : 4)));
+  const int c = (blockIdx.x * 256 + threadIdx.x) * V;
+  if (c >= p.N) return;
+  const int64_t stride = (int64_t)p.M * p.N;
+  double sb[V], bz[V];
+#pragma unroll
+  for (int k = 0; k < V; k++) {
+    sb[k] = p.b_scales[c + k];
+    bz[k] = p.bias ? DT::load(reinterpret_cast<const T*>(p.bias)[c + k]) : 0.f;
+  }
+  for (int64_t r = blockIdx.y; r < p.M; r += gridDim.y) {
+    const int* src = p.part + r * p.N + c;
+    const double sa = p.a_scales[r];
+    int64_t sum[V] = {};
+    for (int s = 0; s < p.splits; s += 8) {
+      vec x[8];
+#pragma unroll
+      for (int k = 0; k < 8; k++) x[k] = *reinterpret_cast<const vec*>(src + (s + k < p.splits ? s + k : p.splits - 1) * stride);
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        if (s + k >= p.splits) continue;
+#pragma unroll
+        for (int e = 0; e < V; e++) sum[e] += x[k][e];
+      }
+    }
+    T* y = reinterpret_cast<T*>(p.y) + r * p.ldy + c;
+#pragma unroll
+    for (int k = 0; k < V; k++) y[k] = DT::store((float)((double)sum[k] * sa * sb[k] + bz[k]));
+  }
+}
+
+}  // namespace dev
+
+using namespace dev;
+
+// Compute units of the chip: what a plan spreads a product over. Stages whose int32 sums cannot overflow: 2^17 codes.
+constexpr int kCus = 256, kExactStages = 2048;
+
+typedef I8Cfg<64, 64, 2, 2, 4> Tile64;
+typedef I8Cfg<128, 128, 4, 2, 2> Tile128;
+typedef I8Cfg<256, 256, 4, 2, 2> Tile256;
+
+static MxForm plan_of(int64_t M, int64_t N, int kq) {
+  if (M <= 64 && kq <= kExactStages) return i8_decode_form(M, N, kq);
+  MxForm best{0, 0, 1, 1};
+  double best_t = 1e30;
+  const int cand[3][2] = {{64, 64}, {128, 128}, {256, 256}};
+  for (int c = 0; c < 3; c++) {
+    const int64_t tiles = ((M + cand[c][0] - 1) / cand[c][0]) * ((N + cand[c][1] - 1) / cand[c][1]);
+    for (int s = 1; s <= kq / 2; s *= 2) {
+      const bool exact = (kq / 2 + s - 1) / s * 2 <= kExactStages;
+      if (!exact) continue;
+      if (s > 1 && best.bm && (kq / 2 / s < 4 || tiles * s > 2 * kCus)) break;
+      const double rounds = (double)(tiles * s) / kCus, st = (double)kq / s;
+      const double whole = (double)((tiles * s) / kCus), rest = rounds - whole;
+      double t;
+      if (c == 0)
+        t = 3 + st * (rounds > 1.5 ? 0.1 * rounds : 0.155);
+      else if (c == 1)
+        t = 3.5 + st * (rounds > 1 ? 0.265 * rounds : 0.25);
+      else
+        t = whole * (6 + 0.82 * st) + (rest > 0 ? 6 + st * (0.6 + 0.2 * rest) : 0);
+      if (s > 1) t += 3.0 + (double)M * N * 4 * 2 * s / 4e6;
+      if (t < best_t) best = MxForm{cand[c][0], cand[c][1], s, 1}, best_t = t;
+    }
+  }
+  return best;
+}
+
+MxForm i8_product_form(int64_t M, int64_t N, int kq) { return plan_of(M, N, kq); }
+
+size_t i8_product_part_bytes(int64_t M, int64_t N, int kq) {
+  const MxForm f = plan_of(M, N, kq);
+  return f.splits > 1 ? (size_t)f.splits * M * N * 4 : 0;
+}
+
+// Blocks of output tiles in `splits` shares of K, in whole runs for each XCD.
+static int64_t tile_blocks(int64_t M, int64_t N, const MxForm& f) {
+  return ((M + f.bm - 1) / f.bm * ((N + f.bn - 1) / f.bn) * f.splits + 7) / 8 * 8;
+}
+
+bool i8_product_fits(int64_t M, int64_t N, int kq) {
+  const MxForm f = plan_of(M, N, kq);
+  return f.waves > 1 ? i8_decode_fits(M, N, kq) : mx_fits_grid(tile_blocks(M, N, f), 512);
+}
+
+template <class DT, class C, bool SPLIT>
+static hipError_t launch_tile(const I8GemmParams& p, const MxForm& f, hipStream_t stream) {
+  const int64_t blocks = tile_blocks(p.M, p.N, f);
+  if (!mx_fits_grid(blocks, 64 * C::NWV)) return hipErrorInvalidConfiguration;
+  // once per process and device; a second thread at most repeats the same call
+  static std::atomic<uint64_t> configured;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!bit || !(configured.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_i8_tile<DT, C, SPLIT>), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            C::ALL);
+    if (e != hipSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_relaxed);
+  }
+  k_i8_tile<DT, C, SPLIT><<<dim3((unsigned)blocks), 64 * C::NWV, C::ALL, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <class DT, bool SPLIT>
+static hipError_t launch_form(const I8GemmParams& p, const MxForm& f, hipStream_t stream) {
+  if (f.bm == 64) return launch_tile<DT, Tile64, SPLIT>(p, f, stream);
+  if (f.bm == 256) return launch_tile<DT, Tile256, SPLIT>(p, f, stream);
+  return launch_tile<DT, Tile128, SPLIT>(p, f, stream);
+}
+
+template <class DT>
+static hipError_t launch_product_t(const I8GemmParams& p0, const MxForm& f, hipStream_t stream) {
+  I8GemmParams p = p0;
+  p.splits = f.splits;
+  if (p.splits == 1) return launch_form<DT, false>(p, f, stream);
+  // the parts are int32 whatever the output's type
+  const hipError_t e = launch_form<MxF32, true>(p, f, stream);
+  if (e != hipSuccess) return e;
+  const unsigned rows = p.M < 65535 ? p.M : 65535;
+  if (p.N % 4 == 0)
+    k_i8_join<DT, 4><<<dim3((unsigned)((p.N / 4 + 255) / 256), rows), 256, 0, stream>>>(p);
+  else
+    k_i8_join<DT, 1><<<dim3((unsigned)((p.N + 255) / 256), rows), 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_i8_product(const I8GemmParams& p, int dtype, hipStream_t stream) {
+  const MxForm f = plan_of(p.M, p.N, p.kq);
+  if (f.waves > 1) return launch_i8_decode(p, dtype, stream);
+  switch (dtype) {
+    case SVDQ_F32: return launch_product_t<MxF32>(p, f, stream);
+    case SVDQ_BF16: return launch_product_t<MxBF16>(p, f, stream);
+    default: return launch_product_t<MxF16>(p, f, stream);
+  }
+}
+
+}  // namespace svdq

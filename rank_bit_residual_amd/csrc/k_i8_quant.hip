@@ -1,0 +1,358 @@
+// Elementwise kernels on 8-bit tensors for gfx950:
+//   * k_i8_rows        Q(x) of each row: its largest magnitude, its scale, its codes;
+//   * k_i8_colmax, k_i8_colscale, k_i8_cols   the same of each column, as a tensor of the transpose;
+//   * k_i8_dequantize  the values of a tensor.
+//
+// s = float32(max|x| / 127), and a code is the nearest integer to x / s, ties to even, decided exactly (code8_sure).
+//
+// A row is read once: it stays in the registers of the threads that share it while they agree on its maximum. A column's maximum
+// comes before its first code, so columns are read twice: partial maxima (and sums) of strips of rows, their join, then the codes,
+// which change places through LDS as bytes. All kernels are bound by memory.
+#include <type_traits>
+
+#include "i8.h"
+#include "i8_device.h"
+
+namespace svdq {
+namespace dev {
+
+// Elements [c, c + 8) of a row of C elements with step sc, zeros past its end.
+template <class DT>
+__device__ inline Vec8<DT> load8_step(const typename DT::T* row, int64_t c, int64_t C, int64_t sc) {
+  if (sc == 1) return load8<DT>(row, c, C);
+  Vec8<DT> v = zero8<DT>();
+#pragma unroll
+  for (int q = 0; q < 8; q++) {
+    if (c + q >= C) continue;
+    const typename DT::T e = row[(c + q) * sc];
+    if constexpr (DT::size == 4)
+      v.w[q] = __float_as_uint(e);
+    else
+      v.w[q >> 1] |= (u32)e << (16 * (q & 1));
+  }
+  return v;
+}
+
+template <class DT>
+__device__ inline void store_codes8(const I8Out& o, int64_t row, int64_t c, const Vec8<DT>& v, const Scale8& q) {
+  float e[8];
+#pragma unroll
+  for (int k = 0; k < 8; k++) e[k] = elem<DT>(v, k);
+  *reinterpret_cast<v2u*>(o.codes + i8_at(row, c, o.kq)) = codes8x8(e, q);
+}
+
+// ------------------------------------------------------------------------------ rows
+// T threads share a row and hold NV times eight elements each; NV = 0: the row is read twice instead, whatever its length.
+template <class DT, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_i8_rows(I8QuantParams p) {
+  typedef typename DT::T E;
+  constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64;
+  __shared__ u32 red[2][WAVES];
+  const int t = threadIdx.x % T, sub = threadIdx.x / T, wave = t >> 6;
+  const int64_t Kp = (int64_t)p.rows.kq * 64;
+  int flip = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < p.R; row += (int64_t)gridDim.x * RPB, flip ^= 1) {
+    const E* x = reinterpret_cast<const E*>(p.x) + row * p.sr;
+    Vec8<DT> v[NV ? NV : 1];
+    u32 most = 0;
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; j++) v[j] = load8_step<DT>(x, (int64_t)(j * T + t) * 8, p.C, p.sc);
+#pragma unroll
+      for (int j = 0; j < NV; j++) most = max(most, amax_bits<DT>(v[j].w));
+    } else {
+      for (int64_t c = (int64_t)t * 8; c < p.C; c += T * 8) {
+        v[0] = load8_step<DT>(x, c, p.C, p.sc);
+        most = max(most, amax_bits<DT>(v[0].w));
+      }
+    }
+    most = wave_umax(most);
+    if constexpr (WAVES > 1) {
+      // two buffers: a wave may reach the next row's write while others still read this one's
+      if ((t & 63) == 0) red[flip][wave] = most;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WAVES; w++) most = max(most, red[flip][w]);
+    }
+    const Scale8 q = scale8(most);
+    if (t == 0) p.rows.scales[row] = q.s;
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; j++) {
+        const int64_t c = (int64_t)(j * T + t) * 8;
+        if (c < Kp) store_codes8<DT>(p.rows, row, c, v[j], q);
+      }
+    } else {
+      for (int64_t c = (int64_t)t * 8; c < Kp; c += T * 8) store_codes8<DT>(p.rows, row, c, load8_step<DT>(x, c, p.C, p.sc), q);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ columns
+// Partial maxima (bits of float32) and, SUMS, sums of strip `blockIdx.y` of rows: 512 columns a block, a wave a row.
+template <class DT, bool SUMS>
+__global__ __launch_bounds__(256) void k_i8_colmax(I8QuantParams p, u32* part, float* sums, int64_t strip_rows) {
+  typedef typename DT::T E;
+  __shared__ u32 most[4][512];
+  __shared__ float sum[SUMS ? 4 : 1][SUMS ? 512 : 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 512 + 8 * lane;
+  const int64_t r0 = blockIdx.y * strip_rows, r1 = min(r0 + strip_rows, p.R);
+  u32 m[8] = {};
+  float s[8] = {};
+  const E* x = reinterpret_cast<const E*>(p.x) + c * p.sc;
+#pragma unroll 4
+  for (int64_t r = r0 + wave; r < r1; r += 4) {
+    const Vec8<DT> v = load8_step<DT>(x + r * p.sr, 0, p.C - c, p.sc);
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const float e = elem<DT>(v, k);
+      m[k] = max(m[k], __float_as_uint(e) & 0x7FFFFFFFu);
+      if (SUMS) s[k] += e;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    most[wave][8 * lane + k] = m[k];
+    if (SUMS) sum[wave][8 * lane + k] = s[k];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int64_t col = (int64_t)blockIdx.x * 512 + i;
+    if (col >= p.C) continue;
+    part[blockIdx.y * p.C + col] = max(max(most[0][i], most[1][i]), max(most[2][i], most[3][i]));
+    if (SUMS) sums[blockIdx.y * p.C + col] = (sum[0][i] + sum[1][i]) + (sum[2][i] + sum[3][i]);
+  }
+}
+
+// The strips' join: scales and their reciprocals, and the column sums. 64 columns a block, a wave for every sixteenth strip.
+template <class DT, bool SUMS>
+__global__ __launch_bounds__(1024) void k_i8_colscale(const u32* part, const float* sums, int strips, int64_t C, float* scales,
+                                                      float* recip, typename DT::T* out) {
+  __shared__ u32 most[16][64];
+  __shared__ double sum[SUMS ? 16 : 1][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = (int64_t)blockIdx.x * 64 + lane, c = col < C ? col : C - 1;
+  u32 m = 0;
+  double s = 0;
+#pragma unroll 4
+  for (int k = wave; k < strips; k += 16) {
+    m = max(m, part[k * C + c]);
+    if (SUMS) s += (double)sums[k * C + c];
+  }
+  most[wave][lane] = m;
+  if (SUMS) sum[wave][lane] = s;
+  __syncthreads();
+  if (wave || col >= C) return;
+#pragma unroll
+  for (int w = 1; w < 16; w++) {
+    m = max(m, most[w][lane]);
+    if (SUMS) s += sum[w][lane];
+  }
+  const Scale8 q = scale8(m);
+  scales[col] = q.s;
+  recip[col] = q.r;
+  if (SUMS) out[col] = DT::store((float)s);
+}
+
+// Codes of a tile of 64 rows x 128 columns of x as the transpose's: a thread takes four rows of eight columns, makes a word
+// of four codes for each column, and the words change places in LDS. Word `rg` of column 8 lc + j lies at lc * 132 + 16 j + rg:
+// a wave's 64 writes (16 lc, four rg) and 16 lanes' 16-byte reads each meet 64 distinct banks.
+template <class DT>
+__global__ __launch_bounds__(256) void k_i8_cols(I8QuantParams p, const float* recip, int64_t tiles_c, int64_t tiles) {
+  typedef typename DT::T E;
+  __shared__ __align__(16) u32 words[16 * 132];
+  const int t = threadIdx.x, lc = t & 15, rg = t >> 4;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t tr = tile / tiles_c, tc = tile - tr * tiles_c;
+    const int64_t c = tc * 128 + 8 * lc, r = tr * 64 + 4 * rg;
+    const E* x = reinterpret_cast<const E*>(p.x) + r * p.sr + c * p.sc;
+    Vec8<DT> v[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = r + i < p.R ? load8_step<DT>(x + i * p.sr, 0, p.C - c, p.sc) : zero8<DT>();
+    Scale8 q[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const int64_t col = c + j < p.C ? c + j : p.C - 1;
+      q[j] = {p.cols.scales[col], recip[col]};
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      float u[4], far = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; i++) u[i] = code8_fast(elem<DT>(v[i], j), q[j].r, far);
+      if (far > kSure8) {
+        asm volatile("");  // rarely taken: keep it a branch
+#pragma unroll
+        for (int i = 0; i < 4; i++) u[i] = code8_sure(elem<DT>(v[i], j), q[j].s, q[j].r);
+      }
+      words[lc * 132 + 16 * j + rg] = q[j].r == 0.f ? 0u : bytes4(u[0], u[1], u[2], u[3]);
+    }
+    __syncthreads();
+    // 16 columns x 64 codes are a kilobyte of the tensor: a lane stores 16 codes of one
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int i = t + 256 * h, cc = i >> 2, w4 = i & 3;
+      const v4i word = *reinterpret_cast<const v4i*>(&words[(cc >> 3) * 132 + 16 * (cc & 7) + 4 * w4]);
+      const int64_t col = tc * 128 + cc;
+      if (col < p.C) *reinterpret_cast<v4i*>(p.cols.codes + i8_at(col, tr * 64 + 16 * w4, p.cols.kq)) = word;
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------------------ dequantise
+// 64 rows x 64 codes a block: a lane turns 16 codes into 16 neighbouring outputs.
+template <class DT>
+__global__ __launch_bounds__(256) void k_i8_dequantize(I8DequantParams p, int64_t tiles) {
+  typedef typename DT::T E;
+  const int t = threadIdx.x;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t tr = tile / p.kq, st = tile - tr * p.kq;
+    const int64_t r = tr * 64 + (t >> 2), c = st * 64 + 16 * (t & 3);
+    if (r >= p.rows || c >= p.K) continue;
+    const v4i w = *reinterpret_cast<const v4i*>(p.codes + i8_at(r, c, p.kq));
+    const float s = p.scales[r];
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 16; k++) v[k] = (float)(int8_t)((u32)w[k >> 2] >> (8 * (k & 3))) * s;
+    E* dst = reinterpret_cast<E*>(p.out) + r * p.ldo + c;
+    if (c + 16 <= p.K) {
+      u32 o[DT::size * 4];
+#pragma unroll
+      for (int q = 0; q < DT::size * 4; q++) {
+        if constexpr (DT::size == 4)
+          o[q] = __float_as_uint(v[q]);
+        else
+          o[q] = DT::pack(v[2 * q], v[2 * q + 1]);
+      }
+      __builtin_memcpy(dst, o, sizeof o);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; k++)
+        if (c + k < p.K) dst[k] = DT::store(v[k]);
+    }
+  }
+}
+
+}  // namespace dev
+
+using namespace dev;
+
+constexpr int64_t kMostBlocks = 1 << 20;  // of kernels that walk over what is left
+static unsigned blocks_of(int64_t n) { return (unsigned)(n < kMostBlocks ? n : kMostBlocks); }
+
+template <class DT, int T, int NV>
+static void launch_rows(const I8QuantParams& p, hipStream_t stream) {
+  constexpr int RPB = T < 256 ? 256 / T : 1;
+  k_i8_rows<DT, T, NV><<<blocks_of((p.R + RPB - 1) / RPB), T < 256 ? 256 : T, 0, stream>>>(p);
+}
+
+template <class DT>
+static hipError_t rows_t(const I8QuantParams& p, hipStream_t stream) {
+  const int64_t Kp = (int64_t)p.rows.kq * 64;
+  if (Kp <= 512)
+    launch_rows<DT, 64, 1>(p, stream);
+  else if (Kp <= 1024)
+    launch_rows<DT, 64, 2>(p, stream);
+  else if (Kp <= 2048)
+    launch_rows<DT, 256, 1>(p, stream);
+  else if (Kp <= 4096)
+    launch_rows<DT, 256, 2>(p, stream);
+  else if (Kp <= 8192)
+    launch_rows<DT, 1024, 1>(p, stream);
+  else if (Kp <= 16384)
+    launch_rows<DT, 1024, 2>(p, stream);
+  else if (Kp <= 32768)
+    launch_rows<DT, 1024, 4>(p, stream);
+  else
+    launch_rows<DT, 1024, 0>(p, stream);
+  return hipGetLastError();
+}
+
+// Strips of rows that a column's maximum is taken over: enough blocks for the chip, at least 16 rows each.
+static int64_t strips_of(int64_t R, int64_t C) {
+  const int64_t chunks = (C + 511) / 512;
+  int64_t strips = (2048 + chunks - 1) / chunks;
+  const int64_t most = (R + 15) / 16;
+  if (strips > most) strips = most;
+  if (strips > 256) strips = 256;
+  const int64_t rows = (R + strips - 1) / strips;
+  return (R + rows - 1) / rows;
+}
+
+static int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// A matrix whose columns are contiguous is its transpose, with the outputs exchanged.
+static bool exchanged(int64_t sr, int64_t sc) { return sr == 1 && sc != 1; }
+
+size_t i8_quantize_bytes(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows, bool cols) {
+  if (exchanged(sr, sc)) {
+    const int64_t r = R;
+    const bool k = rows;
+    R = C, C = r, rows = cols, cols = k;
+  }
+  return cols ? (size_t)(round256(C * 4) + 2 * round256(strips_of(R, C) * C * 4)) : 0;
+}
+
+bool i8_quantize_fits(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows, bool cols) {
+  const bool swap = exchanged(sr, sc);
+  return !(swap ? rows : cols) || mx_fits_grid(((swap ? R : C) + 63) / 64, 1024);
+}
+
+template <class DT>
+static hipError_t cols_t(const I8QuantParams& p, hipStream_t stream) {
+  const int64_t strips = strips_of(p.R, p.C), strip_rows = (p.R + strips - 1) / strips;
+  float* recip = reinterpret_cast<float*>(p.workspace);
+  u32* part = reinterpret_cast<u32*>((uint8_t*)p.workspace + round256(p.C * 4));
+  float* sums = reinterpret_cast<float*>((uint8_t*)part + round256(strips * p.C * 4));
+  const dim3 grid((unsigned)((p.C + 511) / 512), (unsigned)strips);
+  const unsigned joins = (unsigned)((p.C + 63) / 64);
+  if (p.sums) {
+    k_i8_colmax<DT, true><<<grid, 256, 0, stream>>>(p, part, sums, strip_rows);
+    if (p.sums_dtype == SVDQ_F32)
+      k_i8_colscale<MxF32, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (float*)p.sums);
+    else if (p.sums_dtype == SVDQ_BF16)
+      k_i8_colscale<MxBF16, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (uint16_t*)p.sums);
+    else
+      k_i8_colscale<MxF16, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (uint16_t*)p.sums);
+  } else {
+    k_i8_colmax<DT, false><<<grid, 256, 0, stream>>>(p, part, sums, strip_rows);
+    k_i8_colscale<MxF32, false><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, nullptr);
+  }
+  // the transpose's stages come in pairs, so the last tile of rows may hold nothing but padding
+  const int64_t tiles_c = (p.C + 127) / 128, tiles = (int64_t)p.cols.kq * tiles_c;
+  k_i8_cols<DT><<<blocks_of(tiles), 256, 0, stream>>>(p, recip, tiles_c, tiles);
+  return hipGetLastError();
+}
+
+template <class DT>
+static hipError_t quantize_t(const I8QuantParams& p0, hipStream_t stream) {
+  I8QuantParams p = p0;
+  if (exchanged(p.sr, p.sc)) p.R = p0.C, p.C = p0.R, p.sr = p0.sc, p.sc = p0.sr, p.rows = p0.cols, p.cols = p0.rows;
+  if (p.rows.codes) {
+    const hipError_t e = rows_t<DT>(p, stream);
+    if (e != hipSuccess) return e;
+  }
+  return p.cols.codes ? cols_t<DT>(p, stream) : hipSuccess;
+}
+
+hipError_t launch_i8_quantize(const I8QuantParams& p, int dtype, hipStream_t stream) {
+  switch (dtype) {
+    case SVDQ_F32: return quantize_t<MxF32>(p, stream);
+    case SVDQ_BF16: return quantize_t<MxBF16>(p, stream);
+    default: return quantize_t<MxF16>(p, stream);
+  }
+}
+
+hipError_t launch_i8_dequantize(const I8DequantParams& p, int dtype, hipStream_t stream) {
+  const int64_t tiles = (p.rows + 63) / 64 * p.kq;
+  switch (dtype) {
+    case SVDQ_F32: k_i8_dequantize<MxF32><<<blocks_of(tiles), 256, 0, stream>>>(p, tiles); break;
+    case SVDQ_BF16: k_i8_dequantize<MxBF16><<<blocks_of(tiles), 256, 0, stream>>>(p, tiles); break;
+    default: k_i8_dequantize<MxF16><<<blocks_of(tiles), 256, 0, stream>>>(p, tiles);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace svdq

@@ -1,0 +1,507 @@
+// Layer norm on gfx950: y = (x - mean) / sqrt(var + eps) * weight + bias of each row, as it is or as the 8-bit or MXFP4 tensor of y,
+// and its backward pass.
+//
+// Forward: a row is read once and stays in the registers of the threads that share it. Sums and y are binary64, whose adds and
+// multiply-adds take this chip no longer than float32's: with d = x - x[0], mean = x[0] + sum d / K and var = sum d^2 / K - (sum d /
+// K)^2 come from one reduction, and since (x[0] - mean)^2 <= K var the subtraction costs log2 K of 53 bits at most. y is rounded to
+// float32 once, and that is what is quantised or rounded on to the output's type; a code is decided by comparing with a border, so
+// rounding earlier would move one now and then.
+//
+// Backward: with xh = (x - mean) rstd and g = dy weight, dx = rstd (g - mean(g) - xh mean(g xh)): one reduction, with dy and x in
+// registers. A thread keeps the same columns in every row of its block, so dweight = sum dy xh and dbias = sum dy are running sums
+// in registers; each block leaves its own, and a second kernel adds them in the blocks' order. All kernels are bound by memory.
+#include <type_traits>
+
+#include "i8.h"
+#include "i8_device.h"
+#include "mx_rows.h"
+
+namespace svdq {
+namespace dev {
+
+enum { NORM_Y, NORM_I8, NORM_MX };
+
+// Elements [c, c + 8) of a parameter vector of K, or `none` without one; zeros past its end.
+template <class DT>
+__device__ inline void param8(float (&w)[8], const void* src, bool f32, int64_t c, int64_t K, float none) {
+  if (!src) {
+#pragma unroll
+    for (int k = 0; k < 8; k++) w[k] = none;
+  } else if (f32) {
+    const Vec8<MxF32> v = load8<MxF32>(reinterpret_cast<const float*>(src), c, K);
+#pragma unroll
+    for (int k = 0; k < 8; k++) w[k] = elem<MxF32>(v, k);
+  } else {
+    const Vec8<DT> v = load8<DT>(reinterpret_cast<const typename DT::T*>(src), c, K);
+#pragma unroll
+    for (int k = 0; k < 8; k++) w[k] = elem<DT>(v, k);
+  }
+}
+
+template <class DT>
+__device__ inline void store8(typename DT::T* row, int64_t c, int64_t K, const float (&v)[8]) {
+  if (c + 8 <= K) {
+    u32 o[DT::size * 2];
+#pragma unroll
+    for (int q = 0; q < DT::size * 2; q++) {
+      if constexpr (DT::size == 4)
+        o[q] = __float_as_uint(v[q]);
+      else
+        o[q] = DT::pack(v[2 * q], v[2 * q + 1]);
+    }
+    __builtin_memcpy(row + c, o, sizeof o);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      if (c + k < K) row[c + k] = DT::store(v[k]);
+  }
+}
+
+// ------------------------------------------------------------------------------ forward
+struct RowStats {
+  double mean, rstd;
+};
+
+// This thread's share of sum d and sum d^2 from eight elements at c.
+template <class DT>
+__device__ inline void add_stats(const Vec8<DT>& v, int64_t c, int64_t K, double pivot, double& s, double& q) {
+  const int64_t n = K - c;
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    const double d = k < n ? (double)elem<DT>(v, k) - pivot : 0.0;
+    s += d;
+    q = __builtin_fma(d, d, q);
+  }
+}
+
+// y of eight elements, as float32; zeros past the row's end.
+template <class DT>
+__device__ inline void norm8(float (&y)[8], const Vec8<DT>& v, int64_t c, const NormParams& p, const RowStats& st) {
+  float w[8], b[8];
+  param8<DT>(w, p.weight, p.param_f32, c, p.K, 1.f);
+  param8<DT>(b, p.bias, p.param_f32, c, p.K, 0.f);
+  const int64_t n = p.K - c;
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    const double xh = ((double)elem<DT>(v, k) - st.mean) * st.rstd;
+    y[k] = k < n ? (float)__builtin_fma(xh, (double)w[k], (double)b[k]) : 0.f;
+  }
+}
+
+__device__ inline u32 amax8(const float (&y)[8]) {
+  u32 m = 0;
+#pragma unroll
+  for (int k = 0; k < 8; k++) m = max(m, __float_as_uint(y[k]) & 0x7FFFFFFFu);
+  return m;
+}
+
+template <class DT, int OUT>
+__device__ inline void put8(const NormParams& p, int64_t row, int64_t c, const float (&y)[8], const Scale8& q) {
+  if constexpr (OUT == NORM_Y) {
+    if (c < p.K) store8<DT>(reinterpret_cast<typename DT::T*>(p.y) + row * p.ldy, c, p.K, y);
+  } else if constexpr (OUT == NORM_I8) {
+    if (c < (int64_t)p.i8.kq * 64) *reinterpret_cast<v2u*>(p.i8.codes + i8_at(row, c, p.i8.kq)) = codes8x8(y, q);
+  } else {
+    Vec8<MxF32> v;
+#pragma unroll
+    for (int k = 0; k < 8; k++) v.w[k] = __float_as_uint(y[k]);
+    const int64_t stage = c >> 7;
+    put_row<MxF32>(group_of(p.mx, row >> 4, stage), v, (u32)(row & 15), (u32)(c & 127), c < (int64_t)p.mx.kq * 128);
+  }
+}
+
+// T threads share a row and hold NV times eight elements each; NV = 0: a row of any length, read once for its statistics and
+// again for y (twice for 8-bit codes).
+template <class DT, int T, int NV, int OUT>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm(NormParams p) {
+  typedef typename DT::T E;
+  constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64;
+  __shared__ double red[2][2][WAVES];
+  __shared__ u32 redm[2][WAVES];
+  const int t = threadIdx.x % T, sub = threadIdx.x / T, wave = t >> 6;
+  // threads past the end of a row take part up to the end of the codes' padding
+  const int64_t Kp = OUT == NORM_Y ? p.K : (OUT == NORM_I8 ? (int64_t)p.i8.kq * 64 : (int64_t)p.mx.kq * 128);
+  int flip = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < p.M; row += (int64_t)gridDim.x * RPB, flip ^= 1) {
+    const E* x = reinterpret_cast<const E*>(p.x) + row * p.ldx;
+    const double pivot = DT::load(x[0]);
+    double s = 0, q = 0;
+    Vec8<DT> v[NV ? NV : 1];
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; j++) v[j] = load8<DT>(x, (int64_t)(j * T + t) * 8, p.K);
+#pragma unroll
+      for (int j = 0; j < NV; j++) add_stats<DT>(v[j], (int64_t)(j * T + t) * 8, p.K, pivot, s, q);
+    } else {
+      for (int64_t c = (int64_t)t * 8; c < p.K; c += T * 8) add_stats<DT>(load8<DT>(x, c, p.K), c, p.K, pivot, s, q);
+    }
+    s = wave_sum(s);
+    q = wave_sum(q);
+    if constexpr (WAVES > 1) {
+      // two buffers: a wave may reach the next row's write while others still read this one's
+      if ((t & 63) == 0) red[flip][0][wave] = s, red[flip][1][wave] = q;
+      __syncthreads();
+      s = q = 0;
+#pragma unroll
+      for (int w = 0; w < WAVES; w++) s += red[flip][0][w], q += red[flip][1][w];
+    }
+    const double k1 = 1.0 / (double)p.K, ds = s * k1;
+    double var = __builtin_fma(q, k1, -ds * ds);
+    var = var < 0 ? 0 : var;  // NaN stays
+    const RowStats st{pivot + ds, 1.0 / sqrt(var + p.eps)};
+    if (t == 0 && p.mean) p.mean[row] = (float)st.mean, p.rstd[row] = (float)st.rstd;
+
+    Scale8 scale{0.f, 0.f};
+    float y[NV ? NV : 1][8];
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; j++) norm8<DT>(y[j], v[j], (int64_t)(j * T + t) * 8, p, st);
+    }
+    if constexpr (OUT == NORM_I8) {
+      u32 most = 0;
+      if constexpr (NV > 0) {
+#pragma unroll
+        for (int j = 0; j < NV; j++) most = max(most, amax8(y[j]));
+      } else {
+        for (int64_t c = (int64_t)t * 8; c < p.K; c += T * 8) {
+          norm8<DT>(y[0], load8<DT>(x, c, p.K), c, p, st);
+          most = max(most, amax8(y[0]));
+        }
+      }
+      most = wave_umax(most);
+      if constexpr (WAVES > 1) {
+        if ((t & 63) == 0) redm[flip][wave] = most;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WAVES; w++) most = max(most, redm[flip][w]);
+      }
+      scale = scale8(most);
+      if (t == 0) p.i8.scales[row] = scale.s;
+    }
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; j++) put8<DT, OUT>(p, row, (int64_t)(j * T + t) * 8, y[j], scale);
+    } else {
+      // whole waves: an MXFP4 block's four lanes agree on its maximum
+      for (int64_t c0 = (int64_t)(t & ~63) * 8; c0 < Kp; c0 += T * 8) {
+        const int64_t c = c0 + 8 * (t & 63);
+        norm8<DT>(y[0], load8<DT>(x, c, p.K), c, p, st);
+        put8<DT, OUT>(p, row, c, y[0], scale);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ backward
+template <class DT>
+struct GradRow {
+  Vec8<DT> dy, x;
+};
+
+// T threads share a row, NV times eight columns each, the same ones in every row that the block takes.
+template <class DT, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradParams p, float* part) {
+  typedef typename DT::T E;
+  constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64;
+  __shared__ float red[2][2][WAVES];
+  __shared__ float wide[RPB > 1 ? RPB * NV * 16 * T : 1];
+  const int t = threadIdx.x % T, sub = threadIdx.x / T, wave = t >> 6;
+  float w[NV][8], dw[NV][8] = {}, db[NV][8] = {};
+#pragma unroll
+  for (int j = 0; j < NV; j++) param8<DT>(w[j], p.weight, p.param_f32, (int64_t)(j * T + t) * 8, p.K, 1.f);
+  const float k1 = 1.f / (float)p.K;
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + sub;
+  GradRow<DT> cur[NV];
+  float mean = 0.f, rstd = 0.f;
+  auto load = [&](GradRow<DT>(&to)[NV], int64_t r, float& mu, float& rs) {
+    if (r >= p.M) return;
+    mu = p.mean[r], rs = p.rstd[r];
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      const int64_t c = (int64_t)(j * T + t) * 8;
+      to[j].dy = load8<DT>(reinterpret_cast<const E*>(p.dy) + r * p.lddy, c, p.K);
+      to[j].x = load8<DT>(reinterpret_cast<const E*>(p.x) + r * p.ldx, c, p.K);
+    }
+  };
+  load(cur, row, mean, rstd);
+  int flip = 0;
+  for (; row < p.M; row += step, flip ^= 1) {
+    GradRow<DT> next[NV];
+    float mu = 0.f, rs = 0.f;
+    load(next, row + step, mu, rs);
+    float c1 = 0.f, c2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float dy = elem<DT>(cur[j].dy, k), xh = (elem<DT>(cur[j].x, k) - mean) * rstd, g = dy * w[j][k];
+        c1 += g;
+        c2 = __builtin_fmaf(g, xh, c2);
+        dw[j][k] = __builtin_fmaf(dy, xh, dw[j][k]);
+        db[j][k] += dy;
+      }
+    c1 = wave_sum(c1);
+    c2 = wave_sum(c2);
+    if constexpr (WAVES > 1) {
+      if ((t & 63) == 0) red[flip][0][wave] = c1, red[flip][1][wave] = c2;
+      lds_barrier();
+      c1 = c2 = 0.f;
+#pragma unroll
+      for (int u = 0; u < WAVES; u++) c1 += red[flip][0][u], c2 += red[flip][1][u];
+    }
+    c1 *= k1;
+    c2 *= k1;
+    E* dx = reinterpret_cast<E*>(p.dx) + row * p.lddx;
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      const int64_t c = (int64_t)(j * T + t) * 8;
+      float o[8];
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float xh = (elem<DT>(cur[j].x, k) - mean) * rstd, g = elem<DT>(cur[j].dy, k) * w[j][k];
+        o[k] = rstd * (g - c1 - xh * c2);
+      }
+      if (c < p.K) store8<DT>(dx, c, p.K, o);
+      cur[j] = next[j];
+    }
+    mean = mu, rstd = rs;
+  }
+  if (!part) return;
+  float* out = part + (int64_t)blockIdx.x * 2 * p.K;
+  if constexpr (RPB > 1) {
+    // the block's rows were taken by RPB waves: their sums, in order
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        wide[((sub * NV + j) * 16 + k) * T + t] = dw[j][k];
+        wide[((sub * NV + j) * 16 + 8 + k) * T + t] = db[j][k];
+      }
+    __syncthreads();
+    if (sub) return;
+    for (int u = 1; u < RPB; u++)
+#pragma unroll
+      for (int j = 0; j < NV; j++)
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          dw[j][k] += wide[((u * NV + j) * 16 + k) * T + t];
+          db[j][k] += wide[((u * NV + j) * 16 + 8 + k) * T + t];
+        }
+  }
+#pragma unroll
+  for (int j = 0; j < NV; j++) {
+    const int64_t c = (int64_t)(j * T + t) * 8;
+    if (c >= p.K) continue;
+    store8<MxF32>(out, c, p.K, dw[j]);
+    store8<MxF32>(out + p.K, c, p.K, db[j]);
+  }
+}
+
+// Rows of any length: dx alone, dy and x read twice.
+template <class DT>
+__global__ __launch_bounds__(1024) void k_norm_grad_long(NormGradParams p) {
+  typedef typename DT::T E;
+  __shared__ float red[2][2][16];
+  const int t = threadIdx.x, wave = t >> 6;
+  const float k1 = 1.f / (float)p.K;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, flip ^= 1) {
+    const E *dy = reinterpret_cast<const E*>(p.dy) + row * p.lddy, *x = reinterpret_cast<const E*>(p.x) + row * p.ldx;
+    E* dx = reinterpret_cast<E*>(p.dx) + row * p.lddx;
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    float c1 = 0.f, c2 = 0.f;
+    for (int64_t c = (int64_t)t * 8; c < p.K; c += 8192) {
+      const Vec8<DT> a = load8<DT>(dy, c, p.K), b = load8<DT>(x, c, p.K);
+      float w[8];
+      param8<DT>(w, p.weight, p.param_f32, c, p.K, 1.f);
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float g = elem<DT>(a, k) * w[k];
+        c1 += g;
+        c2 = __builtin_fmaf(g, (elem<DT>(b, k) - mean) * rstd, c2);
+      }
+    }
+    c1 = wave_sum(c1);
+    c2 = wave_sum(c2);
+    if ((t & 63) == 0) red[flip][0][wave] = c1, red[flip][1][wave] = c2;
+    __syncthreads();
+    c1 = c2 = 0.f;
+#pragma unroll
+    for (int u = 0; u < 16; u++) c1 += red[flip][0][u], c2 += red[flip][1][u];
+    c1 *= k1;
+    c2 *= k1;
+    for (int64_t c = (int64_t)t * 8; c < p.K; c += 8192) {
+      const Vec8<DT> a = load8<DT>(dy, c, p.K), b = load8<DT>(x, c, p.K);
+      float w[8], o[8];
+      param8<DT>(w, p.weight, p.param_f32, c, p.K, 1.f);
+#pragma unroll
+      for (int k = 0; k < 8; k++) o[k] = rstd * (elem<DT>(a, k) * w[k] - c1 - (elem<DT>(b, k) - mean) * rstd * c2);
+      store8<DT>(dx, c, p.K, o);
+    }
+  }
+}
+
+// Partial dweight and dbias of strip `blockIdx.y` of rows, for rows of any length: 512 columns a block, a wave a row.
+template <class DT>
+__global__ __launch_bounds__(256) void k_norm_grad_cols(NormGradParams p, float* part, int64_t strip_rows) {
+  typedef typename DT::T E;
+  __shared__ float sum[4][2][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 512 + 8 * lane;
+  const int64_t r0 = blockIdx.y * strip_rows, r1 = min(r0 + strip_rows, p.M);
+  float dw[8] = {}, db[8] = {};
+  for (int64_t r = r0 + wave; r < r1; r += 4) {
+    const Vec8<DT> a = load8<DT>(reinterpret_cast<const E*>(p.dy) + r * p.lddy, c, p.K);
+    const Vec8<DT> b = load8<DT>(reinterpret_cast<const E*>(p.x) + r * p.ldx, c, p.K);
+    const float mean = p.mean[r], rstd = p.rstd[r];
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const float dy = elem<DT>(a, k);
+      dw[k] = __builtin_fmaf(dy, (elem<DT>(b, k) - mean) * rstd, dw[k]);
+      db[k] += dy;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; k++) sum[wave][0][8 * lane + k] = dw[k], sum[wave][1][8 * lane + k] = db[k];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 1024; i += 256) {
+    const int64_t col = (int64_t)blockIdx.x * 512 + (i & 511);
+    const int which = i >> 9, at = i & 511;
+    if (col >= p.K) continue;
+    part[((int64_t)blockIdx.y * 2 + which) * p.K + col] =
+        (sum[0][which][at] + sum[1][which][at]) + (sum[2][which][at] + sum[3][which][at]);
+  }
+}
+
+// The blocks' sums, added in their order by 16 waves: 64 columns a block.
+template <class DT>
+__global__ __launch_bounds__(1024) void k_norm_join(const float* part, int parts, int64_t K, void* dweight, void* dbias) {
+  typedef typename DT::T E;
+  __shared__ float sum[16][2][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = (int64_t)blockIdx.x * 64 + lane, c = col < K ? col : K - 1;
+  float a = 0.f, b = 0.f;
+#pragma unroll 4
+  for (int k = wave; k < parts; k += 16) {
+    a += part[(int64_t)(2 * k) * K + c];
+    b += part[(int64_t)(2 * k + 1) * K + c];
+  }
+  sum[wave][0][lane] = a;
+  sum[wave][1][lane] = b;
+  __syncthreads();
+  if (wave > 1 || col >= K) return;
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 16; w++) s += sum[w][wave][lane];
+  reinterpret_cast<E*>(wave ? dbias : dweight)[col] = DT::store(s);
+}
+
+}  // namespace dev
+
+using namespace dev;
+
+constexpr int64_t kMostBlocks = 1 << 20;  // of kernels that walk over what is left
+static unsigned blocks_of(int64_t n) { return (unsigned)(n < kMostBlocks ? n : kMostBlocks); }
+
+template <class DT, int T, int NV, int OUT>
+static void launch_rows(const NormParams& p, hipStream_t stream) {
+  constexpr int RPB = T < 256 ? 256 / T : 1;
+  k_norm<DT, T, NV, OUT><<<blocks_of((p.M + RPB - 1) / RPB), T < 256 ? 256 : T, 0, stream>>>(p);
+}
+
+template <class DT, int OUT>
+static hipError_t norm_t(const NormParams& p, hipStream_t stream) {
+  const int64_t Kp = OUT == NORM_Y ? p.K : (OUT == NORM_I8 ? (int64_t)p.i8.kq * 64 : (int64_t)p.mx.kq * 128);
+  if (Kp <= 512)
+    launch_rows<DT, 64, 1, OUT>(p, stream);
+  else if (Kp <= 2048)
+    launch_rows<DT, 256, 1, OUT>(p, stream);
+  else if (Kp <= 4096)
+    launch_rows<DT, 256, 2, OUT>(p, stream);
+  else if (Kp <= 8192)
+    launch_rows<DT, 1024, 1, OUT>(p, stream);
+  else if (Kp <= 16384)
+    launch_rows<DT, 1024, 2, OUT>(p, stream);
+  else
+    launch_rows<DT, 1024, 0, OUT>(p, stream);
+  return hipGetLastError();
+}
+
+template <class DT>
+static hipError_t norm_dt(const NormParams& p, hipStream_t stream) {
+  if (p.i8.codes) return norm_t<DT, NORM_I8>(p, stream);
+  if (p.mx.codes) return norm_t<DT, NORM_MX>(p, stream);
+  return norm_t<DT, NORM_Y>(p, stream);
+}
+
+hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t stream) {
+  switch (dtype) {
+    case SVDQ_F32: return norm_dt<MxF32>(p, stream);
+    case SVDQ_BF16: return norm_dt<MxBF16>(p, stream);
+    default: return norm_dt<MxF16>(p, stream);
+  }
+}
+
+constexpr int64_t kLongRow = 16384;
+
+// Blocks (or strips of rows) that leave a part of dweight and dbias each.
+static int64_t grad_parts(int64_t M, int64_t K) {
+  if (K > kLongRow) {
+    int64_t strips = (M + 15) / 16;
+    if (strips > 64) strips = 64;
+    const int64_t rows = (M + strips - 1) / strips;
+    return (M + rows - 1) / rows;
+  }
+  const int64_t per = K <= 512 ? 16 : 4;
+  const int64_t blocks = (M + per - 1) / per;
+  return blocks < 512 ? blocks : 512;
+}
+
+size_t norm_grad_bytes(int64_t M, int64_t K, bool params) { return params ? (size_t)(grad_parts(M, K) * 2 * K * 4 + 255) / 256 * 256 : 0; }
+
+bool norm_grad_fits(int64_t K) { return mx_fits_grid((K + 63) / 64, 1024); }
+
+template <class DT, int T, int NV>
+static void launch_grad(const NormGradParams& p, float* part, hipStream_t stream) {
+  k_norm_grad<DT, T, NV><<<(unsigned)grad_parts(p.M, p.K), T < 256 ? 256 : T, 0, stream>>>(p, part);
+}
+
+template <class DT>
+static hipError_t grad_t(const NormGradParams& p, hipStream_t stream) {
+  float* part = p.weight ? reinterpret_cast<float*>(p.workspace) : nullptr;
+  const int64_t parts = grad_parts(p.M, p.K);
+  if (p.K > kLongRow) {
+    k_norm_grad_long<DT><<<blocks_of(p.M), 1024, 0, stream>>>(p);
+    if (part)
+      k_norm_grad_cols<DT><<<dim3((unsigned)((p.K + 511) / 512), (unsigned)parts), 256, 0, stream>>>(p, part, (p.M + parts - 1) / parts);
+  } else if (p.K <= 512) {
+    launch_grad<DT, 64, 1>(p, part, stream);
+  } else if (p.K <= 2048) {
+    launch_grad<DT, 256, 1>(p, part, stream);
+  } else if (p.K <= 4096) {
+    launch_grad<DT, 256, 2>(p, part, stream);
+  } else if (p.K <= 8192) {
+    launch_grad<DT, 512, 2>(p, part, stream);
+  } else {
+    launch_grad<DT, 1024, 2>(p, part, stream);
+  }
+  if (part) {
+    const unsigned blocks = (unsigned)((p.K + 63) / 64);
+    if (p.param_f32)
+      k_norm_join<MxF32><<<blocks, 1024, 0, stream>>>(part, (int)parts, p.K, p.dweight, p.dbias);
+    else
+      k_norm_join<DT><<<blocks, 1024, 0, stream>>>(part, (int)parts, p.K, p.dweight, p.dbias);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_grad(const NormGradParams& p, int dtype, hipStream_t stream) {
+  switch (dtype) {
+    case SVDQ_F32: return grad_t<MxF32>(p, stream);
+    case SVDQ_BF16: return grad_t<MxBF16>(p, stream);
+    default: return grad_t<MxF16>(p, stream);
+  }
+}
+
+}  // namespace svdq
