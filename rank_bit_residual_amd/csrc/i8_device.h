@@ -46,6 +46,29 @@ __device__ inline u32 wave_umax(u32 v) {
   return max(max(lane_of(v, 0), lane_of(v, 16)), max(lane_of(v, 32), lane_of(v, 48)));
 }
 
+// Over the waves (16 at most) that share a row, from their values in LDS: a lane takes one wave's, and every
+// group of lanes that the steps below join has them all.
+template <int WAVES>
+__device__ inline double waves_sum(const double* part) {
+  static_assert(WAVES == 2 || WAVES == 4 || WAVES == 8 || WAVES == 16, "whole groups of lanes");
+  double v = part[threadIdx.x & (WAVES - 1)];
+  v += dpp<kQuad1>(v);
+  if constexpr (WAVES > 2) v += dpp<kQuad2>(v);
+  if constexpr (WAVES > 4) v += dpp<kHalfMirror>(v);
+  if constexpr (WAVES > 8) v += dpp<kMirror>(v);
+  return v;
+}
+template <int WAVES>
+__device__ inline u32 waves_umax(const u32* part) {
+  static_assert(WAVES == 2 || WAVES == 4 || WAVES == 8 || WAVES == 16, "whole groups of lanes");
+  u32 v = part[threadIdx.x & (WAVES - 1)];
+  v = max(v, dpp<kQuad1>(v));
+  if constexpr (WAVES > 2) v = max(v, dpp<kQuad2>(v));
+  if constexpr (WAVES > 4) v = max(v, dpp<kHalfMirror>(v));
+  if constexpr (WAVES > 8) v = max(v, dpp<kMirror>(v));
+  return v;
+}
+
 // ---- 8-bit codes --------------------------------------------------------------------------
 // A row's scale from the bits of its largest magnitude: float32(max / 127), 2^-126 at least (so that every step below is
 // exact), 0 for a row of zeros, NaN if the row holds an infinity or a NaN.

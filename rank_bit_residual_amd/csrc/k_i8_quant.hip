@@ -42,22 +42,60 @@ __device__ inline void store_codes8(const I8Out& o, int64_t row, int64_t c, cons
 }
 
 // ------------------------------------------------------------------------------ rows
-// T threads share a row and hold NV times eight elements each; NV = 0: the row is read twice instead, whatever its length.
-template <class DT, int T, int NV>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void k_i8_rows(I8QuantParams p) {
+// Largest magnitudes of eight columns: pairs of bits in 16-bit types.
+template <class DT>
+struct Most8 {
+  u32 w[DT::size * 2];
+};
+template <class DT>
+__device__ inline void add_most(Most8<DT>& m, const Vec8<DT>& v) {
+#pragma unroll
+  for (int k = 0; k < DT::size * 2; k++) {
+    if constexpr (DT::size == 4)
+      m.w[k] = max(m.w[k], v.w[k] & 0x7FFFFFFFu);
+    else
+      m.w[k] = max_pairs(m.w[k], v.w[k] & 0x7FFF7FFFu);
+  }
+}
+template <class DT>
+__device__ inline u32 most_at(const Most8<DT>& m, int k) {
+  if constexpr (DT::size == 4)
+    return m.w[k];
+  else
+    return __float_as_uint(DT::load((uint16_t)(m.w[k >> 1] >> (16 * (k & 1)))));
+}
+
+// T threads share a row and hold NV times eight elements each; NV = 0: the row is read twice instead, whatever its length. A
+// block takes rows one after another, the next on its way while one is worked on. COLS: its threads keep the maxima of their columns too
+// (and SUMS, their sums), over all the rows that the block takes, and leave them in row blockIdx.x of `part` (`sums`).
+enum { ROWS_ALONE, ROWS_AND_MAXIMA, ROWS_MAXIMA_AND_SUMS };
+template <class DT, int T, int NV, int COLS>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_i8_rows(I8QuantParams p, u32* part, float* sums) {
   typedef typename DT::T E;
-  constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64;
-  __shared__ u32 red[2][WAVES];
+  constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64, N = NV ? NV : 1;
+  static_assert(COLS == ROWS_ALONE || (NV && RPB == 1), "a block's threads own their columns");
+  __shared__ u32 red[2][RPB][WAVES];
   const int t = threadIdx.x % T, sub = threadIdx.x / T, wave = t >> 6;
-  const int64_t Kp = (int64_t)p.rows.kq * 64;
-  int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < p.R; row += (int64_t)gridDim.x * RPB, flip ^= 1) {
+  const int64_t Kp = (int64_t)p.rows.kq * 64, step = (int64_t)gridDim.x * RPB;
+  auto at = [&](int j) { return (int64_t)(j * T + t) * 8; };
+  auto load = [&](Vec8<DT>(&v)[N], int64_t row) {
     const E* x = reinterpret_cast<const E*>(p.x) + row * p.sr;
-    Vec8<DT> v[NV ? NV : 1];
+#pragma unroll
+    for (int j = 0; j < NV; j++) v[j] = load8_step<DT>(x, at(j), p.C, p.sc);
+  };
+  // the threads of a block stay together (they share barriers): past the last row some repeat it
+  int64_t first = (int64_t)blockIdx.x * RPB;
+  Vec8<DT> v[N], next[N];
+  load(v, min(first + sub, p.R - 1));
+  Most8<DT> cmax[COLS ? N : 1] = {};
+  float csum[COLS == ROWS_MAXIMA_AND_SUMS ? N : 1][8] = {};
+  int flip = 0;
+  for (; first < p.R; first += step, flip ^= 1) {
+    const int64_t row = min(first + sub, p.R - 1);
+    if (first + step < p.R) load(next, min(first + step + sub, p.R - 1));
+    const E* x = reinterpret_cast<const E*>(p.x) + row * p.sr;
     u32 most = 0;
     if constexpr (NV > 0) {
-#pragma unroll
-      for (int j = 0; j < NV; j++) v[j] = load8_step<DT>(x, (int64_t)(j * T + t) * 8, p.C, p.sc);
 #pragma unroll
       for (int j = 0; j < NV; j++) most = max(most, amax_bits<DT>(v[j].w));
     } else {
@@ -69,22 +107,36 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_i8_rows(I8QuantParams p) 
     most = wave_umax(most);
     if constexpr (WAVES > 1) {
       // two buffers: a wave may reach the next row's write while others still read this one's
-      if ((t & 63) == 0) red[flip][wave] = most;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < WAVES; w++) most = max(most, red[flip][w]);
+      if ((t & 63) == 0) red[flip][sub][wave] = most;
+      lds_barrier();
+      most = waves_umax<WAVES>(red[flip][sub]);
     }
     const Scale8 q = scale8(most);
     if (t == 0) p.rows.scales[row] = q.s;
     if constexpr (NV > 0) {
 #pragma unroll
       for (int j = 0; j < NV; j++) {
-        const int64_t c = (int64_t)(j * T + t) * 8;
-        if (c < Kp) store_codes8<DT>(p.rows, row, c, v[j], q);
+        if (at(j) < Kp) store_codes8<DT>(p.rows, row, at(j), v[j], q);
+        if constexpr (COLS != ROWS_ALONE) add_most<DT>(cmax[j], v[j]);
+        if constexpr (COLS == ROWS_MAXIMA_AND_SUMS) {
+#pragma unroll
+          for (int k = 0; k < 8; k++) csum[j][k] += elem<DT>(v[j], k);
+        }
+        v[j] = next[j];
       }
     } else {
       for (int64_t c = (int64_t)t * 8; c < Kp; c += T * 8) store_codes8<DT>(p.rows, row, c, load8_step<DT>(x, c, p.C, p.sc), q);
     }
+  }
+  if constexpr (COLS != ROWS_ALONE) {
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        if (at(j) + k >= p.C) continue;
+        part[blockIdx.x * p.C + at(j) + k] = most_at<DT>(cmax[j], k);
+        if constexpr (COLS == ROWS_MAXIMA_AND_SUMS) sums[blockIdx.x * p.C + at(j) + k] = csum[j][k];
+      }
   }
 }
 
@@ -135,10 +187,21 @@ __global__ __launch_bounds__(1024) void k_i8_colscale(const u32* part, const flo
   const int64_t col = (int64_t)blockIdx.x * 64 + lane, c = col < C ? col : C - 1;
   u32 m = 0;
   double s = 0;
-#pragma unroll 4
-  for (int k = wave; k < strips; k += 16) {
-    m = max(m, part[k * C + c]);
-    if (SUMS) s += (double)sums[k * C + c];
+  // eight strips requested at a time
+  for (int k = wave; k < strips; k += 128) {
+    u32 a[8];
+    float b[SUMS ? 8 : 1];
+#pragma unroll
+    for (int u = 0; u < 8; u++) {
+      const int64_t at = (int64_t)min(k + 16 * u, strips - 1) * C + c;  // past the last: it again, for its maximum
+      a[u] = part[at];
+      if (SUMS) b[u] = sums[at];
+    }
+#pragma unroll
+    for (int u = 0; u < 8; u++) {
+      m = max(m, a[u]);
+      if (SUMS && k + 16 * u < strips) s += (double)b[u];
+    }
   }
   most[wave][lane] = m;
   if (SUMS) sum[wave][lane] = s;
@@ -170,23 +233,19 @@ __global__ __launch_bounds__(256) void k_i8_cols(I8QuantParams p, const float* r
     Vec8<DT> v[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) v[i] = r + i < p.R ? load8_step<DT>(x + i * p.sr, 0, p.C - c, p.sc) : zero8<DT>();
-    Scale8 q[8];
+    const Vec8<MxF32> rv = load8<MxF32>(recip, c, p.C);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const int64_t col = c + j < p.C ? c + j : p.C - 1;
-      q[j] = {p.cols.scales[col], recip[col]};
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
+      const float r = elem<MxF32>(rv, j);
       float u[4], far = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; i++) u[i] = code8_fast(elem<DT>(v[i], j), q[j].r, far);
-      if (far > kSure8) {
-        asm volatile("");  // rarely taken: keep it a branch
+      for (int i = 0; i < 4; i++) u[i] = code8_fast(elem<DT>(v[i], j), r, far);
+      if (far > kSure8) {  // rarely taken
+        const float s = p.cols.scales[c + j];
 #pragma unroll
-        for (int i = 0; i < 4; i++) u[i] = code8_sure(elem<DT>(v[i], j), q[j].s, q[j].r);
+        for (int i = 0; i < 4; i++) u[i] = code8_sure(elem<DT>(v[i], j), s, r);
       }
-      words[lc * 132 + 16 * j + rg] = q[j].r == 0.f ? 0u : bytes4(u[0], u[1], u[2], u[3]);
+      words[lc * 132 + 16 * j + rg] = r == 0.f ? 0u : bytes4(u[0], u[1], u[2], u[3]);
     }
     __syncthreads();
     // 16 columns x 64 codes are a kilobyte of the tensor: a lane stores 16 codes of one
@@ -244,10 +303,13 @@ static unsigned blocks_of(int64_t n) { return (unsigned)(n < kMostBlocks ? n : k
 
 template <class DT, int T, int NV>
 static void launch_rows(const I8QuantParams& p, hipStream_t stream) {
-  constexpr int RPB = T < 256 ? 256 / T : 1;
-  k_i8_rows<DT, T, NV><<<blocks_of((p.R + RPB - 1) / RPB), T < 256 ? 256 : T, 0, stream>>>(p);
+  constexpr int RPB = T < 256 ? 256 / T : 1, THREADS = T < 256 ? 256 : T;
+  const int64_t blocks = (p.R + RPB - 1) / RPB, most = 2048 * 256 / THREADS;  // as many as the chip holds at once
+  k_i8_rows<DT, T, NV, ROWS_ALONE><<<(unsigned)(blocks < most ? blocks : most), THREADS, 0, stream>>>(p, nullptr, nullptr);
 }
 
+// Two vectors a thread and two or more rows on a compute unit: 8192 x 12288 bf16 70 us with 512 threads of three (four 98, 1024 of
+// two 84), 8192 x 8192 48 with 512 of two, 4096 x 4096 15 with 256 of two (128 of four 20).
 template <class DT>
 static hipError_t rows_t(const I8QuantParams& p, hipStream_t stream) {
   const int64_t Kp = (int64_t)p.rows.kq * 64;
@@ -256,24 +318,34 @@ static hipError_t rows_t(const I8QuantParams& p, hipStream_t stream) {
   else if (Kp <= 1024)
     launch_rows<DT, 64, 2>(p, stream);
   else if (Kp <= 2048)
-    launch_rows<DT, 256, 1>(p, stream);
+    launch_rows<DT, 128, 2>(p, stream);
   else if (Kp <= 4096)
     launch_rows<DT, 256, 2>(p, stream);
   else if (Kp <= 8192)
-    launch_rows<DT, 1024, 1>(p, stream);
+    launch_rows<DT, 512, 2>(p, stream);
+  else if (Kp <= 12288)
+    launch_rows<DT, 512, 3>(p, stream);
   else if (Kp <= 16384)
     launch_rows<DT, 1024, 2>(p, stream);
-  else if (Kp <= 32768)
-    launch_rows<DT, 1024, 4>(p, stream);
   else
     launch_rows<DT, 1024, 0>(p, stream);
   return hipGetLastError();
 }
 
-// Strips of rows that a column's maximum is taken over: enough blocks for the chip, at least 16 rows each.
-static int64_t strips_of(int64_t R, int64_t C) {
+// Rows whose codes and column maxima come from one reading: they fit a block's registers.
+constexpr int64_t kSharedRow = 16384;
+
+// Strips of rows that a column's maximum is taken over. Read with the rows (`shared`): the blocks that the chip holds, of four rows or
+// more once that many are there. Alone: enough blocks for the chip, of 16 rows or more.
+static int64_t strips_of(int64_t R, int64_t C, bool shared) {
+  int64_t strips;
+  if (shared) {
+    strips = R / 4 < 512 ? R / 4 : 512;
+    if (strips < 256) strips = R < 256 ? R : 256;
+    return strips;
+  }
   const int64_t chunks = (C + 511) / 512;
-  int64_t strips = (2048 + chunks - 1) / chunks;
+  strips = (2048 + chunks - 1) / chunks;
   const int64_t most = (R + 15) / 16;
   if (strips > most) strips = most;
   if (strips > 256) strips = 256;
@@ -286,13 +358,15 @@ static int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 // A matrix whose columns are contiguous is its transpose, with the outputs exchanged.
 static bool exchanged(int64_t sr, int64_t sc) { return sr == 1 && sc != 1; }
 
+static bool shares(int64_t C, bool rows) { return rows && i8_kq(C) * 64 <= kSharedRow; }
+
 size_t i8_quantize_bytes(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows, bool cols) {
   if (exchanged(sr, sc)) {
     const int64_t r = R;
     const bool k = rows;
     R = C, C = r, rows = cols, cols = k;
   }
-  return cols ? (size_t)(round256(C * 4) + 2 * round256(strips_of(R, C) * C * 4)) : 0;
+  return cols ? (size_t)(round256(C * 4) + 2 * round256(strips_of(R, C, shares(C, rows)) * C * 4)) : 0;
 }
 
 bool i8_quantize_fits(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows, bool cols) {
@@ -300,26 +374,50 @@ bool i8_quantize_fits(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows, b
   return !(swap ? rows : cols) || mx_fits_grid(((swap ? R : C) + 63) / 64, 1024);
 }
 
+template <class DT, int T, int NV>
+static void launch_shared(const I8QuantParams& p, int64_t strips, u32* part, float* sums, hipStream_t stream) {
+  if (p.sums)
+    k_i8_rows<DT, T, NV, ROWS_MAXIMA_AND_SUMS><<<(unsigned)strips, T, 0, stream>>>(p, part, sums);
+  else
+    k_i8_rows<DT, T, NV, ROWS_AND_MAXIMA><<<(unsigned)strips, T, 0, stream>>>(p, part, sums);
+}
+
 template <class DT>
 static hipError_t cols_t(const I8QuantParams& p, hipStream_t stream) {
-  const int64_t strips = strips_of(p.R, p.C), strip_rows = (p.R + strips - 1) / strips;
+  const bool shared = shares(p.C, p.rows.codes != nullptr);
+  const int64_t strips = strips_of(p.R, p.C, shared);
   float* recip = reinterpret_cast<float*>(p.workspace);
   u32* part = reinterpret_cast<u32*>((uint8_t*)p.workspace + round256(p.C * 4));
   float* sums = reinterpret_cast<float*>((uint8_t*)part + round256(strips * p.C * 4));
-  const dim3 grid((unsigned)((p.C + 511) / 512), (unsigned)strips);
-  const unsigned joins = (unsigned)((p.C + 63) / 64);
-  if (p.sums) {
-    k_i8_colmax<DT, true><<<grid, 256, 0, stream>>>(p, part, sums, strip_rows);
-    if (p.sums_dtype == SVDQ_F32)
-      k_i8_colscale<MxF32, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (float*)p.sums);
-    else if (p.sums_dtype == SVDQ_BF16)
-      k_i8_colscale<MxBF16, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (uint16_t*)p.sums);
+  if (shared) {
+    const int64_t Kp = (int64_t)p.rows.kq * 64;
+    if (Kp <= 2048)
+      launch_shared<DT, 256, 1>(p, strips, part, sums, stream);
+    else if (Kp <= 4096)
+      launch_shared<DT, 256, 2>(p, strips, part, sums, stream);
+    else if (Kp <= 8192)
+      launch_shared<DT, 512, 2>(p, strips, part, sums, stream);
+    else if (Kp <= 12288)
+      launch_shared<DT, 512, 3>(p, strips, part, sums, stream);
     else
-      k_i8_colscale<MxF16, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (uint16_t*)p.sums);
+      launch_shared<DT, 1024, 2>(p, strips, part, sums, stream);
   } else {
-    k_i8_colmax<DT, false><<<grid, 256, 0, stream>>>(p, part, sums, strip_rows);
-    k_i8_colscale<MxF32, false><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, nullptr);
+    const int64_t strip_rows = (p.R + strips - 1) / strips;
+    const dim3 grid((unsigned)((p.C + 511) / 512), (unsigned)strips);
+    if (p.sums)
+      k_i8_colmax<DT, true><<<grid, 256, 0, stream>>>(p, part, sums, strip_rows);
+    else
+      k_i8_colmax<DT, false><<<grid, 256, 0, stream>>>(p, part, sums, strip_rows);
   }
+  const unsigned joins = (unsigned)((p.C + 63) / 64);
+  if (!p.sums)
+    k_i8_colscale<MxF32, false><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, nullptr);
+  else if (p.sums_dtype == SVDQ_F32)
+    k_i8_colscale<MxF32, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (float*)p.sums);
+  else if (p.sums_dtype == SVDQ_BF16)
+    k_i8_colscale<MxBF16, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (uint16_t*)p.sums);
+  else
+    k_i8_colscale<MxF16, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (uint16_t*)p.sums);
   // the transpose's stages come in pairs, so the last tile of rows may hold nothing but padding
   const int64_t tiles_c = (p.C + 127) / 128, tiles = (int64_t)p.cols.kq * tiles_c;
   k_i8_cols<DT><<<blocks_of(tiles), 256, 0, stream>>>(p, recip, tiles_c, tiles);
@@ -330,7 +428,7 @@ template <class DT>
 static hipError_t quantize_t(const I8QuantParams& p0, hipStream_t stream) {
   I8QuantParams p = p0;
   if (exchanged(p.sr, p.sc)) p.R = p0.C, p.C = p0.R, p.sr = p0.sc, p.sc = p0.sr, p.rows = p0.cols, p.cols = p0.rows;
-  if (p.rows.codes) {
+  if (p.rows.codes && !(p.cols.codes && shares(p.C, true))) {
     const hipError_t e = rows_t<DT>(p, stream);
     if (e != hipSuccess) return e;
   }

@@ -62,30 +62,73 @@ struct RowStats {
   double mean, rstd;
 };
 
-// This thread's share of sum d and sum d^2 from eight elements at c.
+// Elements [c, c + 8) of a row of K, the row's first element in the places past its end: those add nothing to sums of differences
+// from it.
 template <class DT>
-__device__ inline void add_stats(const Vec8<DT>& v, int64_t c, int64_t K, double pivot, double& s, double& q) {
-  const int64_t n = K - c;
+__device__ inline Vec8<DT> load8_padded(const typename DT::T* row, int64_t c, int64_t K) {
+  Vec8<DT> v;
+  if (c + 8 <= K) {
+    __builtin_memcpy(&v, row + c, sizeof v);
+    return v;
+  }
+  v = zero8<DT>();
 #pragma unroll
   for (int k = 0; k < 8; k++) {
-    const double d = k < n ? (double)elem<DT>(v, k) - pivot : 0.0;
+    const typename DT::T e = row[c + k < K ? c + k : 0];
+    if constexpr (DT::size == 4)
+      v.w[k] = __float_as_uint(e);
+    else
+      v.w[k >> 1] |= (u32)e << (16 * (k & 1));
+  }
+  asm volatile("");  // keeps the two branches' loads apart: whole vectors there, elements here
+  return v;
+}
+
+// This thread's share of sum d and sum d^2.
+template <class DT>
+__device__ inline void add_stats(const Vec8<DT>& v, double pivot, double& s, double& q) {
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    const double d = (double)elem<DT>(v, k) - pivot;
     s += d;
     q = __builtin_fma(d, d, q);
   }
 }
 
+// Keeps the elements in their own type, so that their float64 values do not live on in registers.
+template <class DT>
+__device__ __forceinline__ void settle(Vec8<DT>& v) {
+#pragma unroll
+  for (int k = 0; k < DT::size * 2; k++) asm volatile("" : "+v"(v.w[k]));
+}
+
+// Eight columns' weight and bias.
+struct Params8 {
+  float w[8], b[8];
+};
+template <class DT>
+__device__ inline void load_params(Params8& q, const NormParams& p, int64_t c) {
+  param8<DT>(q.w, p.weight, p.param_f32, c, p.K, 1.f);
+  param8<DT>(q.b, p.bias, p.param_f32, c, p.K, 0.f);
+}
+
 // y of eight elements, as float32; zeros past the row's end.
 template <class DT>
-__device__ inline void norm8(float (&y)[8], const Vec8<DT>& v, int64_t c, const NormParams& p, const RowStats& st) {
-  float w[8], b[8];
-  param8<DT>(w, p.weight, p.param_f32, c, p.K, 1.f);
-  param8<DT>(b, p.bias, p.param_f32, c, p.K, 0.f);
-  const int64_t n = p.K - c;
+__device__ inline void norm8(float (&y)[8], const Vec8<DT>& v, int64_t c, int64_t K, const Params8& q, const RowStats& st) {
 #pragma unroll
   for (int k = 0; k < 8; k++) {
     const double xh = ((double)elem<DT>(v, k) - st.mean) * st.rstd;
-    y[k] = k < n ? (float)__builtin_fma(xh, (double)w[k], (double)b[k]) : 0.f;
+    y[k] = (float)__builtin_fma(xh, (double)q.w[k], (double)q.b[k]);
   }
+  if (c + 8 > K) {
+#pragma unroll
+    for (int k = 0; k < 8; k++) y[k] = c + k < K ? y[k] : 0.f;
+  }
+}
+
+__device__ __forceinline__ void settle(Params8& q) {
+#pragma unroll
+  for (int k = 0; k < 8; k++) asm volatile("" : "+v"(q.w[k]), "+v"(q.b[k]));
 }
 
 __device__ inline u32 amax8(const float (&y)[8]) {
@@ -111,84 +154,111 @@ __device__ inline void put8(const NormParams& p, int64_t row, int64_t c, const f
 }
 
 // T threads share a row and hold NV times eight elements each; NV = 0: a row of any length, read once for its statistics and
-// again for y (twice for 8-bit codes).
+// again for y (twice for 8-bit codes). A block takes rows one after another: its columns' parameters stay in registers, and
+// the next row is on its way while one is worked on.
 template <class DT, int T, int NV, int OUT>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm(NormParams p) {
+__global__ __launch_bounds__(T < 256 ? 256 : T, NV == 2 ? 4 : 1) void k_norm(NormParams p) {
   typedef typename DT::T E;
-  constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64;
-  __shared__ double red[2][2][WAVES];
-  __shared__ u32 redm[2][WAVES];
+  constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64, N = NV ? NV : 1;
+  __shared__ double red[2][RPB][2][WAVES];
+  __shared__ u32 redm[2][RPB][WAVES];
   const int t = threadIdx.x % T, sub = threadIdx.x / T, wave = t >> 6;
   // threads past the end of a row take part up to the end of the codes' padding
   const int64_t Kp = OUT == NORM_Y ? p.K : (OUT == NORM_I8 ? (int64_t)p.i8.kq * 64 : (int64_t)p.mx.kq * 128);
-  int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < p.M; row += (int64_t)gridDim.x * RPB, flip ^= 1) {
+  auto at = [&](int j) { return (int64_t)(j * T + t) * 8; };
+  auto load = [&](Vec8<DT>(&v)[N], double& pivot, int64_t row) {
     const E* x = reinterpret_cast<const E*>(p.x) + row * p.ldx;
-    const double pivot = DT::load(x[0]);
-    double s = 0, q = 0;
-    Vec8<DT> v[NV ? NV : 1];
+    pivot = DT::load(x[0]);
     if constexpr (NV > 0) {
 #pragma unroll
-      for (int j = 0; j < NV; j++) v[j] = load8<DT>(x, (int64_t)(j * T + t) * 8, p.K);
+      for (int j = 0; j < NV; j++) v[j] = load8_padded<DT>(x, at(j), p.K);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  Vec8<DT> v[N], next[N];
+  double pivot = 0, pivot_next = 0;
+  // rows of a block: its threads stay together (they share barriers), so past the last row some repeat it
+  int64_t first = (int64_t)blockIdx.x * RPB;
+  load(v, pivot, min(first + sub, p.M - 1));
+  Params8 q[N];
+  if constexpr (NV > 0) {
 #pragma unroll
-      for (int j = 0; j < NV; j++) add_stats<DT>(v[j], (int64_t)(j * T + t) * 8, p.K, pivot, s, q);
+    for (int j = 0; j < NV; j++) load_params<DT>(q[j], p, at(j));
+  }
+  int flip = 0;
+  for (; first < p.M; first += step, flip ^= 1) {
+    const int64_t row = min(first + sub, p.M - 1);
+    if (first + step < p.M) load(next, pivot_next, min(first + step + sub, p.M - 1));
+    const E* x = reinterpret_cast<const E*>(p.x) + row * p.ldx;
+    double s = 0, sq = 0;
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; j++) {
+        add_stats<DT>(v[j], pivot, s, sq);
+        settle(v[j]);
+        settle(q[j]);
+      }
     } else {
-      for (int64_t c = (int64_t)t * 8; c < p.K; c += T * 8) add_stats<DT>(load8<DT>(x, c, p.K), c, p.K, pivot, s, q);
+      for (int64_t c = (int64_t)t * 8; c < p.K; c += T * 8) add_stats<DT>(load8_padded<DT>(x, c, p.K), pivot, s, sq);
     }
     s = wave_sum(s);
-    q = wave_sum(q);
+    sq = wave_sum(sq);
     if constexpr (WAVES > 1) {
       // two buffers: a wave may reach the next row's write while others still read this one's
-      if ((t & 63) == 0) red[flip][0][wave] = s, red[flip][1][wave] = q;
-      __syncthreads();
-      s = q = 0;
-#pragma unroll
-      for (int w = 0; w < WAVES; w++) s += red[flip][0][w], q += red[flip][1][w];
+      if ((t & 63) == 0) red[flip][sub][0][wave] = s, red[flip][sub][1][wave] = sq;
+      lds_barrier();
+      s = waves_sum<WAVES>(red[flip][sub][0]);
+      sq = waves_sum<WAVES>(red[flip][sub][1]);
     }
     const double k1 = 1.0 / (double)p.K, ds = s * k1;
-    double var = __builtin_fma(q, k1, -ds * ds);
+    double var = __builtin_fma(sq, k1, -ds * ds);
     var = var < 0 ? 0 : var;  // NaN stays
     const RowStats st{pivot + ds, 1.0 / sqrt(var + p.eps)};
     if (t == 0 && p.mean) p.mean[row] = (float)st.mean, p.rstd[row] = (float)st.rstd;
 
     Scale8 scale{0.f, 0.f};
-    float y[NV ? NV : 1][8];
-    if constexpr (NV > 0) {
-#pragma unroll
-      for (int j = 0; j < NV; j++) norm8<DT>(y[j], v[j], (int64_t)(j * T + t) * 8, p, st);
-    }
+    float y[N][8];
     if constexpr (OUT == NORM_I8) {
       u32 most = 0;
       if constexpr (NV > 0) {
 #pragma unroll
-        for (int j = 0; j < NV; j++) most = max(most, amax8(y[j]));
+        for (int j = 0; j < NV; j++) {
+          norm8<DT>(y[j], v[j], at(j), p.K, q[j], st);
+          most = max(most, amax8(y[j]));
+        }
       } else {
         for (int64_t c = (int64_t)t * 8; c < p.K; c += T * 8) {
-          norm8<DT>(y[0], load8<DT>(x, c, p.K), c, p, st);
+          load_params<DT>(q[0], p, c);
+          norm8<DT>(y[0], load8<DT>(x, c, p.K), c, p.K, q[0], st);
           most = max(most, amax8(y[0]));
         }
       }
       most = wave_umax(most);
       if constexpr (WAVES > 1) {
-        if ((t & 63) == 0) redm[flip][wave] = most;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < WAVES; w++) most = max(most, redm[flip][w]);
+        if ((t & 63) == 0) redm[flip][sub][wave] = most;
+        lds_barrier();
+        most = waves_umax<WAVES>(redm[flip][sub]);
       }
       scale = scale8(most);
       if (t == 0) p.i8.scales[row] = scale.s;
     }
     if constexpr (NV > 0) {
 #pragma unroll
-      for (int j = 0; j < NV; j++) put8<DT, OUT>(p, row, (int64_t)(j * T + t) * 8, y[j], scale);
+      for (int j = 0; j < NV; j++) {
+        if constexpr (OUT != NORM_I8) norm8<DT>(y[j], v[j], at(j), p.K, q[j], st);
+        put8<DT, OUT>(p, row, at(j), y[j], scale);
+        v[j] = next[j];
+      }
     } else {
       // whole waves: an MXFP4 block's four lanes agree on its maximum
       for (int64_t c0 = (int64_t)(t & ~63) * 8; c0 < Kp; c0 += T * 8) {
         const int64_t c = c0 + 8 * (t & 63);
-        norm8<DT>(y[0], load8<DT>(x, c, p.K), c, p, st);
+        load_params<DT>(q[0], p, c);
+        norm8<DT>(y[0], load8<DT>(x, c, p.K), c, p.K, q[0], st);
         put8<DT, OUT>(p, row, c, y[0], scale);
       }
     }
+    pivot = pivot_next;
   }
 }
 
@@ -407,20 +477,25 @@ static unsigned blocks_of(int64_t n) { return (unsigned)(n < kMostBlocks ? n : k
 template <class DT, int T, int NV, int OUT>
 static void launch_rows(const NormParams& p, hipStream_t stream) {
   constexpr int RPB = T < 256 ? 256 / T : 1;
-  k_norm<DT, T, NV, OUT><<<blocks_of((p.M + RPB - 1) / RPB), T < 256 ? 256 : T, 0, stream>>>(p);
+  const int64_t blocks = (p.M + RPB - 1) / RPB, most = 1024 * 256 / (T < 256 ? 256 : T);  // as many as the chip holds at once
+  k_norm<DT, T, NV, OUT><<<(unsigned)(blocks < most ? blocks : most), T < 256 ? 256 : T, 0, stream>>>(p);
 }
 
 template <class DT, int OUT>
 static hipError_t norm_t(const NormParams& p, hipStream_t stream) {
   const int64_t Kp = OUT == NORM_Y ? p.K : (OUT == NORM_I8 ? (int64_t)p.i8.kq * 64 : (int64_t)p.mx.kq * 128);
+  // Two vectors a thread: 8192 x 8192 bf16 66 us (four of 256 threads 71, one of 1024 85), to codes 74 (four 73, one 102); 777 x 5003
+  // 11.0 (17.0, 13.4)
   if (Kp <= 512)
     launch_rows<DT, 64, 1, OUT>(p, stream);
+  else if (Kp <= 1024)
+    launch_rows<DT, 64, 2, OUT>(p, stream);
   else if (Kp <= 2048)
-    launch_rows<DT, 256, 1, OUT>(p, stream);
+    launch_rows<DT, 128, 2, OUT>(p, stream);
   else if (Kp <= 4096)
     launch_rows<DT, 256, 2, OUT>(p, stream);
   else if (Kp <= 8192)
-    launch_rows<DT, 1024, 1, OUT>(p, stream);
+    launch_rows<DT, 512, 2, OUT>(p, stream);
   else if (Kp <= 16384)
     launch_rows<DT, 1024, 2, OUT>(p, stream);
   else
