@@ -69,6 +69,34 @@ __device__ inline u32 waves_umax(const u32* part) {
   return v;
 }
 
+// ---- elements of a row --------------------------------------------------------------------
+// Elements [c, c + 8) of a row of K >= 8, whole vectors without a branch: where they pass the row's end, its last eight, which
+// `fit8` moves into place, with `past` (bits of an element) behind them. Only waves at a row's end take that branch.
+template <class DT>
+__device__ inline Vec8<DT> load8_last(const typename DT::T* row, int64_t c, int64_t K) {
+  Vec8<DT> v;
+  __builtin_memcpy(&v, row + (c < K - 8 ? c : K - 8), sizeof v);
+  return v;
+}
+template <class DT>
+__device__ inline void fit8(Vec8<DT>& v, int64_t c, int64_t K, u32 past = 0) {
+  if (!__builtin_amdgcn_ballot_w64(c + 8 > K)) return;
+  const int s = (int)(c + 8 <= K ? 0 : (c < K ? c + 8 - K : 8));  // elements to move down by
+  constexpr int W = DT::size * 2, E = W / 4;                      // words of a vector, of two elements
+  const u32 fill = DT::size == 4 ? past : past * 0x10001u;
+#pragma unroll
+  for (int k = 0; k < W; k++) v.w[k] = s & 8 ? fill : v.w[k];
+#pragma unroll
+  for (int k = 0; k < W; k++) v.w[k] = s & 4 ? (k + 2 * E < W ? v.w[(k + 2 * E) % W] : fill) : v.w[k];
+#pragma unroll
+  for (int k = 0; k < W; k++) v.w[k] = s & 2 ? (k + E < W ? v.w[(k + E) % W] : fill) : v.w[k];
+#pragma unroll
+  for (int k = 0; k < W; k++) {
+    const u32 up = k + 1 < W ? v.w[(k + 1) % W] : fill;
+    v.w[k] = s & 1 ? (DT::size == 4 ? up : (v.w[k] >> 16) | (up << 16)) : v.w[k];
+  }
+}
+
 // ---- 8-bit codes --------------------------------------------------------------------------
 // A row's scale from the bits of its largest magnitude: float32(max / 127), 2^-126 at least (so that every step below is
 // exact), 0 for a row of zeros, NaN if the row holds an infinity or a NaN.

@@ -65,12 +65,13 @@ __device__ inline u32 most_at(const Most8<DT>& m, int k) {
     return __float_as_uint(DT::load((uint16_t)(m.w[k >> 1] >> (16 * (k & 1)))));
 }
 
-// T threads share a row and hold NV times eight elements each; NV = 0: the row is read twice instead, whatever its length. A
+// T threads share a row of contiguous elements, eight at least, and hold NV times eight each; NV = 0: the row is read twice instead,
+// whatever its length and step. A
 // block takes rows one after another, the next on its way while one is worked on. COLS: its threads keep the maxima of their columns too
 // (and SUMS, their sums), over all the rows that the block takes, and leave them in row blockIdx.x of `part` (`sums`).
 enum { ROWS_ALONE, ROWS_AND_MAXIMA, ROWS_MAXIMA_AND_SUMS };
 template <class DT, int T, int NV, int COLS>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void k_i8_rows(I8QuantParams p, u32* part, float* sums) {
+__global__ __launch_bounds__(T < 256 ? 256 : T, COLS ? 4 : 1) void k_i8_rows(I8QuantParams p, u32* part, float* sums) {
   typedef typename DT::T E;
   constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64, N = NV ? NV : 1;
   static_assert(COLS == ROWS_ALONE || (NV && RPB == 1), "a block's threads own their columns");
@@ -81,7 +82,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_i8_rows(I8QuantParams p, 
   auto load = [&](Vec8<DT>(&v)[N], int64_t row) {
     const E* x = reinterpret_cast<const E*>(p.x) + row * p.sr;
 #pragma unroll
-    for (int j = 0; j < NV; j++) v[j] = load8_step<DT>(x, at(j), p.C, p.sc);
+    for (int j = 0; j < NV; j++) {
+      v[j] = load8_last<DT>(x, at(j), p.C);
+    }
   };
   // the threads of a block stay together (they share barriers): past the last row some repeat it
   int64_t first = (int64_t)blockIdx.x * RPB;
@@ -97,7 +100,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_i8_rows(I8QuantParams p, 
     u32 most = 0;
     if constexpr (NV > 0) {
 #pragma unroll
-      for (int j = 0; j < NV; j++) most = max(most, amax_bits<DT>(v[j].w));
+      for (int j = 0; j < NV; j++) {
+        fit8<DT>(v[j], at(j), p.C);
+        most = max(most, amax_bits<DT>(v[j].w));
+      }
     } else {
       for (int64_t c = (int64_t)t * 8; c < p.C; c += T * 8) {
         v[0] = load8_step<DT>(x, c, p.C, p.sc);
@@ -301,6 +307,9 @@ using namespace dev;
 constexpr int64_t kMostBlocks = 1 << 20;  // of kernels that walk over what is left
 static unsigned blocks_of(int64_t n) { return (unsigned)(n < kMostBlocks ? n : kMostBlocks); }
 
+// Rows that are read in whole vectors.
+static bool one_vector(int64_t C, int64_t sc) { return C >= 8 && sc == 1; }
+
 template <class DT, int T, int NV>
 static void launch_rows(const I8QuantParams& p, hipStream_t stream) {
   constexpr int RPB = T < 256 ? 256 / T : 1, THREADS = T < 256 ? 256 : T;
@@ -308,12 +317,14 @@ static void launch_rows(const I8QuantParams& p, hipStream_t stream) {
   k_i8_rows<DT, T, NV, ROWS_ALONE><<<(unsigned)(blocks < most ? blocks : most), THREADS, 0, stream>>>(p, nullptr, nullptr);
 }
 
-// Two vectors a thread and two or more rows on a compute unit: 8192 x 12288 bf16 70 us with 512 threads of three (four 98, 1024 of
-// two 84), 8192 x 8192 48 with 512 of two, 4096 x 4096 15 with 256 of two (128 of four 20).
+// Two or three vectors a thread, so that several rows are on a compute unit: 8192 x 12288 bf16 70 to 74 us with 512 threads of three, 4096 x
+// 4096 15 with 256 of two (128 of four 20).
 template <class DT>
 static hipError_t rows_t(const I8QuantParams& p, hipStream_t stream) {
   const int64_t Kp = (int64_t)p.rows.kq * 64;
-  if (Kp <= 512)
+  if (!one_vector(p.C, p.sc))
+    launch_rows<DT, 1024, 0>(p, stream);
+  else if (Kp <= 512)
     launch_rows<DT, 64, 1>(p, stream);
   else if (Kp <= 1024)
     launch_rows<DT, 64, 2>(p, stream);
@@ -358,15 +369,15 @@ static int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 // A matrix whose columns are contiguous is its transpose, with the outputs exchanged.
 static bool exchanged(int64_t sr, int64_t sc) { return sr == 1 && sc != 1; }
 
-static bool shares(int64_t C, bool rows) { return rows && i8_kq(C) * 64 <= kSharedRow; }
+static bool shares(int64_t C, int64_t sc, bool rows) { return rows && one_vector(C, sc) && i8_kq(C) * 64 <= kSharedRow; }
 
 size_t i8_quantize_bytes(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows, bool cols) {
   if (exchanged(sr, sc)) {
-    const int64_t r = R;
+    const int64_t r = R, s = sr;
     const bool k = rows;
-    R = C, C = r, rows = cols, cols = k;
+    R = C, C = r, sr = sc, sc = s, rows = cols, cols = k;
   }
-  return cols ? (size_t)(round256(C * 4) + 2 * round256(strips_of(R, C, shares(C, rows)) * C * 4)) : 0;
+  return cols ? (size_t)(round256(C * 4) + 2 * round256(strips_of(R, C, shares(C, sc, rows)) * C * 4)) : 0;
 }
 
 bool i8_quantize_fits(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows, bool cols) {
@@ -384,7 +395,7 @@ static void launch_shared(const I8QuantParams& p, int64_t strips, u32* part, flo
 
 template <class DT>
 static hipError_t cols_t(const I8QuantParams& p, hipStream_t stream) {
-  const bool shared = shares(p.C, p.rows.codes != nullptr);
+  const bool shared = shares(p.C, p.sc, p.rows.codes != nullptr);
   const int64_t strips = strips_of(p.R, p.C, shared);
   float* recip = reinterpret_cast<float*>(p.workspace);
   u32* part = reinterpret_cast<u32*>((uint8_t*)p.workspace + round256(p.C * 4));
@@ -428,7 +439,7 @@ template <class DT>
 static hipError_t quantize_t(const I8QuantParams& p0, hipStream_t stream) {
   I8QuantParams p = p0;
   if (exchanged(p.sr, p.sc)) p.R = p0.C, p.C = p0.R, p.sr = p0.sc, p.sc = p0.sr, p.rows = p0.cols, p.cols = p0.rows;
-  if (p.rows.codes && !(p.cols.codes && shares(p.C, true))) {
+  if (p.rows.codes && !(p.cols.codes && shares(p.C, p.sc, true))) {
     const hipError_t e = rows_t<DT>(p, stream);
     if (e != hipSuccess) return e;
   }

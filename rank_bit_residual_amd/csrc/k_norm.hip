@@ -62,34 +62,28 @@ struct RowStats {
   double mean, rstd;
 };
 
-// Elements [c, c + 8) of a row of K, the row's first element in the places past its end: those add nothing to sums of differences
-// from it.
+// A row's first element, as bits and as a value.
 template <class DT>
-__device__ inline Vec8<DT> load8_padded(const typename DT::T* row, int64_t c, int64_t K) {
-  Vec8<DT> v;
-  if (c + 8 <= K) {
-    __builtin_memcpy(&v, row + c, sizeof v);
-    return v;
-  }
-  v = zero8<DT>();
-#pragma unroll
-  for (int k = 0; k < 8; k++) {
-    const typename DT::T e = row[c + k < K ? c + k : 0];
-    if constexpr (DT::size == 4)
-      v.w[k] = __float_as_uint(e);
-    else
-      v.w[k >> 1] |= (u32)e << (16 * (k & 1));
-  }
-  asm volatile("");  // keeps the two branches' loads apart: whole vectors there, elements here
-  return v;
+__device__ inline u32 first_bits(const typename DT::T* x) {
+  if constexpr (DT::size == 4)
+    return __float_as_uint(x[0]);
+  else
+    return x[0];
+}
+template <class DT>
+__device__ inline double bits_value(u32 bits) {
+  if constexpr (DT::size == 4)
+    return __uint_as_float(bits);
+  else
+    return DT::load((uint16_t)bits);
 }
 
 // This thread's share of sum d and sum d^2.
 template <class DT>
-__device__ inline void add_stats(const Vec8<DT>& v, double pivot, double& s, double& q) {
+__device__ inline void add_stats(const Vec8<DT>& v, double pivot, double& s, double& q, int64_t n = 8) {
 #pragma unroll
   for (int k = 0; k < 8; k++) {
-    const double d = (double)elem<DT>(v, k) - pivot;
+    const double d = k < n ? (double)elem<DT>(v, k) - pivot : 0.0;
     s += d;
     q = __builtin_fma(d, d, q);
   }
@@ -153,7 +147,7 @@ __device__ inline void put8(const NormParams& p, int64_t row, int64_t c, const f
   }
 }
 
-// T threads share a row and hold NV times eight elements each; NV = 0: a row of any length, read once for its statistics and
+// T threads share a row of eight elements or more and hold NV times eight each; NV = 0: a row of any length, read once for its statistics and
 // again for y (twice for 8-bit codes). A block takes rows one after another: its columns' parameters stay in registers, and
 // the next row is on its way while one is worked on.
 template <class DT, int T, int NV, int OUT>
@@ -166,20 +160,20 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, NV == 2 ? 4 : 1) void k_norm(Nor
   // threads past the end of a row take part up to the end of the codes' padding
   const int64_t Kp = OUT == NORM_Y ? p.K : (OUT == NORM_I8 ? (int64_t)p.i8.kq * 64 : (int64_t)p.mx.kq * 128);
   auto at = [&](int j) { return (int64_t)(j * T + t) * 8; };
-  auto load = [&](Vec8<DT>(&v)[N], double& pivot, int64_t row) {
+  auto load = [&](Vec8<DT>(&v)[N], u32& pivot, int64_t row) {
     const E* x = reinterpret_cast<const E*>(p.x) + row * p.ldx;
-    pivot = DT::load(x[0]);
+    pivot = first_bits<DT>(x);
     if constexpr (NV > 0) {
 #pragma unroll
-      for (int j = 0; j < NV; j++) v[j] = load8_padded<DT>(x, at(j), p.K);
+      for (int j = 0; j < NV; j++) v[j] = load8_last<DT>(x, at(j), p.K);
     }
   };
   const int64_t step = (int64_t)gridDim.x * RPB;
   Vec8<DT> v[N], next[N];
-  double pivot = 0, pivot_next = 0;
+  u32 pivot_bits = 0, pivot_next = 0;
   // rows of a block: its threads stay together (they share barriers), so past the last row some repeat it
   int64_t first = (int64_t)blockIdx.x * RPB;
-  load(v, pivot, min(first + sub, p.M - 1));
+  load(v, pivot_bits, min(first + sub, p.M - 1));
   Params8 q[N];
   if constexpr (NV > 0) {
 #pragma unroll
@@ -190,16 +184,18 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, NV == 2 ? 4 : 1) void k_norm(Nor
     const int64_t row = min(first + sub, p.M - 1);
     if (first + step < p.M) load(next, pivot_next, min(first + step + sub, p.M - 1));
     const E* x = reinterpret_cast<const E*>(p.x) + row * p.ldx;
+    const double pivot = bits_value<DT>(pivot_bits);
     double s = 0, sq = 0;
     if constexpr (NV > 0) {
 #pragma unroll
       for (int j = 0; j < NV; j++) {
+        fit8<DT>(v[j], at(j), p.K, pivot_bits);  // past the row's end its first element: it adds nothing to the differences
         add_stats<DT>(v[j], pivot, s, sq);
         settle(v[j]);
         settle(q[j]);
       }
     } else {
-      for (int64_t c = (int64_t)t * 8; c < p.K; c += T * 8) add_stats<DT>(load8_padded<DT>(x, c, p.K), pivot, s, sq);
+      for (int64_t c = (int64_t)t * 8; c < p.K; c += T * 8) add_stats<DT>(load8<DT>(x, c, p.K), pivot, s, sq, p.K - c);
     }
     s = wave_sum(s);
     sq = wave_sum(sq);
@@ -258,7 +254,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, NV == 2 ? 4 : 1) void k_norm(Nor
         put8<DT, OUT>(p, row, c, y[0], scale);
       }
     }
-    pivot = pivot_next;
+    pivot_bits = pivot_next;
   }
 }
 
@@ -268,7 +264,7 @@ struct GradRow {
   Vec8<DT> dy, x;
 };
 
-// T threads share a row, NV times eight columns each, the same ones in every row that the block takes.
+// T threads share a row of eight elements or more, NV times eight columns each, the same ones in every row that the block takes.
 template <class DT, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradParams p, float* part) {
   typedef typename DT::T E;
@@ -290,8 +286,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradParams 
 #pragma unroll
     for (int j = 0; j < NV; j++) {
       const int64_t c = (int64_t)(j * T + t) * 8;
-      to[j].dy = load8<DT>(reinterpret_cast<const E*>(p.dy) + r * p.lddy, c, p.K);
-      to[j].x = load8<DT>(reinterpret_cast<const E*>(p.x) + r * p.ldx, c, p.K);
+      to[j].dy = load8_last<DT>(reinterpret_cast<const E*>(p.dy) + r * p.lddy, c, p.K);
+      to[j].x = load8_last<DT>(reinterpret_cast<const E*>(p.x) + r * p.ldx, c, p.K);
     }
   };
   load(cur, row, mean, rstd);
@@ -302,7 +298,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradParams 
     load(next, row + step, mu, rs);
     float c1 = 0.f, c2 = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; j++)
+    for (int j = 0; j < NV; j++) {
+      fit8<DT>(cur[j].dy, (int64_t)(j * T + t) * 8, p.K);
+      fit8<DT>(cur[j].x, (int64_t)(j * T + t) * 8, p.K);
 #pragma unroll
       for (int k = 0; k < 8; k++) {
         const float dy = elem<DT>(cur[j].dy, k), xh = (elem<DT>(cur[j].x, k) - mean) * rstd, g = dy * w[j][k];
@@ -311,6 +309,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradParams 
         dw[j][k] = __builtin_fmaf(dy, xh, dw[j][k]);
         db[j][k] += dy;
       }
+    }
     c1 = wave_sum(c1);
     c2 = wave_sum(c2);
     if constexpr (WAVES > 1) {
@@ -484,9 +483,12 @@ static void launch_rows(const NormParams& p, hipStream_t stream) {
 template <class DT, int OUT>
 static hipError_t norm_t(const NormParams& p, hipStream_t stream) {
   const int64_t Kp = OUT == NORM_Y ? p.K : (OUT == NORM_I8 ? (int64_t)p.i8.kq * 64 : (int64_t)p.mx.kq * 128);
-  // Two vectors a thread: 8192 x 8192 bf16 66 us (four of 256 threads 71, one of 1024 85), to codes 74 (four 73, one 102); 777 x 5003
-  // 11.0 (17.0, 13.4)
-  if (Kp <= 512)
+  // Two vectors a thread; four of 256 threads past 4096 columns where there are many rows, unless their codes wait for a second
+  // maximum. 8192 x 8192 bf16, four of 256, two of 512, one of 1024: 57, 64 and 78 us, to 8 bits 75, 74 and 105, to MXFP4 54, 61 and 83;
+  // 777 x 5003 14.0, 10.6 and 11.6
+  if (p.K < 8)
+    launch_rows<DT, 1024, 0, OUT>(p, stream);
+  else if (Kp <= 512)
     launch_rows<DT, 64, 1, OUT>(p, stream);
   else if (Kp <= 1024)
     launch_rows<DT, 64, 2, OUT>(p, stream);
@@ -494,6 +496,8 @@ static hipError_t norm_t(const NormParams& p, hipStream_t stream) {
     launch_rows<DT, 128, 2, OUT>(p, stream);
   else if (Kp <= 4096)
     launch_rows<DT, 256, 2, OUT>(p, stream);
+  else if (Kp <= 8192 && OUT != NORM_I8 && p.M > 2048)
+    launch_rows<DT, 256, 4, OUT>(p, stream);
   else if (Kp <= 8192)
     launch_rows<DT, 512, 2, OUT>(p, stream);
   else if (Kp <= 16384)
@@ -518,11 +522,12 @@ hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t stream) {
   }
 }
 
-constexpr int64_t kLongRow = 16384;
+// Rows whose columns a block's threads do not keep: longer than their registers, or shorter than a vector.
+static bool apart(int64_t K) { return K > 16384 || K < 8; }
 
 // Blocks (or strips of rows) that leave a part of dweight and dbias each.
 static int64_t grad_parts(int64_t M, int64_t K) {
-  if (K > kLongRow) {
+  if (apart(K)) {
     int64_t strips = (M + 15) / 16;
     if (strips > 64) strips = 64;
     const int64_t rows = (M + strips - 1) / strips;
@@ -546,7 +551,7 @@ template <class DT>
 static hipError_t grad_t(const NormGradParams& p, hipStream_t stream) {
   float* part = p.weight ? reinterpret_cast<float*>(p.workspace) : nullptr;
   const int64_t parts = grad_parts(p.M, p.K);
-  if (p.K > kLongRow) {
+  if (apart(p.K)) {
     k_norm_grad_long<DT><<<blocks_of(p.M), 1024, 0, stream>>>(p);
     if (part)
       k_norm_grad_cols<DT><<<dim3((unsigned)((p.K + 511) / 512), (unsigned)parts), 256, 0, stream>>>(p, part, (p.M + parts - 1) / parts);
