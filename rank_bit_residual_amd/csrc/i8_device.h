@@ -111,23 +111,25 @@ __device__ inline Scale8 scale8(u32 amax_bits) {
   return {s, 1.0f / s};
 }
 
-// The nearest integer to x / s, ties to even, in the low byte.
-// x r differs from x / s by less than 127 * 2^-24 + 2^-24 < 2^-16.9, so adding 1.5 * 2^23 to it (one rounding, to an integer)
-// gives that integer unless x r lies within 2^-16 of a border, and how far it lies from the integer says which. There the
-// remainder x - k s decides, which one fma gives exactly: it is at most s / 2 (1 + 2^-15) in size and a multiple of the
-// smaller unit of x and s.
-constexpr float kMagic8 = 12582912.f, kSure8 = 0.5f - 0x1p-16f;
-__device__ inline float code8_fast(float x, float r, float& far) {
-  const float u = __builtin_fmaf(x, r, kMagic8);
-  far = fmaxf(far, fabsf(__builtin_fmaf(x, r, kMagic8 - u)));
-  return u;
+// The nearest integer to x / s, ties to even, in the low byte of u.
+// x r differs from x / s by less than 2^-16.9, so adding 1.5 * 2^23 to it (one rounding, to an integer k) gives that integer or, next
+// to a border, its neighbour. The remainder x - k s, which one fma gives exactly, says which: k is right if it is smaller than s / 2 in
+// size, or equal and k even. (Exactly: the remainder is a multiple of the smaller unit of x and s, and at most s / 2 (1 + 2^-15).)
+// Borders are no rare case in 16-bit types, whose x 127 / max are often half a whole number but for the rounding of s: the
+// test of a vector costs one operation an element, mending it seven more.
+constexpr float kMagic8 = 12582912.f;
+struct Code8 {
+  float u, rem;
+};
+__device__ inline Code8 code8(float x, float s, float r, float& far) {
+  const float u = __builtin_fmaf(x, r, kMagic8), rem = __builtin_fmaf(kMagic8 - u, s, x);
+  far = fmaxf(far, fabsf(rem));
+  return {u, rem};
 }
-__device__ inline float code8_sure(float x, float s, float r) {
-  const float u = __builtin_fmaf(x, r, kMagic8);
-  const float k = u - kMagic8, rem = __builtin_fmaf(-k, s, x), half = 0.5f * s, size = fabsf(rem);
-  const bool odd = __float_as_uint(u) & 1u;
-  if (size > half || (size == half && odd)) return u + (rem > 0.f ? 1.f : -1.f);
-  return u;
+__device__ inline void mend8(Code8& c, float half) {
+  // |rem| > half, or equal where k is odd: by their bits
+  const bool off = (__float_as_uint(c.rem) & 0x7FFFFFFFu) + (__float_as_uint(c.u) & 1u) > __float_as_uint(half);
+  c.u += off ? copysignf(1.f, c.rem) : 0.f;
 }
 __device__ inline u32 bytes4(float a, float b, float c, float d) {
   const u32 lo = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x0C0C0400u);
@@ -137,16 +139,17 @@ __device__ inline u32 bytes4(float a, float b, float c, float d) {
 
 // Eight codes of v[0..7], in order.
 __device__ inline v2u codes8x8(const float (&v)[8], const Scale8& q) {
-  float u[8], far = 0.f;
+  const float half = 0.5f * q.s;
+  Code8 c[8];
+  float far = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; k++) u[k] = code8_fast(v[k], q.r, far);
-  if (far > kSure8) {
-    asm volatile("");  // rarely taken: keep it a branch
+  for (int k = 0; k < 8; k++) c[k] = code8(v[k], q.s, q.r, far);
+  if (__builtin_amdgcn_ballot_w64(far >= half)) {
 #pragma unroll
-    for (int k = 0; k < 8; k++) u[k] = code8_sure(v[k], q.s, q.r);
+    for (int k = 0; k < 8; k++) mend8(c[k], half);
   }
-  const v2u c = {bytes4(u[0], u[1], u[2], u[3]), bytes4(u[4], u[5], u[6], u[7])};
-  return q.r == 0.f ? v2u{0, 0} : c;
+  const v2u w = {bytes4(c[0].u, c[1].u, c[2].u, c[3].u), bytes4(c[4].u, c[5].u, c[6].u, c[7].u)};
+  return q.r == 0.f ? v2u{0, 0} : w;
 }
 
 // Where code k of row r lies.

@@ -3,7 +3,7 @@
 //   * k_i8_colmax, k_i8_colscale, k_i8_cols   the same of each column, as a tensor of the transpose;
 //   * k_i8_dequantize  the values of a tensor.
 //
-// s = float32(max|x| / 127), and a code is the nearest integer to x / s, ties to even, decided exactly (code8_sure).
+// s = float32(max|x| / 127), and a code is the nearest integer to x / s, ties to even, decided exactly (code8, mend8).
 //
 // A row is read once: it stays in the registers of the threads that share it while they agree on its maximum. A column's maximum
 // comes before its first code, so columns are read twice: partial maxima (and sums) of strips of rows, their join, then the codes,
@@ -239,19 +239,19 @@ __global__ __launch_bounds__(256) void k_i8_cols(I8QuantParams p, const float* r
     Vec8<DT> v[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) v[i] = r + i < p.R ? load8_step<DT>(x + i * p.sr, 0, p.C - c, p.sc) : zero8<DT>();
-    const Vec8<MxF32> rv = load8<MxF32>(recip, c, p.C);
+    const Vec8<MxF32> rv = load8<MxF32>(recip, c, p.C), sv = load8<MxF32>(p.cols.scales, c, p.C);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const float r = elem<MxF32>(rv, j);
-      float u[4], far = 0.f;
+      const float r = elem<MxF32>(rv, j), s = elem<MxF32>(sv, j), half = 0.5f * s;
+      Code8 q[4];
+      float far = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; i++) u[i] = code8_fast(elem<DT>(v[i], j), r, far);
-      if (far > kSure8) {  // rarely taken
-        const float s = p.cols.scales[c + j];
+      for (int i = 0; i < 4; i++) q[i] = code8(elem<DT>(v[i], j), s, r, far);
+      if (__builtin_amdgcn_ballot_w64(far >= half)) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) u[i] = code8_sure(elem<DT>(v[i], j), s, r);
+        for (int i = 0; i < 4; i++) mend8(q[i], half);
       }
-      words[lc * 132 + 16 * j + rg] = r == 0.f ? 0u : bytes4(u[0], u[1], u[2], u[3]);
+      words[lc * 132 + 16 * j + rg] = r == 0.f ? 0u : bytes4(q[0].u, q[1].u, q[2].u, q[3].u);
     }
     __syncthreads();
     // 16 columns x 64 codes are a kilobyte of the tensor: a lane stores 16 codes of one
