@@ -213,7 +213,7 @@ int svdq_i8_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_t sc, 
     I8GemmParams p = params_of(M, q, nullptr);
     p.x = x;
     p.ldx = sr;
-    return hip_status(launch_i8_decode(p, dtype, s), "8-bit product launch");
+    return hip_status(launch_i8_decode(p, i8_product_form(M, N, p.kq), dtype, s), "8-bit product launch");
   }
   uint8_t* ws = (uint8_t*)workspace;
   const size_t codes = (size_t)i8_code_bytes(M, K), scales = (size_t)i8_scale_bytes(M);

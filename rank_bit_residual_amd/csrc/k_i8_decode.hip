@@ -178,6 +178,7 @@ static hipError_t launch_rows(const I8GemmParams& p, hipStream_t stream) {
   const dim3 grid((unsigned)blocks, (unsigned)((p.M + 16 * MT - 1) / (16 * MT)));
   const unsigned lds = RAW ? (unsigned)(p.M * p.kq * 64) : 0;
   if (RAW) {
+    // static and dynamic LDS together may pass what a launch has without asking
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_i8_decode<DT, MT, NT, WAVES, RAW>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, kRawBytes);
     if (e != hipSuccess) return e;
@@ -186,40 +187,45 @@ static hipError_t launch_rows(const I8GemmParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-MxForm i8_decode_form(int64_t M, int64_t N, int kq) {
-  (void)kq;
-  const int bm = M <= 16 ? 16 : (M <= 32 ? 32 : 64);
-  return MxForm{bm, (N + 15) / 16 <= 512 && bm < 64 ? 16 : 32, 1, 8};
+// The block shape for M x N outputs with the least estimated time in us. A wave's chain is kq / 8 stages; measured (M x K x N): 16 x 4096 x 4096
+// with 16 x 16 5.2, 64 x 8192 x 1024 6.6, 128 x 8192 x 1024 with 16 x 32 8.4, 64 x
+// 4096 x 4096 with 32 x 32 7.0, 64 x 8192 x 4096 12.0, 256 x 1024 x 1024 3.7, 128 x 4096 x 4096 with 64 x 32 9.3. No less than b's bytes
+// from memory, slower with the rows that a block computes: 16 x 8192 x 8192 14.5, 32 x 8192 x 12288 25, 64 x 8192 x 8192 20.
+double i8_decode_cost(int64_t M, int64_t N, int kq, MxForm* form) {
+  const struct {
+    int bm, bn;
+    double alone, shared;  // us for a stage of the chain: of one block a unit, of several (each)
+  } cand[4] = {{16, 16, 0.29, 0.25}, {16, 32, 0.40, 0.33}, {32, 32, 0.60, 0.50}, {64, 32, 0.89, 1.0}};
+  double best = 1e30;
+  for (const auto& c : cand) {
+    if (c.bm > 16 && c.bm >= 2 * M) continue;
+    if ((M + c.bm - 1) / c.bm > 65535) continue;  // the grid's second dimension
+    const double b = (double)(((M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn) + 255) / 256), ch = (kq + 7) / 8;
+    const double t = 1.9 + 0.5 * b + ch * (c.shared * b > c.alone ? c.shared * b : c.alone);
+    const double rows = (double)(M < c.bm ? M : c.bm), bytes = 1.5 + (double)N * kq * 64e-6 / 5.8 * (1 + 0.01 * rows);
+    const double least = t > bytes ? t : bytes;
+    if (least < best) best = least, *form = MxForm{c.bm, c.bn, 1, 8};
+  }
+  return best;
 }
 
-bool i8_decode_fits(int64_t M, int64_t N, int kq) {
-  const MxForm f = i8_decode_form(M, N, kq);
-  return mx_fits_grid(decode_blocks(N, f.bn), 64 * f.waves);
-}
-
-template <class DT, int MT, bool RAW>
-static hipError_t launch_cols(const I8GemmParams& p, const MxForm& f, hipStream_t stream) {
-  if (f.bn == 32) return launch_rows<DT, MT, 2, 8, RAW>(p, stream);
-  if constexpr (MT <= 2) return launch_rows<DT, MT, 1, 8, RAW>(p, stream);
-  return hipErrorInvalidConfiguration;
+bool i8_decode_fits(int64_t M, int64_t N, const MxForm& f) {
+  return (M + f.bm - 1) / f.bm <= 65535 && mx_fits_grid(decode_blocks(N, f.bn), 64 * f.waves);
 }
 
 template <class DT>
-static hipError_t launch_decode_t(const I8GemmParams& p, hipStream_t stream) {
-  const MxForm f = i8_decode_form(p.M, p.N, p.kq);
-  if (p.x) return launch_cols<DT, 1, true>(p, f, stream);
-  switch (f.bm) {
-    case 16: return launch_cols<DT, 1, false>(p, f, stream);
-    case 32: return launch_cols<DT, 2, false>(p, f, stream);
-    default: return launch_cols<DT, 4, false>(p, f, stream);
-  }
+static hipError_t launch_decode_t(const I8GemmParams& p, const MxForm& f, hipStream_t stream) {
+  if (p.x) return f.bn == 32 ? launch_rows<DT, 1, 2, 8, true>(p, stream) : launch_rows<DT, 1, 1, 8, true>(p, stream);
+  if (f.bm == 64) return launch_rows<DT, 4, 2, 8, false>(p, stream);
+  if (f.bm == 32) return launch_rows<DT, 2, 2, 8, false>(p, stream);
+  return f.bn == 32 ? launch_rows<DT, 1, 2, 8, false>(p, stream) : launch_rows<DT, 1, 1, 8, false>(p, stream);
 }
 
-hipError_t launch_i8_decode(const I8GemmParams& p, int dtype, hipStream_t stream) {
+hipError_t launch_i8_decode(const I8GemmParams& p, const MxForm& f, int dtype, hipStream_t stream) {
   switch (dtype) {
-    case SVDQ_F32: return launch_decode_t<MxF32>(p, stream);
-    case SVDQ_BF16: return launch_decode_t<MxBF16>(p, stream);
-    default: return launch_decode_t<MxF16>(p, stream);
+    case SVDQ_F32: return launch_decode_t<MxF32>(p, f, stream);
+    case SVDQ_BF16: return launch_decode_t<MxBF16>(p, f, stream);
+    default: return launch_decode_t<MxF16>(p, f, stream);
   }
 }
 

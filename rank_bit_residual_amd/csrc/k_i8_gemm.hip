@@ -303,34 +303,62 @@ using namespace dev;
 constexpr int kCus = 256, kExactStages = 2048;
 
 typedef I8Cfg<64, 64, 2, 2, 4> Tile64;
+typedef I8Cfg<64, 128, 2, 2, 4> Tile64n;
 typedef I8Cfg<128, 128, 4, 2, 2> Tile128;
 typedef I8Cfg<256, 256, 4, 2, 2> Tile256;
 
-static MxForm plan_of(int64_t M, int64_t N, int kq) {
-  if (M <= 64 && kq <= kExactStages) return i8_decode_form(M, N, kq);
+// The form with the least estimated time in us, from the times measured on this chip (M x K x N, us; K = 4096 is 64 stages of 64):
+//   64 x 64    three blocks a compute unit (b: blocks for each): 2048 x 2048 x 512 (b 1) 8.7, 512 x 4096 x 4096 (2) 16.8, 4096^3 (16) 110,
+//              4096 x 512 x 4096 (16) 27
+//   64 x 128   two: 512 x 4096 x 4096 (1) 15.2, 1000 x 4096 x 4096 (2) 26, 4096^3 (8) 89, 4096 x 512 x 4096 (8) 25
+//   128 x 128  two: 1000 x 4096 x 4096 (1) 22.3, 2048 x 4096 x 4096 (2) 37, 4096^3 (4) 71, 4096 x 512 x 4096 (4) 26
+//   256 x 256  one: 1024 x 4096 x 4096 (64 blocks) 41, 1000 x 4096 x 11000 (172) 52, 4096^3 (256) 62, 4096 x 512 x 4096 (256) 19.6,
+//              8192^3 (1024) 431
+// Operands past the last-level cache cost the smaller tiles a quarter more, as they read them more often: 1024 x 65536 x 1024 in four
+// shares of 128 x 128 105, in 16 of 256 x 256 81. Shares of K add the joining launch and the parts' way through memory.
+// The kernel for few rows has its own estimate (i8_decode_cost).
+static MxForm choose(int64_t M, int64_t N, int kq) {
   MxForm best{0, 0, 1, 1};
   double best_t = 1e30;
-  const int cand[3][2] = {{64, 64}, {128, 128}, {256, 256}};
-  for (int c = 0; c < 3; c++) {
-    const int64_t tiles = ((M + cand[c][0] - 1) / cand[c][0]) * ((N + cand[c][1] - 1) / cand[c][1]);
+  if (kq <= kExactStages) best_t = i8_decode_cost(M, N, kq, &best);
+  struct Cost {
+    int bm, bn;
+    double first, alone, shared, out;  // us: a block's own, a stage of one block a unit, of several (each), a further block's epilogue
+  };
+  const Cost cand[4] = {{64, 64, 3.5, 0.15, 0.095, 0.65}, {64, 128, 4.0, 0.17, 0.149, 1.3}, {128, 128, 4.5, 0.265, 0.21, 4.6}, {256, 256, 0, 0, 0, 0}};
+  const double least = 3.5 + ((double)M + (double)N) * kq * 64e-6 / 5.0;  // the operands' bytes from memory
+  const double cold = ((double)M + (double)N) * kq * 64 > 64e6 ? 1.25 : 1.0;
+  for (const Cost& c : cand) {
+    const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
     for (int s = 1; s <= kq / 2; s *= 2) {
-      const bool exact = (kq / 2 + s - 1) / s * 2 <= kExactStages;
-      if (!exact) continue;
-      if (s > 1 && best.bm && (kq / 2 / s < 4 || tiles * s > 2 * kCus)) break;
-      const double rounds = (double)(tiles * s) / kCus, st = (double)kq / s;
-      const double whole = (double)((tiles * s) / kCus), rest = rounds - whole;
+      if ((kq / 2 + s - 1) / s * 2 > kExactStages) continue;
+      if (s > 1 && best_t < 1e30 && (kq / 2 / s < 4 || tiles * s > 2 * kCus)) break;
+      const double st = (double)kq / s;
       double t;
-      if (c == 0)
-        t = 3 + st * (rounds > 1.5 ? 0.1 * rounds : 0.155);
-      else if (c == 1)
-        t = 3.5 + st * (rounds > 1 ? 0.265 * rounds : 0.25);
-      else
-        t = whole * (6 + 0.82 * st) + (rest > 0 ? 6 + st * (0.6 + 0.2 * rest) : 0);
-      if (s > 1) t += 3.0 + (double)M * N * 4 * 2 * s / 4e6;
-      if (t < best_t) best = MxForm{cand[c][0], cand[c][1], s, 1}, best_t = t;
+      if (c.bm == 256) {
+        const double whole = (double)((tiles * s) / kCus), rest = (double)(tiles * s) / kCus - whole;
+        t = whole * (10.8 + 0.764 * st) + (rest > 0 ? 4 + 7 * rest + st * (0.52 + 0.22 * rest) : 0);
+      } else {
+        const double b = (double)((tiles * s + kCus - 1) / kCus);
+        const double rate = b <= 1 ? c.alone : (c.shared * b > c.alone + c.shared * 0.6 ? c.shared * b : c.alone + c.shared * 0.6);
+        t = c.first + st * rate * cold + (b > 1 ? c.out * (b - 1) : 0);
+      }
+      if (t < least) t = least;
+      if (M == 1) t += 2.0;  // the launch that quantises a row, which the other kernel does itself
+      if (s > 1) t += 3.0 + (double)M * N * 4 * 2 * s / 5.5e6;
+      if (t < best_t) best = MxForm{c.bm, c.bn, s, 1}, best_t = t;
     }
   }
   return best;
+}
+
+// (A call asks several times for the sizes that it was given.)
+static MxForm plan_of(int64_t M, int64_t N, int kq) {
+  static thread_local int64_t m = 0, n = 0;
+  static thread_local int k = 0;
+  static thread_local MxForm f;
+  if (m != M || n != N || k != kq) f = choose(M, N, kq), m = M, n = N, k = kq;
+  return f;
 }
 
 MxForm i8_product_form(int64_t M, int64_t N, int kq) { return plan_of(M, N, kq); }
@@ -347,7 +375,7 @@ static int64_t tile_blocks(int64_t M, int64_t N, const MxForm& f) {
 
 bool i8_product_fits(int64_t M, int64_t N, int kq) {
   const MxForm f = plan_of(M, N, kq);
-  return f.waves > 1 ? i8_decode_fits(M, N, kq) : mx_fits_grid(tile_blocks(M, N, f), 512);
+  return f.waves > 1 ? i8_decode_fits(M, N, f) : mx_fits_grid(tile_blocks(M, N, f), 512);
 }
 
 template <class DT, class C, bool SPLIT>
@@ -372,7 +400,8 @@ static hipError_t launch_tile(const I8GemmParams& p, const MxForm& f, hipStream_
 
 template <class DT, bool SPLIT>
 static hipError_t launch_form(const I8GemmParams& p, const MxForm& f, hipStream_t stream) {
-  if (f.bm == 64) return launch_tile<DT, Tile64, SPLIT>(p, f, stream);
+  if (f.bm == 64 && f.bn == 64) return launch_tile<DT, Tile64, SPLIT>(p, f, stream);
+  if (f.bm == 64) return launch_tile<DT, Tile64n, SPLIT>(p, f, stream);
   if (f.bm == 256) return launch_tile<DT, Tile256, SPLIT>(p, f, stream);
   return launch_tile<DT, Tile128, SPLIT>(p, f, stream);
 }
@@ -395,7 +424,7 @@ static hipError_t launch_product_t(const I8GemmParams& p0, const MxForm& f, hipS
 
 hipError_t launch_i8_product(const I8GemmParams& p, int dtype, hipStream_t stream) {
   const MxForm f = plan_of(p.M, p.N, p.kq);
-  if (f.waves > 1) return launch_i8_decode(p, dtype, stream);
+  if (f.waves > 1) return launch_i8_decode(p, f, dtype, stream);
   switch (dtype) {
     case SVDQ_F32: return launch_product_t<MxF32>(p, f, stream);
     case SVDQ_BF16: return launch_product_t<MxBF16>(p, f, stream);

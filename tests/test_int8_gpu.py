@@ -218,7 +218,8 @@ def _exact_sums(M, K, N, seed):
 
 
 FORMS = [(1000, 130, 1500), (65, 128, 64), (129, 4096, 100), (2048, 256, 2048), (4096, 128, 4096), (4096, 1024, 2100), (1024, 16384, 1024),
-         (300, 65536, 300), (3000, 640, 5000), (513, 8192, 700), (4000, 2048, 4090)]
+         (300, 65536, 300), (3000, 640, 5000), (513, 8192, 700), (4000, 2048, 4090), (100, 2368, 3500),
+         (128, 4465, 1205), (3, 12000, 5690), (355, 123, 3788), (600, 45000, 78), (1467, 3134, 583)]
 
 
 @pytest.mark.parametrize("M,K,N", FORMS)
@@ -233,10 +234,11 @@ def test_matmul_exact(M, K, N):
 
 
 def test_every_form_is_met():
-    tiles = {_form(M, N, K)[:2] for M, K, N in FORMS + SIZES}
-    assert {(64, 64), (128, 128), (256, 256)} <= tiles, tiles
-    assert {16, 32, 64} <= {f[0] for f in tiles}
-    assert any(_form(M, N, K)[2] > 1 for M, K, N in FORMS)
+    forms = {_form(M, N, K) for M, K, N in FORMS + SIZES}
+    want = {(16, 16), (16, 32), (32, 32), (64, 32), (64, 64), (64, 128), (128, 128), (256, 256)}
+    assert want == {f[:2] for f in forms}
+    for shared in (False, True):
+        assert {(64, 64), (64, 128), (128, 128)} <= {f[:2] for f in forms if (f[2] > 1) == shared}
 
 
 def test_sums_past_32_bits():
