@@ -202,7 +202,8 @@ double i8_decode_cost(int64_t M, int64_t N, int kq, MxForm* form) {
     if ((M + c.bm - 1) / c.bm > 65535) continue;  // the grid's second dimension
     const double b = (double)(((M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn) + 255) / 256), ch = (kq + 7) / 8;
     const double t = 1.9 + 0.5 * b + ch * (c.shared * b > c.alone ? c.shared * b : c.alone);
-    const double rows = (double)(M < c.bm ? M : c.bm), bytes = 1.5 + (double)N * kq * 64e-6 / 5.8 * (1 + 0.01 * rows);
+    const double rows = (double)(M < c.bm ? M : c.bm), again = (double)((M + c.bm - 1) / c.bm - 1);
+    const double bytes = 1.5 + (double)N * kq * 64e-6 / 5.8 * (1 + 0.01 * rows) * (1 + 0.3 * again);
     const double least = t > bytes ? t : bytes;
     if (least < best) best = least, *form = MxForm{c.bm, c.bn, 1, 8};
   }

@@ -325,7 +325,7 @@ static MxForm choose(int64_t M, int64_t N, int kq) {
     int bm, bn;
     double first, alone, shared, out;  // us: a block's own, a stage of one block a unit, of several (each), a further block's epilogue
   };
-  const Cost cand[4] = {{64, 64, 3.5, 0.15, 0.095, 0.65}, {64, 128, 4.0, 0.17, 0.149, 1.3}, {128, 128, 4.5, 0.265, 0.21, 4.6}, {256, 256, 0, 0, 0, 0}};
+  const Cost cand[4] = {{64, 64, 3.5, 0.15, 0.095, 0.65}, {64, 128, 4.0, 0.17, 0.16, 1.6}, {128, 128, 4.5, 0.265, 0.21, 3.0}, {256, 256, 0, 0, 0, 0}};
   const double least = 3.5 + ((double)M + (double)N) * kq * 64e-6 / 5.0;  // the operands' bytes from memory
   const double cold = ((double)M + (double)N) * kq * 64 > 64e6 ? 1.25 : 1.0;
   for (const Cost& c : cand) {
