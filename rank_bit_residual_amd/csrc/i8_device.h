@@ -97,6 +97,26 @@ __device__ inline void fit8(Vec8<DT>& v, int64_t c, int64_t K, u32 past = 0) {
   }
 }
 
+// Elements [c, c + 8) of a row of K.
+template <class DT>
+__device__ inline void store8(typename DT::T* row, int64_t c, int64_t K, const float (&v)[8]) {
+  if (c + 8 <= K) {
+    u32 o[DT::size * 2];
+#pragma unroll
+    for (int q = 0; q < DT::size * 2; q++) {
+      if constexpr (DT::size == 4)
+        o[q] = __float_as_uint(v[q]);
+      else
+        o[q] = DT::pack(v[2 * q], v[2 * q + 1]);
+    }
+    __builtin_memcpy(row + c, o, sizeof o);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      if (c + k < K) row[c + k] = DT::store(v[k]);
+  }
+}
+
 // ---- 8-bit codes --------------------------------------------------------------------------
 // A row's scale from the bits of its largest magnitude: float32(max / 127), 2^-126 at least (so that every step below is
 // exact), 0 for a row of zeros, NaN if the row holds an infinity or a NaN.

@@ -136,13 +136,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, COLS ? 4 : 1) void k_i8_rows(I8Q
   }
   if constexpr (COLS != ROWS_ALONE) {
 #pragma unroll
-    for (int j = 0; j < NV; j++)
+    for (int j = 0; j < NV; j++) {
+      if (at(j) >= p.C) continue;
+      float m[8];
 #pragma unroll
-      for (int k = 0; k < 8; k++) {
-        if (at(j) + k >= p.C) continue;
-        part[blockIdx.x * p.C + at(j) + k] = most_at<DT>(cmax[j], k);
-        if constexpr (COLS == ROWS_MAXIMA_AND_SUMS) sums[blockIdx.x * p.C + at(j) + k] = csum[j][k];
-      }
+      for (int k = 0; k < 8; k++) m[k] = __uint_as_float(most_at<DT>(cmax[j], k));
+      store8<MxF32>(reinterpret_cast<float*>(part) + blockIdx.x * p.C, at(j), p.C, m);
+      if constexpr (COLS == ROWS_MAXIMA_AND_SUMS) store8<MxF32>(sums + blockIdx.x * p.C, at(j), p.C, csum[j]);
+    }
   }
 }
 
@@ -346,12 +347,20 @@ static hipError_t rows_t(const I8QuantParams& p, hipStream_t stream) {
 // Rows whose codes and column maxima come from one reading: they fit a block's registers.
 constexpr int64_t kSharedRow = 16384;
 
-// Strips of rows that a column's maximum is taken over. Read with the rows (`shared`): the blocks that the chip holds, of four rows or
-// more once that many are there. Alone: enough blocks for the chip, of 16 rows or more.
+// Threads of a block of the kernel for both: a vector a thread, two past 8192 columns.
+static int shared_threads(int64_t C) {
+  const int64_t Kp = i8_kq(C) * 64;
+  return Kp <= 2048 ? 256 : (Kp <= 4096 ? 512 : 1024);
+}
+
+// Strips of rows that a column's maximum is taken over. Read with the rows (`shared`): as many as the chip holds at once, of four rows or
+// more once there are 256 (8192 x 12288 bf16 in 128, 256, 512 strips 140, 81 and 89 us; 777 x 5003 12.9, 10.5 and 12.6). Alone: enough
+// blocks for the chip, of 16 rows or more.
 static int64_t strips_of(int64_t R, int64_t C, bool shared) {
   int64_t strips;
   if (shared) {
-    strips = R / 4 < 512 ? R / 4 : 512;
+    const int64_t most = 256 * 1024 / shared_threads(C);
+    strips = R / 4 < most ? R / 4 : most;
     if (strips < 256) strips = R < 256 ? R : 256;
     return strips;
   }
@@ -401,17 +410,15 @@ static hipError_t cols_t(const I8QuantParams& p, hipStream_t stream) {
   u32* part = reinterpret_cast<u32*>((uint8_t*)p.workspace + round256(p.C * 4));
   float* sums = reinterpret_cast<float*>((uint8_t*)part + round256(strips * p.C * 4));
   if (shared) {
-    const int64_t Kp = (int64_t)p.rows.kq * 64;
-    if (Kp <= 2048)
-      launch_shared<DT, 256, 1>(p, strips, part, sums, stream);
-    else if (Kp <= 4096)
-      launch_shared<DT, 256, 2>(p, strips, part, sums, stream);
-    else if (Kp <= 8192)
-      launch_shared<DT, 512, 2>(p, strips, part, sums, stream);
-    else if (Kp <= 12288)
-      launch_shared<DT, 512, 3>(p, strips, part, sums, stream);
-    else
-      launch_shared<DT, 1024, 2>(p, strips, part, sums, stream);
+    switch (shared_threads(p.C)) {
+      case 256: launch_shared<DT, 256, 1>(p, strips, part, sums, stream); break;
+      case 512: launch_shared<DT, 512, 1>(p, strips, part, sums, stream); break;
+      default:
+        if (p.rows.kq <= 128)
+          launch_shared<DT, 1024, 1>(p, strips, part, sums, stream);
+        else
+          launch_shared<DT, 1024, 2>(p, strips, part, sums, stream);
+    }
   } else {
     const int64_t strip_rows = (p.R + strips - 1) / strips;
     const dim3 grid((unsigned)((p.C + 511) / 512), (unsigned)strips);

@@ -38,25 +38,6 @@ __device__ inline void param8(float (&w)[8], const void* src, bool f32, int64_t 
   }
 }
 
-template <class DT>
-__device__ inline void store8(typename DT::T* row, int64_t c, int64_t K, const float (&v)[8]) {
-  if (c + 8 <= K) {
-    u32 o[DT::size * 2];
-#pragma unroll
-    for (int q = 0; q < DT::size * 2; q++) {
-      if constexpr (DT::size == 4)
-        o[q] = __float_as_uint(v[q]);
-      else
-        o[q] = DT::pack(v[2 * q], v[2 * q + 1]);
-    }
-    __builtin_memcpy(row + c, o, sizeof o);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; k++)
-      if (c + k < K) row[c + k] = DT::store(v[k]);
-  }
-}
-
 // ------------------------------------------------------------------------------ forward
 struct RowStats {
   double mean, rstd;
