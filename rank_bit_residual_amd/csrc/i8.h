@@ -106,7 +106,7 @@ hipError_t launch_i8_product(const I8GemmParams& p, int dtype, hipStream_t strea
 // The kernel for few rows: its estimated time and block shape, whether its grid fits, and whether it quantises A itself.
 double i8_decode_cost(int64_t M, int64_t N, int kq, MxForm* form);
 bool i8_decode_fits(int64_t M, int64_t N, const MxForm& f);
-bool i8_raw_rows(int64_t M, int64_t N, int64_t K, int64_t sc, int dtype_bytes);
+bool i8_raw_rows(int64_t M, int64_t N, int64_t K, int64_t sc);
 hipError_t launch_i8_decode(const I8GemmParams& p, const MxForm& f, int dtype, hipStream_t stream);
 
 hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t stream);

@@ -54,14 +54,14 @@ I8GemmParams params_of(int64_t M, const Product& q, void* part) {
 size_t round_ws(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 // Whether the product quantises its rows itself.
-bool raw_rows(int64_t M, int64_t N, int64_t K, int64_t sc, int dtype) {
-  return i8_raw_rows(M, N, K, sc, (int)size_of(dtype)) && i8_product_form(M, N, (int)i8_kq(K)).waves > 1;
+bool raw_rows(int64_t M, int64_t N, int64_t K, int64_t sc) {
+  return i8_raw_rows(M, N, K, sc) && i8_product_form(M, N, (int)i8_kq(K)).waves > 1;
 }
 
 // Workspace of an unquantised A: its codes and scales, then the scratch of quantising it and the product's parts, which take
 // turns.
-size_t linear_bytes(int64_t M, int64_t N, int64_t K, int64_t sr, int64_t sc, int dtype) {
-  if (raw_rows(M, N, K, sc, dtype)) return 0;
+size_t linear_bytes(int64_t M, int64_t N, int64_t K, int64_t sr, int64_t sc) {
+  if (raw_rows(M, N, K, sc)) return 0;
   const size_t part = round_ws(i8_product_part_bytes(M, N, (int)i8_kq(K))), quant = i8_quantize_bytes(M, K, sr, sc, true, false);
   return (size_t)(i8_code_bytes(M, K) + i8_scale_bytes(M)) + (part > quant ? part : quant);
 }
@@ -196,7 +196,7 @@ int svdq_i8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t sr, 
   int st = svdq_i8_workspace_bytes(M, N, K, bytes_out);
   if (st || (st = check_mx_dtype(dtype))) return st;
   if (sr < 0 || sc < 0) return set_error(SVDQ_EINVAL, "strides must not be negative");
-  *bytes_out = linear_bytes(M, N, K, sr, sc, dtype);
+  *bytes_out = linear_bytes(M, N, K, sr, sc);
   return SVDQ_OK;
 }
 
@@ -205,11 +205,11 @@ int svdq_i8_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_t sc, 
   const Product q{b_codes, b_scales, N, K, dtype, bias, y, ldy};
   int st = begin(dtype);
   if (st || (st = check_product(M, q)) || (st = check_strided(x, sr, sc, dtype, "x")) ||
-      (st = check_workspace(workspace, workspace_bytes, linear_bytes(M, N, K, sr, sc, dtype))))
+      (st = check_workspace(workspace, workspace_bytes, linear_bytes(M, N, K, sr, sc))))
     return st;
   hipStream_t s = (hipStream_t)stream;
   if ((st = check_grid(i8_product_fits(M, N, (int)i8_kq(K)), "8-bit product launch"))) return st;
-  if (raw_rows(M, N, K, sc, dtype)) {
+  if (raw_rows(M, N, K, sc)) {
     I8GemmParams p = params_of(M, q, nullptr);
     p.x = x;
     p.ldx = sr;

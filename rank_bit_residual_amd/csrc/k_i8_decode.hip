@@ -16,7 +16,7 @@ namespace dev {
 template <class DT, int MT, int NT, int WAVES, bool RAW>
 __global__ __launch_bounds__(64 * WAVES) void k_i8_decode(I8GemmParams p) {
   typedef typename DT::T T;
-  constexpr int BATCH = MT * NT >= 4 ? 4 : 8;
+  constexpr int BATCH = MT * NT >= 4 ? 4 : 8, SLOTS = 4;
   __shared__ int red[WAVES][MT][NT][4][64];
   __shared__ float row_scale[16];
   __shared__ u32 row_max[WAVES][16];
@@ -84,29 +84,60 @@ __global__ __launch_bounds__(64 * WAVES) void k_i8_decode(I8GemmParams p) {
 #pragma unroll
     for (int u = 0; u < BATCH; u++) load(ahead[u], s0 + u < p.kq ? s0 + u : p.kq - 1);
     __builtin_amdgcn_sched_barrier(0);
-    // a wave takes the stages of its share of every row
+    // a wave takes its share of K of every row: in SLOTS vectors a lane, requested together and kept, where they suffice, else row by
+    // row and read again
     const T* x = reinterpret_cast<const T*>(p.x);
-    for (int m = 0; m < p.M; m++) {
-      u32 most = 0;
-      for (int64_t c = (int64_t)s0 * 64 + 8 * lane; c < (int64_t)s1 * 64; c += 512)
-        most = max(most, amax_bits<DT>(load8<DT>(x + m * p.ldx, c, p.K).w));
-      most = wave_umax(most);
-      if (lane == 0) row_max[wave][m] = most;
+    const int64_t c0 = (int64_t)s0 * 64 + 8 * lane, c1 = (int64_t)s1 * 64;
+    const int per_row = (s1 - s0 + 7) / 8;  // vectors of 512 elements of a row's share
+    const bool kept = p.M * per_row <= SLOTS;
+    Vec8<DT> v[SLOTS];
+    int slot_row[SLOTS];
+    int64_t slot_c[SLOTS];
+    if (lane < 16) row_max[wave][lane] = 0;
+    if (kept) {
+#pragma unroll
+      for (int u = 0; u < SLOTS; u++) {
+        slot_row[u] = per_row ? u / per_row : p.M;
+        slot_c[u] = c0 + 512 * (per_row ? u % per_row : 0);
+        v[u] = zero8<DT>();
+        if (slot_row[u] < p.M && slot_c[u] < c1) v[u] = load8<DT>(x + slot_row[u] * p.ldx, slot_c[u], p.K);
+      }
+#pragma unroll
+      for (int u = 0; u < SLOTS; u++) {
+        if (slot_row[u] >= p.M) continue;
+        const u32 most = wave_umax(amax_bits<DT>(v[u].w));
+        if (lane == 0) row_max[wave][slot_row[u]] = max(row_max[wave][slot_row[u]], most);
+      }
+    } else {
+      for (int m = 0; m < p.M; m++) {
+        u32 most = 0;
+        for (int64_t c = c0; c < c1; c += 512) most = max(most, amax_bits<DT>(load8<DT>(x + m * p.ldx, c, p.K).w));
+        most = wave_umax(most);
+        if (lane == 0) row_max[wave][m] = most;
+      }
     }
     lds_barrier();
-    for (int m = 0; m < p.M; m++) {
-      u32 most = 0;
+    // lane m has row m's scale
+    u32 most = 0;
 #pragma unroll
-      for (int w = 0; w < WAVES; w++) most = max(most, row_max[w][m]);
-      const Scale8 q = scale8(most);
-      if (t == 0) row_scale[m] = q.s;
-      for (int64_t c = (int64_t)s0 * 64 + 8 * lane; c < (int64_t)s1 * 64; c += 512) {
-        const Vec8<DT> v = load8<DT>(x + m * p.ldx, c, p.K);
-        float e[8];
+    for (int w = 0; w < WAVES; w++) most = max(most, row_max[w][lane & 15]);
+    const Scale8 own = scale8(most);
+    if (t < 16) row_scale[t] = own.s;
+    auto put = [&](int m, int64_t c, const Vec8<DT>& w) {
+      const Scale8 q{lane_of(own.s, m), lane_of(own.r, m)};
+      float e[8];
 #pragma unroll
-        for (int k = 0; k < 8; k++) e[k] = elem<DT>(v, k);
-        *reinterpret_cast<v2u*>(xcodes + (int64_t)m * p.kq * 64 + c) = codes8x8(e, q);
-      }
+      for (int k = 0; k < 8; k++) e[k] = elem<DT>(w, k);
+      const v2u codes = codes8x8(e, q);
+      if (c < c1) *reinterpret_cast<v2u*>(xcodes + (int64_t)m * p.kq * 64 + c) = codes;
+    };
+    if (kept) {
+#pragma unroll
+      for (int u = 0; u < SLOTS; u++)
+        if (slot_row[u] < p.M) put(slot_row[u], slot_c[u], v[u]);
+    } else {
+      for (int m = 0; m < p.M; m++)
+        for (int64_t c = c0; c - 8 * lane < c1; c += 512) put(m, c, load8<DT>(x + m * p.ldx, c, p.K));
     }
     // a wave reads the codes that it wrote itself
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -166,9 +197,14 @@ static int64_t decode_blocks(int64_t N, int64_t cols) { return ((N + cols - 1) /
 
 constexpr int kRawBytes = 64 * 1024;  // of LDS for the codes of unquantised rows
 
-bool i8_raw_rows(int64_t M, int64_t N, int64_t K, int64_t sc, int dtype_bytes) {
-  (void)N;
-  return sc == 1 && M <= 4 && M * i8_kq(K) * 64 <= kRawBytes && M * K * dtype_bytes <= 65536;
+// One row always; two to four while their shares fit a wave's registers and the columns do not repeat the work too often. As one launch
+// against two, us on the GPU's clock (a launch costs 2.7 us of the host's besides): one row x 8192 x 8192 15.7 and 17.4, x 4096 x 4096 6.3 and 7.9,
+// x 1024 x 1024 4.2 and 5.1; two rows x 8192 x 4096 11.0 and 11.5; four x 4096 x 4096 7.6 and 8.0, x 1024 x 1024 5.6 and 5.3, x 8192 x 1024 9.5
+// and 8.6.
+bool i8_raw_rows(int64_t M, int64_t N, int64_t K, int64_t sc) {
+  const int64_t kq = i8_kq(K);
+  if (sc != 1 || M * kq * 64 > kRawBytes) return false;
+  return M == 1 || (M <= 4 && N <= 8192 && M * ((kq + 63) / 64) <= 4);
 }
 
 template <class DT, int MT, int NT, int WAVES, bool RAW>
@@ -177,7 +213,7 @@ static hipError_t launch_rows(const I8GemmParams& p, hipStream_t stream) {
   if (!mx_fits_grid(blocks, 64 * WAVES)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks, (unsigned)((p.M + 16 * MT - 1) / (16 * MT)));
   const unsigned lds = RAW ? (unsigned)(p.M * p.kq * 64) : 0;
-  if (RAW) {
+  if (RAW && lds > 32 * 1024) {
     // static and dynamic LDS together may pass what a launch has without asking
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_i8_decode<DT, MT, NT, WAVES, RAW>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, kRawBytes);

@@ -157,11 +157,32 @@ __global__ __launch_bounds__(64 * C::NWV) void k_i8_tile(I8GemmParams p) {
   // wave's reads of stage s - 1 were consumed before it.
   constexpr int NR = C::MT + C::NT, NM = C::MT * C::NT;
   constexpr int P1 = NM - 1 < NR ? NM - 1 : NR;
+  float sb[C::NT], bz[C::NT];  // the lane's columns: scales and bias, on hand before the loop
+  if constexpr (!SPLIT) {
+#pragma unroll
+    for (int j = 0; j < C::NT; j++)
+      bz[j] = p.bias ? DT::load(reinterpret_cast<const T*>(p.bias)[b_row(wn * C::TN + 32 * j + l32)]) : 0.f;
+  }
   const int first = nst < C::DIST ? nst : C::DIST;
   for (int s = 0; s < first; s++) issue(s);
   wait_stage_upto<C::LPS, C::DIST - 1>(first - 1);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  const float* scales = reinterpret_cast<const float*>(smem + C::SMEM);
+  bool far = false;
+  if constexpr (!SPLIT) {
+#pragma unroll
+    for (int j = 0; j < C::NT; j++) {
+      sb[j] = scales[C::BM + wn * C::TN + 32 * j + l32];
+      asm volatile("" : "+v"(sb[j]), "+v"(bz[j]));
+    }
+    // one scale a lane: whether any of the wave's rows and columns is far
+    far = !tame(scales[wm * C::TM + lane % C::TM]);
+#pragma unroll
+    for (int j = 0; j < C::NT; j++) far |= !tame(sb[j]);
+    static_assert(C::TM <= 64, "a wave's rows fit its lanes");
+    far = __builtin_amdgcn_ballot_w64(far) != 0;
+  }
   Frag fa, fb, f1;
   read_frag(smem, 0, fa);
 
@@ -217,16 +238,6 @@ __global__ __launch_bounds__(64 * C::NWV) void k_i8_tile(I8GemmParams p) {
     store_tile<MxF32, C, C::BM, C::NT>(smem, reinterpret_cast<float*>(p.part) + (int64_t)split * p.M * p.N, p.N, p.M, p.N, m0, n0,
                                        wm, wn, lane, [&](int i, int j, int v) { return __int_as_float(acc[i][j][v]); });
   } else {
-    const float* scales = reinterpret_cast<const float*>(smem + C::SMEM);
-    float sb[C::NT], bz[C::NT];
-    bool far = false;
-#pragma unroll
-    for (int j = 0; j < C::NT; j++) {
-      const int cc = wn * C::TN + 32 * j + l32;
-      sb[j] = scales[C::BM + cc];
-      bz[j] = p.bias ? DT::load(reinterpret_cast<const T*>(p.bias)[b_row(cc)]) : 0.f;
-      far |= !tame(sb[j]);
-    }
 #pragma unroll
     for (int i = 0; i < C::MT; i++) {
       // entry v of the lane lies in row 8 (v / 4) + 4 g + v % 4

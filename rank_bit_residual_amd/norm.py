@@ -22,15 +22,16 @@ from .int8 import Int8Tensor, _scratch
 from .mx import _DT, MxTensor, _call, _matrix, _no_graph, _output, _parts, _rows, _same_device, _workspace_bytes
 
 
-def _param(t, name: str, x: torch.Tensor):
+def _param(t, name: str, K: int, dtype, device) -> torch.Tensor:
     """A [K] vector of x's dtype or float32, with unit stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dim() != 1 or t.shape[0] != x.shape[1] or t.dtype not in (x.dtype, torch.float32):
-        raise ValueError(f"{name} must be a [{x.shape[1]}] tensor of x's dtype or float32")
+    if t.dim() != 1 or t.shape[0] != K or (t.dtype != dtype and t.dtype != torch.float32):
+        raise ValueError(f"{name} must be a [{K}] tensor of x's dtype or float32")
+    if t.device != device:
+        raise ValueError("all tensors of a call must be on one device")
     _no_graph(t, name)
-    _same_device(x.device, t)
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, eps: float = 1e-5,
@@ -51,10 +52,10 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     (M, K), device = x.shape, x.device
     pt = dt
     if weight is not None:
-        weight = _param(weight, "weight", x)
+        weight = _param(weight, "weight", K, x.dtype, device)
         pt = _DT[weight.dtype]
         if bias is not None:
-            bias = _param(bias, "bias", x)
+            bias = _param(bias, "bias", K, x.dtype, device)
             if bias.dtype != weight.dtype:
                 raise ValueError("weight and bias must share one dtype")
     x, ldx = _rows(x)
@@ -69,7 +70,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
         fn, tail = L.load().svdq_layer_norm_mx, _parts(result)
     mean = rstd = None
     if save:
-        mean, rstd = torch.empty(M, dtype=torch.float32, device=device), torch.empty(M, dtype=torch.float32, device=device)
+        mean = torch.empty(M, dtype=torch.float32, device=device)
+        rstd = torch.empty(M, dtype=torch.float32, device=device)
     _call(fn, device.index, x.data_ptr(), ldx, M, K, weight.data_ptr() if weight is not None else None,
           bias.data_ptr() if bias is not None else None, pt, float(eps), dt, *tail, mean.data_ptr() if save else None,
           rstd.data_ptr() if save else None)
@@ -92,10 +94,11 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
             raise ValueError(f"{name} must be a [{M}] float32 tensor")
         _no_graph(t, name)
     _same_device(device, dy, mean, rstd)
-    mean, rstd = mean.contiguous(), rstd.contiguous()
+    mean = mean if mean.is_contiguous() else mean.contiguous()
+    rstd = rstd if rstd.is_contiguous() else rstd.contiguous()
     pt, dweight, dbias = dt, None, None
     if weight is not None:
-        weight = _param(weight, "weight", x)
+        weight = _param(weight, "weight", K, x.dtype, device)
         pt = _DT[weight.dtype]
         dweight, dbias = torch.empty_like(weight), torch.empty_like(weight)
     dy, lddy = _rows(dy)
