@@ -79,6 +79,19 @@ def test_quantize(dtype, rows, cols):
         _check_tensor(t, w)
 
 
+@pytest.mark.parametrize("rows,cols,dtype", [(9001, 64, "bf16"), (9001, 300, "f16"), (4500, 1000, "f32"), (4999, 1500, "bf16"), (2100, 4000, "f16"),
+                                             (1100, 5003, "f32"), (1100, 8195, "bf16"), (1030, 12300, "bf16"), (600, 16500, "f16"),
+                                             (9, 5, "f32"), (700, 7, "bf16"), (5, 8, "f16"), (2000, 9, "bf16")])
+def test_quantize_many_rows(rows, cols, dtype):
+    """More rows than the blocks of a launch, so that each takes several, and a last one that is not full."""
+    x = _gpu(_wide(np.random.default_rng(rows + cols), rows, cols), dtype)
+    want = _np(x)
+    _check_tensor(R.int8_quantize(x), want)
+    r, c = R.int8_quantize(x, axis=None)
+    _check_tensor(r, want)
+    _check_tensor(c, want.T)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_quantize_strides(dtype):
     rng = np.random.default_rng(5)
@@ -379,6 +392,36 @@ def test_training_step_and_serving_together_on_a_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
         assert all(torch.equal(a, b) for a, b in zip(step(), want))
+
+
+def test_two_streams_and_two_graphs_at_once():
+    """Calls that overlap in time share nothing: two streams without a wait between them, then two graphs replayed in turn."""
+    steps = [_calls(), _calls()]
+    want = [s() for s in steps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(steps[k]())
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for out in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[k]))
+    graphs, outs = [], []
+    for k in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(steps[k]())
+        graphs.append(g)
+    for _ in range(3):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                graphs[k].replay()
+        torch.cuda.synchronize()
+        for k in (0, 1):
+            assert all(torch.equal(a, b) for a, b in zip(outs[k], want[k]))
 
 
 def test_calls_refuse_what_they_cannot_record():

@@ -90,6 +90,28 @@ def test_quantised_norm_is_the_quantised_float32_norm(M, K, dtype):
     assert not past.any() and (np.abs(codes).max(1) == 127).sum() == (np.abs(_np(y)).max(1) > 0).sum()
 
 
+@pytest.mark.parametrize("M,K,dtype", [(5001, 300, "bf16"), (4999, 1000, "f16"), (2501, 1500, "f32"), (1100, 4000, "bf16"), (2100, 5003, "f32"),
+                                       (2100, 8190, "bf16"), (600, 8000, "f16"), (300, 16384, "bf16"), (300, 16390, "f32"), (1100, 5, "bf16"),
+                                       (2000, 8, "f32"), (40, 7, "f16")])
+def test_many_rows(M, K, dtype):
+    """More rows than the blocks of a launch, so that each takes several, and a last one that is not full; forward, quantised and backward."""
+    rng = np.random.default_rng(M + K)
+    x, w, b = _inputs(rng, M, K, dtype, "f32")
+    nx, nw, nb = _np(x), _np(w), _np(b)
+    ref, mean, rstd = X.layer_norm(nx, nw, nb)
+    y, mu, rs = R.layer_norm(x, w, b, save=True)
+    assert (np.abs(_np(y) - ref) <= _forward_bound(nx, nw, nb, ref, dtype)).all()
+    assert (np.abs(_np(rs) - rstd) <= (2.0**-24 + 2.0**-30) * rstd).all()
+    full = R.layer_norm(x.float(), w, b)
+    for how, make, back in (("int8", R.int8_quantize, R.int8_dequantize), ("mx", R.mx_quantize, R.mx_dequantize)):
+        assert torch.equal(back(R.layer_norm(x, w, b, quantize=how), torch.float32), back(make(full), torch.float32))
+    dy = _gpu(rng.standard_normal((M, K)), dtype)
+    got = R.layer_norm_backward(dy, x, mu, rs, w)
+    refs = X.layer_norm_grad(_np(dy), nx, _np(mu), _np(rs), nw)
+    for g, r, bound in zip(got, refs, _grad_bounds(_np(dy), nx, _np(mu), _np(rs), nw, refs, dtype, "f32")):
+        assert (np.abs(_np(g) - r) <= bound).all()
+
+
 def test_far_means_and_outliers():
     """Means 10^4 standard deviations off, a first element that is the row's outlier, constant rows, and the ends of the range."""
     rng = np.random.default_rng(2)
