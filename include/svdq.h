@@ -535,7 +535,7 @@ int svdq_i8_backward(const void* dy, int64_t lddy, int64_t M, int64_t N, int dty
  * dtype), with mean = sum x / K and var = sum (x - mean)^2 / K. All of it is computed in binary64 and rounded to float32 once;
  * svdq_layer_norm rounds on to dtype (y, row stride ldy >= K), _i8 and _mx write the 8-bit or MXFP4 tensor of the float32
  * values (the arrays of svdq_i8_layout or svdq_mx_layout for M x K), ready for a product. weight, bias: [K] of param_dtype,
- * dtype or SVDQ_F32; both NULL, or bias alone. eps: finite, >= 0. mean, rstd: float32 [M] receiving mean and 1 / sqrt(var + eps), or
+ * dtype or SVDQ_F32; NULL both, or the bias alone. eps: finite, >= 0. mean, rstd: float32 [M] receiving mean and 1 / sqrt(var + eps), or
  * both NULL. A row with an infinity or a NaN is NaN throughout. Errors: EINVAL, EDTYPE, EHIP.
  * ------------------------------------------------------------------------------------ */
 int svdq_layer_norm(const void* x, int64_t ldx, int64_t M, int64_t K, const void* weight, const void* bias, int param_dtype,

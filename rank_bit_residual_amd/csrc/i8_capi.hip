@@ -269,7 +269,7 @@ int svdq_i8_backward(const void* dy, int64_t lddy, int64_t M, int64_t N, int dty
   if ((st = check_workspace(workspace, workspace_bytes, backward_bytes(M, N, K, at)))) return st;
   uint8_t* ws = (uint8_t*)workspace;
   hipStream_t s = (hipStream_t)stream;
-  // rows that do not overlap: a matrix of one column is read as rows, so that the sums are those of its columns
+  // a column step of 1 whatever lddy: read as given, never as its transpose, so that the sums are those of dy's columns
   const I8QuantParams p{dy, M, N, lddy, 1, out_of(ws + at[0], ws + at[1], N), out_of(ws + at[2], ws + at[3], M), db, out_dtype, ws + at[4]};
   if ((st = check_grid(i8_quantize_fits(M, N, lddy, 1, true, true), "i8_quantize launch")) ||
       (st = check_grid(i8_product_fits(M, K, (int)i8_kq(N)), "launch of the product for dx")) ||

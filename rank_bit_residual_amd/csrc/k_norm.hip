@@ -245,8 +245,10 @@ struct GradRow {
   Vec8<DT> dy, x;
 };
 
-// T threads share a row of eight elements or more, NV times eight columns each, the same ones in every row that the block takes.
-template <class DT, int T, int NV>
+// T threads share a row of eight elements or more, NV times eight columns each, the same ones in every row that the block takes. AHEAD: the
+// next row is requested before this one is worked on; with four vectors a thread it has no room (4096 x 16384 bf16 97 us without, 108
+// with, float32 179 and 243; two vectors of 1024 threads, which have half the registers, 130 and 286).
+template <class DT, int T, int NV, bool AHEAD>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradParams p, float* part) {
   typedef typename DT::T E;
   constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64;
@@ -274,9 +276,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradParams 
   load(cur, row, mean, rstd);
   int flip = 0;
   for (; row < p.M; row += step, flip ^= 1) {
-    GradRow<DT> next[NV];
+    GradRow<DT> next[AHEAD ? NV : 1];
     float mu = 0.f, rs = 0.f;
-    load(next, row + step, mu, rs);
+    if constexpr (AHEAD) load(next, row + step, mu, rs);
     float c1 = 0.f, c2 = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
@@ -313,9 +315,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradParams 
         o[k] = rstd * (g - c1 - xh * c2);
       }
       if (c < p.K) store8<DT>(dx, c, p.K, o);
-      cur[j] = next[j];
+      if constexpr (AHEAD) cur[j] = next[j];
     }
-    mean = mu, rstd = rs;
+    if constexpr (AHEAD)
+      mean = mu, rstd = rs;
+    else
+      load(cur, row + step, mean, rstd);
   }
   if (!part) return;
   float* out = part + (int64_t)blockIdx.x * 2 * p.K;
@@ -466,7 +471,7 @@ static hipError_t norm_t(const NormParams& p, hipStream_t stream) {
   const int64_t Kp = OUT == NORM_Y ? p.K : (OUT == NORM_I8 ? (int64_t)p.i8.kq * 64 : (int64_t)p.mx.kq * 128);
   // Two vectors a thread; four of 256 threads past 4096 columns where there are many rows, unless their codes wait for a second
   // maximum. 8192 x 8192 bf16, four of 256, two of 512, one of 1024: 57, 64 and 78 us, to 8 bits 75, 74 and 105, to MXFP4 54, 61 and 83;
-  // 777 x 5003 14.0, 10.6 and 11.6
+  // 777 x 5003 14.0, 10.6 and 11.6. Three of 512 past 8192 columns: 8192 x 12288 bf16 88 us, two of 1024 104, to 8 bits 116 and 135
   if (p.K < 8)
     launch_rows<DT, 1024, 0, OUT>(p, stream);
   else if (Kp <= 512)
@@ -481,6 +486,8 @@ static hipError_t norm_t(const NormParams& p, hipStream_t stream) {
     launch_rows<DT, 256, 4, OUT>(p, stream);
   else if (Kp <= 8192)
     launch_rows<DT, 512, 2, OUT>(p, stream);
+  else if (Kp <= 12288)
+    launch_rows<DT, 512, 3, OUT>(p, stream);
   else if (Kp <= 16384)
     launch_rows<DT, 1024, 2, OUT>(p, stream);
   else
@@ -526,9 +533,9 @@ size_t norm_grad_bytes(int64_t M, int64_t K, bool params) { return params ? (siz
 
 bool norm_grad_fits(int64_t K) { return mx_fits_grid((K + 63) / 64, 1024); }
 
-template <class DT, int T, int NV>
+template <class DT, int T, int NV, bool AHEAD = true>
 static void launch_grad(const NormGradParams& p, float* part, hipStream_t stream) {
-  k_norm_grad<DT, T, NV><<<(unsigned)grad_parts(p.M, p.K), T < 256 ? 256 : T, 0, stream>>>(p, part);
+  k_norm_grad<DT, T, NV, AHEAD><<<(unsigned)grad_parts(p.M, p.K), T < 256 ? 256 : T, 0, stream>>>(p, part);
 }
 
 template <class DT>
@@ -547,8 +554,10 @@ static hipError_t grad_t(const NormGradParams& p, hipStream_t stream) {
     launch_grad<DT, 512, 1>(p, part, stream);
   } else if (p.K <= 8192) {
     launch_grad<DT, 512, 2>(p, part, stream);
+  } else if (p.K <= 12288) {
+    launch_grad<DT, 512, 3>(p, part, stream);
   } else {
-    launch_grad<DT, 1024, 2>(p, part, stream);
+    launch_grad<DT, 512, 4, false>(p, part, stream);
   }
   if (part) {
     const unsigned blocks = (unsigned)((p.K + 63) / 64);

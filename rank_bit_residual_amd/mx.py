@@ -113,7 +113,7 @@ def _no_graph(t: torch.Tensor, name: str) -> None:
     """Refuses an input whose gradient would be lost in silence."""
     if t.requires_grad and torch.is_grad_enabled():
         raise RuntimeError(f"{name} requires grad, and this call records no graph: detach it, or call under torch.no_grad() or in a "
-                           "torch.autograd.Function (mx_gated_backward is the backward pass of mx_gated)")
+                           "torch.autograd.Function, whose backward calls mx_gated_backward, int8_backward or layer_norm_backward")
 
 
 def _mx(t, name: str) -> None:

@@ -91,7 +91,7 @@ def test_quantised_norm_is_the_quantised_float32_norm(M, K, dtype):
 
 
 @pytest.mark.parametrize("M,K,dtype", [(5001, 300, "bf16"), (4999, 1000, "f16"), (2501, 1500, "f32"), (1100, 4000, "bf16"), (2100, 5003, "f32"),
-                                       (2100, 8190, "bf16"), (600, 8000, "f16"), (300, 16384, "bf16"), (300, 16390, "f32"), (1100, 5, "bf16"),
+                                       (2100, 8190, "bf16"), (600, 8000, "f16"), (600, 9001, "bf16"), (700, 12288, "f32"), (300, 16384, "bf16"), (300, 16390, "f32"), (1100, 5, "bf16"),
                                        (2000, 8, "f32"), (40, 7, "f16")])
 def test_many_rows(M, K, dtype):
     """More rows than the blocks of a launch, so that each takes several, and a last one that is not full; forward, quantised and backward."""
@@ -195,7 +195,7 @@ def _grad_bounds(dy, x, mean, rstd, w, refs, dtype, ptype):
 
 @pytest.mark.parametrize("params", ["same", "f32"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("M,K", SIZES + [(600, 100), (70, 600), (2100, 65), (130, 3000), (1500, 513), (40, 12000), (70, 17000)])
+@pytest.mark.parametrize("M,K", SIZES + [(600, 100), (70, 600), (2100, 65), (130, 3000), (1500, 513), (40, 12000), (300, 9001), (300, 13001), (70, 17000)])
 def test_layer_norm_backward(M, K, dtype, params):
     rng = np.random.default_rng(M * 3 + K)
     x, w, _ = _inputs(rng, M, K, dtype, params)
