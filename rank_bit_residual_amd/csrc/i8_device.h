@@ -29,43 +29,53 @@ __device__ inline double lane_of(double v, int lane) {
   return __builtin_bit_cast(double, (u64)lane_of((u32)u, lane) | ((u64)lane_of((u32)(u >> 32), lane) << 32));
 }
 
-// Over all 64 lanes of a wave (all of them active), the same value in every lane.
+// Two sums that travel together.
+struct __align__(16) Sums2 {
+  double a, b;
+};
+template <int CTRL>
+__device__ inline Sums2 dpp(const Sums2& v) {
+  return {dpp<CTRL>(v.a), dpp<CTRL>(v.b)};
+}
+__device__ inline Sums2 lane_of(const Sums2& v, int lane) { return {lane_of(v.a, lane), lane_of(v.b, lane)}; }
+__device__ inline Sums2 add2(const Sums2& u, const Sums2& v) { return {u.a + v.a, u.b + v.b}; }
+__device__ inline u32 umax2(u32 a, u32 b) { return max(a, b); }
+
+// Over the 16 lanes of a row (all lanes of the wave active), the same value in each of them; `add` joins two values.
+template <class V, class F>
+__device__ inline V row_join(V v, F add) {
+  v = add(v, dpp<kQuad1>(v));
+  v = add(v, dpp<kQuad2>(v));
+  v = add(v, dpp<kHalfMirror>(v));
+  return add(v, dpp<kMirror>(v));
+}
+// Over all 64 lanes of a wave, the same value in every lane.
+template <class V, class F>
+__device__ inline V wave_join(V v, F add) {
+  v = row_join(v, add);
+  return add(add(lane_of(v, 0), lane_of(v, 16)), add(lane_of(v, 32), lane_of(v, 48)));
+}
 template <class V>
 __device__ inline V wave_sum(V v) {
-  v += dpp<kQuad1>(v);
-  v += dpp<kQuad2>(v);
-  v += dpp<kHalfMirror>(v);
-  v += dpp<kMirror>(v);
-  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+  return wave_join(v, [](V a, V b) { return a + b; });
 }
 __device__ inline u32 wave_umax(u32 v) {
-  v = max(v, dpp<kQuad1>(v));
-  v = max(v, dpp<kQuad2>(v));
-  v = max(v, dpp<kHalfMirror>(v));
-  v = max(v, dpp<kMirror>(v));
-  return max(max(lane_of(v, 0), lane_of(v, 16)), max(lane_of(v, 32), lane_of(v, 48)));
+  return wave_join(v, umax2);
 }
 
-// Over the waves (16 at most) that share a row, from their values in LDS: a lane takes one wave's, and every
-// group of lanes that the steps below join has them all.
-template <int WAVES>
-__device__ inline double waves_sum(const double* part) {
+// Over the waves (2, 4, 8 or 16) that share a row, from what `row_join` left for each 16 of their threads, in LDS: four values a wave. A lane
+// takes every sixteenth, and every group of lanes that the steps below join has them all.
+template <int WAVES, class V, class F>
+__device__ inline V waves_join(const V* part, F add) {
   static_assert(WAVES == 2 || WAVES == 4 || WAVES == 8 || WAVES == 16, "whole groups of lanes");
-  double v = part[threadIdx.x & (WAVES - 1)];
-  v += dpp<kQuad1>(v);
-  if constexpr (WAVES > 2) v += dpp<kQuad2>(v);
-  if constexpr (WAVES > 4) v += dpp<kHalfMirror>(v);
-  if constexpr (WAVES > 8) v += dpp<kMirror>(v);
-  return v;
-}
-template <int WAVES>
-__device__ inline u32 waves_umax(const u32* part) {
-  static_assert(WAVES == 2 || WAVES == 4 || WAVES == 8 || WAVES == 16, "whole groups of lanes");
-  u32 v = part[threadIdx.x & (WAVES - 1)];
-  v = max(v, dpp<kQuad1>(v));
-  if constexpr (WAVES > 2) v = max(v, dpp<kQuad2>(v));
-  if constexpr (WAVES > 4) v = max(v, dpp<kHalfMirror>(v));
-  if constexpr (WAVES > 8) v = max(v, dpp<kMirror>(v));
+  constexpr int LANES = WAVES < 4 ? 4 * WAVES : 16;
+  V v = part[threadIdx.x & (LANES - 1)];
+#pragma unroll
+  for (int k = 1; k < WAVES / 4; k++) v = add(v, part[(threadIdx.x & 15) + 16 * k]);
+  v = add(v, dpp<kQuad1>(v));
+  v = add(v, dpp<kQuad2>(v));
+  v = add(v, dpp<kHalfMirror>(v));
+  if constexpr (LANES == 16) v = add(v, dpp<kMirror>(v));
   return v;
 }
 

@@ -75,8 +75,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, COLS ? 4 : 1) void k_i8_rows(I8Q
   typedef typename DT::T E;
   constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64, N = NV ? NV : 1;
   static_assert(COLS == ROWS_ALONE || (NV && RPB == 1), "a block's threads own their columns");
-  __shared__ u32 red[2][RPB][WAVES];
-  const int t = threadIdx.x % T, sub = threadIdx.x / T, wave = t >> 6;
+  __shared__ u32 red[2][RPB][4 * WAVES];
+  const int t = threadIdx.x % T, sub = threadIdx.x / T;
   const int64_t Kp = (int64_t)p.rows.kq * 64, step = (int64_t)gridDim.x * RPB;
   auto at = [&](int j) { return (int64_t)(j * T + t) * 8; };
   auto load = [&](Vec8<DT>(&v)[N], int64_t row) {
@@ -110,12 +110,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, COLS ? 4 : 1) void k_i8_rows(I8Q
         most = max(most, amax_bits<DT>(v[0].w));
       }
     }
-    most = wave_umax(most);
     if constexpr (WAVES > 1) {
+      most = row_join(most, umax2);
       // two buffers: a wave may reach the next row's write while others still read this one's
-      if ((t & 63) == 0) red[flip][sub][wave] = most;
+      if ((t & 15) == 0) red[flip][sub][t >> 4] = most;
       lds_barrier();
-      most = waves_umax<WAVES>(red[flip][sub]);
+      most = waves_join<WAVES>(red[flip][sub], umax2);
+    } else {
+      most = wave_umax(most);
     }
     const Scale8 q = scale8(most);
     if (t == 0) p.rows.scales[row] = q.s;

@@ -43,6 +43,13 @@ struct RowStats {
   double mean, rstd;
 };
 
+// 1 / sqrt(v), to 2^-51: the hardware's estimate is off by less than 2^-22, and one step of third order cubes that.
+__device__ inline double rsqrt64(double v) {
+  if (!(v >= 0x1p-1000)) return 1.0 / sqrt(v);  // near or at zero, or NaN
+  const double r = __builtin_amdgcn_rsq(v), e = __builtin_fma(-(v * r), r, 1.0);
+  return __builtin_fma(r * e, __builtin_fma(0.375, e, 0.5), r);
+}
+
 // A row's first element, as bits and as a value.
 template <class DT>
 __device__ inline u32 first_bits(const typename DT::T* x) {
@@ -61,12 +68,12 @@ __device__ inline double bits_value(u32 bits) {
 
 // This thread's share of sum d and sum d^2.
 template <class DT>
-__device__ inline void add_stats(const Vec8<DT>& v, double pivot, double& s, double& q, int64_t n = 8) {
+__device__ inline void add_stats(const Vec8<DT>& v, double pivot, Sums2& sum, int64_t n = 8) {
 #pragma unroll
   for (int k = 0; k < 8; k++) {
     const double d = k < n ? (double)elem<DT>(v, k) - pivot : 0.0;
-    s += d;
-    q = __builtin_fma(d, d, q);
+    sum.a += d;
+    sum.b = __builtin_fma(d, d, sum.b);
   }
 }
 
@@ -135,9 +142,9 @@ template <class DT, int T, int NV, int OUT>
 __global__ __launch_bounds__(T < 256 ? 256 : T, NV == 2 ? 4 : 1) void k_norm(NormParams p) {
   typedef typename DT::T E;
   constexpr int RPB = T < 256 ? 256 / T : 1, WAVES = T / 64, N = NV ? NV : 1;
-  __shared__ double red[2][RPB][2][WAVES];
-  __shared__ u32 redm[2][RPB][WAVES];
-  const int t = threadIdx.x % T, sub = threadIdx.x / T, wave = t >> 6;
+  __shared__ Sums2 red[2][RPB][4 * WAVES];
+  __shared__ u32 redm[2][RPB][4 * WAVES];
+  const int t = threadIdx.x % T, sub = threadIdx.x / T;
   // threads past the end of a row take part up to the end of the codes' padding
   const int64_t Kp = OUT == NORM_Y ? p.K : (OUT == NORM_I8 ? (int64_t)p.i8.kq * 64 : (int64_t)p.mx.kq * 128);
   auto at = [&](int j) { return (int64_t)(j * T + t) * 8; };
@@ -150,6 +157,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, NV == 2 ? 4 : 1) void k_norm(Nor
     }
   };
   const int64_t step = (int64_t)gridDim.x * RPB;
+  const double k1 = 1.0 / (double)p.K;
   Vec8<DT> v[N], next[N];
   u32 pivot_bits = 0, pivot_next = 0;
   // rows of a block: its threads stay together (they share barriers), so past the last row some repeat it
@@ -166,31 +174,31 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, NV == 2 ? 4 : 1) void k_norm(Nor
     if (first + step < p.M) load(next, pivot_next, min(first + step + sub, p.M - 1));
     const E* x = reinterpret_cast<const E*>(p.x) + row * p.ldx;
     const double pivot = bits_value<DT>(pivot_bits);
-    double s = 0, sq = 0;
+    Sums2 sum{0, 0};
     if constexpr (NV > 0) {
 #pragma unroll
       for (int j = 0; j < NV; j++) {
         fit8<DT>(v[j], at(j), p.K, pivot_bits);  // past the row's end its first element: it adds nothing to the differences
-        add_stats<DT>(v[j], pivot, s, sq);
+        add_stats<DT>(v[j], pivot, sum);
         settle(v[j]);
         settle(q[j]);
       }
     } else {
-      for (int64_t c = (int64_t)t * 8; c < p.K; c += T * 8) add_stats<DT>(load8<DT>(x, c, p.K), pivot, s, sq, p.K - c);
+      for (int64_t c = (int64_t)t * 8; c < p.K; c += T * 8) add_stats<DT>(load8<DT>(x, c, p.K), pivot, sum, p.K - c);
     }
-    s = wave_sum(s);
-    sq = wave_sum(sq);
     if constexpr (WAVES > 1) {
+      sum = row_join(sum, add2);
       // two buffers: a wave may reach the next row's write while others still read this one's
-      if ((t & 63) == 0) red[flip][sub][0][wave] = s, red[flip][sub][1][wave] = sq;
+      if ((t & 15) == 0) red[flip][sub][t >> 4] = sum;
       lds_barrier();
-      s = waves_sum<WAVES>(red[flip][sub][0]);
-      sq = waves_sum<WAVES>(red[flip][sub][1]);
+      sum = waves_join<WAVES>(red[flip][sub], add2);
+    } else {
+      sum = wave_join(sum, add2);
     }
-    const double k1 = 1.0 / (double)p.K, ds = s * k1;
-    double var = __builtin_fma(sq, k1, -ds * ds);
+    const double ds = sum.a * k1;
+    double var = __builtin_fma(sum.b, k1, -ds * ds);
     var = var < 0 ? 0 : var;  // NaN stays
-    const RowStats st{pivot + ds, 1.0 / sqrt(var + p.eps)};
+    const RowStats st{pivot + ds, rsqrt64(var + p.eps)};
     if (t == 0 && p.mean) p.mean[row] = (float)st.mean, p.rstd[row] = (float)st.rstd;
 
     Scale8 scale{0.f, 0.f};
@@ -210,11 +218,13 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, NV == 2 ? 4 : 1) void k_norm(Nor
           most = max(most, amax8(y[0]));
         }
       }
-      most = wave_umax(most);
       if constexpr (WAVES > 1) {
-        if ((t & 63) == 0) redm[flip][sub][wave] = most;
+        most = row_join(most, umax2);
+        if ((t & 15) == 0) redm[flip][sub][t >> 4] = most;
         lds_barrier();
-        most = waves_umax<WAVES>(redm[flip][sub]);
+        most = waves_join<WAVES>(redm[flip][sub], umax2);
+      } else {
+        most = wave_umax(most);
       }
       scale = scale8(most);
       if (t == 0) p.i8.scales[row] = scale.s;
