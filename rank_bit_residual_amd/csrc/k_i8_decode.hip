@@ -3,7 +3,8 @@
 // v_mfma_i32_16x16x64_i8 takes 16 rows of A against 16 rows of b, a stage of 64 codes at a time; lane (i, g) holds codes
 // [16 g, 16 g + 16) of row i of either. A block of waves owns 16 NT output columns and splits K evenly over its waves; every byte of
 // b is used once, so it goes straight into registers, a contiguous kilobyte per 16 rows and stage, several stages of requests in
-// flight. The waves' partial tiles are added in LDS (exact: K is at most 2^17 here).
+// flight. The waves' partial tiles are added in LDS (exact: K is at most 2^17 here). 16 x 8192 x 8192 takes 14.5 us (4.6 TB/s), and one
+// unquantised row with b in the last-level cache 12.2 (5.5 TB/s).
 //
 // A may be given unquantised (RAW): every block then takes the maxima of x's rows for itself and lays its codes in LDS, which costs
 // vector instructions next to the reads of b but no launch. Its first reads of b are on their way meanwhile.

@@ -9,6 +9,10 @@
 // barrier per stage publishes them, and a stage's operands are read from LDS under the previous slice's MFMAs. Both operands
 // come in 1 KB tiles of 16 rows, one contiguous kilobyte per wave-wide load. LDS rows are 64 bytes; chunk c of row r sits at
 // c ^ ((r >> 2) & 3), so that 16 consecutive rows' 16-byte reads meet distinct banks.
+//
+// Bound by the matrix cores and, with the chip full of them, by power: 8192^3 takes 431 us (2.55 POP/s; a loop of nothing but the instruction
+// reaches 3.43), 4096 x 4096 x 12288 180. A stage of the 256 x 256 tile takes 1180 cycles, 1024 of them the instructions'; then the epilogue
+// 15000 (6000 for the scales, the rest for stores that all units make at once, at the rate of memory).
 #include <atomic>
 #include <type_traits>
 
@@ -271,7 +275,8 @@ __global__ __launch_bounds__(64 * C::NWV) void k_i8_tile(I8GemmParams p) {
 }
 
 // ------------------------------------------------------------------------------ joining split sums
-// Adds the parts in 64 bits and finishes the outputs, V neighbouring ones per thread.
+// Adds the parts in 64 bits and finishes the outputs, V neighbouring ones per thread. Bound by reading them: eight parts are requested at a
+// time.
 template <class DT, int V>
 __global__ __launch_bounds__(256) void k_i8_join(I8GemmParams p) {
   typedef typename DT::T T;

@@ -7,7 +7,8 @@
 //
 // A row is read once: it stays in the registers of the threads that share it while they agree on its maximum. A column's maximum
 // comes before its first code, so columns are read twice: partial maxima (and sums) of strips of rows, their join, then the codes,
-// which change places through LDS as bytes. All kernels are bound by memory.
+// which change places through LDS as bytes. All kernels are bound by memory; 8192 x 12288 bf16: rows 66 us (4.6 TB/s), columns 99, both 142
+// (rows and maxima 82, the join 5, the columns' codes 55), the values of a tensor 54 (5.6 TB/s).
 #include <type_traits>
 
 #include "i8.h"
@@ -320,8 +321,8 @@ static void launch_rows(const I8QuantParams& p, hipStream_t stream) {
   k_i8_rows<DT, T, NV, ROWS_ALONE><<<(unsigned)(blocks < most ? blocks : most), THREADS, 0, stream>>>(p, nullptr, nullptr);
 }
 
-// Two or three vectors a thread, so that several rows are on a compute unit: 8192 x 12288 bf16 70 to 74 us with 512 threads of three, 4096 x
-// 4096 15 with 256 of two (128 of four 20).
+// Two or three vectors a thread, so that several rows are on a compute unit: 8192 x 12288 bf16 66 us with 512 threads of three, 4096 x
+// 4096 13 with 256 of two (128 of four a third more).
 template <class DT>
 static hipError_t rows_t(const I8QuantParams& p, hipStream_t stream) {
   const int64_t Kp = (int64_t)p.rows.kq * 64;
@@ -349,20 +350,22 @@ static hipError_t rows_t(const I8QuantParams& p, hipStream_t stream) {
 // Rows whose codes and column maxima come from one reading: they fit a block's registers.
 constexpr int64_t kSharedRow = 16384;
 
-// Threads of a block of the kernel for both: a vector a thread, two past 8192 columns.
+// Threads of a block of the kernel for both: a vector a thread, two past 4096 columns (8192 x 8192 bf16 in 512 threads of two 45 us, in 1024 of
+// one 61; float32, whose registers do not hold two and their sums, 91 and 79: it takes 1024 of one).
 static int shared_threads(int64_t C) {
   const int64_t Kp = i8_kq(C) * 64;
-  return Kp <= 2048 ? 256 : (Kp <= 4096 ? 512 : 1024);
+  return Kp <= 2048 ? 256 : (Kp <= 8192 ? 512 : 1024);
 }
 
-// Strips of rows that a column's maximum is taken over. Read with the rows (`shared`): as many as the chip holds at once, of four rows or
-// more once there are 256 (8192 x 12288 bf16 in 128, 256, 512 strips 140, 81 and 89 us; 777 x 5003 12.9, 10.5 and 12.6). Alone: enough
-// blocks for the chip, of 16 rows or more.
+// Strips of rows that a column's maximum is taken over. Read with the rows (`shared`): 256, so that every compute unit has one; more where that
+// leaves each enough rows to be worth its part's way through memory, up to as many as the chip holds at once (8192 x 12288 bf16 in 128, 256, 512
+// strips 140, 81 and 89 us; 777 x 5003 12.9, 10.5 and 12.6; with the join and the codes 4096 x 5000 float32 in 256 and 512 51.5 and 54.5, 2048 x
+// 5000 f16 26.2 and 26.7). Alone: enough blocks for the chip, of 16 rows or more.
 static int64_t strips_of(int64_t R, int64_t C, bool shared) {
   int64_t strips;
   if (shared) {
-    const int64_t most = 256 * 1024 / shared_threads(C);
-    strips = R / 4 < most ? R / 4 : most;
+    const int64_t most = 256 * 1024 / shared_threads(C), rows = i8_kq(C) <= 64 ? 4 : 16;  // of a strip, at least
+    strips = R / rows < most ? R / rows : most;
     if (strips < 256) strips = R < 256 ? R : 256;
     return strips;
   }
@@ -414,12 +417,15 @@ static hipError_t cols_t(const I8QuantParams& p, hipStream_t stream) {
   if (shared) {
     switch (shared_threads(p.C)) {
       case 256: launch_shared<DT, 256, 1>(p, strips, part, sums, stream); break;
-      case 512: launch_shared<DT, 512, 1>(p, strips, part, sums, stream); break;
-      default:
-        if (p.rows.kq <= 128)
-          launch_shared<DT, 1024, 1>(p, strips, part, sums, stream);
+      case 512:
+        if (p.rows.kq <= 64)
+          launch_shared<DT, 512, 1>(p, strips, part, sums, stream);
+        else if constexpr (DT::size == 2)
+          launch_shared<DT, 512, 2>(p, strips, part, sums, stream);
         else
-          launch_shared<DT, 1024, 2>(p, strips, part, sums, stream);
+          launch_shared<DT, 1024, 1>(p, strips, part, sums, stream);
+        break;
+      default: launch_shared<DT, 1024, 2>(p, strips, part, sums, stream);
     }
   } else {
     const int64_t strip_rows = (p.R + strips - 1) / strips;

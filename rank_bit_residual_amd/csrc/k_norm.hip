@@ -5,11 +5,14 @@
 // multiply-adds take this chip no longer than float32's: with d = x - x[0], mean = x[0] + sum d / K and var = sum d^2 / K - (sum d /
 // K)^2 come from one reduction, and since (x[0] - mean)^2 <= K var the subtraction costs log2 K of 53 bits at most. y is rounded to
 // float32 once, and that is what is quantised or rounded on to the output's type; a code is decided by comparing with a border, so
-// rounding earlier would move one now and then.
+// rounding earlier would move one now and then. Memory bounds float32 rows and large 16-bit ones (8192 x 8192 97 us and 56, 5.5 and 4.8
+// TB/s); where fewer bytes leave, the binary64 steps (13 an element) and the codes do: to 8 bits 70 us, to MXFP4 52, of 38 and 32 for the
+// bytes alone. The parameters wait as float32, as binary64 they would cost the third wave of registers.
 //
 // Backward: with xh = (x - mean) rstd and g = dy weight, dx = rstd (g - mean(g) - xh mean(g xh)): one reduction, with dy and x in
 // registers. A thread keeps the same columns in every row of its block, so dweight = sum dy xh and dbias = sum dy are running sums
-// in registers; each block leaves its own, and a second kernel adds them in the blocks' order. All kernels are bound by memory.
+// in registers; each block leaves its own, and a second kernel adds them in the blocks' order. Memory bounds it: 8192 x 8192 bf16 76 us (5.3
+// TB/s) and 5 for the second kernel.
 #include <type_traits>
 
 #include "i8.h"
@@ -480,8 +483,8 @@ template <class DT, int OUT>
 static hipError_t norm_t(const NormParams& p, hipStream_t stream) {
   const int64_t Kp = OUT == NORM_Y ? p.K : (OUT == NORM_I8 ? (int64_t)p.i8.kq * 64 : (int64_t)p.mx.kq * 128);
   // Two vectors a thread; four of 256 threads past 4096 columns where there are many rows, unless their codes wait for a second
-  // maximum. 8192 x 8192 bf16, four of 256, two of 512, one of 1024: 57, 64 and 78 us, to 8 bits 75, 74 and 105, to MXFP4 54, 61 and 83;
-  // 777 x 5003 14.0, 10.6 and 11.6. Three of 512 past 8192 columns: 8192 x 12288 bf16 88 us, two of 1024 104, to 8 bits 116 and 135
+  // maximum. 8192 x 8192 bf16, four of 256, two of 512, one of 1024: 56, 61 and 68 us, to 8 bits 71, 70 and 94, to MXFP4 52, 58 and 73;
+  // 777 x 5003 13.2, 10.2 and 10.3. Three of 512 past 8192 columns: 8192 x 12288 bf16 87 us, two of 1024 107, to 8 bits 120 and 132
   if (p.K < 8)
     launch_rows<DT, 1024, 0, OUT>(p, stream);
   else if (Kp <= 512)

@@ -80,7 +80,7 @@ def test_quantize(dtype, rows, cols):
 
 
 @pytest.mark.parametrize("rows,cols,dtype", [(9001, 64, "bf16"), (9001, 300, "f16"), (4500, 1000, "f32"), (4999, 1500, "bf16"), (2100, 4000, "f16"),
-                                             (1100, 5003, "f32"), (1100, 8195, "bf16"), (1030, 12300, "bf16"), (600, 16500, "f16"),
+                                             (1100, 5003, "f32"), (1100, 8195, "bf16"), (5001, 4200, "bf16"), (4500, 8190, "f16"), (1030, 12300, "bf16"), (600, 16500, "f16"),
                                              (9, 5, "f32"), (700, 7, "bf16"), (5, 8, "f16"), (2000, 9, "bf16")])
 def test_quantize_many_rows(rows, cols, dtype):
     """More rows than the blocks of a launch, so that each takes several, and a last one that is not full."""
@@ -320,7 +320,8 @@ def test_out_and_strides():
 
 # ----------------------------------------------------------------------------- backward
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (3, 70, 33), (100, 96, 130), (515, 333, 144), (64, 2731, 100), (2000, 65, 70), (300, 512, 4000)])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (3, 70, 33), (100, 96, 130), (515, 333, 144), (64, 2731, 100), (2000, 65, 70), (300, 512, 4000), (300, 5000, 64), (4200, 4100, 20),
+                                   (100, 9000, 30)])
 def test_backward(dtype, M, N, K):
     rng = np.random.default_rng(M + N + K)
     dy, x, w = (_gpu(_wide(rng, *shape), dtype) for shape in ((M, N), (M, K), (K, N)))
