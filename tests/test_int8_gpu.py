@@ -347,6 +347,42 @@ def test_backward(dtype, M, N, K):
     assert all(torch.equal(p, q) for p, q in zip(R.int8_backward(room[:, 2: N + 2], wr, xc, bias=True), (dx, dw, db)))
 
 
+# ----------------------------------------------------------------------------- far offsets
+def test_offsets_past_32_bits():
+    """A tensor of 4.6 GB of codes from whole numbers that are their own codes along either axis (a largest of 127 in every row and column):
+    values back, products with its first and last rows on either side, and an output past 2^31 elements. The sums stay below 2^24, so that
+    float32 holds them all and a product in any order."""
+    rows, cols = 140_000, 32_768
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(78)
+    small = lambda *size: torch.randint(-3, 4, size, generator=gen, device=dev(), dtype=torch.int8).to(torch.bfloat16)  # noqa: E731
+    x = small(rows, cols)
+    x[:, ::1024] = 127
+    x[::1024] = 127
+    r, c = R.int8_quantize(x, axis=None)
+    assert r.data.numel() > 2**32 and bool((r.scales == 1).all()) and bool((c.scales == 1).all())
+    assert torch.equal(R.int8_dequantize(r), x)
+    back = R.int8_dequantize(c)
+    assert all(torch.equal(back[k:k + 4096], x[:, k:k + 4096].t()) for k in range(0, cols, 4096))
+    del back, c
+    ends = (slice(1, 300), slice(rows - 300, rows))
+    for M in (1, 40, 200):
+        a = small(M, cols)
+        a[:, 5] = 127
+        want = [a.float() @ x[part].float().t().contiguous() for part in ends]
+        for left in (R.int8_quantize(a), a):
+            y = R.int8_matmul(left, r, dtype=torch.bfloat16)
+            assert all(torch.equal(y[:, part], w.to(torch.bfloat16)) for part, w in zip(ends, want))
+        y = R.int8_matmul(r, R.int8_quantize(a), dtype=torch.float32)
+        assert all(torch.equal(y[part], w.t()) for part, w in zip(ends, want))
+    del y, r
+    a, b = x[:, :128], small(16_384, 128)
+    b[:, 7] = 127
+    y = R.int8_matmul(a, R.int8_quantize(b))
+    assert y.numel() > 2**31
+    assert all(torch.equal(y[part], (a[part].float() @ b.float().t().contiguous()).to(torch.bfloat16)) for part in ends)
+
+
 # ----------------------------------------------------------------------------- streams and graphs
 def _calls():
     rng = np.random.default_rng(21)

@@ -235,6 +235,32 @@ def test_backward_against_differences():
         assert abs((loss(x, w, b + step) - loss(x, w, b - step)) / (2 * h) - db[k]) < 1e-5
 
 
+@pytest.mark.parametrize("M,K", [(280_000, 16_384), (140_000, 32_768), (5_000_000, 900)])
+def test_offsets_past_32_bits(M, K):
+    """More than 2^32 elements: every row's results are those of the row alone, to the last."""
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(79)
+    x = torch.randn(M, K, generator=gen, device=dev(), dtype=torch.bfloat16)
+    w, b = (torch.randn(K, generator=gen, device=dev()) for _ in range(2))
+    assert x.numel() > 2**32
+    ends = (slice(0, 99), slice(M - 99, M))
+    y, mean, rstd = R.layer_norm(x, w, b, save=True)
+    for part in ends:
+        assert all(torch.equal(p[part], q) for p, q in zip((y, mean, rstd), R.layer_norm(x[part], w, b, save=True)))
+    del y
+    for how, back in (("int8", R.int8_dequantize), ("mx", R.mx_dequantize)):
+        t = back(R.layer_norm(x, w, b, quantize=how))
+        assert all(torch.equal(t[part], back(R.layer_norm(x[part], w, b, quantize=how))) for part in ends)
+        del t
+    dx, dw, db = R.layer_norm_backward(x, x, mean, rstd, w)
+    for part in ends:
+        assert torch.equal(dx[part], R.layer_norm_backward(x[part], x[part], mean[part], rstd[part], w)[0])
+    # sums over M rows: each row's part of dbias is of spread 1, float32 sums in parts of M / 256 rows or fewer
+    want = sum(x[k:k + 20_000].double().sum(0) for k in range(0, M, 20_000))
+    size = sum(x[k:k + 20_000].double().abs().sum(0) for k in range(0, M, 20_000))
+    assert bool(((db.double() - want).abs() <= (M / 64 + 300) * 2.0**-24 * size).all())
+
+
 def test_refusals_of_the_binding():
     d = dev()
     x, w = torch.ones(4, 64, device=d), torch.ones(64, device=d)
