@@ -499,8 +499,9 @@ int svdq_i8_product_form(int64_t M, int64_t N, int64_t K, int form[4]);
 
 /* --------------------------------------------------------------------------------------
  * svdq_i8_matmul — y = D( (sum_k a[m, k] b[n, k]) sa[m] sb[n] + bias[n] ) of two 8-bit tensors a [M, K] and b [N, K]: the sum is
- * exact, the scales and the bias enter in float32 (at most three roundings of 2^-24 each of the product, one of the sum with the bias;
- * in binary64 where a scale lies outside [2^-60, 2^40], or K is shared out), one rounding to dtype. bias: [N] of dtype, or NULL.
+ * exact, the scales and the bias enter in float32 (the sum and the product of the scales rounded to it, then one fma: two roundings of 2^-24
+ * each of the product, one of the result; in binary64 where a scale lies outside [2^-60, 2^40] or the sum outside int32), one rounding to
+ * dtype. An output depends on its row of a, its row of b and its bias alone, not on M or N. bias: [N] of dtype, or NULL.
  * y: [M, N] of dtype, row stride ldy >= N. workspace: svdq_i8_workspace_bytes.
  * Errors: EINVAL (shape, stride, alignment, workspace), EDTYPE, EHIP.
  * ------------------------------------------------------------------------------------ */
@@ -526,6 +527,8 @@ int svdq_i8_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_t sc, 
  * workspace: svdq_i8_backward_workspace_bytes. Errors: EINVAL, EDTYPE, EHIP.
  * ------------------------------------------------------------------------------------ */
 int svdq_i8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes_out);
+/* The tile {rows, columns} that the two products share when one launch makes both, or {0, 0} (host query). Errors: EINVAL. */
+int svdq_i8_backward_form(int64_t M, int64_t N, int64_t K, int form[2]);
 int svdq_i8_backward(const void* dy, int64_t lddy, int64_t M, int64_t N, int dtype, const void* w_codes, const void* w_scales,
                      const void* x_codes, const void* x_scales, int64_t K, int out_dtype, void* dx, int64_t lddx, void* dw,
                      int64_t lddw, void* db, void* workspace, size_t workspace_bytes, svdq_stream_t stream);

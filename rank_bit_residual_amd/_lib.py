@@ -79,6 +79,7 @@ SIGNATURES = {
     "svdq_i8_linear": (c_int, [c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_int, c_vp, c_i64, c_vp, c_sz,
                                c_vp]),
     "svdq_i8_backward_workspace_bytes": (c_int, [c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)]),
+    "svdq_i8_backward_form": (c_int, [c_i64, c_i64, c_i64, ctypes.POINTER(c_int)]),
     "svdq_i8_backward": (c_int, [c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_vp, c_vp, c_i64, c_int, c_vp, c_i64, c_vp,
                                  c_i64, c_vp, c_vp, c_sz, c_vp]),
     "svdq_layer_norm": (c_int, [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_int, ctypes.c_double, c_int, c_vp, c_i64, c_vp,

@@ -102,6 +102,9 @@ MxForm i8_product_form(int64_t M, int64_t N, int kq);
 bool i8_product_fits(int64_t M, int64_t N, int kq);
 size_t i8_product_part_bytes(int64_t M, int64_t N, int kq);
 hipError_t launch_i8_product(const I8GemmParams& p, int dtype, hipStream_t stream);
+// Two products, in one launch (in this form, unless bm is 0) or one after another, with the same results; they may share `part`.
+MxForm i8_pair_form(int64_t M0, int64_t N0, int kq0, int64_t M1, int64_t N1, int kq1);
+hipError_t launch_i8_products(const I8GemmParams& p, const I8GemmParams& q, int dtype, hipStream_t stream);
 
 // The kernel for few rows: its estimated time and block shape, whether its grid fits, and whether it quantises A itself.
 double i8_decode_cost(int64_t M, int64_t N, int kq, MxForm* form);

@@ -252,6 +252,17 @@ int svdq_i8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* by
   return SVDQ_OK;
 }
 
+int svdq_i8_backward_form(int64_t M, int64_t N, int64_t K, int form[2]) {
+  size_t bytes;
+  const int st = svdq_i8_backward_workspace_bytes(M, N, K, &bytes);
+  if (st) return st;
+  if (!form) return set_error(SVDQ_EINVAL, "form is NULL");
+  const MxForm f = i8_pair_form(M, K, (int)i8_kq(N), K, N, (int)i8_kq(M));
+  form[0] = f.bm;
+  form[1] = f.bm ? f.bn : 0;
+  return SVDQ_OK;
+}
+
 int svdq_i8_backward(const void* dy, int64_t lddy, int64_t M, int64_t N, int dtype, const void* w_codes, const void* w_scales,
                      const void* x_codes, const void* x_scales, int64_t K, int out_dtype, void* dx, int64_t lddx, void* dw,
                      int64_t lddw, void* db, void* workspace, size_t workspace_bytes, svdq_stream_t stream) {
@@ -279,13 +290,12 @@ int svdq_i8_backward(const void* dy, int64_t lddy, int64_t M, int64_t N, int dty
   I8GemmParams a = params_of(M, q_dx, ws + at[4]);
   a.a_codes = ws + at[0];
   a.a_scales = (const float*)(ws + at[1]);
-  if ((st = hip_status(launch_i8_product(a, out_dtype, s), "8-bit product launch"))) return st;
   q_dw.b_codes = ws + at[2];
   q_dw.b_scales = ws + at[3];
   I8GemmParams b = params_of(K, q_dw, ws + at[4]);
   b.a_codes = (const uint8_t*)x_codes;
   b.a_scales = (const float*)x_scales;
-  return hip_status(launch_i8_product(b, out_dtype, s), "8-bit product launch");
+  return hip_status(launch_i8_products(a, b, out_dtype, s), "8-bit product launch");
 }
 
 int svdq_layer_norm(const void* x, int64_t ldx, int64_t M, int64_t K, const void* weight, const void* bias, int param_dtype,

@@ -182,6 +182,22 @@ __device__ inline v2u codes8x8(const float (&v)[8], const Scale8& q) {
   return q.r == 0.f ? v2u{0, 0} : w;
 }
 
+// Whether a scale may enter a float32 product with another such scale and an int32 without leaving the normal range.
+__device__ inline bool tame(float s) { return s == 0.f || (s >= 0x1p-60f && s <= 0x1p40f); }
+
+// y from a sum and its scales, the same in every kernel: in float32 where they are tame, else in binary64 (an infinite product of scales would make a NaN
+// of a zero sum, a vanished one a zero of a large sum). Which of them depends on the output's own scales alone.
+__device__ inline float scaled(int sum, float sa, float sb, float bias) { return __builtin_fmaf((float)sum, sa * sb, bias); }
+__device__ inline float scaled_far(int sum, float sa, float sb, float bias) {
+  if (tame(sa) && tame(sb)) return scaled(sum, sa, sb, bias);
+  return (float)__builtin_fma((double)sum * (double)sa, (double)sb, (double)bias);
+}
+// Of a sum that may pass 32 bits.
+__device__ inline float scaled_long(int64_t sum, float sa, float sb, float bias) {
+  if (sum == (int)sum) return scaled_far((int)sum, sa, sb, bias);
+  return (float)__builtin_fma((double)sum * (double)sa, (double)sb, (double)bias);
+}
+
 // Where code k of row r lies.
 __device__ inline int64_t i8_at(int64_t r, int64_t k, int kq) { return (((r >> 4) * kq + (k >> 6)) << 10) + ((r & 15) << 6) + (k & 63); }
 

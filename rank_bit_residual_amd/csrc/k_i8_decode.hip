@@ -183,9 +183,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_i8_decode(I8GemmParams p) {
     int sum = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; w++) sum += red[w][m][n][v][el];
-    const double sa = RAW ? row_scale[row] : p.a_scales[row];
-    const double bz = p.bias ? DT::load(reinterpret_cast<const T*>(p.bias)[col]) : 0.f;
-    y[row * p.ldy + col] = DT::store((float)((double)sum * sa * (double)p.b_scales[col] + bz));
+    const float sa = RAW ? row_scale[row] : p.a_scales[row];
+    const float bz = p.bias ? DT::load(reinterpret_cast<const T*>(p.bias)[col]) : 0.f;
+    y[row * p.ldy + col] = DT::store(scaled_far(sum, sa, p.b_scales[col], bz));
   }
 }
 

@@ -2,7 +2,8 @@
 //
 // v_mfma_i32_32x32x32_i8 takes 16 K-consecutive codes per lane and sums in int32, so the sum is exact up to K = 2^17
 // (2^17 * 127^2 < 2^31); a longer K is cut into shares, whose sums are joined in 64 bits. The scales and the bias enter once, in the
-// epilogue: float32 of the sum, times float32(sa sb), plus the bias with one rounding (fma), then the output's own.
+// epilogue: float32 of the sum, times float32(sa sb), plus the bias with one rounding (fma), then the output's own. The same in every form, so an
+// output depends on its two rows and its bias alone, not on how many others there are.
 //
 // Tiles (k_i8_tile): a BM x BN output tile per block of WM x WN waves. K advances in stages of 64 codes (64 bytes per row), which
 // land in a ring of LDS buffers through direct global->LDS loads issued DIST stages ahead; a wave waits on its own loads, one
@@ -40,33 +41,27 @@ struct I8Cfg {
   static constexpr int ALL = SMEM + (BM + BN) * 4;  // behind the ring: the scales of the tile's rows and columns
 };
 
-// Whether a scale may enter a float32 product with another such scale and an int32 without leaving the normal range.
-__device__ inline bool tame(float s) { return s == 0.f || (s >= 0x1p-60f && s <= 0x1p40f); }
-
-// y from a sum and its scales: in float32 where they are tame, else in binary64 (an infinite product of scales would make a NaN
-// of a zero sum, a vanished one a zero of a large sum). Which of them depends on the output's own scales alone.
-__device__ inline float scaled(int sum, float sa, float sb, float bias) { return __builtin_fmaf((float)sum, sa * sb, bias); }
-__device__ inline float scaled_far(int sum, float sa, float sb, float bias) {
-  if (tame(sa) && tame(sb)) return scaled(sum, sa, sb, bias);
-  return (float)((double)sum * (double)sa * (double)sb + (double)bias);
+// Blocks i, i + 8, ... share an XCD and its L2, so each XCD takes a run of a product's (share of K, tile): few shares, and within one groups
+// of 4 row tiles walked column by column. The place of XCD `xcd`'s block `i` in that order, or -1 past its end.
+__device__ inline int run_of(int xcd, int i, int all) {
+  const int run = xcd * ((all + 7) >> 3) + i;
+  return i >= (all + 7) >> 3 || run >= all ? -1 : run;
+}
+template <class C>
+__device__ inline int tiles_of(const I8GemmParams& p) {
+  return ((p.M + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
 }
 
-// Block: tile `tid` of tiles_m x tiles_n, stages [s0, s0 + nst) of K (an even number, at least two). SPLIT: the block's share of K,
+// Tile `tid` of tiles_m x tiles_n, stages [s0, s0 + nst) of K (an even number, at least two). SPLIT: the block's share of K,
 // as int32 sums into its part of p.part; else the finished output.
 template <class DT, class C, bool SPLIT>
-__global__ __launch_bounds__(64 * C::NWV) void k_i8_tile(I8GemmParams p) {
+__device__ __forceinline__ void do_tile(const I8GemmParams& p, int run, uint8_t* smem) {
   typedef typename DT::T T;
-  extern __shared__ __align__(1024) uint8_t smem[];
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int l32 = lane & 31, g = lane >> 5;
 
-  // ---- tile order: blocks i, i + 8, ... share an XCD and its L2, so each XCD takes a run of (share of K, tile): few shares,
-  // and within one groups of 4 row tiles walked column by column
-  const int tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN;
-  const int ntiles = tiles_m * tiles_n, all = SPLIT ? ntiles * p.splits : ntiles;
-  const int run = (blockIdx.x & 7) * ((all + 7) >> 3) + (blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= (all + 7) >> 3 || run >= all) return;
+  const int tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN, ntiles = tiles_m * tiles_n;
   const int split = SPLIT ? run / ntiles : 0, tid = SPLIT ? run - split * ntiles : run;
   const int GM = 4;
   const int group = tid / (GM * tiles_n), gm0 = group * GM;
@@ -274,6 +269,26 @@ __global__ __launch_bounds__(64 * C::NWV) void k_i8_tile(I8GemmParams p) {
   }
 }
 
+template <class DT, class C, bool SPLIT>
+__global__ __launch_bounds__(64 * C::NWV) void k_i8_tile(I8GemmParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int run = run_of(blockIdx.x & 7, blockIdx.x >> 3, SPLIT ? tiles_of<C>(p) * p.splits : tiles_of<C>(p));
+  if (run >= 0) do_tile<DT, C, SPLIT>(p, run, smem);
+}
+
+// Two products that do not wait for each other in one launch, the one with the longer tiles first: the second fills the units that the first
+// leaves, and their epilogues do not all meet the memory at once.
+template <class DT, class C>
+__global__ __launch_bounds__(64 * C::NWV) void k_i8_tile2(I8GemmParams p0, I8GemmParams p1) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int n0 = tiles_of<C>(p0), i = blockIdx.x >> 3, per0 = (n0 + 7) >> 3;
+  const bool second = i >= per0;
+  I8GemmParams p = p0;
+  if (second) p = p1;
+  const int run = run_of(blockIdx.x & 7, second ? i - per0 : i, second ? tiles_of<C>(p1) : n0);
+  if (run >= 0) do_tile<DT, C, false>(p, run, smem);
+}
+
 // ------------------------------------------------------------------------------ joining split sums
 // Adds the parts in 64 bits and finishes the outputs, V neighbouring ones per thread. Bound by reading them: eight parts are requested at a
 // time.
@@ -284,7 +299,7 @@ __global__ __launch_bounds__(256) void k_i8_join(I8GemmParams p) {
   const int c = (blockIdx.x * 256 + threadIdx.x) * V;
   if (c >= p.N) return;
   const int64_t stride = (int64_t)p.M * p.N;
-  double sb[V], bz[V];
+  float sb[V], bz[V];
 #pragma unroll
   for (int k = 0; k < V; k++) {
     sb[k] = p.b_scales[c + k];
@@ -292,7 +307,7 @@ __global__ __launch_bounds__(256) void k_i8_join(I8GemmParams p) {
   }
   for (int64_t r = blockIdx.y; r < p.M; r += gridDim.y) {
     const int* src = p.part + r * p.N + c;
-    const double sa = p.a_scales[r];
+    const float sa = p.a_scales[r];
     int64_t sum[V] = {};
     for (int s = 0; s < p.splits; s += 8) {
       vec x[8];
@@ -307,7 +322,7 @@ __global__ __launch_bounds__(256) void k_i8_join(I8GemmParams p) {
     }
     T* y = reinterpret_cast<T*>(p.y) + r * p.ldy + c;
 #pragma unroll
-    for (int k = 0; k < V; k++) y[k] = DT::store((float)((double)sum[k] * sa * sb[k] + bz[k]));
+    for (int k = 0; k < V; k++) y[k] = DT::store(scaled_long(sum[k], sa, sb[k], bz[k]));
   }
 }
 
@@ -317,6 +332,7 @@ using namespace dev;
 
 // Compute units of the chip: what a plan spreads a product over. Stages whose int32 sums cannot overflow: 2^17 codes.
 constexpr int kCus = 256, kExactStages = 2048;
+constexpr double kLaunch = 2.0;  // us that a launch of its own costs the second of two products
 
 typedef I8Cfg<64, 64, 2, 2, 4> Tile64;
 typedef I8Cfg<64, 128, 2, 2, 4> Tile64n;
@@ -333,48 +349,64 @@ typedef I8Cfg<256, 256, 4, 2, 2> Tile256;
 // Operands past the last-level cache cost the smaller tiles a quarter more, as they read them more often: 1024 x 65536 x 1024 in four
 // shares of 128 x 128 105, in 16 of 256 x 256 81. Shares of K add the joining launch and the parts' way through memory.
 // The kernel for few rows has its own estimate (i8_decode_cost).
-static MxForm choose(int64_t M, int64_t N, int kq) {
-  MxForm best{0, 0, 1, 1};
-  double best_t = 1e30;
-  if (kq <= kExactStages) best_t = i8_decode_cost(M, N, kq, &best);
-  struct Cost {
-    int bm, bn;
-    double first, alone, shared, out;  // us: a block's own, a stage of one block a unit, of several (each), a further block's epilogue
-  };
-  const Cost cand[4] = {{64, 64, 3.5, 0.15, 0.095, 0.65}, {64, 128, 4.0, 0.17, 0.16, 1.6}, {128, 128, 4.5, 0.265, 0.21, 3.0}, {256, 256, 0, 0, 0, 0}};
+struct Cost {
+  int bm, bn;
+  double first, alone, shared, out;  // us: a block's own, a stage of one block a unit, of several (each), a further block's epilogue
+};
+static const Cost kForms[4] = {{64, 64, 3.5, 0.15, 0.095, 0.65}, {64, 128, 4.0, 0.17, 0.16, 1.6}, {128, 128, 4.5, 0.265, 0.21, 3.0}, {256, 256, 0, 0, 0, 0}};
+
+static double tile_time(const Cost& c, int64_t M, int64_t N, int kq, int s) {
   const double least = 3.5 + ((double)M + (double)N) * kq * 64e-6 / 5.0;  // the operands' bytes from memory
   const double cold = ((double)M + (double)N) * kq * 64 > 64e6 ? 1.25 : 1.0;
-  for (const Cost& c : cand) {
+  const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+  const double st = (double)kq / s;
+  double t;
+  if (c.bm == 256) {
+    const double whole = (double)((tiles * s) / kCus), rest = (double)(tiles * s) / kCus - whole;
+    t = whole * (10.8 + 0.764 * st) + (rest > 0 ? 4 + 7 * rest + st * (0.52 + 0.22 * rest) : 0);
+  } else {
+    const double b = (double)((tiles * s + kCus - 1) / kCus);
+    const double rate = b <= 1 ? c.alone : (c.shared * b > c.alone + c.shared * 0.6 ? c.shared * b : c.alone + c.shared * 0.6);
+    t = c.first + st * rate * cold + (b > 1 ? c.out * (b - 1) : 0);
+  }
+  if (t < least) t = least;
+  if (M == 1) t += 2.0;  // the launch that quantises a row, which the other kernel does itself
+  if (s > 1) t += 3.0 + (double)M * N * 4 * 2 * s / 5.5e6;
+  return t;
+}
+
+static MxForm choose(int64_t M, int64_t N, int kq, double& best_t) {
+  MxForm best{0, 0, 1, 1};
+  best_t = 1e30;
+  if (kq <= kExactStages) best_t = i8_decode_cost(M, N, kq, &best);
+  for (const Cost& c : kForms) {
     const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
     for (int s = 1; s <= kq / 2; s *= 2) {
       if ((kq / 2 + s - 1) / s * 2 > kExactStages) continue;
       if (s > 1 && best_t < 1e30 && (kq / 2 / s < 4 || tiles * s > 2 * kCus)) break;
-      const double st = (double)kq / s;
-      double t;
-      if (c.bm == 256) {
-        const double whole = (double)((tiles * s) / kCus), rest = (double)(tiles * s) / kCus - whole;
-        t = whole * (10.8 + 0.764 * st) + (rest > 0 ? 4 + 7 * rest + st * (0.52 + 0.22 * rest) : 0);
-      } else {
-        const double b = (double)((tiles * s + kCus - 1) / kCus);
-        const double rate = b <= 1 ? c.alone : (c.shared * b > c.alone + c.shared * 0.6 ? c.shared * b : c.alone + c.shared * 0.6);
-        t = c.first + st * rate * cold + (b > 1 ? c.out * (b - 1) : 0);
-      }
-      if (t < least) t = least;
-      if (M == 1) t += 2.0;  // the launch that quantises a row, which the other kernel does itself
-      if (s > 1) t += 3.0 + (double)M * N * 4 * 2 * s / 5.5e6;
+      const double t = tile_time(c, M, N, kq, s);
       if (t < best_t) best = MxForm{c.bm, c.bn, s, 1}, best_t = t;
     }
   }
   return best;
 }
 
-// (A call asks several times for the sizes that it was given.)
-static MxForm plan_of(int64_t M, int64_t N, int kq) {
-  static thread_local int64_t m = 0, n = 0;
-  static thread_local int k = 0;
-  static thread_local MxForm f;
-  if (m != M || n != N || k != kq) f = choose(M, N, kq), m = M, n = N, k = kq;
-  return f;
+// (A call asks several times for the sizes that it was given; a backward pass has two of them.)
+static MxForm plan_of(int64_t M, int64_t N, int kq, double* time = nullptr) {
+  struct Plan {
+    int64_t M, N;
+    int kq;
+    MxForm f;
+    double t;
+  };
+  static thread_local Plan last[2] = {};
+  static thread_local int older = 0;
+  auto is = [&](const Plan& p) { return p.M == M && p.N == N && p.kq == kq; };
+  const int at = is(last[0]) ? 0 : (is(last[1]) ? 1 : older);
+  Plan& p = last[at];
+  if (!is(p)) p.f = choose(M, N, kq, p.t), p.M = M, p.N = N, p.kq = kq, older = 1 - at;
+  if (time) *time = p.t;
+  return p.f;
 }
 
 MxForm i8_product_form(int64_t M, int64_t N, int kq) { return plan_of(M, N, kq); }
@@ -394,23 +426,38 @@ bool i8_product_fits(int64_t M, int64_t N, int kq) {
   return f.waves > 1 ? i8_decode_fits(M, N, f) : mx_fits_grid(tile_blocks(M, N, f), 512);
 }
 
-template <class DT, class C, bool SPLIT>
-static hipError_t launch_tile(const I8GemmParams& p, const MxForm& f, hipStream_t stream) {
-  const int64_t blocks = tile_blocks(p.M, p.N, f);
-  if (!mx_fits_grid(blocks, 64 * C::NWV)) return hipErrorInvalidConfiguration;
-  // once per process and device; a second thread at most repeats the same call
-  static std::atomic<uint64_t> configured;
+// Lets `kernel` have the LDS of C: once per process and device; a second thread at most repeats the same call.
+template <class C>
+static hipError_t configure(const void* kernel, std::atomic<uint64_t>& configured) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!bit || !(configured.load(std::memory_order_relaxed) & bit)) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_i8_tile<DT, C, SPLIT>), hipFuncAttributeMaxDynamicSharedMemorySize,
-                            C::ALL);
-    if (e != hipSuccess) return e;
-    configured.fetch_or(bit, std::memory_order_relaxed);
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, C::ALL);
+    if (e == hipSuccess) configured.fetch_or(bit, std::memory_order_relaxed);
   }
+  return e;
+}
+
+template <class DT, class C, bool SPLIT>
+static hipError_t launch_tile(const I8GemmParams& p, const MxForm& f, hipStream_t stream) {
+  const int64_t blocks = tile_blocks(p.M, p.N, f);
+  if (!mx_fits_grid(blocks, 64 * C::NWV)) return hipErrorInvalidConfiguration;
+  static std::atomic<uint64_t> configured;
+  const hipError_t e = configure<C>(reinterpret_cast<const void*>(&k_i8_tile<DT, C, SPLIT>), configured);
+  if (e != hipSuccess) return e;
   k_i8_tile<DT, C, SPLIT><<<dim3((unsigned)blocks), 64 * C::NWV, C::ALL, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <class DT, class C>
+static hipError_t launch_tile2(const I8GemmParams& p, const I8GemmParams& q, const MxForm& f, hipStream_t stream) {
+  static std::atomic<uint64_t> configured;
+  const hipError_t e = configure<C>(reinterpret_cast<const void*>(&k_i8_tile2<DT, C>), configured);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = tile_blocks(p.M, p.N, f) + tile_blocks(q.M, q.N, f);
+  k_i8_tile2<DT, C><<<dim3((unsigned)blocks), 64 * C::NWV, C::ALL, stream>>>(p, q);
   return hipGetLastError();
 }
 
@@ -436,6 +483,62 @@ static hipError_t launch_product_t(const I8GemmParams& p0, const MxForm& f, hipS
   else
     k_i8_join<DT, 1><<<dim3((unsigned)((p.N + 255) / 256), rows), 256, 0, stream>>>(p);
   return hipGetLastError();
+}
+
+// Two products in one launch with tiles of one form, us: the stages that a unit gets of both, or the longest block alone. Measured (M x K x N of
+// y; dx and dw in 64 x 64, 64 x 128, 128 x 128, 256 x 256 tiles, and in two launches): 512 x 512 x 2048 9.1, 9.9, 12.2, 24.8, 13.8; 515 x 1440 x 2731 15.1,
+// 14.6, 17.5, 31.2, 19.6; 1024 x 4096 x 1024 22.2, 20.0, 16.0, 19.5, 19.9; 2048 x 4096 x 4096 111, 95, 75, 66, 76; 4096 x 4096 x 12288 256 x 256
+// 339, two launches 348. Where dw is much larger than dx the stores count and two launches stay: 16 x 4096 x 12288 61, 60, 71, 112 and 47.
+static double pair_time(const Cost& c, int64_t M0, int64_t N0, int kq0, int64_t M1, int64_t N1, int kq1) {
+  const double tiles0 = (double)((M0 + c.bm - 1) / c.bm) * (double)((N0 + c.bn - 1) / c.bn);
+  const double tiles1 = (double)((M1 + c.bm - 1) / c.bm) * (double)((N1 + c.bn - 1) / c.bn);
+  const double b = (tiles0 + tiles1) / kCus, stages = (tiles0 * kq0 + tiles1 * kq1) / kCus, longest = kq0 > kq1 ? kq0 : kq1;
+  if (c.bm == 256) {
+    const double full = b < 1 ? b : 1, all = 10.8 * b + 0.764 * stages, one = 4 + 7 * full + longest * (0.52 + 0.22 * full);
+    return all > one ? all : one;
+  }
+  const double cold = (((double)M0 + (double)N0) * kq0 + ((double)M1 + (double)N1) * kq1) * 64 > 64e6 ? 1.25 : 1.0;
+  const double all = c.first + stages * c.shared * cold + (b > 1 ? c.out * (b - 1) : 0), one = c.first + longest * c.alone * cold;
+  const double crowd = c.bn == 64 ? 1.1 : 1.0;  // of the smallest tiles' stores
+  return (all > one ? all : one) * crowd;
+}
+
+// The form that two products share in one launch, or none (bm 0): the one of the least time, if that is less than two launches'.
+MxForm i8_pair_form(int64_t M0, int64_t N0, int kq0, int64_t M1, int64_t N1, int kq1) {
+  MxForm best{0, 0, 1, 1};
+  if (kq0 > kExactStages || kq1 > kExactStages) return best;
+  double t0, t1;
+  plan_of(M0, N0, kq0, &t0);
+  plan_of(M1, N1, kq1, &t1);
+  double best_t = t0 + t1 + kLaunch;
+  for (const Cost& c : kForms) {
+    const MxForm f{c.bm, c.bn, 1, 1};
+    const double t = pair_time(c, M0, N0, kq0, M1, N1, kq1);
+    if (t < best_t && mx_fits_grid(tile_blocks(M0, N0, f) + tile_blocks(M1, N1, f), 512)) best = f, best_t = t;
+  }
+  return best;
+}
+
+template <class DT>
+static hipError_t launch_pair(const I8GemmParams& p, const I8GemmParams& q, const MxForm& f, hipStream_t stream) {
+  if (f.bm == 64 && f.bn == 64) return launch_tile2<DT, Tile64>(p, q, f, stream);
+  if (f.bm == 64) return launch_tile2<DT, Tile64n>(p, q, f, stream);
+  if (f.bm == 256) return launch_tile2<DT, Tile256>(p, q, f, stream);
+  return launch_tile2<DT, Tile128>(p, q, f, stream);
+}
+
+hipError_t launch_i8_products(const I8GemmParams& p, const I8GemmParams& q, int dtype, hipStream_t stream) {
+  if (q.kq > p.kq) return launch_i8_products(q, p, dtype, stream);
+  const MxForm f = i8_pair_form(p.M, p.N, p.kq, q.M, q.N, q.kq);
+  if (!f.bm) {
+    const hipError_t e = launch_i8_product(p, dtype, stream);
+    return e != hipSuccess ? e : launch_i8_product(q, dtype, stream);
+  }
+  switch (dtype) {
+    case SVDQ_F32: return launch_pair<MxF32>(p, q, f, stream);
+    case SVDQ_BF16: return launch_pair<MxBF16>(p, q, f, stream);
+    default: return launch_pair<MxF16>(p, q, f, stream);
+  }
 }
 
 hipError_t launch_i8_product(const I8GemmParams& p, int dtype, hipStream_t stream) {

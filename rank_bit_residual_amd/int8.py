@@ -125,7 +125,8 @@ def int8_dequantize(t: Int8Tensor, dtype: torch.dtype = torch.bfloat16, out: tor
 def int8_matmul(a, b: Int8Tensor, bias: torch.Tensor | None = None, dtype: torch.dtype | None = None,
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """Y = A B^T (+ bias) [M, N] of a [M, K] and b [N, K]: exact integer sums, times the scales of their row and column plus the bias in
-    float32 (float64 where a scale is far from 1), rounded once to dtype. a: an Int8Tensor, or a matrix, which is quantised along
+    float32 (float64 where a scale is far from 1), rounded once to dtype; an output depends on its row of a and of b and its bias
+    alone, bit for bit, whatever M and N. a: an Int8Tensor, or a matrix, which is quantised along
     its rows. dtype: a matrix's own, else bfloat16. bias: [N] of that dtype. For a layer with weight [K, N],
     b = int8_quantize(weight, axis=0)."""
     _i8(b, "b")

@@ -203,6 +203,16 @@ def test_linear_workspace_query():
         _refused(EINVAL, lib.svdq_i8_linear_workspace_bytes(*bad, BF16, ctypes.byref(n)))
 
 
+def test_backward_form_query():
+    lib, form = _lib.load(), (ctypes.c_int * 2)()
+    for sizes, want in (((4096, 12288, 4096), (256, 256)), ((1, 1, 1), (0, 0)), ((1 << 26, 64, 64), None)):
+        assert lib.svdq_i8_backward_form(*sizes, form) == 0
+        assert want is None or tuple(form) == want
+    for bad in ((0, 4, 4), (4, 0, 4), (4, 4, 0), ((1 << 26) + 1, 4, 4), (4, (1 << 26) + 1, 4)):
+        _refused(EINVAL, lib.svdq_i8_backward_form(*bad, form))
+    _refused(EINVAL, lib.svdq_i8_backward_form(4, 4, 4, None))
+
+
 def test_backward_workspace_query():
     lib, n = _lib.load(), ctypes.c_size_t()
     d = sum(_layout(100, 96)[1:]) + sum(_layout(96, 100)[1:])

@@ -318,6 +318,25 @@ def test_out_and_strides():
         R.int8_matmul(big[:90, :130], w, out=big[:90, :90])
 
 
+@pytest.mark.parametrize("K,N", [(40, 300), (1500, 2000), (12000, 130), (140_000, 65)])
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_an_output_depends_on_its_own_rows_alone(dtype, K, N):
+    """The same bits from whatever form the numbers of rows and columns lead to."""
+    rng = np.random.default_rng(K)
+    a, w, bias = _gpu(rng.standard_normal((1500, K)), dtype), _gpu(rng.standard_normal((K, N)), dtype), _gpu(rng.standard_normal(N), dtype)
+    a[3] *= 2.0**-24  # f32: a scale far below the others
+    b = R.int8_quantize(w, axis=0)
+    y = R.int8_matmul(a, b, bias=bias)
+    forms = {_form(1500, N, K)}
+    for M in (1, 3, 17, 64, 200, 700):
+        forms.add(_form(M, N, K))
+        assert torch.equal(R.int8_matmul(a[:M], b, bias=bias), y[:M])
+        assert torch.equal(R.int8_matmul(R.int8_quantize(a[:M]), b, bias=bias, dtype=a.dtype), y[:M])
+    c = R.int8_quantize(w[:, :33], axis=0)
+    assert torch.equal(R.int8_matmul(a, c, bias=bias[:33]), y[:, :33])
+    assert len(forms) > 2
+
+
 # ----------------------------------------------------------------------------- backward
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (3, 70, 33), (100, 96, 130), (515, 333, 144), (64, 2731, 100), (2000, 65, 70), (300, 512, 4000), (300, 5000, 64), (4200, 4100, 20),
@@ -345,6 +364,33 @@ def test_backward(dtype, M, N, K):
     room = torch.zeros(M, N + 5, dtype=TD[dtype], device=dy.device)
     room[:, 2: N + 2] = dy
     assert all(torch.equal(p, q) for p, q in zip(R.int8_backward(room[:, 2: N + 2], wr, xc, bias=True), (dx, dw, db)))
+
+
+BACKWARD_SIZES = {(512, 512, 2048): (64, 64), (700, 700, 1100): (64, 64), (10, 300, 500): (64, 64), (2000, 500, 4000): (64, 128),
+                  (515, 1440, 2731): (64, 128), (800, 800, 8000): (64, 128), (3000, 1000, 5000): (128, 128), (1024, 4096, 1024): (128, 128),
+                  (2048, 4096, 4096): (256, 256), (4096, 2000, 8190): (256, 256), (16, 4096, 12288): (0, 0), (1000, 100, 12000): (0, 0)}  # M, K, N: the tiles that both products share
+
+
+@pytest.mark.parametrize("M,K,N", list(BACKWARD_SIZES))
+def test_both_products_in_one_launch(M, K, N):
+    """Bit for bit those of two calls, in every form; values beside a float64 product of the same codes."""
+    got = (ctypes.c_int * 2)()
+    assert _lib.load().svdq_i8_backward_form(M, N, K, got) == 0
+    assert tuple(got) == BACKWARD_SIZES[(M, K, N)]
+    rng = np.random.default_rng(M + K)
+    dy, x, w = (_gpu(rng.standard_normal(shape), "bf16") for shape in ((M, N), (M, K), (K, N)))
+    dy[:, 7] *= 2.0**-100  # a column of dw whose scales are far from 1
+    wr, xc = R.int8_quantize(w, axis=1), R.int8_quantize(x, axis=0)
+    r, c = R.int8_quantize(dy, axis=None)
+    for dtype in (torch.bfloat16, torch.float32, torch.float16):
+        dx, dw = R.int8_backward(dy, wr, xc, dtype=dtype)
+        assert torch.equal(dx, R.int8_matmul(r, wr, dtype=dtype)) and torch.equal(dw, R.int8_matmul(xc, c, dtype=dtype))
+        if dtype == torch.float32:
+            for y, a, b in ((dx, r, wr), (dw, xc, c)):
+                rows, cols = slice(y.shape[0] - 70, None), slice(y.shape[1] - 70, None)
+                ref = _np(R.int8_dequantize(a, torch.float32)[rows]) @ _np(R.int8_dequantize(b, torch.float32)[cols]).T
+                mass = np.abs(_np(R.int8_dequantize(a, torch.float32)[rows])) @ np.abs(_np(R.int8_dequantize(b, torch.float32)[cols])).T
+                assert (np.abs(_np(y[rows, cols]) - ref) <= 5.1 * 2.0**-24 * mass).all()  # three roundings, and two of the values'
 
 
 # ----------------------------------------------------------------------------- far offsets
