@@ -276,8 +276,8 @@ __global__ __launch_bounds__(64 * C::NWV) void k_i8_tile(I8GemmParams p) {
   if (run >= 0) do_tile<DT, C, SPLIT>(p, run, smem);
 }
 
-// Two products that do not wait for each other in one launch, the one with the longer tiles first: the second fills the units that the first
-// leaves, and their epilogues do not all meet the memory at once.
+// Two products that do not wait for each other in one launch, the one with the longer tiles first: the second's fill the units that the
+// first's leave, and a launch less waits for the one before it (measured beside pair_time).
 template <class DT, class C>
 __global__ __launch_bounds__(64 * C::NWV) void k_i8_tile2(I8GemmParams p0, I8GemmParams p1) {
   extern __shared__ __align__(1024) uint8_t smem[];
