@@ -205,9 +205,9 @@ def test_linear_workspace_query():
 
 def test_backward_form_query():
     lib, form = _lib.load(), (ctypes.c_int * 2)()
-    for sizes, want in (((4096, 12288, 4096), (256, 256)), ((1, 1, 1), (0, 0)), ((1 << 26, 64, 64), None)):
+    for sizes, want in (((4096, 12288, 4096), (256, 256)), ((1, 1, 1), (64, 64)), ((16, 12288, 4096), (0, 0)), ((1 << 26, 64, 64), (0, 0))):
         assert lib.svdq_i8_backward_form(*sizes, form) == 0
-        assert want is None or tuple(form) == want
+        assert tuple(form) == want
     for bad in ((0, 4, 4), (4, 0, 4), (4, 4, 0), ((1 << 26) + 1, 4, 4), (4, (1 << 26) + 1, 4)):
         _refused(EINVAL, lib.svdq_i8_backward_form(*bad, form))
     _refused(EINVAL, lib.svdq_i8_backward_form(4, 4, 4, None))
