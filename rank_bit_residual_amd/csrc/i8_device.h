@@ -143,8 +143,9 @@ __device__ inline Scale8 scale8(u32 amax_bits) {
 
 // The nearest integer to x / s, ties to even, in the low byte of u.
 // x r differs from x / s by less than 2^-16.9, so adding 1.5 * 2^23 to it (one rounding, to an integer k) gives that integer or, next
-// to a border, its neighbour. The remainder x - k s, which one fma gives exactly, says which: k is right if it is smaller than s / 2 in
-// size, or equal and k even. (Exactly: the remainder is a multiple of the smaller unit of x and s, and at most s / 2 (1 + 2^-15).)
+// to a border, its neighbour. The remainder x - k s, which one fma gives exactly, says which: k is right if its double is smaller than s in
+// size, or equal and k even. (Exactly: the remainder is a multiple of the smaller unit of x and s, and at most s / 2 (1 + 2^-15). It is
+// doubled, and not s halved: half of a scale below 2^-125 may be no float32.)
 // Borders are no rare case in 16-bit types, whose x 127 / max are often half a whole number but for the rounding of s: the
 // test of a vector costs one operation an element, mending it seven more.
 constexpr float kMagic8 = 12582912.f;
@@ -156,9 +157,11 @@ __device__ inline Code8 code8(float x, float s, float r, float& far) {
   far = fmaxf(far, fabsf(rem));
   return {u, rem};
 }
-__device__ inline void mend8(Code8& c, float half) {
-  // |rem| > half, or equal where k is odd: by their bits
-  const bool off = (__float_as_uint(c.rem) & 0x7FFFFFFFu) + (__float_as_uint(c.u) & 1u) > __float_as_uint(half);
+// Whether a vector holds an element at a border or past it, from the largest of its remainders.
+__device__ inline bool border8(float far, float s) { return far + far >= s; }
+__device__ inline void mend8(Code8& c, float s) {
+  // 2 |rem| > s, or equal where k is odd: by their bits
+  const bool off = (__float_as_uint(c.rem + c.rem) & 0x7FFFFFFFu) + (__float_as_uint(c.u) & 1u) > __float_as_uint(s);
   c.u += off ? copysignf(1.f, c.rem) : 0.f;
 }
 __device__ inline u32 bytes4(float a, float b, float c, float d) {
@@ -169,14 +172,13 @@ __device__ inline u32 bytes4(float a, float b, float c, float d) {
 
 // Eight codes of v[0..7], in order.
 __device__ inline v2u codes8x8(const float (&v)[8], const Scale8& q) {
-  const float half = 0.5f * q.s;
   Code8 c[8];
   float far = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; k++) c[k] = code8(v[k], q.s, q.r, far);
-  if (__builtin_amdgcn_ballot_w64(far >= half)) {
+  if (__builtin_amdgcn_ballot_w64(border8(far, q.s))) {
 #pragma unroll
-    for (int k = 0; k < 8; k++) mend8(c[k], half);
+    for (int k = 0; k < 8; k++) mend8(c[k], q.s);
   }
   const v2u w = {bytes4(c[0].u, c[1].u, c[2].u, c[3].u), bytes4(c[4].u, c[5].u, c[6].u, c[7].u)};
   return q.r == 0.f ? v2u{0, 0} : w;

@@ -246,14 +246,14 @@ __global__ __launch_bounds__(256) void k_i8_cols(I8QuantParams p, const float* r
     const Vec8<MxF32> rv = load8<MxF32>(recip, c, p.C), sv = load8<MxF32>(p.cols.scales, c, p.C);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const float r = elem<MxF32>(rv, j), s = elem<MxF32>(sv, j), half = 0.5f * s;
+      const float r = elem<MxF32>(rv, j), s = elem<MxF32>(sv, j);
       Code8 q[4];
       float far = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; i++) q[i] = code8(elem<DT>(v[i], j), s, r, far);
-      if (__builtin_amdgcn_ballot_w64(far >= half)) {
+      if (__builtin_amdgcn_ballot_w64(border8(far, s))) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) mend8(q[i], half);
+        for (int i = 0; i < 4; i++) mend8(q[i], s);
       }
       words[lc * 132 + 16 * j + rg] = r == 0.f ? 0u : bytes4(q[0].u, q[1].u, q[2].u, q[3].u);
     }

@@ -140,6 +140,51 @@ def test_codes_next_to_a_border():
     _check_tensor(R.int8_quantize(torch.from_numpy(np.ascontiguousarray(x.T)).to(dev()), axis=0), x.astype(np.float64))
 
 
+def _smallest_scales(dtype):
+    """[90, 382] values whose rows' scales fill [2^-126, 2^-124): those next to every border between two codes, and the row's largest. (Half
+    of such a scale may be no float32.)"""
+    rng = np.random.default_rng(31)
+    step = {"f32": 2.0**-23, "bf16": 2.0**-7}[dtype]
+    most = np.concatenate([127 * (1 + rng.random(60)) * 2.0**-126, 127 * (1 + rng.random(20)) * 2.0**-125,
+                           127 * 2.0**-126 * (1 + step * np.arange(9)), [2.0**-119]])
+    most = _gpu(most, dtype)
+    s = (_np(most) / 127).astype(np.float32)
+    t = _gpu((np.arange(127) + 0.5) * s[:, None].astype(np.float64), dtype)
+    x = torch.cat([t, torch.nextafter(t, t * 0), -torch.nextafter(t, t + 1), most[:, None]], 1)
+    x = torch.minimum(x.abs(), x[:, -1:]) * torch.where(x < 0, -1, 1)
+    x[0, :-1:2] = x[0, -1:] / 2
+    return x.to(TD[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_codes_next_to_a_border_of_the_smallest_scales(dtype):
+    x = _smallest_scales(dtype)
+    want = _np(x)
+    s = X.quantize(want)[1]
+    assert (s >= 2.0**-126).all() and (s < 2.0**-124).all() and ((s > 2.0**-126) & (s < 2.0**-125)).sum() >= 60
+    both = R.int8_quantize(x, axis=None)
+    _check_tensor(both[0], want)
+    _check_tensor(both[1], want.T)
+    _check_tensor(R.int8_quantize(x), want)
+    _check_tensor(R.int8_quantize(x.t().contiguous(), axis=0), want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_codes_of_the_smallest_scales_in_a_norm_and_a_product(dtype):
+    x = _smallest_scales(dtype)
+    want = _np(x)
+    # a norm's output is its bias where the weight is zero
+    z = torch.randn(3, x.shape[1], device=x.device, dtype=x.dtype)
+    for r in range(0, x.shape[0], 7):
+        _check_tensor(R.layer_norm(z, torch.zeros_like(x[r]), x[r], quantize="int8"), np.tile(want[r], (3, 1)))
+    # times 127 I the codes come back, rounded once
+    eye = R.int8_quantize(127 * torch.eye(x.shape[1], device=x.device))
+    codes, s = X.quantize(want)
+    y = (127.0 * codes * s[:, None].astype(np.float64)).astype(np.float32)
+    for M in (1, 2, 40, 90):
+        assert np.array_equal(R.int8_matmul(x[:M].float(), eye).cpu().numpy(), y[:M])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_infinities_and_nan_poison_their_row_alone(dtype):
     x = np.random.default_rng(8).standard_normal((70, 300))
