@@ -107,6 +107,46 @@ __device__ inline void fit8(Vec8<DT>& v, int64_t c, int64_t K, u32 past = 0) {
   }
 }
 
+// The same with elements of the row in the places past its end, for what a product with 0 must take back out: they are infinite or NaN
+// only if the row's own are.
+template <class DT>
+__device__ inline void turn8(Vec8<DT>& v, int64_t c, int64_t K) {
+  if (!__builtin_amdgcn_ballot_w64(c + 8 > K)) return;
+  const int s = c + 8 <= K ? 0 : (int)(c + 8 - K) & 7;  // elements to turn by
+  constexpr int W = DT::size * 2, E = W / 4;
+  u32 first[E];
+#pragma unroll
+  for (int k = 0; k < W / 2; k++) {
+    const u32 low = v.w[k];
+    v.w[k] = s & 4 ? v.w[k + W / 2] : low;
+    v.w[k + W / 2] = s & 4 ? low : v.w[k + W / 2];
+  }
+#pragma unroll
+  for (int k = 0; k < E; k++) first[k] = v.w[k];
+#pragma unroll
+  for (int k = 0; k < W; k++) v.w[k] = s & 2 ? (k + E < W ? v.w[(k + E) % W] : first[(k + E) % E]) : v.w[k];
+  first[0] = v.w[0];
+#pragma unroll
+  for (int k = 0; k < W; k++) {
+    const u32 up = k + 1 < W ? v.w[(k + 1) % W] : first[0];
+    v.w[k] = s & 1 ? (DT::size == 4 ? up : (v.w[k] >> 16) | (up << 16)) : v.w[k];
+  }
+}
+// And of a vector of which the first n elements, one at least, are the row's.
+template <class DT>
+__device__ inline void repeat8(Vec8<DT>& v, int64_t n) {
+  if (n >= 8) return;
+  const u32 first = DT::size == 4 ? v.w[0] : v.w[0] & 0xFFFFu;
+#pragma unroll
+  for (int q = 1; q < 8; q++) {
+    if (q < n) continue;
+    if constexpr (DT::size == 4)
+      v.w[q] = first;
+    else
+      v.w[q >> 1] = q & 1 ? (v.w[q >> 1] & 0xFFFFu) | (first << 16) : (v.w[q >> 1] & 0xFFFF0000u) | first;
+  }
+}
+
 // Elements [c, c + 8) of a row of K.
 template <class DT>
 __device__ inline void store8(typename DT::T* row, int64_t c, int64_t K, const float (&v)[8]) {

@@ -258,7 +258,8 @@ struct GradRow {
   Vec8<DT> dy, x;
 };
 
-// T threads share a row of eight elements or more, NV times eight columns each, the same ones in every row that the block takes. AHEAD: the
+// T threads share a row of eight elements or more, NV times eight columns each, the same ones in every row that the block takes; only the last
+// of a thread's vectors may pass the row's end (K > 8 T (NV - 1)). AHEAD: the
 // next row is requested before this one is worked on; with four vectors a thread it has no room (4096 x 16384 bf16 97 us without, 108
 // with, float32 179 and 243; two vectors of 1024 threads, which have half the registers, 130 and 286).
 template <class DT, int T, int NV, bool AHEAD>
@@ -295,8 +296,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradParams 
     float c1 = 0.f, c2 = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; j++) {
-      fit8<DT>(cur[j].dy, (int64_t)(j * T + t) * 8, p.K);
-      fit8<DT>(cur[j].x, (int64_t)(j * T + t) * 8, p.K);
+      if (j == NV - 1) {
+        fit8<DT>(cur[j].dy, (int64_t)(j * T + t) * 8, p.K);
+        turn8<DT>(cur[j].x, (int64_t)(j * T + t) * 8, p.K);  // not zeros: (0 - mean) rstd may be infinite, and 0 times it NaN
+      }
 #pragma unroll
       for (int k = 0; k < 8; k++) {
         const float dy = elem<DT>(cur[j].dy, k), xh = (elem<DT>(cur[j].x, k) - mean) * rstd, g = dy * w[j][k];
@@ -380,7 +383,9 @@ __global__ __launch_bounds__(1024) void k_norm_grad_long(NormGradParams p) {
     const float mean = p.mean[row], rstd = p.rstd[row];
     float c1 = 0.f, c2 = 0.f;
     for (int64_t c = (int64_t)t * 8; c < p.K; c += 8192) {
-      const Vec8<DT> a = load8<DT>(dy, c, p.K), b = load8<DT>(x, c, p.K);
+      const Vec8<DT> a = load8<DT>(dy, c, p.K);
+      Vec8<DT> b = load8<DT>(x, c, p.K);
+      repeat8<DT>(b, p.K - c);
       float w[8];
       param8<DT>(w, p.weight, p.param_f32, c, p.K, 1.f);
 #pragma unroll

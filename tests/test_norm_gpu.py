@@ -214,6 +214,25 @@ def test_layer_norm_backward(M, K, dtype, params):
         assert all(a is b or torch.equal(a, b) for a, b in zip(R.layer_norm_backward(dy, x, mean, rstd, weight), got))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [3, 40, 512, 1001, 2731, 5003, 9001, 13001, 17003])
+def test_backward_of_rows_whose_mean_times_rstd_is_infinite(K, dtype):
+    """Constant rows far from zero: x - mean is 0 in them, and what lies past a row's end must not count as if it were x = 0."""
+    rng = np.random.default_rng(K)
+    x, w, _ = _inputs(rng, 9, K, dtype, "f32")
+    x[2], x[7] = 2e36, -2e36
+    dy = _gpu(rng.standard_normal((9, K)), dtype)
+    _, mean, rstd = R.layer_norm(x, save=True)
+    assert (mean.abs() * rstd)[[2, 7]].isinf().all()
+    for weight in (w, None):
+        got = R.layer_norm_backward(dy, x, mean, rstd, weight)
+        nw = None if weight is None else _np(weight)
+        refs = X.layer_norm_grad(_np(dy), _np(x), _np(mean), _np(rstd), nw)
+        for g, ref, bound in zip(got, refs, _grad_bounds(_np(dy), _np(x), _np(mean), _np(rstd), nw, refs, dtype, "f32")):
+            if g is not None:
+                assert (np.abs(_np(g) - ref) <= bound).all()
+
+
 def test_backward_against_differences():
     """The loss sum(dy y) moves as the gradients say: central differences of the float64 oracle at the inputs of the call. Their error is
     h^2 / 6 of the third derivative (a few units here) plus 2^-52 / h of the loss's terms; the call adds float32 roundings."""
