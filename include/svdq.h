@@ -552,7 +552,8 @@ int svdq_layer_norm_mx(const void* x, int64_t ldx, int64_t M, int64_t K, const v
  * svdq_layer_norm_backward — the backward pass, with xh = (x - mean) rstd and g = dy weight (dy without one):
  *   dx = rstd (g - mean over the row of g - xh times the mean over the row of g xh),
  *   dweight = sum over the rows of dy xh, dbias = sum over the rows of dy,
- * in float32, rounded once. dy, x, dx: [M, K] of dtype with row strides >= K; mean, rstd: as the forward call left them;
+ * in float32, rounded once; the sums over the rows in float32 over groups of them, none through more than 1030 additions (below 2^28
+ * rows), the groups in binary64. dy, x, dx: [M, K] of dtype with row strides >= K; mean, rstd: as the forward call left them;
  * weight: [K] of param_dtype (dtype or SVDQ_F32) or NULL; dweight, dbias: [K] of param_dtype, given with a weight and NULL
  * without. workspace: svdq_layer_norm_backward_workspace_bytes, params whether a weight is given.
  * Errors: EINVAL, EDTYPE, EHIP.

@@ -11,7 +11,7 @@
 //
 // Backward: with xh = (x - mean) rstd and g = dy weight, dx = rstd (g - mean(g) - xh mean(g xh)): one reduction, with dy and x in
 // registers. A thread keeps the same columns in every row of its block, so dweight = sum dy xh and dbias = sum dy are running sums
-// in registers; each block leaves its own, and a second kernel adds them in the blocks' order. Memory bounds it: 8192 x 8192 bf16 76 us (5.3
+// in registers, over 1024 rows at most; each block leaves its own, and a last kernel adds them in binary64 in the blocks' order. Memory bounds it: 8192 x 8192 bf16 76 us (5.3
 // TB/s) and 5 for the second kernel.
 #include <type_traits>
 
@@ -447,27 +447,36 @@ __global__ __launch_bounds__(256) void k_norm_grad_cols(NormGradParams p, float*
   }
 }
 
-// The blocks' sums, added in their order by 16 waves: 64 columns a block.
+// The blocks' sums, added by 16 waves: four at a time in float32, these in binary64 (each alone takes 0.3 us more of 4.5 with 512 parts, for its
+// conversions). 64 columns a block.
 template <class DT>
 __global__ __launch_bounds__(1024) void k_norm_join(const float* part, int parts, int64_t K, void* dweight, void* dbias) {
   typedef typename DT::T E;
-  __shared__ float sum[16][2][64];
+  __shared__ double sum[16][2][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t col = (int64_t)blockIdx.x * 64 + lane, c = col < K ? col : K - 1;
-  float a = 0.f, b = 0.f;
-#pragma unroll 4
-  for (int k = wave; k < parts; k += 16) {
-    a += part[(int64_t)(2 * k) * K + c];
-    b += part[(int64_t)(2 * k + 1) * K + c];
+  double a = 0, b = 0;
+  for (int k = wave; k < parts; k += 64) {
+    float u[4], v[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const float* at = part + (int64_t)min(k + 16 * i, parts - 1) * 2 * K + c;
+      u[i] = at[0], v[i] = at[K];
+    }
+#pragma unroll
+    for (int i = 1; i < 4; i++)
+      if (k + 16 * i >= parts) u[i] = v[i] = 0.f;
+    a += (double)((u[0] + u[1]) + (u[2] + u[3]));
+    b += (double)((v[0] + v[1]) + (v[2] + v[3]));
   }
   sum[wave][0][lane] = a;
   sum[wave][1][lane] = b;
   __syncthreads();
   if (wave > 1 || col >= K) return;
-  float s = 0.f;
+  double s = 0;
 #pragma unroll
   for (int w = 0; w < 16; w++) s += sum[w][wave][lane];
-  reinterpret_cast<E*>(wave ? dbias : dweight)[col] = DT::store(s);
+  reinterpret_cast<E*>(wave ? dbias : dweight)[col] = DT::store((float)s);
 }
 
 }  // namespace dev
@@ -531,11 +540,17 @@ hipError_t launch_norm(const NormParams& p, int dtype, hipStream_t stream) {
 // Rows whose columns a block's threads do not keep: longer than their registers, or shorter than a vector.
 static bool apart(int64_t K) { return K > 16384 || K < 8; }
 
-// Blocks (or strips of rows) that leave a part of dweight and dbias each.
-static int64_t grad_parts(int64_t M, int64_t K) {
+// Rows that a wave adds up in float32, at most (more only where a grid would pass 65535 strips: 2^28 rows). A longer chain's error grows with
+// the rows.
+constexpr int64_t kChain = 1024;
+
+// Blocks of a launch (or strips of rows) that leave a part of dweight and dbias each.
+static int64_t grad_blocks(int64_t M, int64_t K) {
   if (apart(K)) {
     int64_t strips = (M + 15) / 16;
     if (strips > 64) strips = 64;
+    const int64_t least = (M + 4 * kChain - 1) / (4 * kChain);
+    if (strips < least) strips = least < 65535 ? least : 65535;
     const int64_t rows = (M + strips - 1) / strips;
     return (M + rows - 1) / rows;
   }
@@ -547,13 +562,33 @@ static int64_t grad_parts(int64_t M, int64_t K) {
   return parts;
 }
 
+// Launches, of as many rows each. (As many more blocks in one launch instead: its last round does not fill the chip, 600000 x 4096 bf16 3.0 to
+// 3.7 ms and in three launches 2.7. Parts that a block leaves on its way: the kernel's registers, 122 of them spilled in rows of 16384.)
+static int64_t grad_runs(int64_t M, int64_t K) {
+  if (apart(K)) return 1;
+  const int64_t most = grad_blocks(M, K) * (K <= 512 ? 4 : 1) * kChain;
+  return (M + most - 1) / most;
+}
+static int64_t grad_parts(int64_t M, int64_t K) { return grad_blocks(M, K) * grad_runs(M, K); }
+
 size_t norm_grad_bytes(int64_t M, int64_t K, bool params) { return params ? (size_t)(grad_parts(M, K) * 2 * K * 4 + 255) / 256 * 256 : 0; }
 
 bool norm_grad_fits(int64_t K) { return mx_fits_grid((K + 63) / 64, 1024); }
 
 template <class DT, int T, int NV, bool AHEAD = true>
 static void launch_grad(const NormGradParams& p, float* part, hipStream_t stream) {
-  k_norm_grad<DT, T, NV, AHEAD><<<(unsigned)grad_parts(p.M, p.K), T < 256 ? 256 : T, 0, stream>>>(p, part);
+  const int64_t blocks = grad_blocks(p.M, p.K), runs = grad_runs(p.M, p.K), rows = (p.M + runs - 1) / runs;
+  for (int64_t k = 0; k < runs; k++) {
+    const int64_t r = k * rows;
+    NormGradParams q = p;
+    q.dy = reinterpret_cast<const typename DT::T*>(p.dy) + r * p.lddy;
+    q.x = reinterpret_cast<const typename DT::T*>(p.x) + r * p.ldx;
+    q.dx = reinterpret_cast<typename DT::T*>(p.dx) + r * p.lddx;
+    q.mean = p.mean + r;
+    q.rstd = p.rstd + r;
+    q.M = rows < p.M - r ? rows : p.M - r;
+    k_norm_grad<DT, T, NV, AHEAD><<<(unsigned)blocks, T < 256 ? 256 : T, 0, stream>>>(q, part ? part + k * blocks * 2 * p.K : nullptr);
+  }
 }
 
 template <class DT>

@@ -81,7 +81,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor | None = None):
     """(dx [M, K], dweight [K], dbias [K]) of y = layer_norm(x, weight, bias) from dy [M, K], with the mean and rstd that it saved:
     with xh = (x - mean) rstd and g = dy weight, dx = rstd (g - mean of g - xh times the mean of g xh) over each row, dweight the
-    sum of dy xh and dbias the sum of dy over the rows, in weight's dtype (None without a weight). Sums are float32."""
+    sum of dy xh and dbias the sum of dy over the rows, in weight's dtype (None without a weight). A row's sums are float32, those over
+    the rows float32 in groups, through 1030 additions at most, and float64 from there."""
     dt = _matrix(dy, "dy")
     _matrix(x, "x")
     if dy.shape != x.shape or dy.dtype != x.dtype:

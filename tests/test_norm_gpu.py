@@ -233,6 +233,19 @@ def test_backward_of_rows_whose_mean_times_rstd_is_infinite(K, dtype):
                 assert (np.abs(_np(g) - ref) <= bound).all()
 
 
+@pytest.mark.parametrize("M,K,c", [(1 << 25, 8, 1 + 2.0**-11 - 2.0**-23), (7_000_000, 520, 1 + 2.0**-11 - 2.0**-23), (1 << 25, 4, 1 + 2.0**-9 - 2.0**-23),
+                                   (1 << 20, 4100, 1 + 2.0**-12 - 2.0**-23), (3_000_001, 2, 1 + 2.0**-11 - 2.0**-23)])
+def test_sums_over_many_rows(M, K, c):
+    """dy = c and xh = 1: a running sum of some thousand c rounds every addition to the same side. No sum goes through more than 1030
+    float32 additions, and the result is rounded once."""
+    dy, x = torch.full((M, K), c, device=dev()), torch.ones(M, K, device=dev())
+    rstd, w = torch.ones(M, device=dev()), torch.ones(K, device=dev())
+    _, dw, db = R.layer_norm_backward(dy, x, torch.zeros_like(rstd), rstd, w)
+    want = M * float(dy[0, 0])
+    for g in (dw, db):
+        assert bool(((g.double() - want).abs() <= 1032 * 2.0**-24 * want).all())
+
+
 def test_backward_against_differences():
     """The loss sum(dy y) moves as the gradients say: central differences of the float64 oracle at the inputs of the call. Their error is
     h^2 / 6 of the third derivative (a few units here) plus 2^-52 / h of the loss's terms; the call adds float32 roundings."""
