@@ -521,8 +521,8 @@ int svdq_i8_linear(const void* x, int64_t M, int64_t K, int64_t sr, int64_t sc, 
 /* --------------------------------------------------------------------------------------
  * svdq_i8_backward — the backward pass of y = Q(x) Q(w^T)^T + b with w [K, N] in one call: Q(dy) and Q(dy^T) of dy [M, N] (row
  * stride lddy >= N, of dtype) into the workspace, then dx = Q(dy) Q(w)^T [M, K] and dw = Q(x^T) Q(dy^T)^T [K, N] by
- * svdq_i8_matmul, with the same results, and db [N] = the sums of dy's columns (summed in float32 over strips of
- * rows, the strips in binary64), unless db is NULL. w_codes / w_scales: w quantised along its rows; x_codes / x_scales: x^T,
+ * svdq_i8_matmul, with the same results, and db [N] = the sums of dy's columns (in float32 over groups of rows, none through more than 1030
+ * additions below 2^28 rows, the groups in binary64), unless db is NULL. w_codes / w_scales: w quantised along its rows; x_codes / x_scales: x^T,
  * [K, M], the input quantised along its columns. out_dtype: of dx, dw and db. M and N are at most 2^26.
  * workspace: svdq_i8_backward_workspace_bytes. Errors: EINVAL, EDTYPE, EHIP.
  * ------------------------------------------------------------------------------------ */

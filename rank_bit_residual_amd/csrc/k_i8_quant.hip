@@ -357,6 +357,10 @@ static int shared_threads(int64_t C) {
   return Kp <= 2048 ? 256 : (Kp <= 8192 ? 512 : 1024);
 }
 
+// Rows that a thread adds up in float32, at most (more only where a grid would pass 65535 strips: 2^28 rows). A longer chain's error grows with
+// the rows.
+constexpr int64_t kChain = 1024;
+
 // Strips of rows that a column's maximum is taken over. Read with the rows (`shared`): 256, so that every compute unit has one; more where that
 // leaves each enough rows to be worth its part's way through memory, up to as many as the chip holds at once (8192 x 12288 bf16 in 128, 256, 512
 // strips 140, 81 and 89 us; 777 x 5003 12.9, 10.5 and 12.6; with the join and the codes 4096 x 5000 float32 in 256 and 512 51.5 and 54.5, 2048 x
@@ -374,9 +378,15 @@ static int64_t strips_of(int64_t R, int64_t C, bool shared) {
   const int64_t most = (R + 15) / 16;
   if (strips > most) strips = most;
   if (strips > 256) strips = 256;
+  const int64_t least = (R + 4 * kChain - 1) / (4 * kChain);
+  if (strips < least) strips = least < 65535 ? least : 65535;
   const int64_t rows = (R + strips - 1) / strips;
   return (R + rows - 1) / rows;
 }
+
+// Launches that leave so many strips each, of rows read once for their codes, maxima and sums: no sum over more than kChain rows. (More
+// strips in one launch instead: 600000 x 4096 bf16 3.6 ms, not 3.3.)
+static int64_t runs_of(int64_t R, int64_t strips) { return (R + strips * kChain - 1) / (strips * kChain); }
 
 static int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -391,7 +401,10 @@ size_t i8_quantize_bytes(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows
     const bool k = rows;
     R = C, C = r, sr = sc, sc = s, rows = cols, cols = k;
   }
-  return cols ? (size_t)(round256(C * 4) + 2 * round256(strips_of(R, C, shares(C, sc, rows)) * C * 4)) : 0;
+  if (!cols) return 0;
+  const bool shared = shares(C, sc, rows);
+  const int64_t strips = strips_of(R, C, shared), parts = shared ? strips * runs_of(R, strips) : strips;
+  return (size_t)(round256(C * 4) + 2 * round256(parts * C * 4));
 }
 
 bool i8_quantize_fits(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows, bool cols) {
@@ -401,8 +414,16 @@ bool i8_quantize_fits(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows, b
 
 template <class DT, int T, int NV>
 static void launch_shared(const I8QuantParams& p, int64_t strips, u32* part, float* sums, hipStream_t stream) {
+  const int64_t runs = runs_of(p.R, strips), rows = ((p.R + runs - 1) / runs + 15) / 16 * 16;  // whole tiles of codes
   if (p.sums)
-    k_i8_rows<DT, T, NV, ROWS_MAXIMA_AND_SUMS><<<(unsigned)strips, T, 0, stream>>>(p, part, sums);
+    for (int64_t k = 0; k < runs; k++) {
+      I8QuantParams q = p;
+      q.x = reinterpret_cast<const typename DT::T*>(p.x) + k * rows * p.sr;
+      q.rows.codes += k * (rows >> 4) * p.rows.kq * 1024;
+      q.rows.scales += k * rows;
+      q.R = min(rows, p.R - k * rows);
+      k_i8_rows<DT, T, NV, ROWS_MAXIMA_AND_SUMS><<<(unsigned)strips, T, 0, stream>>>(q, part + k * strips * p.C, sums + k * strips * p.C);
+    }
   else
     k_i8_rows<DT, T, NV, ROWS_AND_MAXIMA><<<(unsigned)strips, T, 0, stream>>>(p, part, sums);
 }
@@ -413,7 +434,8 @@ static hipError_t cols_t(const I8QuantParams& p, hipStream_t stream) {
   const int64_t strips = strips_of(p.R, p.C, shared);
   float* recip = reinterpret_cast<float*>(p.workspace);
   u32* part = reinterpret_cast<u32*>((uint8_t*)p.workspace + round256(p.C * 4));
-  float* sums = reinterpret_cast<float*>((uint8_t*)part + round256(strips * p.C * 4));
+  const int64_t parts = shared && p.sums ? strips * runs_of(p.R, strips) : strips;
+  float* sums = reinterpret_cast<float*>((uint8_t*)part + round256(parts * p.C * 4));
   if (shared) {
     switch (shared_threads(p.C)) {
       case 256: launch_shared<DT, 256, 1>(p, strips, part, sums, stream); break;
@@ -437,13 +459,13 @@ static hipError_t cols_t(const I8QuantParams& p, hipStream_t stream) {
   }
   const unsigned joins = (unsigned)((p.C + 63) / 64);
   if (!p.sums)
-    k_i8_colscale<MxF32, false><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, nullptr);
+    k_i8_colscale<MxF32, false><<<joins, 1024, 0, stream>>>(part, sums, (int)parts, p.C, p.cols.scales, recip, nullptr);
   else if (p.sums_dtype == SVDQ_F32)
-    k_i8_colscale<MxF32, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (float*)p.sums);
+    k_i8_colscale<MxF32, true><<<joins, 1024, 0, stream>>>(part, sums, (int)parts, p.C, p.cols.scales, recip, (float*)p.sums);
   else if (p.sums_dtype == SVDQ_BF16)
-    k_i8_colscale<MxBF16, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (uint16_t*)p.sums);
+    k_i8_colscale<MxBF16, true><<<joins, 1024, 0, stream>>>(part, sums, (int)parts, p.C, p.cols.scales, recip, (uint16_t*)p.sums);
   else
-    k_i8_colscale<MxF16, true><<<joins, 1024, 0, stream>>>(part, sums, (int)strips, p.C, p.cols.scales, recip, (uint16_t*)p.sums);
+    k_i8_colscale<MxF16, true><<<joins, 1024, 0, stream>>>(part, sums, (int)parts, p.C, p.cols.scales, recip, (uint16_t*)p.sums);
   // the transpose's stages come in pairs, so the last tile of rows may hold nothing but padding
   const int64_t tiles_c = (p.C + 127) / 128, tiles = (int64_t)p.cols.kq * tiles_c;
   k_i8_cols<DT><<<blocks_of(tiles), 256, 0, stream>>>(p, recip, tiles_c, tiles);

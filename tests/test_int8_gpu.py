@@ -411,6 +411,31 @@ def test_backward(dtype, M, N, K):
     assert all(torch.equal(p, q) for p, q in zip(R.int8_backward(room[:, 2: N + 2], wr, xc, bias=True), (dx, dw, db)))
 
 
+@pytest.mark.parametrize("M,N,c", [(1 << 25, 8, 1 + 2.0**-10 - 2.0**-23), (1 << 25, 4, 1 + 2.0**-10 - 2.0**-23), (1 << 23, 600, 1 + 2.0**-12 - 2.0**-23),
+                                   (1 << 22, 2, 1 + 2.0**-14 - 2.0**-23)])
+def test_sums_over_many_rows(M, N, c):
+    """dy = c: a running sum of some thousand c rounds every addition to the same side. No sum goes through more than 1030 float32
+    additions, and the result is rounded once."""
+    dy = torch.full((M, N), c, device=dev())
+    w, xc = R.int8_quantize(torch.ones(1, N, device=dev())), R.int8_quantize(torch.ones(1, M, device=dev()))
+    want = M * float(dy[0, 0])
+    db = R.int8_backward(dy, w, xc, bias=True)[2]
+    assert bool(((db.double() - want).abs() <= 1031 * 2.0**-24 * want).all())
+
+
+def test_backward_of_more_rows_than_a_launch_sums():
+    """270000 rows of 8200 are read in two launches, whose codes, scales and maxima make one tensor of each direction."""
+    M, N, K = 270_000, 8200, 3
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(80)
+    dy = torch.randn(M, N, generator=gen, device=dev(), dtype=torch.bfloat16)
+    wr, xc = (R.int8_quantize(torch.randn(K, n, generator=gen, device=dev())) for n in (N, M))
+    dx, dw, db = R.int8_backward(dy, wr, xc, bias=True)
+    assert torch.equal(dx, R.int8_matmul(R.int8_quantize(dy), wr)) and torch.equal(dw, R.int8_matmul(xc, R.int8_quantize(dy, axis=0)))
+    want, size = (sum(f(dy[k: k + 30_000].double()).sum(0) for k in range(0, M, 30_000)) for f in (lambda t: t, torch.abs))
+    assert bool(((db.double() - want).abs() <= 1031 * 2.0**-24 * size + STEP["bf16"] * 1.01 * want.abs()).all())
+
+
 BACKWARD_SIZES = {(512, 512, 2048): (64, 64), (700, 700, 1100): (64, 64), (10, 300, 500): (64, 64), (2000, 500, 4000): (64, 128),
                   (515, 1440, 2731): (64, 128), (800, 800, 8000): (64, 128), (3000, 1000, 5000): (128, 128), (1024, 4096, 1024): (128, 128),
                   (2048, 4096, 4096): (256, 256), (4096, 2000, 8190): (256, 256), (16, 4096, 12288): (0, 0), (1000, 100, 12000): (0, 0)}  # M, K, N: the tiles that both products share
