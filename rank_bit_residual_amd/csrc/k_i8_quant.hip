@@ -351,10 +351,11 @@ static hipError_t rows_t(const I8QuantParams& p, hipStream_t stream) {
 constexpr int64_t kSharedRow = 16384;
 
 // Threads of a block of the kernel for both: a vector a thread, two past 4096 columns (8192 x 8192 bf16 in 512 threads of two 45 us, in 1024 of
-// one 61; float32, whose registers do not hold two and their sums, 91 and 79: it takes 1024 of one).
-static int shared_threads(int64_t C) {
+// one 61; float32, whose registers do not hold two and their sums, 91 and 79: it takes 1024 of one). size: of an element.
+static int shared_threads(int64_t C, int size) {
   const int64_t Kp = i8_kq(C) * 64;
-  return Kp <= 2048 ? 256 : (Kp <= 8192 ? 512 : 1024);
+  if (Kp <= 2048) return 256;
+  return Kp <= (size == 2 ? 8192 : 4096) ? 512 : 1024;
 }
 
 // Rows that a thread adds up in float32, at most (more only where a grid would pass 65535 strips: 2^28 rows). A longer chain's error grows with
@@ -364,11 +365,14 @@ constexpr int64_t kChain = 1024;
 // Strips of rows that a column's maximum is taken over. Read with the rows (`shared`): 256, so that every compute unit has one; more where that
 // leaves each enough rows to be worth its part's way through memory, up to as many as the chip holds at once (8192 x 12288 bf16 in 128, 256, 512
 // strips 140, 81 and 89 us; 777 x 5003 12.9, 10.5 and 12.6; with the join and the codes 4096 x 5000 float32 in 256 and 512 51.5 and 54.5, 2048 x
-// 5000 f16 26.2 and 26.7). Alone: enough blocks for the chip, of 16 rows or more.
-static int64_t strips_of(int64_t R, int64_t C, bool shared) {
+// 5000 f16 26.2 and 26.7). 1024 threads fill a unit, but those that keep one float32 vector's maxima leave room for a second block, which pays
+// where a quarter of them or more has no columns (both ways in 256 and 512 strips: 20000 x 4300 202 and 178, 16384 x 6000 226 and 213, 8192 x 7000 124
+// and 127, 8192 x 8192 143 and 152; with sums 8192 x 5000 122 and 130). Alone: enough blocks for the chip, of 16 rows or more.
+static int64_t strips_of(int64_t R, int64_t C, bool shared, int size, bool sums) {
   int64_t strips;
   if (shared) {
-    const int64_t most = 256 * 1024 / shared_threads(C), rows = i8_kq(C) <= 64 ? 4 : 16;  // of a strip, at least
+    const bool two = size == 4 && !sums && i8_kq(C) * 64 <= 6144;
+    const int64_t most = 256 * 1024 / shared_threads(C, two ? 2 : size), rows = i8_kq(C) <= 64 ? 4 : 16;  // of a strip, at least
     strips = R / rows < most ? R / rows : most;
     if (strips < 256) strips = R < 256 ? R : 256;
     return strips;
@@ -403,7 +407,8 @@ size_t i8_quantize_bytes(int64_t R, int64_t C, int64_t sr, int64_t sc, bool rows
   }
   if (!cols) return 0;
   const bool shared = shares(C, sc, rows);
-  const int64_t strips = strips_of(R, C, shared), parts = shared ? strips * runs_of(R, strips) : strips;
+  // 16-bit elements have as many strips as float32 ones, or more
+  const int64_t strips = strips_of(R, C, shared, 2, true), parts = shared ? strips * runs_of(R, strips) : strips;
   return (size_t)(round256(C * 4) + 2 * round256(parts * C * 4));
 }
 
@@ -431,23 +436,29 @@ static void launch_shared(const I8QuantParams& p, int64_t strips, u32* part, flo
 template <class DT>
 static hipError_t cols_t(const I8QuantParams& p, hipStream_t stream) {
   const bool shared = shares(p.C, p.sc, p.rows.codes != nullptr);
-  const int64_t strips = strips_of(p.R, p.C, shared);
+  const int64_t strips = strips_of(p.R, p.C, shared, DT::size, p.sums != nullptr);
   float* recip = reinterpret_cast<float*>(p.workspace);
   u32* part = reinterpret_cast<u32*>((uint8_t*)p.workspace + round256(p.C * 4));
   const int64_t parts = shared && p.sums ? strips * runs_of(p.R, strips) : strips;
   float* sums = reinterpret_cast<float*>((uint8_t*)part + round256(parts * p.C * 4));
   if (shared) {
-    switch (shared_threads(p.C)) {
+    switch (shared_threads(p.C, DT::size)) {
       case 256: launch_shared<DT, 256, 1>(p, strips, part, sums, stream); break;
       case 512:
-        if (p.rows.kq <= 64)
-          launch_shared<DT, 512, 1>(p, strips, part, sums, stream);
-        else if constexpr (DT::size == 2)
-          launch_shared<DT, 512, 2>(p, strips, part, sums, stream);
-        else
-          launch_shared<DT, 1024, 1>(p, strips, part, sums, stream);
+        if constexpr (DT::size == 2)
+          if (p.rows.kq > 64) {
+            launch_shared<DT, 512, 2>(p, strips, part, sums, stream);
+            break;
+          }
+        launch_shared<DT, 512, 1>(p, strips, part, sums, stream);
         break;
-      default: launch_shared<DT, 1024, 2>(p, strips, part, sums, stream);
+      default:
+        if constexpr (DT::size == 4)
+          if (p.rows.kq <= 128) {
+            launch_shared<DT, 1024, 1>(p, strips, part, sums, stream);
+            break;
+          }
+        launch_shared<DT, 1024, 2>(p, strips, part, sums, stream);
     }
   } else {
     const int64_t strip_rows = (p.R + strips - 1) / strips;
