@@ -5,6 +5,7 @@ float32(sa sb), each off by half a step, plus the bias with one rounding, then t
 2^-23 |S sa sb| + (2^-24 + STEP) |y|, and a small multiple of the smallest magnitude below the normal range.
 """
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -299,6 +300,19 @@ def test_every_form_is_met():
         assert {(64, 64), (64, 128), (128, 128)} <= {f[:2] for f in forms if (f[2] > 1) == shared}
 
 
+@pytest.mark.parametrize("M,K,N", [(1024, 65536, 1024), (199, 53501, 4423), (700, 90001, 900)])
+def test_matmul_exact_in_shares_of_the_largest_tiles(M, K, N):
+    assert _form(M, N, K)[:2] == (256, 256) and _form(M, N, K)[2] > 1
+    a, b = _exact_sums(M, K, N, M + K + N)
+    ref = (a.double() @ b.double().t().contiguous()).float()
+    assert ref.abs().max() < 2**24
+    y = R.int8_matmul(R.int8_quantize(a), R.int8_quantize(b), dtype=torch.float32)
+    assert torch.equal(y, ref)
+    assert torch.equal(R.int8_matmul(a, R.int8_quantize(b)), ref)
+    half = R.int8_matmul(R.int8_quantize(a), R.int8_quantize(b), bias=torch.ones(N, device=a.device, dtype=torch.bfloat16))
+    assert torch.equal(half, (ref + 1).to(torch.bfloat16))
+
+
 def test_sums_past_32_bits():
     """K past 2^17 with every product at 127^2: the sums leave int32, and are exact all the same."""
     K = 140001
@@ -575,6 +589,50 @@ def test_two_streams_and_two_graphs_at_once():
         torch.cuda.synchronize()
         for k in (0, 1):
             assert all(torch.equal(a, b) for a, b in zip(outs[k], want[k]))
+
+
+def test_calls_from_several_threads_at_once():
+    """Host threads, each on a stream of its own, with sizes of their own, so that nothing that one thread's call planned serves another's."""
+    def step(k):
+        rng = np.random.default_rng(90 + k)
+        x, w, dy = (_gpu(rng.standard_normal(s), "bf16") for s in ((200 + 61 * k, 700), (700, 500 + 40 * k), (200 + 61 * k, 500 + 40 * k)))
+        g = _gpu(1 + 0.1 * rng.standard_normal(700), "f32")
+        torch.cuda.synchronize()  # the inputs are made on the default stream
+
+        def call():
+            wr, wc = R.int8_quantize(w, axis=None)
+            y, mean, rstd = R.layer_norm(x, g, save=True)
+            xr, xc = R.int8_quantize(y, axis=None)
+            z = R.int8_matmul(xr, wc)
+            dh, dw, db = R.int8_backward(dy, wr, xc, bias=True)
+            one = R.int8_matmul(R.layer_norm(x[:1 + k], g, quantize="int8"), wc)
+            return [y, z, dh, dw, db, one, R.int8_matmul(x[:1 + k], wc), *R.layer_norm_backward(dh, x, mean, rstd, g)]
+
+        return call
+
+    steps = [step(k) for k in range(4)]
+    want = [s() for s in steps]
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in steps], []
+
+    def go(k):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(10):
+                    got[k].append(steps[k]())
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=go, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for k in range(4):
+        assert len(got[k]) == 10 and all(torch.equal(a, b) for out in got[k] for a, b in zip(out, want[k]))
 
 
 def test_calls_refuse_what_they_cannot_record():
