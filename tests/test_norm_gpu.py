@@ -293,6 +293,28 @@ def test_offsets_past_32_bits(M, K):
     assert bool(((db.double() - want).abs() <= (M / 64 + 300) * 2.0**-24 * size).all())
 
 
+@pytest.mark.parametrize("M,K", [(280_000, 16_384), (140_000, 32_768), (5_000_000, 900)])
+def test_weight_gradients_past_32_bits(M, K):
+    """More than 2^32 elements of dy and of another x: both sums over all rows, in float64 chunk by chunk beside them. No sum goes through more
+    than 1030 float32 additions; a term of dweight has three roundings, the result one."""
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(81)
+    x, dy = (torch.randn(M, K, generator=gen, device=dev(), dtype=torch.bfloat16) for _ in range(2))
+    mean, rstd = torch.randn(M, generator=gen, device=dev()), 1 + torch.rand(M, generator=gen, device=dev())
+    dx, dw, db = R.layer_norm_backward(dy, x, mean, rstd, torch.ones(K, device=dev()))
+    del dx
+    assert x.numel() > 2**32
+    want, size = torch.zeros(2, K, dtype=torch.float64, device=dev()), torch.zeros(2, K, dtype=torch.float64, device=dev())
+    step = 2**28 // K
+    for k in range(0, M, step):
+        d = dy[k: k + step].double()
+        for i, t in enumerate(((x[k: k + step].double() - mean[k: k + step, None]).mul_(rstd[k: k + step, None]).mul_(d), d)):
+            want[i] += t.sum(0)
+            size[i] += t.abs_().sum(0)
+    for i, g in enumerate((dw, db)):
+        assert bool(((g.double() - want[i]).abs() <= 1034 * 2.0**-24 * size[i]).all())
+
+
 def test_refusals_of_the_binding():
     d = dev()
     x, w = torch.ones(4, 64, device=d), torch.ones(64, device=d)
