@@ -95,6 +95,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_i8_decode(I8GemmParams p) {
     int slot_row[SLOTS];
     int64_t slot_c[SLOTS];
     if (lane < 16) row_max[wave][lane] = 0;
+    // lane 0 goes on from what the others wrote
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (kept) {
 #pragma unroll
       for (int u = 0; u < SLOTS; u++) {
