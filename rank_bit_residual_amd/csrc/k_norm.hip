@@ -497,8 +497,13 @@ template <class DT, int OUT>
 static hipError_t norm_t(const NormParams& p, hipStream_t stream) {
   const int64_t Kp = OUT == NORM_Y ? p.K : (OUT == NORM_I8 ? (int64_t)p.i8.kq * 64 : (int64_t)p.mx.kq * 128);
   // Two vectors a thread; four of 256 threads past 4096 columns where there are many rows, unless their codes wait for a second
-  // maximum. 8192 x 8192 bf16, four of 256, two of 512, one of 1024: 56, 61 and 68 us, to 8 bits 71, 70 and 94, to MXFP4 52, 58 and 73;
-  // 777 x 5003 13.2, 10.2 and 10.3. Three of 512 past 8192 columns: 8192 x 12288 bf16 87 us, two of 1024 107, to 8 bits 120 and 132
+  // maximum or float32 rows leave as float32. Four of 256 and two of 512, us: bf16 1024 x 5003 14.7 and 10.5, 4096 x 5003 32.6 and 30.1,
+  // 6000 x 6144 39.0 and 40.7, 8192 x 8192 51.7 and 54.0, 16384 x 6144 90 and 99; to MXFP4 2048 x 5003 18.4 and 17.2, 3000 x 6144 23.1 and 23.9, 8192 x
+  // 8192 51.9 and 57.7; to 8 bits 8192 x 5003 71 and 69, 8192 x 8192 68.0 and 68.9; float32 4096 x 8192 52.2 and 50.2, 16384 x 8192 204 and 193, to
+  // MXFP4 4096 x 5003 34.9 and 31.8, 8192 x 8192 67.2 and 67.4, 16384 x 6144 111 and 117. (One of 1024: 8192 x 8192 bf16 68, to 8 bits 94.) Three of
+  // 512 past 8192 columns: 8192 x 12288 bf16 87 us, two of 1024 107, to 8 bits 120 and 132
+  constexpr bool four = OUT == NORM_MX || (OUT == NORM_Y && DT::size == 2);
+  constexpr int64_t many = DT::size == 4 ? 8192 : (OUT == NORM_MX ? 3000 : 5000);
   if (p.K < 8)
     launch_rows<DT, 1024, 0, OUT>(p, stream);
   else if (Kp <= 512)
@@ -509,11 +514,14 @@ static hipError_t norm_t(const NormParams& p, hipStream_t stream) {
     launch_rows<DT, 128, 2, OUT>(p, stream);
   else if (Kp <= 4096)
     launch_rows<DT, 256, 2, OUT>(p, stream);
-  else if (Kp <= 8192 && OUT != NORM_I8 && p.M > 2048)
-    launch_rows<DT, 256, 4, OUT>(p, stream);
-  else if (Kp <= 8192)
+  else if (Kp <= 8192) {
+    if constexpr (four)
+      if (p.M > many) {
+        launch_rows<DT, 256, 4, OUT>(p, stream);
+        return hipGetLastError();
+      }
     launch_rows<DT, 512, 2, OUT>(p, stream);
-  else if (Kp <= 12288)
+  } else if (Kp <= 12288)
     launch_rows<DT, 512, 3, OUT>(p, stream);
   else if (Kp <= 16384)
     launch_rows<DT, 1024, 2, OUT>(p, stream);

@@ -112,6 +112,12 @@ def test_many_rows(M, K, dtype):
         assert (np.abs(_np(g) - r) <= bound).all()
 
 
+@pytest.mark.parametrize("M,K,dtype", [(5200, 4500, "bf16"), (6100, 8190, "f16"), (3100, 5003, "bf16"), (8300, 4200, "f32")])
+def test_many_rows_of_four_vectors_a_thread(M, K, dtype):
+    """The form of many rows of 4096 to 8192 columns, of 16-bit values and of MXFP4 tensors."""
+    test_many_rows(M, K, dtype)
+
+
 def test_far_means_and_outliers():
     """Means 10^4 standard deviations off, a first element that is the row's outlier, constant rows, and the ends of the range."""
     rng = np.random.default_rng(2)
