@@ -107,29 +107,23 @@ __device__ inline void fit8(Vec8<DT>& v, int64_t c, int64_t K, u32 past = 0) {
   }
 }
 
-// The same with elements of the row in the places past its end, for what a product with 0 must take back out: they are infinite or NaN
-// only if the row's own are.
+// The same where the places past the row's end keep elements of the row, for what a product with 0 must take back out: they are infinite or
+// NaN only if the row's own are.
 template <class DT>
 __device__ inline void turn8(Vec8<DT>& v, int64_t c, int64_t K) {
   if (!__builtin_amdgcn_ballot_w64(c + 8 > K)) return;
-  const int s = c + 8 <= K ? 0 : (int)(c + 8 - K) & 7;  // elements to turn by
+  const int s = c + 8 <= K || c >= K ? 0 : (int)(c + 8 - K);  // elements to move down by, as masks for each power of two
+  const u32 m4 = 0u - (u32)(s >> 2 & 1), m2 = 0u - (u32)(s >> 1 & 1), m1 = 0u - (u32)(s & 1);
+  auto pick = [](u32 m, u32 a, u32 b) { return (a & m) | (b & ~m); };
   constexpr int W = DT::size * 2, E = W / 4;
-  u32 first[E];
 #pragma unroll
-  for (int k = 0; k < W / 2; k++) {
-    const u32 low = v.w[k];
-    v.w[k] = s & 4 ? v.w[k + W / 2] : low;
-    v.w[k + W / 2] = s & 4 ? low : v.w[k + W / 2];
-  }
+  for (int k = 0; k < W - 2 * E; k++) v.w[k] = pick(m4, v.w[k + 2 * E], v.w[k]);
 #pragma unroll
-  for (int k = 0; k < E; k++) first[k] = v.w[k];
-#pragma unroll
-  for (int k = 0; k < W; k++) v.w[k] = s & 2 ? (k + E < W ? v.w[(k + E) % W] : first[(k + E) % E]) : v.w[k];
-  first[0] = v.w[0];
+  for (int k = 0; k < W - E; k++) v.w[k] = pick(m2, v.w[k + E], v.w[k]);
 #pragma unroll
   for (int k = 0; k < W; k++) {
-    const u32 up = k + 1 < W ? v.w[(k + 1) % W] : first[0];
-    v.w[k] = s & 1 ? (DT::size == 4 ? up : (v.w[k] >> 16) | (up << 16)) : v.w[k];
+    const u32 up = v.w[k + 1 < W ? k + 1 : k];
+    v.w[k] = pick(m1, DT::size == 4 ? up : (v.w[k] >> 16) | (k + 1 < W ? up << 16 : up & 0xFFFF0000u), v.w[k]);
   }
 }
 // And of a vector of which the first n elements, one at least, are the row's.

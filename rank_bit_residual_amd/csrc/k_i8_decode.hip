@@ -203,7 +203,7 @@ constexpr int kRawBytes = 64 * 1024;  // of LDS for the codes of unquantised row
 // One row always; two to four while their shares fit a wave's registers and the columns do not repeat the work too often. As one launch
 // against two, us on the GPU's clock (a launch costs 2.7 us of the host's besides): one row x 8192 x 8192 15.7 and 17.4, x 4096 x 4096 6.3 and 7.9,
 // x 1024 x 1024 4.2 and 5.1; two rows x 8192 x 4096 11.0 and 11.5; four x 4096 x 4096 7.6 and 8.0, x 1024 x 1024 5.6 and 5.3, x 8192 x 1024 9.5
-// and 8.6.
+// and 8.6. (Four x 1024 x 1024 lose 0.3 us on the GPU's clock for the host's 2.7; in a captured graph only the loss counts.)
 bool i8_raw_rows(int64_t M, int64_t N, int64_t K, int64_t sc) {
   const int64_t kq = i8_kq(K);
   if (sc != 1 || M * kq * 64 > kRawBytes) return false;

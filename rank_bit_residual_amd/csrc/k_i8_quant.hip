@@ -7,8 +7,9 @@
 //
 // A row is read once: it stays in the registers of the threads that share it while they agree on its maximum. A column's maximum
 // comes before its first code, so columns are read twice: partial maxima (and sums) of strips of rows, their join, then the codes,
-// which change places through LDS as bytes. All kernels are bound by memory; 8192 x 12288 bf16: rows 66 us (4.6 TB/s), columns 99, both 142
-// (rows and maxima 82, the join 5, the columns' codes 55), the values of a tensor 54 (5.6 TB/s).
+// which change places through LDS as bytes. All kernels are bound by memory; 8192 x 12288 bf16: rows 62 us (4.8 TB/s), columns 97, both 139
+// in captured calls (by trace of eager ones 92 for rows and maxima, 5 for the join and 55 for the columns' codes), the values of a tensor 54
+// (5.6 TB/s).
 #include <type_traits>
 
 #include "i8.h"
@@ -321,8 +322,8 @@ static void launch_rows(const I8QuantParams& p, hipStream_t stream) {
   k_i8_rows<DT, T, NV, ROWS_ALONE><<<(unsigned)(blocks < most ? blocks : most), THREADS, 0, stream>>>(p, nullptr, nullptr);
 }
 
-// Two or three vectors a thread, so that several rows are on a compute unit: 8192 x 12288 bf16 66 us with 512 threads of three, 4096 x
-// 4096 13 with 256 of two (128 of four a third more).
+// Two or three vectors a thread, so that several rows are on a compute unit: 8192 x 12288 bf16 62 us with 512 threads of three, 4096 x
+// 4096 11.6 with 256 of two (128 of four a third more).
 template <class DT>
 static hipError_t rows_t(const I8QuantParams& p, hipStream_t stream) {
   const int64_t Kp = (int64_t)p.rows.kq * 64;

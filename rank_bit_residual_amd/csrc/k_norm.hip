@@ -1,18 +1,19 @@
 // Layer norm on gfx950: y = (x - mean) / sqrt(var + eps) * weight + bias of each row, as it is or as the 8-bit or MXFP4 tensor of y,
 // and its backward pass.
 //
-// Forward: a row is read once and stays in the registers of the threads that share it. Sums and y are binary64, whose adds and
-// multiply-adds take this chip no longer than float32's: with d = x - x[0], mean = x[0] + sum d / K and var = sum d^2 / K - (sum d /
-// K)^2 come from one reduction, and since (x[0] - mean)^2 <= K var the subtraction costs log2 K of 53 bits at most. y is rounded to
+// Forward: a row is read once and stays in the registers of the threads that share it. Sums and y are binary64, whose sums and
+// products issue nearly as fast as float32's where waves share a SIMD (with eight, 2.0 to 2.2 ns an instruction against 1.8; conversions to
+// it take 3.6): with d = x - x[0], mean = x[0] + sum d / K and var = sum d^2 / K - (sum d / K)^2 come from one reduction, and since
+// (x[0] - mean)^2 <= K var the subtraction costs log2 K of 53 bits at most. y is rounded to
 // float32 once, and that is what is quantised or rounded on to the output's type; a code is decided by comparing with a border, so
-// rounding earlier would move one now and then. Memory bounds float32 rows and large 16-bit ones (8192 x 8192 97 us and 56, 5.5 and 4.8
-// TB/s); where fewer bytes leave, the binary64 steps (13 an element) and the codes do: to 8 bits 70 us, to MXFP4 52, of 38 and 32 for the
-// bytes alone. The parameters wait as float32, as binary64 they would cost the third wave of registers.
+// rounding earlier would move one now and then. Memory bounds float32 rows and large 16-bit ones (8192 x 8192 98 us and 53, 5.5 and 5.1
+// TB/s); where fewer bytes leave, the binary64 steps (12 an element, four of them conversions to it) and the codes do: to 8 bits 69 us, to MXFP4 52,
+// of 38 and 32 for the bytes alone. The parameters wait as float32, as binary64 they would cost the third wave of registers.
 //
 // Backward: with xh = (x - mean) rstd and g = dy weight, dx = rstd (g - mean(g) - xh mean(g xh)): one reduction, with dy and x in
 // registers. A thread keeps the same columns in every row of its block, so dweight = sum dy xh and dbias = sum dy are running sums
-// in registers, over 1024 rows at most; each block leaves its own, and a last kernel adds them in binary64 in the blocks' order. Memory bounds it: 8192 x 8192 bf16 76 us (5.3
-// TB/s) and 5 for the second kernel.
+// in registers, over 1024 rows at most; each block leaves its own, and a last kernel adds them in binary64 in the blocks' order. Memory
+// bounds it: 8192 x 8192 bf16 75 us (5.4 TB/s) and 5 for the last kernel.
 #include <type_traits>
 
 #include "i8.h"
@@ -299,6 +300,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_grad(NormGradParams 
       if (j == NV - 1) {
         fit8<DT>(cur[j].dy, (int64_t)(j * T + t) * 8, p.K);
         turn8<DT>(cur[j].x, (int64_t)(j * T + t) * 8, p.K);  // not zeros: (0 - mean) rstd may be infinite, and 0 times it NaN
+        if constexpr (!AHEAD) {  // or float32 rows of 16384 spill twice as much, 188 us and not 177
+          settle(cur[j].dy);
+          settle(cur[j].x);
+        }
       }
 #pragma unroll
       for (int k = 0; k < 8; k++) {
